@@ -38,6 +38,13 @@ __all__ = [
     "gather_workspace_bytes",
     "gather_qmm_noalloc",
     "quantize",
+    "qk_norm_rope",
+    "rope_inv_freq",
+    "kv_block_bytes",
+    "kv_append",
+    "kv_read",
+    "kv_attention",
+    "kv_attention_workspace_bytes",
     "set_wait_budget",
     "NOALLOC_SCRATCH_BYTES",
     "MxqError",
@@ -45,6 +52,9 @@ __all__ = [
     "DEV_UNSORTED_IDS",
     "DEV_BAD_ROW_SRC",
     "DEV_TIMEOUT",
+    "DEV_BAD_SLOT",
+    "DEV_BAD_PAGE",
+    "DEV_BAD_SEQUENCE",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -66,6 +76,9 @@ DEV_BAD_EXPERT_ID = 0x1
 DEV_UNSORTED_IDS = 0x2
 DEV_BAD_ROW_SRC = 0x4
 DEV_TIMEOUT = 0x8
+DEV_BAD_SLOT = 0x10
+DEV_BAD_PAGE = 0x20
+DEV_BAD_SEQUENCE = 0x40
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # MXQ_NOALLOC_SCRATCH_BYTES
 
 EXPORTED_SYMBOLS = (
@@ -79,6 +92,12 @@ EXPORTED_SYMBOLS = (
     "mxq_gather_workspace_bytes",
     "mxq_gather_qmm_noalloc",
     "mxq_quantize",
+    "mxq_qk_norm_rope",
+    "mxq_kv_block_bytes",
+    "mxq_kv_append",
+    "mxq_kv_read",
+    "mxq_kv_attention",
+    "mxq_kv_attention_workspace_bytes",
     "mxq_status_string",
     "mxq_version",
     "mxq_debug_set_wait_budget",
@@ -124,6 +143,21 @@ def lib():
         L.mxq_gather_qmm_noalloc.restype = I
         L.mxq_quantize.argtypes = [P, P, P, P, I, I, I, I, P]
         L.mxq_quantize.restype = I
+        J, F = ctypes.c_longlong, ctypes.c_float
+        L.mxq_qk_norm_rope.argtypes = [P, J, J, P, J, J, P, P, P, P, P, J, J, P, J, J, I, I, I, I,
+                                       I, I, F, F, F, P]
+        L.mxq_qk_norm_rope.restype = I
+        L.mxq_kv_block_bytes.argtypes = [I, I, I]
+        L.mxq_kv_block_bytes.restype = Z
+        L.mxq_kv_append.argtypes = [P, J, J, P, J, J, P, P, I, I, I, I, I, I, P, P]
+        L.mxq_kv_append.restype = I
+        L.mxq_kv_read.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P]
+        L.mxq_kv_read.restype = I
+        L.mxq_kv_attention.argtypes = [P, J, J, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F,
+                                       I, I, P, Z, P, P]
+        L.mxq_kv_attention.restype = I
+        L.mxq_kv_attention_workspace_bytes.argtypes = [I, I, I, I]
+        L.mxq_kv_attention_workspace_bytes.restype = Z
         L.mxq_gather_workspace_bytes.argtypes = [I, I, I, I]
         L.mxq_gather_workspace_bytes.restype = Z
         L.mxq_status_string.argtypes = [I]
@@ -537,6 +571,297 @@ def gather_qmm_gateup(x, w_gate, s_gate, b_gate, w_up, s_up, b_up, expert_ids, r
             group_size, _ptr(workspace), workspace.numel(), _ptr(dev_status), st),
             "mxq_gather_qmm_gateup")
     return outs[0], outs[1]
+
+
+# ------------------------------------------------- 4-bit key/value cache
+
+def _heads(t, name, device=None, out=False):
+    """Checks a bf16 [T, heads, D] tensor whose heads are contiguous; returns
+    its (row, head) strides in values."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype is not torch.bfloat16:
+        raise TypeError("%s has dtype %s, expected torch.bfloat16" % (name, t.dtype))
+    if t.dim() != 3:
+        raise ValueError("%s must be 3-D [T, heads, D]" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    (n, h, d), (rs, hs, vs) = t.shape, t.stride()
+    if vs != 1 and d > 1:
+        raise ValueError("the values of a head of %s must be contiguous" % name)
+    hs = hs if h > 1 else d
+    rs = rs if n > 1 else h * d
+    if rs % 8 or hs % 8:
+        raise ValueError("the strides of %s must be multiples of 8 values" % name)
+    if out and ((h > 1 and hs < d) or (n > 1 and rs < d) or
+                (n > 1 and h > 1 and rs < h * hs and hs < n * rs)):
+        raise ValueError("the rows of %s overlap" % name)
+    return rs, hs
+
+
+def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling=None, factor: float = 1.0,
+                  original_len: int = 0, low: float = 1.0, high: float = 4.0,
+                  beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """The rotation's frequencies ``theta^(-2 j / rot_dim)`` (fp32
+    [rot_dim/2]) and the factor of its cosines and sines, ``(inv_freq,
+    rope_scale)`` for ``qk_norm_rope``; computed in 64 bits.
+
+    ``scaling`` stretches them for contexts ``factor`` times as long as the
+    ``original_len`` tokens that a model was trained on:
+
+    * ``"linear"``: every frequency divided by ``factor``;
+    * ``"base"``: theta raised to ``theta * factor^(rot_dim / (rot_dim - 2))``,
+      which leaves the highest frequency and divides the lowest by ``factor``;
+    * ``"bands"``: by the turns that a frequency makes in ``original_len``
+      tokens: below ``low`` divided by ``factor``, above ``high`` kept, between
+      them mixed linearly in the turns;
+    * ``"yarn"``: divided by ``factor`` from the value whose frequency makes
+      ``beta_slow`` turns on, kept up to the one that makes ``beta_fast``,
+      mixed linearly in the index between; ``rope_scale = 0.1 ln(factor) + 1``.
+    """
+    import math
+
+    torch = _torch()
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be positive and even")
+    if not theta > 0 or not factor >= 1.0:
+        raise ValueError("theta must be positive and factor at least 1")
+    j = torch.arange(rot_dim // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "base":
+        if rot_dim <= 2:
+            raise ValueError("base scaling needs rot_dim > 2")
+        theta = theta * factor ** (rot_dim / (rot_dim - 2.0))
+    freq = theta ** (-2.0 * j / rot_dim)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling in ("bands", "yarn"):
+        if original_len <= 0:
+            raise ValueError("%s scaling needs original_len" % scaling)
+        if scaling == "bands":
+            if not high > low:
+                raise ValueError("high must be above low")
+            turns = original_len * freq / (2.0 * math.pi)
+            keep = ((turns - low) / (high - low)).clamp(0.0, 1.0)
+        else:
+            def index(turns):
+                return rot_dim * math.log(original_len / (turns * 2.0 * math.pi)) / (
+                    2.0 * math.log(theta))
+
+            first = max(math.floor(index(beta_fast)), 0)
+            last = min(math.ceil(index(beta_slow)), rot_dim - 1)
+            keep = 1.0 - ((j - first) / max(last - first, 0.001)).clamp(0.0, 1.0)
+            scale = 0.1 * math.log(factor) + 1.0
+        freq = freq * (keep + (1.0 - keep) / factor)
+    elif scaling not in (None, "base"):
+        raise ValueError("unknown scaling %r" % (scaling,))
+    return freq.to(torch.float32).to(device if device is not None else "cpu"), scale
+
+
+def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+                 weight_offset=0.0, interleaved=False, rope_scale=1.0, q_out=None, k_out=None,
+                 stream=None):
+    """RMS norm of query and key heads (``q_weight``/``k_weight`` bf16 [D];
+    None: no norm) and the rotary position (``positions`` int32 [T],
+    ``inv_freq`` fp32 [rot_dim/2]; None: no rotation) in one pass.
+
+    ``q`` bf16 [T, Hq, D] and ``k`` bf16 [T, Hk, D] or None may be slices of
+    one projection's output (heads contiguous, strides multiples of 8);
+    ``q_out``/``k_out`` may be ``q``/``k`` themselves.  Returns (q_out, k_out)."""
+    torch = _torch()
+    q_rs, q_hs = _heads(q, "q")
+    dev = q.device
+    T, Hq, D = q.shape
+    Hk = k_rs = k_hs = k_ors = k_ohs = 0
+    if k is not None:
+        k_rs, k_hs = _heads(k, "k", dev)
+        Hk = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("k has shape %s, expected [%d, heads, %d]" % (tuple(k.shape), T, D))
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    rot = 0
+    if inv_freq is not None:
+        _require(inv_freq, "inv_freq", (torch.float32,), dev)
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _require(positions, "positions", (torch.int32,), dev)
+        if positions.numel() != T:
+            raise ValueError("positions must have T entries")
+        rot = 2 * inv_freq.numel()
+        if inv_freq.dim() != 1 or rot == 0:
+            raise ValueError("inv_freq must be 1-D [rot_dim/2]")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _require(w, name, (torch.bfloat16,), dev)
+            if tuple(w.shape) != (D,):
+                raise ValueError("%s has shape %s, expected %s" % (name, tuple(w.shape), (D,)))
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
+    for o, i, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if o is not None and o.shape != i.shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(o.shape), tuple(i.shape)))
+    q_ors, q_ohs = _heads(q_out, "q_out", dev, out=True)
+    if k is not None:
+        k_ors, k_ohs = _heads(k_out, "k_out", dev, out=True)
+    ctx, st = _launch_on(dev, stream)
+    with ctx:
+        _check(lib().mxq_qk_norm_rope(
+            _ptr(q), q_rs, q_hs, _ptr(k), k_rs, k_hs, _ptr(positions) if rot else None,
+            _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(q_out), q_ors, q_ohs,
+            _ptr(k_out), k_ors, k_ohs, T, Hq, Hk, D, rot, int(interleaved), eps, weight_offset,
+            rope_scale, st), "mxq_qk_norm_rope")
+    return q_out, k_out
+
+
+def kv_block_bytes(head_dim: int, page_size: int, group_size: int = 64) -> int:
+    """Bytes of one page of the 4-bit cache for one key/value head: a cache is
+    a uint8 tensor ``[n_pages, kv_heads, kv_block_bytes(...)]``."""
+    n = int(lib().mxq_kv_block_bytes(head_dim, page_size, group_size))
+    if n == 0:
+        raise ValueError("no cache of head_dim %s, page_size %s, group_size %s" % (
+            head_dim, page_size, group_size))
+    return n
+
+
+def _cache(pages, head_dim, group_size, device, kv_heads=None):
+    """Checks a cache tensor and returns (n_pages, kv_heads, page_size)."""
+    torch = _torch()
+    _require(pages, "pages", (torch.uint8,), device)
+    if pages.dim() != 3:
+        raise ValueError("pages must be [n_pages, kv_heads, block bytes]")
+    n, h, block = pages.shape
+    if kv_heads is not None and h != kv_heads:
+        raise ValueError("pages hold %d heads, expected %d" % (h, kv_heads))
+    if head_dim not in (64, 128, 256) or group_size not in (32, 64, 128) or group_size > head_dim:
+        raise ValueError("no cache of head_dim %s and group_size %s" % (head_dim, group_size))
+    per = head_dim + 8 * (head_dim // group_size)
+    if block % per or block // per not in (16, 32, 64, 128):
+        raise ValueError("a block of %d bytes is no page of head_dim %d, group_size %d" % (
+            block, head_dim, group_size))
+    return n, h, block // per
+
+
+def kv_append(k, v, pages, slots, group_size: int = 64, dev_status=None, stream=None):
+    """Encodes the rows ``k``, ``v`` (bf16 [T, kv_heads, D], heads contiguous)
+    to 4 bits and writes row t to slot ``slots[t]`` (int32 [T], page *
+    page_size + token; negative: skipped) of the cache ``pages``."""
+    torch = _torch()
+    k_rs, k_hs = _heads(k, "k")
+    v_rs, v_hs = _heads(v, "v", k.device)
+    if v.shape != k.shape:
+        raise ValueError("v has shape %s, expected %s" % (tuple(v.shape), tuple(k.shape)))
+    T, H, D = k.shape
+    n_pages, _, page_size = _cache(pages, D, group_size, k.device, H)
+    _require(slots, "slots", (torch.int32,), k.device)
+    if slots.numel() != T:
+        raise ValueError("slots must have T entries")
+    if dev_status is not None:
+        _require(dev_status, "dev_status", (torch.int32,), k.device)
+    ctx, st = _launch_on(k.device, stream)
+    with ctx:
+        _check(lib().mxq_kv_append(_ptr(k), k_rs, k_hs, _ptr(v), v_rs, v_hs, _ptr(pages),
+                                   _ptr(slots), T, H, D, n_pages, page_size, group_size,
+                                   _ptr(dev_status), st), "mxq_kv_append")
+    return pages
+
+
+def kv_read(pages, slots, head_dim: int, group_size: int = 64, k_out=None, v_out=None,
+            dev_status=None, stream=None):
+    """The rows of ``slots`` (int32 [T]) out of the cache: (k, v) bf16 [T,
+    kv_heads, head_dim]; zeros for a negative slot."""
+    torch = _torch()
+    n_pages, H, page_size = _cache(pages, head_dim, group_size, None)
+    dev = pages.device
+    _require(slots, "slots", (torch.int32,), dev)
+    T = slots.numel()
+    outs = []
+    for o, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if o is None:
+            o = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=dev)
+        _require(o, name, (torch.bfloat16,), dev)
+        if tuple(o.shape) != (T, H, head_dim):
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(o.shape),
+                                                               (T, H, head_dim)))
+        outs.append(o)
+    if dev_status is not None:
+        _require(dev_status, "dev_status", (torch.int32,), dev)
+    ctx, st = _launch_on(dev, stream)
+    with ctx:
+        _check(lib().mxq_kv_read(_ptr(pages), _ptr(slots), _ptr(outs[0]), _ptr(outs[1]), T, H,
+                                 head_dim, n_pages, page_size, group_size, _ptr(dev_status), st),
+               "mxq_kv_read")
+    return outs[0], outs[1]
+
+
+def kv_attention_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_q_len: int) -> int:
+    """Workspace bytes for kv_attention."""
+    return int(lib().mxq_kv_attention_workspace_bytes(heads, kv_heads, head_dim, max_q_len))
+
+
+def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int = 1,
+                 group_size: int = 64, scale=None, window: int = 0, sinks: int = 0, out=None,
+                 lse=None, workspace=None, dev_status=None, stream=None):
+    """Causal attention of ``q`` (bf16 [T, heads, D]) over a 4-bit paged cache.
+
+    Sequence i holds ``ctx_lens[i]`` tokens in the pages ``page_table[i]``
+    (int32 [S, max_pages]); its query rows ``q_starts[i]:q_starts[i+1]``
+    (int32 [S+1]; None: one row per sequence) are its last tokens, at most
+    ``max_q_len`` of them.  With ``window`` a row sees the last ``window``
+    tokens up to its own and the first ``sinks``.  ``scale`` defaults to
+    D^-1/2.  ``lse`` (fp32 [T, heads]) receives the log sum exp.  Returns out
+    bf16 [T, heads, D]; a row that sees nothing is 0."""
+    torch = _torch()
+    q_rs, q_hs = _heads(q, "q")
+    dev = q.device
+    T, Hq, D = q.shape
+    n_pages, Hkv, page_size = _cache(pages, D, group_size, dev)
+    if Hq == 0 or Hq % Hkv:
+        raise ValueError("%d query heads do not divide over %d key/value heads" % (Hq, Hkv))
+    _require(page_table, "page_table", (torch.int32,), dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D [S, max_pages]")
+    S, max_pages = page_table.shape
+    _require(ctx_lens, "ctx_lens", (torch.int32,), dev)
+    if ctx_lens.numel() != S:
+        raise ValueError("ctx_lens must have S entries")
+    if q_starts is not None:
+        _require(q_starts, "q_starts", (torch.int32,), dev)
+        if q_starts.numel() != S + 1:
+            raise ValueError("q_starts must have S + 1 entries")
+    elif T != S or max_q_len != 1:
+        raise ValueError("without q_starts every sequence has one row: T must be S, max_q_len 1")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    _require(out, "out", (torch.bfloat16,), dev)
+    if tuple(out.shape) != (T, Hq, D):
+        raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), (T, Hq, D)))
+    if lse is not None:
+        _require(lse, "lse", (torch.float32,), dev)
+        if tuple(lse.shape) != (T, Hq):
+            raise ValueError("lse has shape %s, expected %s" % (tuple(lse.shape), (T, Hq)))
+    if dev_status is not None:
+        _require(dev_status, "dev_status", (torch.int32,), dev)
+    if max_q_len <= 0:
+        raise ValueError("max_q_len must be positive")
+    if workspace is None:
+        need = kv_attention_workspace_bytes(Hq, Hkv, D, max(1, min(max_q_len, T)))
+        workspace = torch.empty((need,),
+                                dtype=torch.uint8, device=dev)
+    _require(workspace, "workspace", (torch.uint8,), dev)
+    ctx, st = _launch_on(dev, stream)
+    with ctx:
+        _check(lib().mxq_kv_attention(
+            _ptr(q), q_rs, q_hs, _ptr(pages), _ptr(page_table), _ptr(ctx_lens), _ptr(q_starts),
+            _ptr(out), _ptr(lse), T, S, Hq, Hkv, D, n_pages, max_pages, page_size, group_size,
+            max_q_len, D ** -0.5 if scale is None else scale, window, sinks, _ptr(workspace),
+            workspace.numel(), _ptr(dev_status), st), "mxq_kv_attention")
+    return out
 
 
 def set_wait_budget(cycles: int) -> int:

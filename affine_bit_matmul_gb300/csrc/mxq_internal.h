@@ -141,4 +141,72 @@ cudaError_t launch_qmv_kn(const void* x, const uint32_t* w, const void* scales, 
 cudaError_t launch_gather_rows(const void* x, const int32_t* row_src, int T, int B, int K,
                                void* x_sorted, cudaStream_t stream);
 
+// One side (queries or keys) of the norm-and-rotation pass; strides in values.
+struct NormRopeSide {
+    const __nv_bfloat16* x;
+    long long row_stride, head_stride;
+    const __nv_bfloat16* weight;  // bf16 [D], or null: no norm
+    __nv_bfloat16* out;
+    long long out_row_stride, out_head_stride;
+};
+
+struct NormRopeParams {
+    NormRopeSide q, k;
+    const int32_t* positions;  // int32 [T] (rot > 0)
+    const float* inv_freq;     // fp32 [rot / 2]
+    int T, Hq, Hk, D, rot, interleaved;
+    float eps, weight_offset, rope_scale;
+};
+
+cudaError_t launch_qk_norm_rope(const NormRopeParams& p, int sms, cudaStream_t stream);
+
+// Rows going into, or coming out of, the pages of a 4-bit key/value cache.
+struct KvRowsParams {
+    const __nv_bfloat16* k;  // append: bf16 [T, H, D], strides in values
+    const __nv_bfloat16* v;
+    long long k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+    __nv_bfloat16* k_out;    // read: bf16 [T, H, D]
+    __nv_bfloat16* v_out;
+    uint8_t* pages;
+    const int32_t* slots;
+    int T, H, n_pages, page_size;
+    int32_t* status;
+};
+
+cudaError_t launch_kv_append(const KvRowsParams& p, int D, int G, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvRowsParams& p, int D, int G, cudaStream_t stream);
+
+// Attention over the cache.  A row tile is up to `tile_rows` rows, each one
+// (token, query head) of one sequence and key/value head; a plane is the row
+// tiles of one index over all sequences.
+struct KvAttnParams {
+    const __nv_bfloat16* q;  // bf16 [T, Hq, D], strides in values
+    long long q_row_stride, q_head_stride;
+    const uint8_t* pages;
+    const int32_t* table;    // int32 [S, max_pages]
+    const int32_t* ctx_lens; // int32 [S]
+    const int32_t* q_starts; // int32 [S + 1], or null: one row a sequence
+    __nv_bfloat16* out;      // bf16 [T, Hq, D]
+    float* lse;              // fp32 [T, Hq], or null
+    int T, S, n_pages, max_pages, Hq, Hkv, page_size, max_q;
+    int window, sinks;
+    float scale_log2;        // softmax scale * log2(e)
+    int head_parts;          // a key/value head's query heads, in so many row tiles ...
+    int part_heads;          // ... of at most this many heads
+    int tile_toks;           // tokens in a row tile
+    int planes, ctas;        // ctas per plane
+    int* segs;               // workspace: 2 descriptors per CTA
+    float* partial;          // workspace: 2 partial results per CTA
+    int32_t* status;
+    long long wait_budget;
+};
+
+cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int G, int tile_rows,
+                           cudaStream_t stream);
+// Workspace of launch_kv_attn: descriptors, then partial results.
+size_t kv_attn_seg_bytes(int planes, int ctas);
+size_t kv_attn_partial_bytes(int planes, int ctas, int tile_rows, int D);
+// CTAs that fit an SM at these sizes.
+int kv_attn_ctas_per_sm(int D, int tile_rows);
+
 }  // namespace mxq

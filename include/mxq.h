@@ -72,6 +72,11 @@ typedef enum {
 #define MXQ_DEV_BAD_ROW_SRC     0x4 /* a row_src entry outside [0, T)          */
 #define MXQ_DEV_TIMEOUT         0x8 /* an on-chip pipeline wait gave up; the
                                        output is incomplete                   */
+#define MXQ_DEV_BAD_SLOT       0x10 /* a cache slot at or past the last one    */
+#define MXQ_DEV_BAD_PAGE       0x20 /* a page that a row sees is outside the
+                                       cache; its tokens count as not visible */
+#define MXQ_DEV_BAD_SEQUENCE   0x40 /* a sequence's length or rows are out of
+                                       range                                  */
 
 /* Decode GEMV, M = 1 (mlxcel issue #1536, Diagnosis item 3: the qmv kernel;
  * fp32 accumulation at every width is the fix that item names).
@@ -285,6 +290,116 @@ mxq_status mxq_gather_qmm_noalloc(const void* x, const uint32_t* w, const void* 
  * N > 0.                                                                    */
 mxq_status mxq_quantize(const float* w, uint32_t* codes, void* scales, void* biases, int N,
                         int K, int bits, int group_size, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged key/value cache held in 4 bits, and what a layer does between its
+ * q/k/v projections and its output projection.  (The pages that define the
+ * matrix products have no counterpart to these calls: they hold the format
+ * of the weights, affine codes with a bf16 scale and bias per group, for the
+ * keys and values of the attention.)
+ *
+ * The cache is one array of n_pages pages, uint8 [n_pages, Hkv, block bytes];
+ * a page holds page_size tokens (16, 32, 64 or 128) of every key/value head,
+ * and a slot is page * page_size + token.  Per (token, head) the D values
+ * (64, 128 or 256) of the key and of the value are codes q of 4 bits and one
+ * (scale, bias) pair of bf16 per group of G = group_size values (32, 64 or
+ * 128, at most D): k^[d] = s[d/G] * q[d] + b[d/G].
+ * Block of one page and head, mxq_kv_block_bytes(D, page_size, G) bytes:
+ *   K codes  page_size * D/2 bytes
+ *   K pairs  bf16 [page_size][D/G][2]: scale, bias
+ *   V codes, V pairs likewise
+ * Codes lie in slabs of 8 tokens x DS = min(D, 128) values, slab (t/8, d/DS)
+ * after slab; a slab is 32 x DS/32 little-endian words, word (4 r + i) * DS/32
+ * + u holding, lowest nibble first,
+ *   K: token r of the 8, values 32 u + 8 i + 0 .. 7 of the DS
+ *   V: tokens 2 i and 2 i + 1, values 32 u + r + 8 n, n = 0 .. 3: token 2 i
+ *      in the low 16 bits, token 2 i + 1 in the high 16
+ * Pages may be copied, shared by several page tables and reused freely: what
+ * lies in slots that no row sees is never used, whatever bits it holds.
+ * Strides are in values (elements), multiples of 8 and not negative; the D
+ * values of a head are contiguous.  T = 0 (nothing to do) is valid.         */
+
+/* Bytes of one page for one key/value head; 0 if the shape is not supported. */
+size_t mxq_kv_block_bytes(int D, int page_size, int group_size);
+
+/* RMS norm of query and key heads and the rotary position, in one pass:
+ *   n = x * rsqrt(mean(x^2) + eps) * (weight + weight_offset)
+ *   (n1, n2) -> (n1 c - n2 s, n2 c + n1 s),  c, s = rope_scale * cos, sin of
+ *   positions[t] * inv_freq[j]
+ * over the pairs (j, j + rot_dim/2), or (2 j, 2 j + 1) if interleaved, of the
+ * first rot_dim values of each head; the rest keep n.  fp32 throughout (the
+ * angle is reduced from the exact product), one rounding to bf16.
+ *   q: bf16 [T, Hq, D], k: bf16 [T, Hk, D] (either count may be 0)
+ *   positions: int32 [T], any sign; inv_freq: fp32 [rot_dim/2]
+ *   q_weight, k_weight: bf16 [D]; NULL leaves that side without a norm
+ *   q_out, k_out: bf16, may be q and k themselves (same strides)
+ * rope_scale multiplies the rotation (the attention factor of position
+ * scaling methods; 1 otherwise).
+ * Requirements: D % 8 == 0, D <= 256; rot_dim % 16 == 0, rot_dim <= D (0: no
+ * rotation; then at least one weight); pointers 16-byte aligned (positions
+ * and inv_freq 4).                                                          */
+mxq_status mxq_qk_norm_rope(const void* q, long long q_row_stride, long long q_head_stride,
+                            const void* k, long long k_row_stride, long long k_head_stride,
+                            const int32_t* positions, const float* inv_freq, const void* q_weight,
+                            const void* k_weight, void* q_out, long long q_out_row_stride,
+                            long long q_out_head_stride, void* k_out,
+                            long long k_out_row_stride, long long k_out_head_stride, int T,
+                            int Hq, int Hk, int D, int rot_dim, int interleaved, float eps,
+                            float weight_offset, float rope_scale, void* stream);
+
+/* Encode new rows and write them into the cache: row t goes to slots[t].
+ * The rule is mxq_quantize's at 4 bits, with its binary32 decisions, so the
+ * stored bits do not depend on the call that wrote them.
+ *   k, v: bf16 [T, Hkv, D], finite, strided; pages 16-byte aligned
+ *   slots: int32 [T]; a negative slot skips the row, one at or past
+ *   n_pages * page_size is skipped and reported (MXQ_DEV_BAD_SLOT).  Two rows
+ *   with one slot leave either's bits, not necessarily of one row.
+ *   dev_status: device int32 or NULL.                                       */
+mxq_status mxq_kv_append(const void* k, long long k_row_stride, long long k_head_stride,
+                         const void* v, long long v_row_stride, long long v_head_stride,
+                         void* pages, const int32_t* slots, int T, int Hkv, int D, int n_pages,
+                         int page_size, int group_size, int32_t* dev_status, void* stream);
+
+/* The rows of given slots: k_out, v_out bf16 [T, Hkv, D] contiguous, each
+ * value s * q + b rounded once.  Rows of negative slots, and of slots past the
+ * last one (reported), are zero.                                            */
+mxq_status mxq_kv_read(const void* pages, const int32_t* slots, void* k_out, void* v_out, int T,
+                       int Hkv, int D, int n_pages, int page_size, int group_size,
+                       int32_t* dev_status, void* stream);
+
+/* Attention over the cache.  Sequence i has ctx_lens[i] tokens in the cache
+ * (its new ones already appended), in the pages page_table[i, 0 ...], and the
+ * query rows q_starts[i] .. q_starts[i + 1] - 1, which are its last tokens:
+ * row j of n has position p = ctx_lens[i] - n + j and sees the tokens
+ *   t <= p, and with a window only t > p - window or t < sinks.
+ *   out = softmax(scale * q . k^) . v^ over those, bf16 [T, Hq, D] contiguous;
+ * query head h uses key/value head h / (Hq / Hkv).  A row that sees nothing
+ * (ctx_lens[i] < n) is 0.
+ *   q: bf16 [T, Hq, D], strided; q_starts: int32 [S + 1], or NULL: one row per
+ *   sequence (T == S); page_table: int32 [S, max_pages], entries of pages that
+ *   no row sees (behind a window, past the end) may hold anything
+ *   lse: fp32 [T, Hq] or NULL: log sum exp of the scaled scores, -inf for a
+ *   row that sees nothing
+ *   max_q_len: the most rows a sequence has, a host-side bound
+ *   window: 0 for none; sinks: first tokens that stay visible
+ *   workspace: mxq_kv_attention_workspace_bytes(Hq, Hkv, D, max_q_len) bytes,
+ *   256-byte aligned, overwritten
+ * A page number outside [0, n_pages) where a row sees it makes its tokens
+ * invisible and is reported (MXQ_DEV_BAD_PAGE).  A length outside [0, max_pages
+ * * page_size] is clamped to it; a sequence whose rows are not within [0, T],
+ * decrease or exceed max_q_len is left out (its rows of out are not written);
+ * both are reported (MXQ_DEV_BAD_SEQUENCE).  Rows that belong to no sequence
+ * are not written.  No invalid entry makes the kernels read or write out of
+ * bounds.  The result is deterministic for given arguments.
+ * Requirements: Hq % Hkv == 0; scale finite; q, pages, out 16-byte aligned.  */
+mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_head_stride,
+                            const void* pages, const int32_t* page_table, const int32_t* ctx_lens,
+                            const int32_t* q_starts, void* out, float* lse, int T, int S, int Hq,
+                            int Hkv, int D, int n_pages, int max_pages, int page_size,
+                            int group_size, int max_q_len, float scale, int window, int sinks,
+                            void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                            void* stream);
+size_t mxq_kv_attention_workspace_bytes(int Hq, int Hkv, int D, int max_q_len);
 
 /* Static description of a status code. */
 const char* mxq_status_string(mxq_status status);

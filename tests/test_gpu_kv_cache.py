@@ -1,0 +1,146 @@
+"""The paged 4-bit key/value cache on the GPU: rows written and read back, bit
+for bit against the format by index arithmetic."""
+
+import numpy as np
+import pytest
+
+from tests import kv_util as ku
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32), (256, 64), (256, 128)]
+
+
+def dev_bf16(x):
+    import torch
+
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).cuda().bfloat16()
+
+
+def i32(x):
+    import torch
+
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def host(t):
+    return t.float().cpu().numpy()
+
+
+def rows(rng, *shape):
+    """Rows with channels of different size, a flat group, signed zeros and large values."""
+    x = rng.standard_normal(shape) * np.where(rng.random(shape[-1]) < 0.1, 8.0, 1.0)
+    x = ku.bf16(x)
+    x[0, 0, :32] = 0.75
+    x[-1, -1, 32:64] = np.where(np.arange(32) % 2, 0.0, -0.0)
+    x[0, -1] = x[0, -1] * np.float32(2.0 ** 90)
+    x[-1, 0] = x[-1, 0] * np.float32(2.0 ** -100)
+    return x
+
+
+@pytest.mark.parametrize("D,G", SHAPES)
+@pytest.mark.parametrize("page,T,H", [(16, 1, 1), (16, 37, 3), (32, 33, 2), (64, 65, 1), (128, 131, 2)])
+def test_append_and_read_bit_for_bit(D, G, page, T, H):
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    rng = np.random.default_rng(D + G + page + T)
+    n_pages = T // page + 3
+    slots = rng.permutation(n_pages * page)[:T].astype(np.int32)
+    k, v = rows(rng, T, H, D), rows(rng, T, H, D)
+    want = ku.Cache(n_pages, H, D, page, G, fill=0xA5)
+    want.write(slots, k, v)
+    pages = torch.full(want.bytes.shape, 0xA5, dtype=torch.uint8, device="cuda")
+    status = i32([-1])
+    mxq.kv_append(dev_bf16(k), dev_bf16(v), pages, i32(slots), group_size=G, dev_status=status)
+    assert int(status.item()) == 0
+    assert np.array_equal(pages.cpu().numpy(), want.bytes)
+    ko, vo = mxq.kv_read(pages, i32(slots), D, group_size=G, dev_status=status)
+    assert int(status.item()) == 0
+    assert np.array_equal(host(ko), ku.bf16(want.k[slots])) and np.array_equal(host(vo), ku.bf16(want.v[slots]))
+
+
+def test_strided_rows_padding_and_bad_slots():
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    rng = np.random.default_rng(5)
+    T, H, D, G, page, n_pages = 21, 2, 128, 64, 16, 4
+    wide = ku.bf16(rng.standard_normal((T, 4 * H, D)))
+    wide_d = dev_bf16(wide)
+    k, v = wide_d[:, H:2 * H], wide_d[:, 2 * H:3 * H]
+    slots = rng.permutation(n_pages * page)[:T].astype(np.int32)
+    slots[3], slots[8], slots[20] = -1, n_pages * page, 2 ** 31 - 1
+    good = (slots >= 0) & (slots < n_pages * page)
+    want = ku.Cache(n_pages, H, D, page, G)
+    want.write(slots[good], wide[good, H:2 * H], wide[good, 2 * H:3 * H])
+    pages = torch.zeros(want.bytes.shape, dtype=torch.uint8, device="cuda")
+    status = i32([0])
+    mxq.kv_append(k, v, pages, i32(slots), group_size=G, dev_status=status)
+    assert int(status.item()) == mxq.DEV_BAD_SLOT
+    assert np.array_equal(pages.cpu().numpy(), want.bytes)
+    ko, vo = mxq.kv_read(pages, i32(slots), D, group_size=G, dev_status=status)
+    assert int(status.item()) == mxq.DEV_BAD_SLOT
+    assert not host(ko)[~good].any() and not host(vo)[~good].any()
+    assert np.array_equal(host(ko)[good], ku.bf16(want.k[slots[good]]))
+    # padding alone is no fault
+    mxq.kv_append(k[:1], v[:1], pages, i32([-7]), group_size=G, dev_status=status)
+    assert int(status.item()) == 0 and np.array_equal(pages.cpu().numpy(), want.bytes)
+
+
+def test_one_key_for_all_heads_by_a_zero_stride():
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    rng = np.random.default_rng(6)
+    k = ku.bf16(rng.standard_normal((5, 1, 64)))
+    pages = torch.zeros(1, 3, ku.block_bytes(64, 16, 32), dtype=torch.uint8, device="cuda")
+    kd = dev_bf16(k).expand(5, 3, 64)
+    mxq.kv_append(kd, kd, pages, i32(np.arange(5)), group_size=32)
+    want = ku.Cache(1, 3, 64, 16, 32)
+    want.write(np.arange(5), np.repeat(k, 3, 1), np.repeat(k, 3, 1))
+    assert np.array_equal(pages.cpu().numpy(), want.bytes)
+
+
+def test_no_rows():
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    pages = torch.zeros(1, 1, ku.block_bytes(128, 16, 64), dtype=torch.uint8, device="cuda")
+    none = torch.empty(0, 1, 128, dtype=torch.bfloat16, device="cuda")
+    status = i32([9])
+    mxq.kv_append(none, none, pages, i32([]), dev_status=status)
+    assert int(status.item()) == 0
+    ko, vo = mxq.kv_read(pages, i32([]), 128)
+    assert ko.shape == (0, 1, 128) and vo.shape == (0, 1, 128)
+
+
+def test_pages_past_four_gigabytes():
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    H, D, G, page = 8, 128, 64, 64
+    block = ku.block_bytes(D, page, G)
+    n_pages = (9 << 29) // (H * block) + 2          # 4.5 GiB
+    pages = torch.zeros(n_pages, H, block, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(7)
+    k, v = ku.bf16(rng.standard_normal((70, H, D))), ku.bf16(rng.standard_normal((70, H, D)))
+    slots = (n_pages - 2) * page + np.arange(70)
+    mxq.kv_append(dev_bf16(k), dev_bf16(v), pages, i32(slots), group_size=G)
+    want = ku.Cache(2, H, D, page, G)
+    want.write(np.arange(70), k, v)
+    assert np.array_equal(pages[-2:].cpu().numpy(), want.bytes)
+    assert int(pages[:-2].max()) == 0
+    ko, vo = mxq.kv_read(pages, i32(slots), D, group_size=G)
+    assert np.array_equal(host(ko), ku.bf16(want.k[:70])) and np.array_equal(host(vo), ku.bf16(want.v[:70]))
+    # and attention over them: one sequence in the last two pages
+    q = ku.bf16(rng.standard_normal((1, H, D)))
+    table = np.asarray([[n_pages - 2, n_pages - 1]], dtype=np.int32)
+    o = mxq.kv_attention(dev_bf16(q), pages, i32(table), i32([70]), group_size=G)
+    ref, _, A, B, E = ku.attention(q, want, [[0, 1]], [70], [0, 1], D ** -0.5)
+    assert (np.abs(host(o) - ref) <= ku.tolerance(ref, A, B, E, False)).all()
