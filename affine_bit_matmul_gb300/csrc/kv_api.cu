@@ -35,10 +35,11 @@ AttnPlan plan_attn(int Hq, int Hkv, int D, int max_q, int sms) {
     const int rep = Hq / Hkv;
     a.head_parts = (rep + 15) / 16;
     a.part_heads = (rep + a.head_parts - 1) / a.head_parts;
-    a.tile_rows = (long long)max_q * a.part_heads <= 8 ? 8 : 16;
+    const long long rows = (long long)max_q * a.part_heads;
+    a.tile_rows = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
     a.tile_toks = a.tile_rows / a.part_heads;
     a.planes = (max_q + a.tile_toks - 1) / a.tile_toks;
-    const int all = sms * mxq::kv_attn_ctas_per_sm(D, a.tile_rows);
+    const int all = sms * mxq::kv_attn_ctas_per_sm();
     a.ctas = a.planes == 1 ? all : (2 * all + a.planes - 1) / a.planes;
     a.seg_bytes = 0;
     a.bytes = 0;
@@ -202,7 +203,7 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     if (T < 0 || S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || n_pages <= 0 || max_pages <= 0 ||
         !cache_shape(D, group_size, page_size))
         return MXQ_ERR_INVALID_ARG;
-    if (max_q_len <= 0 || window < 0 || sinks < 0 || !(scale == scale) || scale - scale != 0.f)
+    if (max_q_len <= 0 || window < 0 || sinks < 0 || !(scale > 0.f) || scale - scale != 0.f)
         return MXQ_ERR_INVALID_ARG;
     if (!q_starts && (T != S || max_q_len != 1)) return MXQ_ERR_INVALID_ARG;
     if (!pages || (T > 0 && S > 0 && (!q || !page_table || !ctx_lens || !out)))
@@ -254,6 +255,8 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     p.tile_toks = a.tile_toks;
     p.planes = a.planes;
     p.ctas = a.ctas;
+    p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    p.eight = 8;
     p.segs = a.ctas > 1 ? static_cast<int*>(workspace) : nullptr;
     p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.seg_bytes);
     p.status = dev_status;

@@ -7,33 +7,40 @@
 // The codes never become rounded values.  Per group,
 //   q . k^_t = sum_g s_tg (q_g . c_t) + b_tg sum(q_g)
 //   sum_t P_t v^_td = sum_t (P_t s_tg) c_td + sum_t P_t b_tg
-// so the matrix instructions (m16n8k16, bf16 operands, fp32 sums) multiply the
-// bf16 queries, or P_t s_tg rounded to bf16, with 16 + code, which bf16 holds
-// exactly and which one shift and one logic operation make out of a pair of
-// nibbles; scales, biases and the offset of 16 are applied in fp32 to a few
-// numbers per token.  The rounding of P_t s_tg is the only one before the
-// output's; it is taken against codes centred on 7.5 (the sum of the rounded
-// P_t s_tg is kept beside the products), which halves its weight.
+// so the matrix instructions multiply codes, and scales and biases are applied
+// in fp32 to a few numbers per token.
 //
-// Tokens are the instruction's rows (K) or its depth (V) and query rows its
-// columns, so 8 rows of a key/value head's queries cost one instruction per
-// 256 codes and 16 rows two.
+// Keys: a byte 0..15 read as an e4m3 number is 2^-9 times its value (the first
+// eight are the type's subnormals, the next eight its first binade), so the
+// nibbles of a code word, masked into bytes, are operands as they are.  A query
+// row is scaled by a power of two and split into two e4m3 numbers, which hold
+// the 8 bits of a bf16 number down to 2^-10 of the row's largest (and 2^-18 of
+// that absolutely): two of the instruction's columns a row, added afterwards.
+// Values: 16 + code is a bf16 number that one shift and one logic operation
+// make out of a pair of nibbles; the other operand, P_t s_tg, is rounded to
+// bf16, which keeps small weights where an 8-bit type would lose them.  That
+// rounding is the only one before the output's, and it is taken against codes
+// centred on 7.5 (the sum of the rounded P_t s_tg is kept beside the products),
+// which halves its weight.
+// Tokens are the instructions' rows (K) or depth (V), query rows the columns.
 //
-// Work split: a unit is (row tile, tile of 64 tokens that it sees); the units
-// of a plane, in order, are cut into equal runs, one per CTA, whatever the
-// lengths of the sequences.  A run that begins or ends inside a row tile
-// leaves its (max, sum, weighted sum) in the workspace and a second kernel
-// joins them in order, so the result does not depend on timing.
+// Work split: a unit is (row tile, tile of tokens that it sees); the units of a
+// plane, in order, are cut into equal runs, one per CTA, whatever the lengths
+// of the sequences.  A run that begins or ends inside a row tile leaves its
+// (max, sum, weighted sum) in the workspace and a second kernel joins them in
+// order, so the result does not depend on timing.
 //
-// A CTA is one warp that copies whole page blocks (K codes, K pairs, V codes
-// and V pairs of a head are contiguous: one bulk copy per page) into a ring of
-// 64-token stages, and four warps that take 16 tokens of each stage with a
-// softmax state of their own, joined at the end of a row tile.  The running
-// maximum is only moved when a score exceeds it by 2^8, so most stages have no
-// reductions across lanes at all.
+// A CTA's warps take the units of its run in turn, each with a softmax state of
+// its own; they are joined at the end of a row tile.  One more warp fills the
+// ring of tiles, lane i slot i, by copying whole page blocks (K codes, K pairs,
+// V codes and V pairs of a head are contiguous: one bulk copy per page), and
+// works out what a tile's tokens are to the rows.  The running maximum is only
+// moved when a score exceeds it by 2^8, so most tiles have no reductions across
+// lanes at all.
 // Bound by HBM for long contexts: 2 (D / 2 + 4 D / G) bytes per token and head.
 #include <cstdint>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "kv_format.cuh"
@@ -44,25 +51,10 @@
 namespace mxq {
 namespace {
 
-constexpr int kWarps = 4;                       // compute warps
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kStages = 4;
 constexpr int kChunk = 64;                      // values joined at a time
-constexpr int kRowPad = kChunk + 4;
+constexpr int kRowPad = kChunk + 8;
 
-enum : int { kNew = 1, kEnd = 2, kBegins = 4, kEnds = 8, kFull = 16, kLast = 32, kEmpty = 64 };
-
-// What the compute warps need to know about a stage.
-struct Stage {
-    int row0;    // first row of q of the row tile
-    int toks;    // its tokens
-    int head0;   // its first query head
-    int heads;   // its query heads
-    int p0;      // position of its first token
-    int t0;      // first token of this stage
-    int flags;
-    int valid;   // bit i: the 16 tokens from t0 + 16 i were copied
-};
+enum : int { kBegins = 1, kEnds = 2 };  // a run's piece holds a row tile's first, last unit
 
 // Descriptor of a run's first or last piece of a row tile (workspace).
 struct Seg {
@@ -71,15 +63,44 @@ struct Seg {
     int pad[3];
 };
 
+// Sizes of a kernel for row tiles of 4 KT rows: tokens of a tile, compute warps,
+// CTAs per SM, tiles in the ring.
+#ifndef W1
+#define W1 7
+#define T1 64
+#define W2 7
+#define W4 3
+#endif
+template <int D, int G, int KT>
+struct Shape {
+    static constexpr int kRows = 4 * KT;
+    static constexpr int kTile = D == 256 ? 32 : T1;
+    static constexpr int kCtas = 2;
+    static constexpr int kStageBytes = kv_block_bytes(D, G, kTile);
+    // the queries lie in shared memory where they would take 32 registers or more
+    static constexpr bool kQueryShared = D * KT >= 512;
+    static constexpr int kQueryBytes = kQueryShared ? KT * D * 8 : 0;
+    static constexpr int kWarps = KT == 4 ? W4 : D == 256 ? 5 : KT == 1 ? W1 : W2;
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kJoinBytes = kWarps * kRows * kRowPad * 4;
+    static constexpr int kStatBytes = kWarps * kRows * 8;
+    static constexpr int kRoom = 109 * 1024 - kJoinBytes - kStatBytes - kQueryBytes;
+    static constexpr int kSlots = kRoom / kStageBytes < 24 ? kRoom / kStageBytes : 24;
+    static constexpr int kRingBytes = kSlots * kStageBytes;
+    static constexpr int kSmem = kRingBytes + kJoinBytes + kStatBytes + kQueryBytes;
+    static constexpr int kPartialFloats = kRows * (D + 2);
+};
+
 // What a row tile of a sequence sees.
 struct Span {
     int row0, toks, p0;  // rows of q, tokens, position of the first
-    int tiles;           // tiles of 64 tokens (at least 1 when it has rows)
+    int tiles;           // tiles of tokens (at least 1 when it has rows)
     int head_tiles;      // the first of them, from token 0 on (sinks) ...
     int tail;            // ... and the tile where the rest begins
     int bad;             // the sequence's arguments are out of range
 };
 
+template <int TILE>
 __device__ __forceinline__ Span span_of(const KvAttnParams& p, int s, int plane) {
     Span r;
     r.bad = 0;
@@ -105,10 +126,10 @@ __device__ __forceinline__ Span span_of(const KvAttnParams& p, int s, int plane)
     r.p0 = len - n + j0;
     if (r.toks <= 0) return r;
     const int hi = r.p0 + r.toks - 1;           // position of the last row
-    const int end = hi < 0 ? 0 : hi / kKvTile + 1;
+    const int end = hi < 0 ? 0 : hi / TILE + 1;
     int lo = 0;
-    if (p.window) lo = max(0, r.p0 - p.window + 1) / kKvTile;
-    int first = min((min(p.sinks, hi + 1) + kKvTile - 1) / kKvTile, end);
+    if (p.window) lo = max(0, r.p0 - p.window + 1) / TILE;
+    int first = min((min(p.sinks, hi + 1) + TILE - 1) / TILE, end);
     if (first < 0) first = 0;
     if (first >= lo) first = lo = 0;
     lo = min(lo, end);
@@ -126,6 +147,49 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same from zero.
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void mma_e4m3_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four fp32 numbers -> four e4m3 numbers, the first in the lowest byte; and the
+// rest of each that the rounding left, in r.
+__device__ __forceinline__ uint32_t e4m3_of(const float (&x)[4], float (&r)[4]) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
+    uint32_t a, b;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"(lo));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(hi));
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    r[0] = x[0] - p.x;
+    r[1] = x[1] - p.y;
+    r[2] = x[2] - q.x;
+    r[3] = x[3] - q.y;
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -138,12 +202,20 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// Nibble N of both halves of a word -> two bf16 numbers 16 + code.
+// Nibble N of both halves of a word -> two bf16 numbers 16 + code.  Logic
+// operations and shifts share the pipe that bounds this kernel; the left shift
+// is a product with an 8 that the compiler does not know, which runs beside it.
 template <int N>
-__device__ __forceinline__ uint32_t codes16(uint32_t w) {
-    constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;
-    const uint32_t x = N == 0 ? w << 3 : w >> (N == 1 ? 1 : N == 2 ? 5 : 9);
-    return (x & mask) | base;
+__device__ __forceinline__ uint32_t codes16(uint32_t w, uint32_t eight) {
+    const uint32_t x = N == 0 ? w * eight : w >> (N == 1 ? 1 : N == 2 ? 5 : 9);
+    return (x & 0x00780078u) | 0x41804180u;
+}
+
+// Sum over the lanes of the same column of the instruction's result.
+__device__ __forceinline__ float sum_rows(float x) {
+    x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
+    x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
+    return x + __shfl_xor_sync(0xFFFFFFFFu, x, 16);
 }
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
@@ -154,16 +226,6 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
 }
-
-template <int D, int G, int NT>
-struct Shape {
-    static constexpr int kRows = NT * 8;
-    static constexpr int kStageBytes = kv_block_bytes(D, G, kKvTile);
-    static constexpr int kJoinBytes = kWarps * kRows * kRowPad * 4;
-    static constexpr int kStatBytes = kWarps * kRows * 8;
-    static constexpr int kSmem = kStages * kStageBytes + kJoinBytes + kStatBytes;
-    static constexpr int kPartialFloats = kRows * (D + 2);
-};
 
 template <int W>
 __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[W]) {
@@ -203,524 +265,663 @@ __device__ __forceinline__ void load_pairs(const uint8_t* at, uint32_t (&w)[NG])
     }
 }
 
-// One thread: walks the CTA's run of units, copies the stages' page blocks and
-// describes each stage.
-template <int D, int G>
-__device__ void produce(const KvAttnParams& p, int plane, int cta, long long u0, long long u1,
-                        int s, long long base, uint8_t* ring, Stage* stages, uint64_t* full,
-                        uint64_t* empty) {
-    constexpr int kStageBytes = kv_block_bytes(D, G, kKvTile);
-    const int vheads = p.Hkv * p.head_parts;
-    const int page = p.page_size;
-    const int piece = page < kKvTile ? page : kKvTile;
-    const long long block = kv_block_bytes(D, G, page);
-    const int rep = p.Hq / p.Hkv;
-    Seg* seg = reinterpret_cast<Seg*>(p.segs) + ((long long)plane * p.ctas + cta) * 2;
-    if (p.segs) seg[0].flags = seg[1].flags = -1;
-    long long issued = 0;
-    uint32_t parity = 1;  // the first round of waits passes at once
-    int slot = 0;
-    bool ok = true;
+// A run's piece of one row tile, for the warps of a CTA (shared memory).
+struct Piece {
+    int row0, toks, p0;       // its rows of q, tokens, position of the first
+    int head0, heads;         // its query heads
+    int s, h;                 // sequence and key/value head
+    int head_tiles, tail;     // which tiles its units are (Span)
+    int k0, seq0, end;        // first unit; numbers of its units in the run
+    int flags;                // kBegins, kEnds
+};
+constexpr int kPieces = 32;   // pieces of the run that are known ahead
 
-    Span sp = span_of(p, s, plane);
-    long long u = u0;
-    while (u < u1 && ok) {
-        while (u >= base + (long long)sp.tiles * vheads) {
-            base += (long long)sp.tiles * vheads;
-            sp = span_of(p, ++s, plane);
+// One thread: lists the pieces of the CTA's run, the first kPieces at once and
+// one more whenever the warps are done with one.
+template <int TILE>
+struct Walk {  // (no constructors: it lies in shared memory)
+    int s, h, part, k, seq, left;
+    Span sp;
+
+    // the run's first unit is unit `at` of sequence s (of all its heads)
+    __device__ void start(const KvAttnParams& p, int plane, int s_, long long at, int units) {
+        s = s_;
+        sp = span_of<TILE>(p, s, plane);
+        const long long vheads = (long long)p.Hkv * p.head_parts;
+        while (at >= sp.tiles * vheads) {
+            at -= sp.tiles * vheads;
+            sp = span_of<TILE>(p, ++s, plane);
         }
-        const int vh = (int)((u - base) / sp.tiles);
-        int k = (int)((u - base) % sp.tiles);
-        const int kend = (int)(u1 - u < sp.tiles - k ? k + (u1 - u) : sp.tiles);
-        const int h = vh / p.head_parts, part = vh % p.head_parts;
-        Stage st;
-        st.row0 = sp.row0;
-        st.toks = sp.toks;
-        st.head0 = h * rep + part * p.part_heads;
-        st.heads = min(p.part_heads, rep - part * p.part_heads);
-        st.p0 = sp.p0;
-        const int whole = (k == 0 ? kBegins : 0) | (kend == sp.tiles ? kEnds : 0);
-        if (whole != (kBegins | kEnds)) {
+        const int vh = (int)(at / sp.tiles);
+        k = (int)(at % sp.tiles);
+        h = vh / p.head_parts;
+        part = vh % p.head_parts;
+        seq = 0;
+        left = units;
+    }
+    __device__ bool next(const KvAttnParams& p, int plane, Piece* out, Seg* seg) {
+        if (left == 0) return false;
+        while (sp.tiles == 0) sp = span_of<TILE>(p, ++s, plane);
+        const int n = min(left, sp.tiles - k), rep = p.Hq / p.Hkv;
+        Piece q;
+        q.row0 = sp.row0;
+        q.toks = sp.toks;
+        q.p0 = sp.p0;
+        q.head0 = h * rep + part * p.part_heads;
+        q.heads = min(p.part_heads, rep - part * p.part_heads);
+        q.s = s;
+        q.h = h;
+        q.head_tiles = sp.head_tiles;
+        q.tail = sp.tail;
+        q.k0 = k;
+        q.seq0 = seq;
+        q.end = seq + n;
+        q.flags = (k == 0 ? kBegins : 0) | (k + n == sp.tiles ? kEnds : 0);
+        *out = q;
+        if (seg && q.flags != (kBegins | kEnds)) {
             Seg g;
-            g.row0 = st.row0;
-            g.toks = st.toks;
-            g.head0 = st.head0;
-            g.heads = st.heads;
-            g.flags = whole;
-            seg[(whole & kBegins) ? 1 : 0] = g;
+            g.row0 = q.row0;
+            g.toks = q.toks;
+            g.head0 = q.head0;
+            g.heads = q.heads;
+            g.flags = q.flags;
+            seg[(q.flags & kBegins) ? 1 : 0] = g;
         }
-        const int p1 = sp.p0 + sp.toks - 1;
-        const int first = k;
-        for (; k < kend; ++k, ++u) {
-            const int tile = k < sp.head_tiles ? k : sp.tail + (k - sp.head_tiles);
-            st.t0 = tile * kKvTile;
-            st.flags = whole | (k == first ? kNew : 0) | (k == kend - 1 ? kEnd : 0) |
-                       (u == u1 - 1 ? kLast : 0);
-            const int tend = st.t0 + kKvTile - 1;
-            if (tend <= sp.p0 && (!p.window || st.t0 > p1 - p.window || tend < p.sinks))
-                st.flags |= kFull;
-            if (!mbar_wait(&empty[slot], parity, p.wait_budget)) {
-                flag_status(p.status, MXQ_DEV_TIMEOUT);
-                ok = false;
-                break;
-            }
-            // which pieces of the tile are there, and where
-            st.valid = 0;
-            uint32_t bytes = 0;
-            const uint8_t* src[4] = {nullptr, nullptr, nullptr, nullptr};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = st.t0 + i * piece;
-                if (i * piece < kKvTile && t <= p1) {
-                    const int id = __ldg(p.table + (long long)s * p.max_pages + t / page);
-                    if (id >= 0 && id < p.n_pages) {
-                        src[i] = p.pages + ((long long)id * p.Hkv + h) * block;
-                        const int sixteens = piece / 16;
-                        st.valid |= ((1 << sixteens) - 1) << (i * sixteens);
-                        bytes += page <= kKvTile ? (uint32_t)block : (uint32_t)kStageBytes;
-                    } else {
-                        // a page that some row sees has to exist
-                        const int te = min(t + piece - 1, p1);
-                        if (!p.window || te > sp.p0 - p.window || t < p.sinks)
-                            flag_status(p.status, MXQ_DEV_BAD_PAGE);
-                    }
+        seq += n;
+        left -= n;
+        k += n;
+        if (k == sp.tiles && left) {
+            k = 0;
+            if (++part == p.head_parts) {
+                part = 0;
+                if (++h == p.Hkv) {
+                    h = 0;
+                    sp = span_of<TILE>(p, ++s, plane);
                 }
             }
-            if (st.valid != 15) st.flags &= ~kFull;
-            stages[slot] = st;
-            mbar_expect_tx(&full[slot], bytes);
-            const uint32_t dst = smem_u32(ring + slot * kStageBytes);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (!src[i]) continue;
-                if (page <= kKvTile) {
-                    bulk_copy(dst + i * (uint32_t)block, src[i], (uint32_t)block, &full[slot]);
-                } else {  // a 64-token part of a longer page: its four regions
-                    const int o = st.t0 % page;
-                    const uint32_t cb = kv_code_bytes(D, kKvTile), pb = kv_pair_bytes(D, G, kKvTile);
-                    const uint8_t* kc = src[i] + kv_code_bytes(D, o);
-                    const uint8_t* kp = src[i] + kv_code_bytes(D, page) + kv_pair_bytes(D, G, o);
-                    const long long v = block / 2;
-                    bulk_copy(dst, kc, cb, &full[slot]);
-                    bulk_copy(dst + cb, kp, pb, &full[slot]);
-                    bulk_copy(dst + cb + pb, kc + v, cb, &full[slot]);
-                    bulk_copy(dst + 2 * cb + pb, kp + v, pb, &full[slot]);
-                }
-            }
-            ++issued;
-            if (++slot == kStages) {
-                slot = 0;
-                parity ^= 1u;
-            }
+        }
+        return true;
+    }
+};
+
+// What a tile in the ring is to the compute warps: the number of its unit, its
+// first token, and in `state` bit i: its 16 tokens from 16 i on exist; kAll: every
+// row sees all of them.  The warps may be a whole round of the ring apart, and
+// the parity of a phase alone does not tell a round from the one two before it:
+// a warp waits for the number first.
+struct Tile {
+    int unit, t0, state;
+};
+constexpr int kAll = 256;
+
+// Waits, within the budget, until a slot is given to unit n (whole warp).
+__device__ __forceinline__ bool unit_comes(const int* unit, int n, long long budget) {
+    const volatile int* u = unit;
+    bool ok = true;
+    if (*u != n) {
+        const long long since = clock64();
+        while (*u != n && ok) {
+            __nanosleep(20);
+            ok = clock64() - since <= budget;
         }
     }
-    drain_ring(full, kStages, issued, kStages);
+    return __all_sync(0xFFFFFFFFu, ok);
 }
 
-template <int D, int G, int NT>
-__global__ void __launch_bounds__(kThreads, (D == 256 || NT == 2) ? 2 : 3)
+// The copying warp, lane i filling slot i: units i, i + SLOTS, ...  Pages of at
+// most a tile are copied whole, of longer ones the four regions of the tile's
+// part.
+template <int D, int G, int TILE, int SLOTS>
+__device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int total, int lane,
+                           uint32_t ring, Tile* tiles, uint64_t* full, uint64_t* empty) {
+    constexpr int kMost = TILE / 16;
+    constexpr uint32_t cb = kv_code_bytes(D, TILE), pb = kv_pair_bytes(D, G, TILE);
+    const int size = min(p.page_size, TILE), count = TILE / size;
+    const uint32_t block = kv_block_bytes(D, G, size);
+    const uint32_t slot = ring + lane * kv_block_bytes(D, G, TILE);
+    int n = lane, end = 0, piece = -1;
+    uint32_t parity = 1;  // the first wait passes at once
+    bool work = lane < SLOTS && n < total;
+    int t0 = 0, id[kMost];
+    Piece q;
+
+    auto look = [&]() {  // the pages of unit n
+        if (n >= end) {
+            do ++piece;
+            while (n >= pieces[piece % kPieces].end);
+            q = pieces[piece % kPieces];
+            end = q.end;
+        }
+        const int k = q.k0 + n - q.seq0;
+        t0 = (k < q.head_tiles ? k : q.tail + k - q.head_tiles) * TILE;
+        const int32_t* row = p.table + (long long)q.s * p.max_pages;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            const int t = t0 + i * size;
+            id[i] = -2;  // not needed
+            if (i < count && t < q.p0 + q.toks) id[i] = __ldg(row + (t >> p.page_shift));
+        }
+    };
+    if (work) look();
+    long long since = clock64();
+    while (__any_sync(0xFFFFFFFFu, work)) {
+        const bool ready = work && mbar_test_wait(&empty[lane], parity);
+        if (ready) {
+            const int p1 = q.p0 + q.toks - 1;
+            uint32_t bytes = 0;
+            int state = 0;
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+                if ((unsigned)id[i] < (unsigned)p.n_pages) {
+                    state |= ((1 << (size / 16)) - 1) << (i * (size / 16));
+                    bytes += block;
+                } else if (id[i] != -2) {
+                    // a page that some row sees has to exist
+                    const int t = t0 + i * size, te = min(t + size - 1, p1);
+                    if (!p.window || te > q.p0 - p.window || t < p.sinks)
+                        flag_status(p.status, MXQ_DEV_BAD_PAGE);
+                }
+            }
+            if (state == (1 << kMost) - 1 && t0 + TILE - 1 <= q.p0 &&
+                (!p.window || t0 > p1 - p.window || t0 + TILE <= p.sinks))
+                state |= kAll;
+            tiles[lane].t0 = t0;
+            tiles[lane].state = state;
+            *const_cast<volatile int*>(&tiles[lane].unit) = n;
+            mbar_expect_tx(&full[lane], bytes);
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+                if ((unsigned)id[i] >= (unsigned)p.n_pages) continue;
+                const uint8_t* src = p.pages + ((long long)id[i] * p.Hkv + q.h) *
+                                                   kv_block_bytes(D, G, p.page_size);
+                if (p.page_size <= TILE) {
+                    bulk_copy(slot + i * block, src, block, &full[lane]);
+                } else {
+                    const int skip = t0 & (p.page_size - 1);
+                    const uint8_t* codes = src + kv_code_bytes(D, skip);
+                    const uint8_t* pairs =
+                        src + kv_code_bytes(D, p.page_size) + kv_pair_bytes(D, G, skip);
+                    const int v = kv_block_bytes(D, G, p.page_size) / 2;
+                    bulk_copy(slot, codes, cb, &full[lane]);
+                    bulk_copy(slot + cb, pairs, pb, &full[lane]);
+                    bulk_copy(slot + cb + pb, codes + v, cb, &full[lane]);
+                    bulk_copy(slot + 2 * cb + pb, pairs + v, pb, &full[lane]);
+                }
+            }
+            parity ^= 1u;
+            n += SLOTS;
+            work = n < total;
+            if (work) look();
+        }
+        if (__any_sync(0xFFFFFFFFu, ready)) {
+            since = clock64();
+        } else {
+            if (clock64() - since > p.wait_budget) {
+                if (work) flag_status(p.status, MXQ_DEV_TIMEOUT);
+                break;
+            }
+            __nanosleep(32);
+        }
+    }
+    // no copy may land after the CTA is gone
+    if (lane < SLOTS && n > lane) mbar_wait(&full[lane], (uint32_t)((n - lane) / SLOTS - 1) & 1u);
+}
+
+template <int D, int G, int KT>
+__global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kCtas)
     kv_attn_kernel(const KvAttnParams p) {
-    using SH = Shape<D, G, NT>;
-    constexpr int NG = D / G;       // groups
-    constexpr int U = D / 32;       // code words of a lane per 8 tokens
-    constexpr int MT = D / 16;      // output tiles of 16 values
+    using SH = Shape<D, G, KT>;
+    constexpr int TILE = SH::kTile, SUB = TILE / 16;  // a warp takes 16 tokens at a time
+    constexpr int kWarps = SH::kWarps, kThreads = SH::kThreads, kSlots = SH::kSlots;
+    constexpr int NG = D / G;          // groups
+    constexpr int U = D / 32;          // code words of a lane per 8 tokens
+    constexpr int MT = D / 16;         // output tiles of 16 values
+    constexpr int VT = (KT + 1) / 2;   // output columns / 8
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[kStages], empty[kStages], joined;
-    __shared__ Stage stages[kStages];
-    __shared__ long long sums[kThreads];
-    uint8_t* ring = smem;
-    float* join = reinterpret_cast<float*>(smem + kStages * SH::kStageBytes);
-    float2* stat = reinterpret_cast<float2*>(smem + kStages * SH::kStageBytes + SH::kJoinBytes);
+    __shared__ uint64_t full[kSlots], empty[kSlots], joined;
+    __shared__ Tile tiles[kSlots];
+    __shared__ Piece pieces[kPieces];
+    __shared__ Walk<TILE> walk;  // thread 0's
+    __shared__ int sums[kThreads];
+    float* join = reinterpret_cast<float*>(smem + SH::kRingBytes);
+    float2* stat = reinterpret_cast<float2*>(smem + SH::kRingBytes + SH::kJoinBytes);
+    uint2* queries = reinterpret_cast<uint2*>(smem + SH::kSmem - SH::kQueryBytes);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int plane = blockIdx.x / p.ctas, cta = blockIdx.x % p.ctas;
+    Seg* seg = p.segs ? reinterpret_cast<Seg*>(p.segs) + ((long long)plane * p.ctas + cta) * 2
+                      : nullptr;
 
-    // every CTA finds its own run: the units of all sequences, then its share
+    // every CTA finds its own run: the tiles of all sequences, then its share
     const int per = (p.S + kThreads - 1) / kThreads;
     {
-        long long sum = 0;
+        int sum = 0;
         for (int i = 0; i < per; ++i) {
             const int s = threadIdx.x * per + i;
             if (s >= p.S) break;
-            const Span sp = span_of(p, s, plane);
+            const Span sp = span_of<TILE>(p, s, plane);
             sum += sp.tiles;
             if (sp.bad && blockIdx.x == 0) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
         }
-        sums[threadIdx.x] = sum * (p.Hkv * p.head_parts);
+        sums[threadIdx.x] = sum;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kWarps);
+            mbar_init(&empty[i], 1);
+            tiles[i].unit = -1;
         }
         mbar_init(&joined, kWarps);
         mbar_init_fence();
     }
     __syncthreads();
-
-    if (warp == kWarps) {
-        // scan of the threads' sums: 5 of them a lane
-        constexpr int kPer = kThreads / 32;
+    // scan of the threads' sums, in every warp
+    int total;           // units of this CTA's run
+    {
         long long mine = 0;
-        for (int i = 0; i < kPer; ++i) mine += sums[lane * kPer + i];
+#pragma unroll
+        for (int i = 0; i < kWarps + 1; ++i) mine += sums[lane * (kWarps + 1) + i];
         long long incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
             if (lane >= o) incl += x;
         }
-        const long long total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-        const long long runs = total < p.ctas ? total : p.ctas;
-        const long long u0 = cta < runs ? cta * total / runs : 0;
-        const long long u1 = cta < runs ? (cta + 1) * total / runs : 0;
-        if (u0 == u1) {
+        const long long vheads = (long long)p.Hkv * p.head_parts;
+        const long long all = __shfl_sync(0xFFFFFFFFu, incl, 31) * vheads;
+        const long long runs = all < p.ctas ? all : p.ctas;
+        if (seg && threadIdx.x == 0) seg[0].flags = seg[1].flags = -1;
+        if (cta >= runs) return;
+        const long long u0 = cta * all / runs, u1 = (cta + 1) * all / runs;
+        total = (int)(u1 - u0);
+        if (warp == 0) {
+            const uint32_t here = __ballot_sync(0xFFFFFFFFu, u0 >= (incl - mine) * vheads &&
+                                                                 u0 < incl * vheads);
+            const int owner = __ffs(here) - 1;
+            long long at = u0 - __shfl_sync(0xFFFFFFFFu, incl - mine, owner) * vheads;
             if (lane == 0) {
-                Seg* seg = reinterpret_cast<Seg*>(p.segs) + ((long long)plane * p.ctas + cta) * 2;
-                if (p.segs) seg[0].flags = seg[1].flags = -1;
-                stages[0].flags = kLast | kEmpty;
-                mbar_arrive(&full[0]);
-            }
-        } else {
-            const uint32_t here = __ballot_sync(0xFFFFFFFFu, u0 >= incl - mine && u0 < incl);
-            if (lane == __ffs(here) - 1) {
-                long long base = incl - mine;
-                int i = lane * kPer;
-                while (u0 >= base + sums[i]) base += sums[i++];
-                // sequences of that thread, one by one (produce skips on)
-                produce<D, G>(p, plane, cta, u0, u1, i * per, base, ring, stages, full, empty);
+                int i = owner * (kWarps + 1);  // the thread whose sequences the run starts in
+                while (at >= sums[i] * vheads) at -= sums[i++] * vheads;
+                walk.start(p, plane, i * per, at, total);
+                for (int n = 0; n < kPieces && walk.next(p, plane, &pieces[n], seg); ++n) {
+                }
             }
         }
+    }
+    __syncthreads();
+
+    if (warp == kWarps) {
+        copy_tiles<D, G, TILE, kSlots>(p, pieces, total, lane, smem_u32(smem), tiles, full, empty);
         return;
     }
 
-    // ------------------------------------------------------- compute warps
     const int r = lane >> 2, i4 = lane & 3;
-    uint32_t qf[NT][U][4];
-    float qsum[NT][NG][2];     // sum of q over a group, rows 2 i4 and 2 i4 + 1
-    float acc[NT][MT][4], psum[NT][NG][4];
-    float pb[NT][NG][2], l[NT][2], m[NT][2], mu[NT][2];
-    int pos[NT][2];
-    int slot = 0;
-    uint32_t parity = 0, jparity = 0;
+    // offsets in a slot of this lane's words and pairs of 16 tokens: a page's
+    // block of `piece` tokens after another
+    const int piece = p.page_size < TILE ? p.page_size : TILE;
+    const int block = kv_block_bytes(D, G, piece), v_off = block / 2;
+    const int words_1 = piece >= 32 ? 8 * D : block, pairs_1 = piece >= 32 ? 64 * NG : block;
+    const int words_2 = piece >= 64 ? 16 * D : piece == 32 ? block : 2 * block;
+    const int pairs_2 = piece >= 64 ? 128 * NG : piece == 32 ? block : 2 * block;
+    auto words_at = [&](int b) {
+        return lane * (D == 64 ? 8 : 16) + (b & 1) * words_1 + (b >> 1) * words_2;
+    };
+    auto pairs_at = [&](int b) {
+        return kv_code_bytes(D, piece) + r * NG * 4 + (b & 1) * pairs_1 + (b >> 1) * pairs_2;
+    };
+    const uint32_t eight = p.eight;
+    uint32_t jparity = 0;
+    int n = warp;  // this warp's units: those whose number in the run is warp modulo kWarps
+    auto gave_up = [&](bool ok) {
+        if (!ok && lane == 0) flag_status(p.status, MXQ_DEV_TIMEOUT);
+        return !ok;
+    };
 
-    const int piece = p.page_size < kKvTile ? p.page_size : kKvTile;
-    const int in_piece = (warp * 16) % piece;
-    const int piece_at = (warp * 16) / piece * kv_block_bytes(D, G, piece);
-    const int kc_at = piece_at + kv_code_bytes(D, in_piece) + lane * (D == 64 ? 8 : 16);
-    const int kp_at = piece_at + kv_code_bytes(D, piece) + (in_piece + r) * NG * 4;
-    const int v_off = kv_block_bytes(D, G, piece) / 2;
-
-    for (;;) {
-        if (!warp_wait(&full[slot], parity, p.wait_budget)) {
-            if (lane == 0) flag_status(p.status, MXQ_DEV_TIMEOUT);
-            return;
-        }
-        const Stage st = stages[slot];
-        if (st.flags & kEmpty) return;
-        if (st.flags & kNew) {
-            // a row tile begins: its queries as the instruction's columns
-            const int rows = st.toks * st.heads;
+    for (int at_piece = 0, done = 0; done < total; ++at_piece) {
+        const Piece& sp = pieces[at_piece % kPieces];
+        const int heads = sp.heads, rows = sp.toks * heads, head0 = sp.head0;
+        const int p0 = sp.p0, p1 = p0 + sp.toks - 1, end = sp.end;
+        // Queries as the instruction's columns: column r of key tile kt is the
+        // first (r even) or second part of row 4 kt + r / 2, so a lane's two
+        // columns of a result are the two parts of row 4 kt + i4.
+        uint2 qf[KT][SH::kQueryShared ? 1 : U];
+        float qsum[KT][NG];    // sum of the row's values over a group, and
+        float unit[KT];        // the factor that makes scores (times log2 e) of the sums
+        int pos[KT];
+        float acc[VT][MT][4];
+        float pb[KT][NG], l[KT], m[KT], mu[KT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int rr = nt * 8 + r;
-                const bool in = rr < rows;
-                const int j = in ? rr / st.heads : 0, hh = in ? rr % st.heads : 0;
-                const __nv_bfloat16* src = p.q + (long long)(st.row0 + j) * p.q_row_stride +
-                                           (long long)(st.head0 + hh) * p.q_head_stride + 8 * i4;
-                float part[NG];
+        for (int kt = 0; kt < KT; ++kt) {
+            const int rr = kt * 4 + (r >> 1);
+            const bool in = rr < rows;
+            const int j = in ? rr / heads : 0, hh = in ? rr % heads : 0;
+            const __nv_bfloat16* src = p.q + (long long)(sp.row0 + j) * p.q_row_stride +
+                                       (long long)(head0 + hh) * p.q_head_stride + 8 * i4;
+            uint4 raw[U];
+            float big = 0.f;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) part[g] = 0.f;
+            for (int u = 0; u < U; ++u) {
+                raw[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (in) raw[u] = __ldg(reinterpret_cast<const uint4*>(src + 32 * u));
+                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (in) v = __ldg(reinterpret_cast<const uint4*>(src + 32 * u));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    // pairs (0, 4), (1, 5), (2, 6), (3, 7), as a code word's nibbles
-                    qf[nt][u][0] = prmt(w[0], w[2], 0x5410u);
-                    qf[nt][u][1] = prmt(w[0], w[2], 0x7632u);
-                    qf[nt][u][2] = prmt(w[1], w[3], 0x5410u);
-                    qf[nt][u][3] = prmt(w[1], w[3], 0x7632u);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        part[u * 32 / G] += __uint_as_float(w[e] << 16) +
-                                            __uint_as_float(w[e] & 0xFFFF0000u);
-                }
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    float x = part[g];
-                    x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-                    x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-                    qsum[nt][g][0] = __shfl_sync(0xFFFFFFFFu, x, 8 * i4);
-                    qsum[nt][g][1] = __shfl_sync(0xFFFFFFFFu, x, 8 * i4 + 4);
-                    pb[nt][g][0] = pb[nt][g][1] = 0.f;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) psum[nt][g][c] = 0.f;
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int col = nt * 8 + 2 * i4 + c;
-                    pos[nt][c] = col < rows ? st.p0 + col / st.heads : -1;
-                    m[nt][c] = -INFINITY;
-                    mu[nt][c] = 0.f;
-                    l[nt][c] = 0.f;
-                }
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[nt][t][c] = 0.f;
+                for (int e = 0; e < 4; ++e)
+                    big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
+                                           fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
             }
-        }
-
-        const uint8_t* at = ring + slot * SH::kStageBytes;
-        // ---- scores of 16 tokens: rows r and r + 8 of the instruction
-        float sc[NT][4];
+            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+            // the largest value becomes 2^7 .. 2^8; e4m3 ends at 448
+            const int ex = max((int)(__float_as_uint(big) >> 23), 16);
+            const float up = __uint_as_float((uint32_t)(261 - ex) << 23);  // 2^(134 - ex)
+            float part[NG];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int g = 0; g < NG; ++g) part[g] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
-        {
-            uint32_t w0[U], w1[U], pr0[NG], pr1[NG];
-            load_words<U>(at + kc_at, w0);
-            load_words<U>(at + kc_at + 4 * D, w1);
-            load_pairs<NG>(at + kp_at, pr0);
-            load_pairs<NG>(at + kp_at + 8 * NG * 4, pr1);
+            for (int u = 0; u < U; ++u) {
+                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                // a code word's low nibbles are values 0, 2, 4, 6, its high ones 1, 3, 5, 7
+                float ev[4], od[4], re[4], ro[4], x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    ev[e] = __uint_as_float(w[e] << 16) * up;
+                    od[e] = __uint_as_float(w[e] & 0xFFFF0000u) * up;
+                    part[u * 32 / G] += ev[e] + od[e];
+                }
+                uint2 f = make_uint2(e4m3_of(ev, re), e4m3_of(od, ro));
+                const uint2 f2 = make_uint2(e4m3_of(re, x), e4m3_of(ro, x));
+                if (r & 1) f = f2;
+                if (SH::kQueryShared) {
+                    if (u % kWarps == warp) queries[(kt * U + u) * 32 + lane] = f;
+                } else {
+                    qf[kt][SH::kQueryShared ? 0 : u] = f;
+                }
+            }
+            // codes as e4m3 numbers are 2^-9 of their values: so are these sums
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                float a[NT][4];
+                float x = part[g];
+                x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+                x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+                qsum[kt][g] = __shfl_sync(0xFFFFFFFFu, x, 8 * i4) * 0x1p-9f;
+                pb[kt][g] = 0.f;
+            }
+            const int down = __shfl_sync(0xFFFFFFFFu, ex, 8 * i4);  // 2^(ex - 134 + 9)
+            unit[kt] = fmaxf(
+                p.scale_log2 * 0x1p9f * __uint_as_float((uint32_t)max(down - 7, 1) << 23), 0x1p-126f);
+            l[kt] = 0.f;
+            m[kt] = -INFINITY;
+            mu[kt] = 0.f;
+            const int mine_row = kt * 4 + i4;
+            pos[kt] = mine_row < rows ? p0 + mine_row / heads : -1;
+        }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+        for (int vt = 0; vt < VT; ++vt) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) a[nt][c] = 0.f;
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
-                    const uint32_t x0 = codes16<0>(w0[u]), y0 = codes16<0>(w1[u]);
-                    const uint32_t x1 = codes16<1>(w0[u]), y1 = codes16<1>(w1[u]);
-                    const uint32_t x2 = codes16<2>(w0[u]), y2 = codes16<2>(w1[u]);
-                    const uint32_t x3 = codes16<3>(w0[u]), y3 = codes16<3>(w1[u]);
+                for (int c = 0; c < 4; ++c) acc[vt][t][c] = 0.f;
+        }
+        if (SH::kQueryShared) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&joined);
+            if (gave_up(warp_wait(&joined, jparity, p.wait_budget))) return;
+            jparity ^= 1u;
+        }
+
+        for (; n < end; n += kWarps) {
+            const int slot = n % kSlots;
+            if (gave_up(unit_comes(&tiles[slot].unit, n, p.wait_budget) &&
+                        warp_wait_sleep(&full[slot], (uint32_t)(n / kSlots) & 1u, p.wait_budget)))
+                return;
+            uint8_t* at = smem + slot * SH::kStageBytes;
+            const Tile tile = tiles[slot];
+            // ---- sums q . c of 16 tokens at a time, tokens r and r + 8 in a lane
+            float sc[SUB][KT][2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_bf16(a[nt], x0, y0, x1, y1, qf[nt][u][0], qf[nt][u][1]);
-                        mma_bf16(a[nt], x2, y2, x3, y3, qf[nt][u][2], qf[nt][u][3]);
+            for (int b = 0; b < SUB; ++b) {
+                uint32_t w0[U], w1[U], pr0[NG], pr1[NG];
+                load_words<U>(at + words_at(b), w0);
+                load_words<U>(at + words_at(b) + 4 * D, w1);
+                load_pairs<NG>(at + pairs_at(b), pr0);
+                load_pairs<NG>(at + pairs_at(b) + 8 * NG * 4, pr1);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    float a[KT][4];
+#pragma unroll
+                    for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
+                        const uint32_t x0 = w0[u] & 0x0F0F0F0Fu, x1 = (w0[u] >> 4) & 0x0F0F0F0Fu;
+                        const uint32_t y0 = w1[u] & 0x0F0F0F0Fu, y1 = (w1[u] >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+                        for (int kt = 0; kt < KT; ++kt) {
+                            const uint2 f = SH::kQueryShared ? queries[(kt * U + u) * 32 + lane]
+                                                             : qf[kt][SH::kQueryShared ? 0 : u];
+                            if (u == g * G / 32)
+                                mma_e4m3_first(a[kt], x0, y0, x1, y1, f.x, f.y);
+                            else
+                                mma_e4m3(a[kt], x0, y0, x1, y1, f.x, f.y);
+                        }
+                    }
+                    const float s0 = __uint_as_float(pr0[g] << 16);
+                    const float s1 = __uint_as_float(pr1[g] << 16);
+                    const float b0 = __uint_as_float(pr0[g] & 0xFFFF0000u);
+                    const float b1 = __uint_as_float(pr1[g] & 0xFFFF0000u);
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt) {
+                        const float qs = qsum[kt][g];
+                        const float z0 = g ? fmaf(b0, qs, sc[b][kt][0]) : b0 * qs;
+                        const float z1 = g ? fmaf(b1, qs, sc[b][kt][1]) : b1 * qs;
+                        sc[b][kt][0] = fmaf(s0, a[kt][0] + a[kt][1], z0);
+                        sc[b][kt][1] = fmaf(s1, a[kt][2] + a[kt][3], z1);
                     }
                 }
-                const float s0 = __uint_as_float(pr0[g] << 16) * p.scale_log2;
-                const float s1 = __uint_as_float(pr1[g] << 16) * p.scale_log2;
-                const float b0 = fmaf(-16.f, s0, __uint_as_float(pr0[g] & 0xFFFF0000u) * p.scale_log2);
-                const float b1 = fmaf(-16.f, s1, __uint_as_float(pr1[g] & 0xFFFF0000u) * p.scale_log2);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    sc[nt][0] = fmaf(s0, a[nt][0], fmaf(b0, qsum[nt][g][0], sc[nt][0]));
-                    sc[nt][1] = fmaf(s0, a[nt][1], fmaf(b0, qsum[nt][g][1], sc[nt][1]));
-                    sc[nt][2] = fmaf(s1, a[nt][2], fmaf(b1, qsum[nt][g][0], sc[nt][2]));
-                    sc[nt][3] = fmaf(s1, a[nt][3], fmaf(b1, qsum[nt][g][1], sc[nt][3]));
-                }
             }
-        }
-        bool live0 = true, live1 = true;  // tokens r and r + 8 are seen by some row
-        if (!(st.flags & kFull)) {
-            const int t0 = st.t0 + warp * 16 + r, t1 = t0 + 8;
-            const bool there = (st.valid >> warp) & 1;
-            const int p1 = st.p0 + st.toks - 1;
-            live0 = there && t0 <= p1 && (!p.window || t0 > st.p0 - p.window || t0 < p.sinks);
-            live1 = there && t1 <= p1 && (!p.window || t1 > st.p0 - p.window || t1 < p.sinks);
+            if (!(tile.state & kAll)) {
+                // some row does not see some token; what no row sees may hold anything
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+                for (int b = 0; b < SUB; ++b) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int q = pos[nt][c];
-                    if (!(live0 && t0 <= q && (!p.window || t0 > q - p.window || t0 < p.sinks)))
-                        sc[nt][c] = -INFINITY;
-                    if (!(live1 && t1 <= q && (!p.window || t1 > q - p.window || t1 < p.sinks)))
-                        sc[nt][2 + c] = -INFINITY;
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = tile.t0 + 16 * b + r + 8 * i;
+                        const bool live = ((tile.state >> b) & 1) && t <= p1 &&
+                                          (!p.window || t > p0 - p.window || t < p.sinks);
+                        if (!live) {
+                            for (int g = i4; g < NG; g += 4)
+                                *reinterpret_cast<uint32_t*>(at + v_off + pairs_at(b) + 8 * i * NG * 4 +
+                                                             g * 4) = 0u;
+                        }
+#pragma unroll
+                        for (int kt = 0; kt < KT; ++kt)
+                            if (!(live && t <= pos[kt] &&
+                                  (!p.window || t > pos[kt] - p.window || t < p.sinks)))
+                                sc[b][kt][i] = -INFINITY;
+                    }
                 }
+                fence_proxy_async_smem();  // the slot's next copy comes after these stores
+                __syncwarp();
             }
-        }
-        // ---- running maximum: moved only when a score is far above it
-        bool over = false;
+            // ---- running maximum: moved only when a score is far above it
+            float top[KT];
+            bool over = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int kt = 0; kt < KT; ++kt) {
+                top[kt] = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                over |= fmaxf(sc[nt][c], sc[nt][2 + c]) > m[nt][c] + 8.f;
-        if (__any_sync(0xFFFFFFFFu, over)) {
+                for (int b = 0; b < SUB; ++b)
+                    top[kt] = fmaxf(top[kt], fmaxf(sc[b][kt][0] * unit[kt], sc[b][kt][1] * unit[kt]));
+                over |= top[kt] > m[kt] + 8.f;
+            }
+            if (__any_sync(0xFFFFFFFFu, over)) {
+                float f[KT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x = fmaxf(sc[nt][c], sc[nt][2 + c]);
+                for (int kt = 0; kt < KT; ++kt) {
+                    float x = top[kt];
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                    const float mn = fmaxf(m[nt][c], x);
-                    const float ref = mn == -INFINITY ? 0.f : mn;
-                    const float f = exp2_approx(m[nt][c] - ref);
-                    m[nt][c] = mn;
-                    mu[nt][c] = ref;
-                    l[nt][c] *= f;
+                    const float mn = fmaxf(m[kt], x);
+                    mu[kt] = mn == -INFINITY ? 0.f : mn;
+                    f[kt] = exp2_approx(m[kt] - mu[kt]);
+                    m[kt] = mn;
+                    l[kt] *= f[kt];
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        pb[nt][g][c] *= f;
-                        psum[nt][g][c] *= f;
-                    }
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        acc[nt][t][c] *= f;
-                        acc[nt][t][2 + c] *= f;
-                    }
-                }
-            }
-        }
-        // ---- weights
-        float w[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) w[nt][c] = exp2_approx(sc[nt][c] - mu[nt][c & 1]);
-            l[nt][0] += w[nt][0] + w[nt][2];
-            l[nt][1] += w[nt][1] + w[nt][3];
-        }
-        // ---- weighted sum of the values
-        {
-            uint32_t w0[U], w1[U], pr0[NG], pr1[NG];
-            load_pairs<NG>(at + v_off + kp_at, pr0);
-            load_pairs<NG>(at + v_off + kp_at + 8 * NG * 4, pr1);
-            load_words<U>(at + v_off + kc_at, w0);
-            load_words<U>(at + v_off + kc_at + 4 * D, w1);
-            constexpr uint32_t one = 0x3F803F80u;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const float s0 = live0 ? __uint_as_float(pr0[g] << 16) : 0.f;
-                const float s1 = live1 ? __uint_as_float(pr1[g] << 16) : 0.f;
-                const float b0 = live0 ? fmaf(7.5f, s0, __uint_as_float(pr0[g] & 0xFFFF0000u)) : 0.f;
-                const float b1 = live1 ? fmaf(7.5f, s1, __uint_as_float(pr1[g] & 0xFFFF0000u)) : 0.f;
-                uint32_t f0[NT], f1[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    f0[nt] = transpose_8x8(cvt_bf16x2(w[nt][0] * s0, w[nt][1] * s0));
-                    f1[nt] = transpose_8x8(cvt_bf16x2(w[nt][2] * s1, w[nt][3] * s1));
-                    pb[nt][g][0] = fmaf(w[nt][0], b0, fmaf(w[nt][2], b1, pb[nt][g][0]));
-                    pb[nt][g][1] = fmaf(w[nt][1], b0, fmaf(w[nt][3], b1, pb[nt][g][1]));
-                    mma_bf16(psum[nt][g], one, one, one, one, f0[nt], f1[nt]);
+                    for (int g = 0; g < NG; ++g) pb[kt][g] *= f[kt];
                 }
 #pragma unroll
-                for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
-                    const uint32_t x0 = codes16<0>(w0[u]), y0 = codes16<0>(w1[u]);
-                    const uint32_t x1 = codes16<1>(w0[u]), y1 = codes16<1>(w1[u]);
-                    const uint32_t x2 = codes16<2>(w0[u]), y2 = codes16<2>(w1[u]);
-                    const uint32_t x3 = codes16<3>(w0[u]), y3 = codes16<3>(w1[u]);
+                for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_bf16(acc[nt][2 * u], x0, x1, y0, y1, f0[nt], f1[nt]);
-                        mma_bf16(acc[nt][2 * u + 1], x2, x3, y2, y3, f0[nt], f1[nt]);
-                    }
-                }
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);
-        if (++slot == kStages) {
-            slot = 0;
-            parity ^= 1u;
-        }
-
-        if (st.flags & kEnd) {
-            // ---- the four warps' results of this row tile become one
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x = l[nt][c];
-                    x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
-                    x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
-                    x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
-                    if (r == 0)
-                        stat[warp * SH::kRows + nt * 8 + 2 * i4 + c] = make_float2(m[nt][c], x);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        float y = pb[nt][g][c];
-                        y += __shfl_xor_sync(0xFFFFFFFFu, y, 4);
-                        y += __shfl_xor_sync(0xFFFFFFFFu, y, 8);
-                        y += __shfl_xor_sync(0xFFFFFFFFu, y, 16);
-                        pb[nt][g][c] = fmaf(-23.5f, psum[nt][g][c], y);
-                    }
-                }
-            }
-            const bool whole = (st.flags & kBegins) && (st.flags & kEnds);
-            float* part = p.partial + (((long long)plane * p.ctas + cta) * 2 +
-                                       ((st.flags & kBegins) ? 1 : 0)) *
-                                          SH::kPartialFloats;
-            const int rows = st.toks * st.heads;
-#pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += kChunk) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    if (t / (kChunk / 16) != d0 / kChunk) continue;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int t = 0; t < MT; ++t)
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            join[(warp * SH::kRows + nt * 8 + 2 * i4 + (c & 1)) * kRowPad +
-                                 (t % (kChunk / 16)) * 16 + r + (c >> 1) * 8] =
-                                acc[nt][t][c] + pb[nt][t * 16 / G][c & 1];
+                            acc[vt][t][c] *= f[KT == 1 ? 0 : 2 * vt + (c & 1)];
+            }
+            // ---- weighted sum of the values
+            float psum[VT][NG][4];  // sum of the rounded weights
+#pragma unroll
+            for (int b = 0; b < SUB; ++b) {
+                uint32_t w0[U], w1[U], pr0[NG], pr1[NG];
+                load_pairs<NG>(at + v_off + pairs_at(b), pr0);
+                load_pairs<NG>(at + v_off + pairs_at(b) + 8 * NG * 4, pr1);
+                load_words<U>(at + v_off + words_at(b), w0);
+                load_words<U>(at + v_off + words_at(b) + 4 * D, w1);
+                float e0[KT], e1[KT];
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    e0[kt] = exp2_approx(fmaf(sc[b][kt][0], unit[kt], -mu[kt]));
+                    e1[kt] = exp2_approx(fmaf(sc[b][kt][1], unit[kt], -mu[kt]));
+                    l[kt] += e0[kt] + e1[kt];
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&joined);
-                if (!warp_wait(&joined, jparity, p.wait_budget)) {
-                    if (lane == 0) flag_status(p.status, MXQ_DEV_TIMEOUT);
-                    return;
-                }
-                jparity ^= 1u;
+                constexpr uint32_t one = 0x3F803F80u;
 #pragma unroll
-                for (int e = 0; e < NT; ++e) {
-                    const int row = e * 8 + threadIdx.x / 16, d = (threadIdx.x % 16) * 4;
-                    float mm = -INFINITY;
+                for (int g = 0; g < NG; ++g) {
+                    const float s0 = __uint_as_float(pr0[g] << 16);
+                    const float s1 = __uint_as_float(pr1[g] << 16);
+                    const float b0 = fmaf(7.5f, s0, __uint_as_float(pr0[g] & 0xFFFF0000u));
+                    const float b1 = fmaf(7.5f, s1, __uint_as_float(pr1[g] & 0xFFFF0000u));
 #pragma unroll
-                    for (int wi = 0; wi < kWarps; ++wi)
-                        mm = fmaxf(mm, stat[wi * SH::kRows + row].x);
-                    const float ref = mm == -INFINITY ? 0.f : mm;
-                    float ll = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int kt = 0; kt < KT; ++kt)
+                        pb[kt][g] = fmaf(b0, e0[kt], fmaf(b1, e1[kt], pb[kt][g]));
+                    uint32_t f0[VT], f1[VT];
 #pragma unroll
-                    for (int wi = 0; wi < kWarps; ++wi) {
-                        const float2 ml = stat[wi * SH::kRows + row];
-                        const float f = exp2_approx(ml.x - ref);
-                        ll = fmaf(ml.y, f, ll);
-                        const float4 x = *reinterpret_cast<const float4*>(
-                            join + (wi * SH::kRows + row) * kRowPad + d);
-                        o.x = fmaf(x.x, f, o.x);
-                        o.y = fmaf(x.y, f, o.y);
-                        o.z = fmaf(x.z, f, o.z);
-                        o.w = fmaf(x.w, f, o.w);
+                    for (int vt = 0; vt < VT; ++vt) {
+                        // columns 2 i and 2 i + 1: rows 8 vt + i and 8 vt + 4 + i
+                        constexpr int other = KT == 1 ? 0 : 1;
+                        f0[vt] = transpose_8x8(
+                            cvt_bf16x2(s0 * e0[2 * vt], other ? s0 * e0[2 * vt + other] : 0.f));
+                        f1[vt] = transpose_8x8(
+                            cvt_bf16x2(s1 * e1[2 * vt], other ? s1 * e1[2 * vt + other] : 0.f));
+                        if (b == 0)
+                            mma_bf16_first(psum[vt][g], one, one, one, one, f0[vt], f1[vt]);
+                        else
+                            mma_bf16(psum[vt][g], one, one, one, one, f0[vt], f1[vt]);
                     }
-                    if (row >= rows) continue;
-                    if (whole) {
-                        const long long to = (long long)(st.row0 + row / st.heads) * p.Hq +
-                                             st.head0 + row % st.heads;
-                        const float inv = ll > 0.f ? 1.f / ll : 0.f;
-                        uint2 v;
-                        v.x = cvt_bf16x2(o.x * inv, o.y * inv);
-                        v.y = cvt_bf16x2(o.z * inv, o.w * inv);
-                        *reinterpret_cast<uint2*>(p.out + to * D + d0 + d) = v;
-                        if (p.lse && d0 + d == 0)
-                            p.lse[to] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718f : -INFINITY;
-                    } else {
-                        *reinterpret_cast<float4*>(part + 2 * SH::kRows + row * D + d0 + d) = o;
-                        if (d0 + d == 0) {
-                            part[2 * row] = mm;
-                            part[2 * row + 1] = ll;
+#pragma unroll
+                    for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
+                        const uint32_t x0 = codes16<0>(w0[u], eight), y0 = codes16<0>(w1[u], eight);
+                        const uint32_t x1 = codes16<1>(w0[u], eight), y1 = codes16<1>(w1[u], eight);
+                        const uint32_t x2 = codes16<2>(w0[u], eight), y2 = codes16<2>(w1[u], eight);
+                        const uint32_t x3 = codes16<3>(w0[u], eight), y3 = codes16<3>(w1[u], eight);
+#pragma unroll
+                        for (int vt = 0; vt < VT; ++vt) {
+                            mma_bf16(acc[vt][2 * u], x0, x1, y0, y1, f0[vt], f1[vt]);
+                            mma_bf16(acc[vt][2 * u + 1], x2, x3, y2, y3, f0[vt], f1[vt]);
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&joined);
-                if (!warp_wait(&joined, jparity, p.wait_budget)) {
-                    if (lane == 0) flag_status(p.status, MXQ_DEV_TIMEOUT);
-                    return;
-                }
-                jparity ^= 1u;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+            // The offset of 16 and the codes' centre of 7.5 leave the sums with every
+            // tile: the instruction cuts its fp32 sums off, so they have to stay as
+            // small as the result.
+#pragma unroll
+            for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[vt][t][c] = fmaf(-23.5f, psum[vt][t * 16 / G][c & 1], acc[vt][t][c]);
         }
-        if (st.flags & kLast) return;
+        done = end;
+
+        // ---- the warps' results of this row tile become one
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            const float x = sum_rows(l[kt]);
+            if (r == 0) stat[warp * SH::kRows + kt * 4 + i4] = make_float2(m[kt], x);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) pb[kt][g] = sum_rows(pb[kt][g]);
+        }
+        const bool whole = sp.flags == (kBegins | kEnds);
+        float* part = p.partial +
+                      (((long long)plane * p.ctas + cta) * 2 + ((sp.flags & kBegins) ? 1 : 0)) *
+                          SH::kPartialFloats;
+#pragma unroll 1
+        for (int d0 = 0; d0 < D; d0 += kChunk) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                if (t / (kChunk / 16) != d0 / kChunk) continue;
+#pragma unroll
+                for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (KT == 1 && (c & 1)) continue;
+                        const int kt = 2 * vt + (c & 1);
+                        join[(warp * SH::kRows + kt * 4 + i4) * kRowPad + (t % (kChunk / 16)) * 16 +
+                             r + (c >> 1) * 8] = acc[vt][t][c] + pb[kt][t * 16 / G];
+                    }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&joined);
+            if (gave_up(warp_wait(&joined, jparity, p.wait_budget))) return;
+            jparity ^= 1u;
+            for (int e = threadIdx.x; e < SH::kRows * (kChunk / 4); e += kThreads - 32) {
+                const int row = e / (kChunk / 4), d = (e % (kChunk / 4)) * 4;
+                if (row >= rows) break;
+                float mm = -INFINITY;
+#pragma unroll
+                for (int wi = 0; wi < kWarps; ++wi)
+                    mm = fmaxf(mm, stat[wi * SH::kRows + row].x);
+                const float ref = mm == -INFINITY ? 0.f : mm;
+                float ll = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int wi = 0; wi < kWarps; ++wi) {
+                    const float2 ml = stat[wi * SH::kRows + row];
+                    const float f = exp2_approx(ml.x - ref);
+                    ll = fmaf(ml.y, f, ll);
+                    const float4 x = *reinterpret_cast<const float4*>(
+                        join + (wi * SH::kRows + row) * kRowPad + d);
+                    o.x = fmaf(x.x, f, o.x);
+                    o.y = fmaf(x.y, f, o.y);
+                    o.z = fmaf(x.z, f, o.z);
+                    o.w = fmaf(x.w, f, o.w);
+                }
+                if (whole) {
+                    const long long to =
+                        (long long)(sp.row0 + row / heads) * p.Hq + head0 + row % heads;
+                    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                    uint2 v;
+                    v.x = cvt_bf16x2(o.x * inv, o.y * inv);
+                    v.y = cvt_bf16x2(o.z * inv, o.w * inv);
+                    *reinterpret_cast<uint2*>(p.out + to * D + d0 + d) = v;
+                    if (p.lse && d0 + d == 0)
+                        p.lse[to] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718f : -INFINITY;
+                } else {
+                    *reinterpret_cast<float4*>(part + 2 * SH::kRows + row * D + d0 + d) = o;
+                    if (d0 + d == 0) {
+                        part[2 * row] = mm;
+                        part[2 * row + 1] = ll;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&joined);
+            if (gave_up(warp_wait(&joined, jparity, p.wait_budget))) return;
+            jparity ^= 1u;
+        }
+        // everyone is done with this piece: its place takes a later one
+        if (threadIdx.x == 0) walk.next(p, plane, &pieces[at_piece % kPieces], seg);
     }
 }
 
@@ -779,14 +980,14 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnParams p, int 
     }
 }
 
-template <int D, int G, int NT>
+template <int D, int G, int KT>
 cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
-    using SH = Shape<D, G, NT>;
-    cudaError_t err = cudaFuncSetAttribute(kv_attn_kernel<D, G, NT>,
+    using SH = Shape<D, G, KT>;
+    cudaError_t err = cudaFuncSetAttribute(kv_attn_kernel<D, G, KT>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kSmem);
     if (err != cudaSuccess) return err;
     const unsigned grid = (unsigned)(p.planes * p.ctas);
-    kv_attn_kernel<D, G, NT><<<grid, kThreads, SH::kSmem, stream>>>(p);
+    kv_attn_kernel<D, G, KT><<<grid, SH::kThreads, SH::kSmem, stream>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess || !p.segs) return err;
     kv_join_kernel<D><<<grid, 256, 0, stream>>>(p, SH::kRows);
@@ -801,13 +1002,15 @@ size_t kv_attn_partial_bytes(int planes, int ctas, int tile_rows, int D) {
     return (size_t)planes * ctas * 2 * tile_rows * (D + 2) * sizeof(float);
 }
 
-int kv_attn_ctas_per_sm(int D, int tile_rows) { return D == 256 || tile_rows > 8 ? 2 : 3; }
+int kv_attn_ctas_per_sm() { return Shape<128, 64, 1>::kCtas; }
 
 cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int G, int tile_rows,
                            cudaStream_t stream) {
-#define MXQ_KV_ATTN(d, g)                                                     \
-    if (D == d && G == g)                                                     \
-        return tile_rows <= 8 ? launch<d, g, 1>(p, stream) : launch<d, g, 2>(p, stream);
+#define MXQ_KV_ATTN(d, g)                                        \
+    if (D == d && G == g)                                        \
+        return tile_rows <= 4   ? launch<d, g, 1>(p, stream)     \
+               : tile_rows <= 8 ? launch<d, g, 2>(p, stream)     \
+                                : launch<d, g, 4>(p, stream);
     MXQ_KV_ATTN(64, 32)
     MXQ_KV_ATTN(64, 64)
     MXQ_KV_ATTN(128, 32)

@@ -23,8 +23,6 @@
 
 namespace mxq {
 
-constexpr int kKvTile = 64;  // tokens of an attention tile (one stage of its ring)
-
 __host__ __device__ constexpr int kv_code_bytes(int D, int page) { return page * (D / 2); }
 __host__ __device__ constexpr int kv_pair_bytes(int D, int G, int page) {
     return page * (D / G) * 4;

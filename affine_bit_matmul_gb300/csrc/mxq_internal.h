@@ -195,6 +195,8 @@ struct KvAttnParams {
     int part_heads;          // ... of at most this many heads
     int tile_toks;           // tokens in a row tile
     int planes, ctas;        // ctas per plane
+    int page_shift;          // log2(page_size)
+    uint32_t eight;          // 8 (the kernel's left shift by a product)
     int* segs;               // workspace: 2 descriptors per CTA
     float* partial;          // workspace: 2 partial results per CTA
     int32_t* status;
@@ -206,7 +208,6 @@ cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int G, int tile_rows,
 // Workspace of launch_kv_attn: descriptors, then partial results.
 size_t kv_attn_seg_bytes(int planes, int ctas);
 size_t kv_attn_partial_bytes(int planes, int ctas, int tile_rows, int D);
-// CTAs that fit an SM at these sizes.
-int kv_attn_ctas_per_sm(int D, int tile_rows);
+int kv_attn_ctas_per_sm();
 
 }  // namespace mxq

@@ -391,7 +391,7 @@ mxq_status mxq_kv_read(const void* pages, const int32_t* slots, void* k_out, voi
  * both are reported (MXQ_DEV_BAD_SEQUENCE).  Rows that belong to no sequence
  * are not written.  No invalid entry makes the kernels read or write out of
  * bounds.  The result is deterministic for given arguments.
- * Requirements: Hq % Hkv == 0; scale finite; q, pages, out 16-byte aligned.  */
+ * Requirements: Hq % Hkv == 0; scale positive; q, pages, out 16-byte aligned.  */
 mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_head_stride,
                             const void* pages, const int32_t* page_table, const int32_t* ctx_lens,
                             const int32_t* q_starts, void* out, float* lse, int T, int S, int Hq,

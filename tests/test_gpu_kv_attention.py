@@ -308,3 +308,41 @@ def test_no_rows_and_no_sequences():
     assert out.shape == (0, 2, 64) and int(status.item()) == 0
     out = mxq.kv_attention(none, c.pages_d, c.table_d, c.ctx_d, i32([0, 0]), max_q_len=4)
     assert out.shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("heads,page", [(8, 64), (20, 16), (32, 128)])
+def test_long_runs_of_tiles(heads, page):
+    # enough tiles for every block to go round its ring several times
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    S, n, H, D, G = 7, 20000, 4, 128, 64
+    rng = np.random.default_rng(20)
+    used = -(-n // page)
+    n_pages = S * used
+    table = rng.permutation(n_pages).reshape(S, used).astype(np.int32)
+    ctx = np.asarray([n, n - 1, n - 63, n // 2, n, 64, n - 500], dtype=np.int32)
+    pages = torch.full((n_pages, H, ku.block_bytes(D, page, G)), 255, dtype=torch.uint8, device="cuda")
+    held = []
+    for i in range(S):
+        k = ku.bf16(rng.standard_normal((ctx[i], H, D), dtype=np.float32))
+        v = ku.bf16(rng.standard_normal((ctx[i], H, D), dtype=np.float32))
+        t = np.arange(ctx[i])
+        mxq.kv_append(dev_bf16(k), dev_bf16(v), pages, i32(table[i, t // page] * page + t % page))
+        held.append((k, v))
+    q = ku.bf16(rng.standard_normal((S, heads, D)))
+    for _ in range(3):
+        o = host(mxq.kv_attention(dev_bf16(q), pages, i32(table), i32(ctx)))
+        for i in range(S):
+            for h in (0, H - 1):
+                K, V = ku.encode(held[i][0][:, h], G), ku.encode(held[i][1][:, h], G)
+                k, v = ku.decode(*K, G), ku.decode(*V, G)
+                a = h * heads // H
+                s = (q[i, a].astype(np.float64) @ k.T) * D ** -0.5
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                ref = w @ v
+                E = np.asarray(D ** -0.5 * (np.abs(k) @ np.abs(q[i, a])).max())
+                A = np.repeat(7.5 * (w @ V[1].astype(np.float64)), G)
+                assert (np.abs(o[i, a] - ref) <= ku.tolerance(ref, A, w @ np.abs(v), E, False)).all()

@@ -75,7 +75,7 @@ def attend(L, q=FAKE, pages=FAKE, table=FAKE, lens=FAKE, starts=FAKE, out=FAKE, 
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), 1), (dict(S=-1), 1), (dict(Hq=7), 1), (dict(Hkv=0), 1), (dict(D=80), 1), (dict(n=0), 1),
     (dict(width=0), 1), (dict(page=20), 1), (dict(G=48), 1), (dict(most=0), 1), (dict(window=-1), 1), (dict(sinks=-1), 1),
-    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(starts=None), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=0.0), 1), (dict(scale=-0.1), 1), (dict(starts=None), 1),
     (dict(starts=None, T=2, S=2), 1), (dict(q=None), 1), (dict(table=None), 1), (dict(out=None), 1), (dict(qrs=4), 1),
     (dict(width=1 << 30, page=128), 3), (dict(q=ODD), 2), (dict(pages=ODD), 2), (dict(out=ODD), 2), (dict(lse=ODD2), 2),
     (dict(lens=ODD2), 2), (dict(st=ODD2), 2), (dict(ws=ODD), 2), (dict(ws=None), 6), (dict(wsb=64), 6),
