@@ -256,7 +256,6 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     p.planes = a.planes;
     p.ctas = a.ctas;
     p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
-    p.eight = 8;
     p.segs = a.ctas > 1 ? static_cast<int*>(workspace) : nullptr;
     p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.seg_bytes);
     p.status = dev_status;

@@ -7,22 +7,21 @@
 // The codes never become rounded values.  Per group,
 //   q . k^_t = sum_g s_tg (q_g . c_t) + b_tg sum(q_g)
 //   sum_t P_t v^_td = sum_t (P_t s_tg) c_td + sum_t P_t b_tg
-// so the matrix instructions multiply codes, and scales and biases are applied
-// in fp32 to a few numbers per token.
-//
-// Keys: a byte 0..15 read as an e4m3 number is 2^-9 times its value (the first
-// eight are the type's subnormals, the next eight its first binade), so the
-// nibbles of a code word, masked into bytes, are operands as they are.  A query
-// row is scaled by a power of two and split into two e4m3 numbers, which hold
-// the 8 bits of a bf16 number down to 2^-10 of the row's largest (and 2^-18 of
-// that absolutely): two of the instruction's columns a row, added afterwards.
-// Values: 16 + code is a bf16 number that one shift and one logic operation
-// make out of a pair of nibbles; the other operand, P_t s_tg, is rounded to
-// bf16, which keeps small weights where an 8-bit type would lose them.  That
-// rounding is the only one before the output's, and it is taken against codes
-// centred on 7.5 (the sum of the rounded P_t s_tg is kept beside the products),
-// which halves its weight.
-// Tokens are the instructions' rows (K) or depth (V), query rows the columns.
+// so the matrix instructions (m16n8k16, f16 operands, fp32 sums) multiply codes,
+// and scales and biases are applied in fp32 to a few numbers per token.  A code
+// in the lowest 4 bits of an f16 number is 2^-24 times its value, in the next 4
+// bits 2^-20 times it (both are subnormals, which the instructions take as they
+// are): a code word's 8 nibbles become 4 operand registers by 4 masks and one
+// shift, with no offset to take out again.
+//   Keys: the other operand is a query row, scaled by a power of two so that its
+// largest value is 2^13 .. 2^14; f16 then holds its bf16 values exactly down to
+// 2^-24 of the largest.
+//   Values: P_t s_tg, scaled by a power of two that keeps it below 2^15 for the
+// scales met so far, rounded to f16: 11 bits down to 2^-29 of the largest, which
+// is the only rounding before the output's.
+// Tokens are the instruction's rows (K) or depth (V), query rows the columns: row
+// i in column 2 i, row 4 + i in column 2 i + 1, so up to 4 rows leave half of a
+// lane's numbers unused and not computed.
 //
 // Work split: a unit is (row tile, tile of tokens that it sees); the units of a
 // plane, in order, are cut into equal runs, one per CTA, whatever the lengths
@@ -78,8 +77,9 @@ struct Shape {
     static constexpr int kCtas = 2;
     static constexpr int kStageBytes = kv_block_bytes(D, G, kTile);
     // the queries lie in shared memory where they would take 32 registers or more
-    static constexpr bool kQueryShared = D * KT >= 512;
-    static constexpr int kQueryBytes = kQueryShared ? KT * D * 8 : 0;
+    static constexpr int kColumns = (KT + 1) / 2;  // tiles of 8 columns
+    static constexpr bool kQueryShared = D * kColumns >= 256;
+    static constexpr int kQueryBytes = kQueryShared ? kColumns * D * 16 : 0;
     static constexpr int kWarps = KT == 4 ? W4 : D == 256 ? 5 : KT == 1 ? W1 : W2;
     static constexpr int kThreads = 32 * (kWarps + 1);
     static constexpr int kJoinBytes = kWarps * kRows * kRowPad * 4;
@@ -139,56 +139,38 @@ __device__ __forceinline__ Span span_of(const KvAttnParams& p, int s, int plane)
     return r;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The same from zero.
-__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                               uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-__device__ __forceinline__ void mma_e4m3_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                               uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Larger of two numbers in each half word.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
-// Four fp32 numbers -> four e4m3 numbers, the first in the lowest byte; and the
-// rest of each that the rounding left, in r.
-__device__ __forceinline__ uint32_t e4m3_of(const float (&x)[4], float (&r)[4]) {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
-    uint32_t a, b;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"(lo));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(hi));
-    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    r[0] = x[0] - p.x;
-    r[1] = x[1] - p.y;
-    r[2] = x[2] - q.x;
-    r[3] = x[3] - q.y;
-    return (uint32_t)lo | ((uint32_t)hi << 16);
-}
+// 2^(e - 127) for a biased exponent 1 <= e <= 254.
+__device__ __forceinline__ float pow2_of(int e) { return __uint_as_float((uint32_t)e << 23); }
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
     uint32_t d;
@@ -202,13 +184,14 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// Nibble N of both halves of a word -> two bf16 numbers 16 + code.  Logic
-// operations and shifts share the pipe that bounds this kernel; the left shift
-// is a product with an 8 that the compiler does not know, which runs beside it.
-template <int N>
-__device__ __forceinline__ uint32_t codes16(uint32_t w, uint32_t eight) {
-    const uint32_t x = N == 0 ? w * eight : w >> (N == 1 ? 1 : N == 2 ? 5 : 9);
-    return (x & 0x00780078u) | 0x41804180u;
+// The four operand registers of a code word: nibbles 0 and 4, 1 and 5, ...; the
+// odd ones are 16 times as large.
+__device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&x)[4]) {
+    x[0] = w & 0x000F000Fu;
+    x[1] = w & 0x00F000F0u;
+    w >>= 8;
+    x[2] = w & 0x000F000Fu;
+    x[3] = w & 0x00F000F0u;
 }
 
 // Sum over the lanes of the same column of the instruction's result.
@@ -460,7 +443,7 @@ __device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int total
                 if (work) flag_status(p.status, MXQ_DEV_TIMEOUT);
                 break;
             }
-            __nanosleep(32);
+            __nanosleep(100);
         }
     }
     // no copy may land after the CTA is gone
@@ -476,7 +459,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     constexpr int NG = D / G;          // groups
     constexpr int U = D / 32;          // code words of a lane per 8 tokens
     constexpr int MT = D / 16;         // output tiles of 16 values
-    constexpr int VT = (KT + 1) / 2;   // output columns / 8
+    constexpr int VT = SH::kColumns;   // tiles of 8 columns
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kSlots], empty[kSlots], joined;
     __shared__ Tile tiles[kSlots];
@@ -485,7 +468,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     __shared__ int sums[kThreads];
     float* join = reinterpret_cast<float*>(smem + SH::kRingBytes);
     float2* stat = reinterpret_cast<float2*>(smem + SH::kRingBytes + SH::kJoinBytes);
-    uint2* queries = reinterpret_cast<uint2*>(smem + SH::kSmem - SH::kQueryBytes);
+    uint4* queries = reinterpret_cast<uint4*>(smem + SH::kSmem - SH::kQueryBytes);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int plane = blockIdx.x / p.ctas, cta = blockIdx.x % p.ctas;
@@ -569,7 +552,6 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     auto pairs_at = [&](int b) {
         return kv_code_bytes(D, piece) + r * NG * 4 + (b & 1) * pairs_1 + (b >> 1) * pairs_2;
     };
-    const uint32_t eight = p.eight;
     uint32_t jparity = 0;
     int n = warp;  // this warp's units: those whose number in the run is warp modulo kWarps
     auto gave_up = [&](bool ok) {
@@ -581,82 +563,80 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         const Piece& sp = pieces[at_piece % kPieces];
         const int heads = sp.heads, rows = sp.toks * heads, head0 = sp.head0;
         const int p0 = sp.p0, p1 = p0 + sp.toks - 1, end = sp.end;
-        // Queries as the instruction's columns: column r of key tile kt is the
-        // first (r even) or second part of row 4 kt + r / 2, so a lane's two
-        // columns of a result are the two parts of row 4 kt + i4.
-        uint2 qf[KT][SH::kQueryShared ? 1 : U];
-        float qsum[KT][NG];    // sum of the row's values over a group, and
+        // Queries as the instruction's columns: column r of tile vt is row 8 vt + r / 2,
+        // and 4 more where r is odd.
+        uint4 qf[VT][SH::kQueryShared ? 1 : U];
+        float qsum[KT][NG];    // sum of a row's values over a group, in the products' unit
         float unit[KT];        // the factor that makes scores (times log2 e) of the sums
         int pos[KT];
         float acc[VT][MT][4];
         float pb[KT][NG], l[KT], m[KT], mu[KT];
+        int v_exp = 20;        // the values' scales are below 2^(v_exp - 126) ...
+        uint32_t v_bound = 0;  // ... whose bf16 bits these are
+        float v_up = 0.f;      // 2^7 over that
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            const int rr = kt * 4 + (r >> 1);
-            const bool in = rr < rows;
+        for (int vt = 0; vt < VT; ++vt) {
+            const int rr = vt * 8 + (r >> 1) + (r & 1) * 4;
+            const bool in = rr < rows && (KT > 1 || !(r & 1));
             const int j = in ? rr / heads : 0, hh = in ? rr % heads : 0;
             const __nv_bfloat16* src = p.q + (long long)(sp.row0 + j) * p.q_row_stride +
                                        (long long)(head0 + hh) * p.q_head_stride + 8 * i4;
             uint4 raw[U];
-            float big = 0.f;
+            uint32_t big = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 raw[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (in) raw[u] = __ldg(reinterpret_cast<const uint4*>(src + 32 * u));
-                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
-                                           fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+                big = max_u16x2(big, max_u16x2(raw[u].x & 0x7FFF7FFFu, raw[u].y & 0x7FFF7FFFu));
+                big = max_u16x2(big, max_u16x2(raw[u].z & 0x7FFF7FFFu, raw[u].w & 0x7FFF7FFFu));
             }
-            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-            // the largest value becomes 2^7 .. 2^8; e4m3 ends at 448
-            const int ex = max((int)(__float_as_uint(big) >> 23), 16);
-            const float up = __uint_as_float((uint32_t)(261 - ex) << 23);  // 2^(134 - ex)
+            big = max(big & 0xFFFFu, big >> 16);
+            big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+            big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+            const int ex = max((int)(big >> 7), 16);  // biased exponent of the largest
+            const float up = pow2_of(267 - ex);       // 2^(140 - ex)
             float part[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) part[g] = 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-                // a code word's low nibbles are values 0, 2, 4, 6, its high ones 1, 3, 5, 7
-                float ev[4], od[4], re[4], ro[4], x[4];
+                float x[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    ev[e] = __uint_as_float(w[e] << 16) * up;
-                    od[e] = __uint_as_float(w[e] & 0xFFFF0000u) * up;
-                    part[u * 32 / G] += ev[e] + od[e];
+                    x[2 * e] = __uint_as_float(w[e] << 16) * up;
+                    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * up;
+                    part[u * 32 / G] += x[2 * e] + x[2 * e + 1];
                 }
-                uint2 f = make_uint2(e4m3_of(ev, re), e4m3_of(od, ro));
-                const uint2 f2 = make_uint2(e4m3_of(re, x), e4m3_of(ro, x));
-                if (r & 1) f = f2;
+                // as a code word's nibbles pair up; the odd ones are 16 times as large
+                const uint4 f = make_uint4(
+                    cvt_f16x2(x[0], x[4]), cvt_f16x2(x[1] * 0.0625f, x[5] * 0.0625f),
+                    cvt_f16x2(x[2], x[6]), cvt_f16x2(x[3] * 0.0625f, x[7] * 0.0625f));
                 if (SH::kQueryShared) {
-                    if (u % kWarps == warp) queries[(kt * U + u) * 32 + lane] = f;
+                    if (u % kWarps == warp) queries[(vt * U + u) * 32 + lane] = f;
                 } else {
-                    qf[kt][SH::kQueryShared ? 0 : u] = f;
+                    qf[vt][SH::kQueryShared ? 0 : u] = f;
                 }
             }
-            // codes as e4m3 numbers are 2^-9 of their values: so are these sums
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                float x = part[g];
-                x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-                x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-                qsum[kt][g] = __shfl_sync(0xFFFFFFFFu, x, 8 * i4) * 0x1p-9f;
-                pb[kt][g] = 0.f;
+            for (int c = 0; c < (KT == 1 ? 1 : 2); ++c) {
+                const int kt = 2 * vt + c, from = 8 * i4 + 4 * c;  // a lane of column 2 i4 + c
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    float x = part[g];
+                    x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+                    x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+                    qsum[kt][g] = __shfl_sync(0xFFFFFFFFu, x, from) * 0x1p-24f;
+                    pb[kt][g] = 0.f;
+                }
+                const int ec = __shfl_sync(0xFFFFFFFFu, ex, from);
+                unit[kt] = fmaxf(p.scale_log2 * 0x1p24f * pow2_of(ec - 13), 0x1p-126f);
+                l[kt] = 0.f;
+                m[kt] = -INFINITY;
+                mu[kt] = 0.f;
+                const int row = kt * 4 + i4;
+                pos[kt] = row < rows ? p0 + row / heads : -1;
             }
-            const int down = __shfl_sync(0xFFFFFFFFu, ex, 8 * i4);  // 2^(ex - 134 + 9)
-            unit[kt] = fmaxf(
-                p.scale_log2 * 0x1p9f * __uint_as_float((uint32_t)max(down - 7, 1) << 23), 0x1p-126f);
-            l[kt] = 0.f;
-            m[kt] = -INFINITY;
-            mu[kt] = 0.f;
-            const int mine_row = kt * 4 + i4;
-            pos[kt] = mine_row < rows ? p0 + mine_row / heads : -1;
-        }
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -687,19 +667,21 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                 load_pairs<NG>(at + pairs_at(b) + 8 * NG * 4, pr1);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    float a[KT][4];
+                    float a[VT][4];
 #pragma unroll
                     for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
-                        const uint32_t x0 = w0[u] & 0x0F0F0F0Fu, x1 = (w0[u] >> 4) & 0x0F0F0F0Fu;
-                        const uint32_t y0 = w1[u] & 0x0F0F0F0Fu, y1 = (w1[u] >> 4) & 0x0F0F0F0Fu;
+                        uint32_t x[4], y[4];
+                        codes_of(w0[u], x);
+                        codes_of(w1[u], y);
 #pragma unroll
-                        for (int kt = 0; kt < KT; ++kt) {
-                            const uint2 f = SH::kQueryShared ? queries[(kt * U + u) * 32 + lane]
-                                                             : qf[kt][SH::kQueryShared ? 0 : u];
+                        for (int vt = 0; vt < VT; ++vt) {
+                            const uint4 f = SH::kQueryShared ? queries[(vt * U + u) * 32 + lane]
+                                                             : qf[vt][SH::kQueryShared ? 0 : u];
                             if (u == g * G / 32)
-                                mma_e4m3_first(a[kt], x0, y0, x1, y1, f.x, f.y);
+                                mma_f16_first(a[vt], x[0], y[0], x[1], y[1], f.x, f.y);
                             else
-                                mma_e4m3(a[kt], x0, y0, x1, y1, f.x, f.y);
+                                mma_f16(a[vt], x[0], y[0], x[1], y[1], f.x, f.y);
+                            mma_f16(a[vt], x[2], y[2], x[3], y[3], f.z, f.w);
                         }
                     }
                     const float s0 = __uint_as_float(pr0[g] << 16);
@@ -711,8 +693,8 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                         const float qs = qsum[kt][g];
                         const float z0 = g ? fmaf(b0, qs, sc[b][kt][0]) : b0 * qs;
                         const float z1 = g ? fmaf(b1, qs, sc[b][kt][1]) : b1 * qs;
-                        sc[b][kt][0] = fmaf(s0, a[kt][0] + a[kt][1], z0);
-                        sc[b][kt][1] = fmaf(s1, a[kt][2] + a[kt][3], z1);
+                        sc[b][kt][0] = fmaf(s0, a[kt / 2][kt & 1], z0);
+                        sc[b][kt][1] = fmaf(s1, a[kt / 2][2 + (kt & 1)], z1);
                     }
                 }
             }
@@ -740,9 +722,21 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                 fence_proxy_async_smem();  // the slot's next copy comes after these stores
                 __syncwarp();
             }
-            // ---- running maximum: moved only when a score is far above it
+            // ---- running maximum: moved only when a score is far above it, and the
+            // values' power of two, when a scale is above it
+            uint32_t scales = 0;  // the low half word
+#pragma unroll
+            for (int b = 0; b < SUB; ++b) {
+                uint32_t pr0[NG], pr1[NG];
+                load_pairs<NG>(at + v_off + pairs_at(b), pr0);
+                load_pairs<NG>(at + v_off + pairs_at(b) + 8 * NG * 4, pr1);
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    scales = max_u16x2(scales, max_u16x2(pr0[g], pr1[g]));
+            }
+            scales &= 0xFFFFu;
             float top[KT];
-            bool over = false;
+            bool over = scales > v_bound;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 top[kt] = -INFINITY;
@@ -752,6 +746,15 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                 over |= top[kt] > m[kt] + 8.f;
             }
             if (__any_sync(0xFFFFFFFFu, over)) {
+                // (a scale with its sign set comes here every time)
+                uint32_t big = __reduce_max_sync(0xFFFFFFFFu, scales & 0x7FFFu);
+                if (scales > 0x7FFFu) big = 0x7F00u;
+                big = __reduce_max_sync(0xFFFFFFFFu, big);
+                const int e_new = max(v_exp, min((int)(big >> 7), 254));
+                const float fv = pow2_of(max(v_exp - e_new + 127, 1));
+                v_exp = e_new;
+                v_bound = ((uint32_t)e_new << 7) | 127u;
+                v_up = pow2_of(260 - e_new);  // 2^(133 - e_new)
                 float f[KT];
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
@@ -766,6 +769,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                     l[kt] *= f[kt];
 #pragma unroll
                     for (int g = 0; g < NG; ++g) pb[kt][g] *= f[kt];
+                    f[kt] *= fv;
                 }
 #pragma unroll
                 for (int vt = 0; vt < VT; ++vt)
@@ -776,7 +780,6 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                             acc[vt][t][c] *= f[KT == 1 ? 0 : 2 * vt + (c & 1)];
             }
             // ---- weighted sum of the values
-            float psum[VT][NG][4];  // sum of the rounded weights
 #pragma unroll
             for (int b = 0; b < SUB; ++b) {
                 uint32_t w0[U], w1[U], pr0[NG], pr1[NG];
@@ -784,63 +787,48 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                 load_pairs<NG>(at + v_off + pairs_at(b) + 8 * NG * 4, pr1);
                 load_words<U>(at + v_off + words_at(b), w0);
                 load_words<U>(at + v_off + words_at(b) + 4 * D, w1);
-                float e0[KT], e1[KT];
+                float e0[KT], e1[KT], h0[KT], h1[KT];
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
                     e0[kt] = exp2_approx(fmaf(sc[b][kt][0], unit[kt], -mu[kt]));
                     e1[kt] = exp2_approx(fmaf(sc[b][kt][1], unit[kt], -mu[kt]));
                     l[kt] += e0[kt] + e1[kt];
+                    h0[kt] = e0[kt] * v_up;
+                    h1[kt] = e1[kt] * v_up;
                 }
-                constexpr uint32_t one = 0x3F803F80u;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const float s0 = __uint_as_float(pr0[g] << 16);
                     const float s1 = __uint_as_float(pr1[g] << 16);
-                    const float b0 = fmaf(7.5f, s0, __uint_as_float(pr0[g] & 0xFFFF0000u));
-                    const float b1 = fmaf(7.5f, s1, __uint_as_float(pr1[g] & 0xFFFF0000u));
+                    const float b0 = __uint_as_float(pr0[g] & 0xFFFF0000u);
+                    const float b1 = __uint_as_float(pr1[g] & 0xFFFF0000u);
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt)
                         pb[kt][g] = fmaf(b0, e0[kt], fmaf(b1, e1[kt], pb[kt][g]));
                     uint32_t f0[VT], f1[VT];
 #pragma unroll
                     for (int vt = 0; vt < VT; ++vt) {
-                        // columns 2 i and 2 i + 1: rows 8 vt + i and 8 vt + 4 + i
                         constexpr int other = KT == 1 ? 0 : 1;
                         f0[vt] = transpose_8x8(
-                            cvt_bf16x2(s0 * e0[2 * vt], other ? s0 * e0[2 * vt + other] : 0.f));
+                            cvt_f16x2(s0 * h0[2 * vt], other ? s0 * h0[2 * vt + other] : 0.f));
                         f1[vt] = transpose_8x8(
-                            cvt_bf16x2(s1 * e1[2 * vt], other ? s1 * e1[2 * vt + other] : 0.f));
-                        if (b == 0)
-                            mma_bf16_first(psum[vt][g], one, one, one, one, f0[vt], f1[vt]);
-                        else
-                            mma_bf16(psum[vt][g], one, one, one, one, f0[vt], f1[vt]);
+                            cvt_f16x2(s1 * h1[2 * vt], other ? s1 * h1[2 * vt + other] : 0.f));
                     }
 #pragma unroll
                     for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
-                        const uint32_t x0 = codes16<0>(w0[u], eight), y0 = codes16<0>(w1[u], eight);
-                        const uint32_t x1 = codes16<1>(w0[u], eight), y1 = codes16<1>(w1[u], eight);
-                        const uint32_t x2 = codes16<2>(w0[u], eight), y2 = codes16<2>(w1[u], eight);
-                        const uint32_t x3 = codes16<3>(w0[u], eight), y3 = codes16<3>(w1[u], eight);
+                        uint32_t x[4], y[4];
+                        codes_of(w0[u], x);
+                        codes_of(w1[u], y);
 #pragma unroll
                         for (int vt = 0; vt < VT; ++vt) {
-                            mma_bf16(acc[vt][2 * u], x0, x1, y0, y1, f0[vt], f1[vt]);
-                            mma_bf16(acc[vt][2 * u + 1], x2, x3, y2, y3, f0[vt], f1[vt]);
+                            mma_f16(acc[vt][2 * u], x[0], x[1], y[0], y[1], f0[vt], f1[vt]);
+                            mma_f16(acc[vt][2 * u + 1], x[2], x[3], y[2], y[3], f0[vt], f1[vt]);
                         }
                     }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
-            // The offset of 16 and the codes' centre of 7.5 leave the sums with every
-            // tile: the instruction cuts its fp32 sums off, so they have to stay as
-            // small as the result.
-#pragma unroll
-            for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        acc[vt][t][c] = fmaf(-23.5f, psum[vt][t * 16 / G][c & 1], acc[vt][t][c]);
         }
         done = end;
 
@@ -852,6 +840,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
 #pragma unroll
             for (int g = 0; g < NG; ++g) pb[kt][g] = sum_rows(pb[kt][g]);
         }
+        const float v_down = pow2_of(max(v_exp - 6, 1));  // 1 / v_up
         const bool whole = sp.flags == (kBegins | kEnds);
         float* part = p.partial +
                       (((long long)plane * p.ctas + cta) * 2 + ((sp.flags & kBegins) ? 1 : 0)) *
@@ -868,7 +857,9 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                         if (KT == 1 && (c & 1)) continue;
                         const int kt = 2 * vt + (c & 1);
                         join[(warp * SH::kRows + kt * 4 + i4) * kRowPad + (t % (kChunk / 16)) * 16 +
-                             r + (c >> 1) * 8] = acc[vt][t][c] + pb[kt][t * 16 / G];
+                             r + (c >> 1) * 8] =
+                            fmaf(acc[vt][t][c] * (c >> 1 ? 0x1p20f : 0x1p24f), v_down,
+                                 pb[kt][t * 16 / G]);
                     }
             }
             __syncwarp();

@@ -196,7 +196,6 @@ struct KvAttnParams {
     int tile_toks;           // tokens in a row tile
     int planes, ctas;        // ctas per plane
     int page_shift;          // log2(page_size)
-    uint32_t eight;          // 8 (the kernel's left shift by a product)
     int* segs;               // workspace: 2 descriptors per CTA
     float* partial;          // workspace: 2 partial results per CTA
     int32_t* status;
