@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     __shared__ Piece pieces[kPieces];
     __shared__ Walk<TILE> walk;  // thread 0's
     __shared__ int sums[kThreads];
+    pdl_launch_dependents();  // the joining kernel waits for this one's end by itself
     float* join = reinterpret_cast<float*>(smem + SH::kRingBytes);
     float2* stat = reinterpret_cast<float2*>(smem + SH::kRingBytes + SH::kJoinBytes);
     uint4* queries = reinterpret_cast<uint4*>(smem + SH::kSmem - SH::kQueryBytes);
@@ -917,9 +918,17 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
 }
 
 // Joins the pieces of the row tiles that were cut: the CTA whose last piece
-// begins one is followed by those that go on with it, in order.
+// begins one is followed by those that go on with it, in order.  One CTA a row
+// tile; its threads share the pieces out and add their sums in a fixed order.
+constexpr int kJoinThreads = 512;
+
 template <int D>
-__global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnParams p, int tile_rows) {
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParams p, int tile_rows) {
+    extern __shared__ float weight[];        // [piece][row]: 2^(max - overall max)
+    __shared__ float4 sums[kJoinThreads];
+    __shared__ float row_inv[16], row_lse[16];
+    __shared__ int last_piece;
+    pdl_wait();
     const int plane = blockIdx.x / p.ctas, cta = blockIdx.x % p.ctas;
     const long long base = (long long)plane * p.ctas;
     const Seg* segs = reinterpret_cast<const Seg*>(p.segs);
@@ -930,44 +939,87 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnParams p, int 
         g.toks * g.heads > tile_rows || g.row0 < 0 || g.row0 > p.T - g.toks || g.head0 < 0 ||
         g.head0 > p.Hq - g.heads)
         return;
-    int last = cta;
-    while (last + 1 < p.ctas) {
-        ++last;
-        const int f = segs[(base + last) * 2].flags;
-        if (f < 0 || (f & kEnds)) break;
-    }
-    const long long stride = (long long)tile_rows * (D + 2);
-    const float* first = p.partial + ((base + cta) * 2 + 1) * stride;
-    const float* next = p.partial + (base + cta) * 2 * stride;  // piece 0 of CTA cta + k: + 2 k
-    const int rows = g.toks * g.heads, n = last - cta;
-    for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
-        const int row = i / (D / 4), d = (i % (D / 4)) * 4;
-        float mm = first[2 * row];
-        for (int k = 1; k <= n; ++k) mm = fmaxf(mm, next[2 * k * stride + 2 * row]);
-        const float ref = mm == -INFINITY ? 0.f : mm;
-        float f = exp2_approx(first[2 * row] - ref);
-        float ll = first[2 * row + 1] * f;
-        const float4 x = *reinterpret_cast<const float4*>(first + 2 * tile_rows + row * D + d);
-        float4 o = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-#pragma unroll 4
-        for (int k = 1; k <= n; ++k) {
-            const float* q = next + 2 * k * stride;
-            const float2 ml = *reinterpret_cast<const float2*>(q + 2 * row);
-            const float4 y = *reinterpret_cast<const float4*>(q + 2 * tile_rows + row * D + d);
-            f = exp2_approx(ml.x - ref);
-            ll = fmaf(ml.y, f, ll);
-            o.x = fmaf(y.x, f, o.x);
-            o.y = fmaf(y.y, f, o.y);
-            o.z = fmaf(y.z, f, o.z);
-            o.w = fmaf(y.w, f, o.w);
+    const int tid = threadIdx.x;
+    if (tid == 0) last_piece = p.ctas - 1;
+    __syncthreads();
+    for (int c = cta + 1 + tid; c < p.ctas; c += kJoinThreads) {
+        const int f = segs[(base + c) * 2].flags;
+        if (f < 0 || (f & kEnds)) {
+            atomicMin(&last_piece, c);
+            break;
         }
-        const long long to = (long long)(g.row0 + row / g.heads) * p.Hq + g.head0 + row % g.heads;
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
-        uint2 v;
-        v.x = cvt_bf16x2(o.x * inv, o.y * inv);
-        v.y = cvt_bf16x2(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(p.out + to * D + d) = v;
-        if (p.lse && d == 0) p.lse[to] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718f : -INFINITY;
+    }
+    __syncthreads();
+    const int rows = g.toks * g.heads, n = last_piece - cta + 1;
+    const long long stride = (long long)tile_rows * (D + 2);
+    // piece 0 is the CTA's second, piece k the first of CTA cta + k
+    auto piece = [&](int k) {
+        return p.partial + ((base + cta + k) * 2 + (k ? 0 : 1)) * stride;
+    };
+    for (int i = tid; i < n * rows; i += kJoinThreads)
+        weight[i] = piece(i / rows)[2 * (i % rows)];
+    __syncthreads();
+    const int lane = tid & 31;
+    for (int row = tid / 32; row < rows; row += kJoinThreads / 32) {
+        float mm = -INFINITY;
+        for (int k = lane; k < n; k += 32) mm = fmaxf(mm, weight[k * rows + row]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        float ll = 0.f;
+        for (int k = lane; k < n; k += 32) {
+            const float f = exp2_approx(weight[k * rows + row] - ref);
+            weight[k * rows + row] = f;
+            ll = fmaf(piece(k)[2 * row + 1], f, ll);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
+        if (lane == 0) {
+            row_inv[row] = ll > 0.f ? 1.f / ll : 0.f;
+            row_lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718f : -INFINITY;
+        }
+    }
+    __syncthreads();
+    const int items = rows * (D / 4);                           // of 4 values
+    const int parts = items < kJoinThreads ? kJoinThreads / items : 1;
+    for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
+        const int part = parts > 1 ? tid / items : 0, i = parts > 1 ? tid % items : i0 + tid;
+        const bool mine = part < parts && i < items;
+        const int row = i / (D / 4), d = (i % (D / 4)) * 4;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mine) {
+#pragma unroll 8
+            for (int k = part; k < n; k += parts) {
+                const float4 y =
+                    *reinterpret_cast<const float4*>(piece(k) + 2 * tile_rows + row * D + d);
+                const float f = weight[k * rows + row];
+                o.x = fmaf(y.x, f, o.x);
+                o.y = fmaf(y.y, f, o.y);
+                o.z = fmaf(y.z, f, o.z);
+                o.w = fmaf(y.w, f, o.w);
+            }
+        }
+        if (parts > 1) {
+            sums[tid] = o;
+            __syncthreads();
+            if (part == 0)
+                for (int k = 1; k < parts; ++k) {
+                    const float4 y = sums[k * items + i];
+                    o.x += y.x;
+                    o.y += y.y;
+                    o.z += y.z;
+                    o.w += y.w;
+                }
+        }
+        if (mine && part == 0) {
+            const long long to = (long long)(g.row0 + row / g.heads) * p.Hq + g.head0 + row % g.heads;
+            const float inv = row_inv[row];
+            uint2 v;
+            v.x = cvt_bf16x2(o.x * inv, o.y * inv);
+            v.y = cvt_bf16x2(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2*>(p.out + to * D + d) = v;
+            if (p.lse && d == 0) p.lse[to] = row_lse[row];
+        }
     }
 }
 
@@ -981,8 +1033,18 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     kv_attn_kernel<D, G, KT><<<grid, SH::kThreads, SH::kSmem, stream>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess || !p.segs) return err;
-    kv_join_kernel<D><<<grid, 256, 0, stream>>>(p, SH::kRows);
-    return cudaGetLastError();
+    // the second kernel's blocks are placed as the first one's finish
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = (size_t)p.ctas * SH::kRows * sizeof(float);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D>, p, (int)SH::kRows);
 }
 
 }  // namespace
