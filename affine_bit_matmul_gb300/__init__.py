@@ -156,7 +156,7 @@ def lib():
         L.mxq_kv_attention.argtypes = [P, J, J, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F,
                                        I, I, P, Z, P, P]
         L.mxq_kv_attention.restype = I
-        L.mxq_kv_attention_workspace_bytes.argtypes = [I, I, I, I]
+        L.mxq_kv_attention_workspace_bytes.argtypes = [I, I, I, I, I, I]
         L.mxq_kv_attention_workspace_bytes.restype = Z
         L.mxq_gather_workspace_bytes.argtypes = [I, I, I, I]
         L.mxq_gather_workspace_bytes.restype = Z
@@ -799,9 +799,11 @@ def kv_read(pages, slots, head_dim: int, group_size: int = 64, k_out=None, v_out
     return outs[0], outs[1]
 
 
-def kv_attention_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_q_len: int) -> int:
-    """Workspace bytes for kv_attention."""
-    return int(lib().mxq_kv_attention_workspace_bytes(heads, kv_heads, head_dim, max_q_len))
+def kv_attention_workspace_bytes(rows: int, seqs: int, heads: int, kv_heads: int, head_dim: int,
+                                 max_q_len: int = 1) -> int:
+    """Workspace bytes for kv_attention of ``rows`` query rows in ``seqs`` sequences."""
+    return int(lib().mxq_kv_attention_workspace_bytes(rows, seqs, heads, kv_heads, head_dim,
+                                                      max_q_len))
 
 
 def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int = 1,
@@ -850,7 +852,7 @@ def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int =
     if max_q_len <= 0:
         raise ValueError("max_q_len must be positive")
     if workspace is None:
-        need = kv_attention_workspace_bytes(Hq, Hkv, D, max(1, min(max_q_len, T)))
+        need = kv_attention_workspace_bytes(T, S, Hq, Hkv, D, max_q_len)
         workspace = torch.empty((need,),
                                 dtype=torch.uint8, device=dev)
     _require(workspace, "workspace", (torch.uint8,), dev)

@@ -24,13 +24,20 @@ bool cache_shape(int D, int G, int page_size) {
 
 bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 
-// How an attention call is cut into row tiles and CTAs.
+// How an attention call is cut into row tiles and CTAs.  Sequences whose rows
+// times query heads of a key/value head are at most 16 go through the kernel for
+// few rows (bound by the cache's bytes), the others through the tensor cores'
+// (bound by their products).  Measured for 8 query heads to a key head over 8192
+// tokens: 2 rows 16, 3 rows 24 of the products' 128.
 struct AttnPlan {
-    int head_parts, part_heads, tile_rows, tile_toks, planes, ctas;
-    size_t seg_bytes, bytes;
+    int head_parts, part_heads, tile_rows, tile_toks, ctas;  // few rows
+    int many, many_parts, many_heads, half_toks, many_toks, many_ctas, max_entries;
+    size_t seg_bytes, few_bytes;
+    size_t many_seg_bytes, many_partial_bytes, seq_bytes, entry_bytes, before_bytes, many_bytes;
+    size_t bytes;
 };
 
-AttnPlan plan_attn(int Hq, int Hkv, int D, int max_q, int sms) {
+AttnPlan plan_attn(int T, int S, int Hq, int Hkv, int D, int max_q, int sms) {
     AttnPlan a;
     const int rep = Hq / Hkv;
     a.head_parts = (rep + 15) / 16;
@@ -38,15 +45,28 @@ AttnPlan plan_attn(int Hq, int Hkv, int D, int max_q, int sms) {
     const long long rows = (long long)max_q * a.part_heads;
     a.tile_rows = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
     a.tile_toks = a.tile_rows / a.part_heads;
-    a.planes = (max_q + a.tile_toks - 1) / a.tile_toks;
-    const int all = sms * mxq::kv_attn_ctas_per_sm();
-    a.ctas = a.planes == 1 ? all : (2 * all + a.planes - 1) / a.planes;
-    a.seg_bytes = 0;
-    a.bytes = 0;
-    if (a.ctas > 1) {  // otherwise no row tile is cut
-        a.seg_bytes = align_up(mxq::kv_attn_seg_bytes(a.planes, a.ctas), 256);
-        a.bytes = a.seg_bytes +
-                  align_up(mxq::kv_attn_partial_bytes(a.planes, a.ctas, a.tile_rows, D), 256);
+    a.ctas = sms * mxq::kv_attn_ctas_per_sm();
+    a.seg_bytes = align_up(mxq::kv_attn_seg_bytes(a.ctas), 256);
+    a.few_bytes = a.seg_bytes + align_up(mxq::kv_attn_partial_bytes(a.ctas, a.tile_rows, D), 256);
+    a.bytes = a.few_bytes;
+    a.many = max_q > a.tile_toks;
+    if (a.many) {
+        a.many_parts = (rep + 127) / 128;
+        a.many_heads = (rep + a.many_parts - 1) / a.many_parts;
+        a.half_toks = 128 / a.many_heads;
+        const int tile_rows = mxq::kv_prefill_rows(D);
+        a.many_toks = a.half_toks * (tile_rows / 128);
+        a.many_ctas = sms;
+        a.max_entries = T / a.many_toks + S;
+        a.many_seg_bytes = align_up(mxq::kv_attn_seg_bytes(a.many_ctas), 256);
+        a.many_partial_bytes =
+            align_up(mxq::kv_attn_partial_bytes(a.many_ctas, tile_rows, D), 256);
+        a.seq_bytes = align_up((size_t)S * sizeof(int), 256);
+        a.entry_bytes = align_up((size_t)a.max_entries * mxq::kv_prefill_entry_bytes(), 256);
+        a.before_bytes = align_up((size_t)a.max_entries * sizeof(int), 256);
+        a.many_bytes = a.many_seg_bytes + a.many_partial_bytes + a.seq_bytes + a.entry_bytes +
+                       a.before_bytes + 256;
+        a.bytes += a.many_bytes;
     }
     return a;
 }
@@ -181,16 +201,12 @@ mxq_status mxq_kv_read(const void* pages, const int32_t* slots, void* k_out, voi
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
-size_t mxq_kv_attention_workspace_bytes(int Hq, int Hkv, int D, int max_q_len) {
-    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_q_len <= 0) return 0;
-    // more SMs never need less, and the longest of shorter rows may need more than
-    // many: the largest need over the numbers of rows up to max_q_len
-    size_t most = 256;
-    for (int n = 1;; n = n < max_q_len / 2 ? 2 * n : max_q_len) {
-        const size_t b = plan_attn(Hq, Hkv, D, n, kMaxSms).bytes;
-        if (b > most) most = b;
-        if (n == max_q_len) return most;
-    }
+size_t mxq_kv_attention_workspace_bytes(int T, int S, int Hq, int Hkv, int D, int max_q_len) {
+    if (T < 0 || S < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_q_len <= 0)
+        return 0;
+    if (max_q_len > T) max_q_len = T > 0 ? T : 1;
+    // more SMs never need less
+    return plan_attn(T, S, Hq, Hkv, D, max_q_len, kMaxSms).bytes;
 }
 
 mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_head_stride,
@@ -218,7 +234,7 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     if (max_q_len > T && T > 0) max_q_len = T;  // no sequence has more rows than there are
     if (T > 0 && S > 0 &&
         (!workspace ||
-         workspace_bytes < mxq_kv_attention_workspace_bytes(Hq, Hkv, D, max_q_len)))
+         workspace_bytes < mxq_kv_attention_workspace_bytes(T, S, Hq, Hkv, D, max_q_len)))
         return MXQ_ERR_WORKSPACE;
     int sms = 0;
     const mxq_status st = mxq::check_current_device(&sms);
@@ -227,7 +243,7 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     if (dev_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess)
         return MXQ_ERR_CUDA;
     if (T == 0 || S == 0) return MXQ_OK;
-    const AttnPlan a = plan_attn(Hq, Hkv, D, max_q_len, sms < kMaxSms ? sms : kMaxSms);
+    const AttnPlan a = plan_attn(T, S, Hq, Hkv, D, max_q_len, sms < kMaxSms ? sms : kMaxSms);
     mxq::KvAttnParams p;
     std::memset(&p, 0, sizeof p);
     p.q = static_cast<const __nv_bfloat16*>(q);
@@ -250,17 +266,41 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     p.window = window < kMaxInt ? window : kMaxInt;
     p.sinks = sinks < kMaxInt ? sinks : kMaxInt;
     p.scale_log2 = (float)(scale * 1.4426950408889634);
+    p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    p.status = dev_status;
+    p.wait_budget = mxq::wait_budget_cycles();
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.head_parts = a.head_parts;
     p.part_heads = a.part_heads;
     p.tile_toks = a.tile_toks;
-    p.planes = a.planes;
+    p.min_rows = 0;
+    p.max_rows = a.tile_toks;
     p.ctas = a.ctas;
-    p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
-    p.segs = a.ctas > 1 ? static_cast<int*>(workspace) : nullptr;
-    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.seg_bytes);
-    p.status = dev_status;
-    p.wait_budget = mxq::wait_budget_cycles();
-    const cudaError_t err = mxq::launch_kv_attn(p, D, group_size, a.tile_rows, s);
+    p.segs = reinterpret_cast<int*>(ws);
+    p.partial = reinterpret_cast<float*>(ws + a.seg_bytes);
+    if (mxq::launch_kv_attn(p, D, group_size, a.tile_rows, s) != cudaSuccess) return MXQ_ERR_CUDA;
+    if (!a.many) return MXQ_OK;
+    ws += a.few_bytes;
+    p.head_parts = a.many_parts;
+    p.part_heads = a.many_heads;
+    p.tile_toks = a.many_toks;
+    p.half_toks = a.half_toks;
+    p.min_rows = a.tile_toks + 1;
+    p.max_rows = kMaxInt;
+    p.ctas = a.many_ctas;
+    p.max_entries = a.max_entries;
+    p.segs = reinterpret_cast<int*>(ws);
+    ws += a.many_seg_bytes;
+    p.partial = reinterpret_cast<float*>(ws);
+    ws += a.many_partial_bytes;
+    p.seq_tiles = reinterpret_cast<int*>(ws);
+    ws += a.seq_bytes;
+    p.entries = ws;
+    ws += a.entry_bytes;
+    p.before = reinterpret_cast<int*>(ws);
+    ws += a.before_bytes;
+    p.counts = reinterpret_cast<int*>(ws);
+    const cudaError_t err = mxq::launch_kv_prefill(p, D, group_size, s);
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 

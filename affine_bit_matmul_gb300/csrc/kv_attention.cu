@@ -24,7 +24,7 @@
 // lane's numbers unused and not computed.
 //
 // Work split: a unit is (row tile, tile of tokens that it sees); the units of a
-// plane, in order, are cut into equal runs, one per CTA, whatever the lengths
+// call, in order, are cut into equal runs, one per CTA, whatever the lengths
 // of the sequences.  A run that begins or ends inside a row tile leaves its
 // (max, sum, weighted sum) in the workspace and a second kernel joins them in
 // order, so the result does not depend on timing.
@@ -39,13 +39,9 @@
 // Bound by HBM for long contexts: 2 (D / 2 + 4 D / G) bytes per token and head.
 #include <cstdint>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "kv_format.cuh"
-#include "mxq_device.cuh"
-#include "mxq_internal.h"
-#include "tc_common.cuh"
+#include "kv_attn_common.cuh"
 
 namespace mxq {
 namespace {
@@ -53,34 +49,19 @@ namespace {
 constexpr int kChunk = 64;                      // values joined at a time
 constexpr int kRowPad = kChunk + 8;
 
-enum : int { kBegins = 1, kEnds = 2 };  // a run's piece holds a row tile's first, last unit
-
-// Descriptor of a run's first or last piece of a row tile (workspace).
-struct Seg {
-    int row0, toks, head0, heads;
-    int flags;  // kBegins, kEnds; -1: none
-    int pad[3];
-};
-
 // Sizes of a kernel for row tiles of 4 KT rows: tokens of a tile, compute warps,
 // CTAs per SM, tiles in the ring.
-#ifndef W1
-#define W1 7
-#define T1 64
-#define W2 7
-#define W4 3
-#endif
 template <int D, int G, int KT>
 struct Shape {
     static constexpr int kRows = 4 * KT;
-    static constexpr int kTile = D == 256 ? 32 : T1;
+    static constexpr int kTile = D == 256 ? 32 : 64;
     static constexpr int kCtas = 2;
     static constexpr int kStageBytes = kv_block_bytes(D, G, kTile);
     // the queries lie in shared memory where they would take 32 registers or more
     static constexpr int kColumns = (KT + 1) / 2;  // tiles of 8 columns
     static constexpr bool kQueryShared = D * kColumns >= 256;
     static constexpr int kQueryBytes = kQueryShared ? kColumns * D * 16 : 0;
-    static constexpr int kWarps = KT == 4 ? W4 : D == 256 ? 5 : KT == 1 ? W1 : W2;
+    static constexpr int kWarps = KT == 4 ? 3 : D == 256 ? 5 : 7;
     static constexpr int kThreads = 32 * (kWarps + 1);
     static constexpr int kJoinBytes = kWarps * kRows * kRowPad * 4;
     static constexpr int kStatBytes = kWarps * kRows * 8;
@@ -90,54 +71,6 @@ struct Shape {
     static constexpr int kSmem = kRingBytes + kJoinBytes + kStatBytes + kQueryBytes;
     static constexpr int kPartialFloats = kRows * (D + 2);
 };
-
-// What a row tile of a sequence sees.
-struct Span {
-    int row0, toks, p0;  // rows of q, tokens, position of the first
-    int tiles;           // tiles of tokens (at least 1 when it has rows)
-    int head_tiles;      // the first of them, from token 0 on (sinks) ...
-    int tail;            // ... and the tile where the rest begins
-    int bad;             // the sequence's arguments are out of range
-};
-
-template <int TILE>
-__device__ __forceinline__ Span span_of(const KvAttnParams& p, int s, int plane) {
-    Span r;
-    r.bad = 0;
-    r.tiles = 0;
-    r.head_tiles = 0;
-    r.tail = 0;
-    int a = s, b = s + 1;
-    if (p.q_starts) {
-        a = __ldg(p.q_starts + s);
-        b = __ldg(p.q_starts + s + 1);
-    }
-    int len = __ldg(p.ctx_lens + s);
-    const int most = p.max_pages * p.page_size;
-    if (a < 0 || b > p.T || a > b || b - a > p.max_q || len < 0 || len > most) {
-        r.bad = 1;
-        if (a < 0 || b > p.T || a > b || b - a > p.max_q) b = a;  // none of its rows
-        len = min(max(len, 0), most);
-    }
-    const int n = b - a;
-    const int j0 = plane * p.tile_toks;
-    r.row0 = a + j0;
-    r.toks = min(p.tile_toks, n - j0);
-    r.p0 = len - n + j0;
-    if (r.toks <= 0) return r;
-    const int hi = r.p0 + r.toks - 1;           // position of the last row
-    const int end = hi < 0 ? 0 : hi / TILE + 1;
-    int lo = 0;
-    if (p.window) lo = max(0, r.p0 - p.window + 1) / TILE;
-    int first = min((min(p.sinks, hi + 1) + TILE - 1) / TILE, end);
-    if (first < 0) first = 0;
-    if (first >= lo) first = lo = 0;
-    lo = min(lo, end);
-    r.head_tiles = first;
-    r.tail = lo;
-    r.tiles = max(1, first + end - lo);
-    return r;
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -156,32 +89,10 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
-// Larger of two numbers in each half word.
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// 2^(e - 127) for a biased exponent 1 <= e <= 254.
-__device__ __forceinline__ float pow2_of(int e) { return __uint_as_float((uint32_t)e << 23); }
-
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // The four operand registers of a code word: nibbles 0 and 4, 1 and 5, ...; the
@@ -199,53 +110,6 @@ __device__ __forceinline__ float sum_rows(float x) {
     x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
     x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
     return x + __shfl_xor_sync(0xFFFFFFFFu, x, 16);
-}
-
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            dst),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
-
-template <int W>
-__device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[W]) {
-    if constexpr (W == 2) {
-        const uint2 v = *reinterpret_cast<const uint2*>(at);
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < W / 4; ++i) {  // slabs of 128 values are 512 bytes apart
-            const uint4 v = *reinterpret_cast<const uint4*>(at + 512 * i);
-            w[4 * i] = v.x;
-            w[4 * i + 1] = v.y;
-            w[4 * i + 2] = v.z;
-            w[4 * i + 3] = v.w;
-        }
-    }
-}
-
-template <int NG>
-__device__ __forceinline__ void load_pairs(const uint8_t* at, uint32_t (&w)[NG]) {
-    if constexpr (NG == 1) {
-        w[0] = *reinterpret_cast<const uint32_t*>(at);
-    } else if constexpr (NG == 2) {
-        const uint2 v = *reinterpret_cast<const uint2*>(at);
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < NG / 4; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(at + 16 * i);
-            w[4 * i] = v.x;
-            w[4 * i + 1] = v.y;
-            w[4 * i + 2] = v.z;
-            w[4 * i + 3] = v.w;
-        }
-    }
 }
 
 // A run's piece of one row tile, for the warps of a CTA (shared memory).
@@ -267,13 +131,13 @@ struct Walk {  // (no constructors: it lies in shared memory)
     Span sp;
 
     // the run's first unit is unit `at` of sequence s (of all its heads)
-    __device__ void start(const KvAttnParams& p, int plane, int s_, long long at, int units) {
+    __device__ void start(const KvAttnParams& p, int s_, long long at, int units) {
         s = s_;
-        sp = span_of<TILE>(p, s, plane);
+        sp = span_of<TILE>(p, s, 0);
         const long long vheads = (long long)p.Hkv * p.head_parts;
         while (at >= sp.tiles * vheads) {
             at -= sp.tiles * vheads;
-            sp = span_of<TILE>(p, ++s, plane);
+            sp = span_of<TILE>(p, ++s, 0);
         }
         const int vh = (int)(at / sp.tiles);
         k = (int)(at % sp.tiles);
@@ -282,9 +146,9 @@ struct Walk {  // (no constructors: it lies in shared memory)
         seq = 0;
         left = units;
     }
-    __device__ bool next(const KvAttnParams& p, int plane, Piece* out, Seg* seg) {
+    __device__ bool next(const KvAttnParams& p, Piece* out, Seg* seg) {
         if (left == 0) return false;
-        while (sp.tiles == 0) sp = span_of<TILE>(p, ++s, plane);
+        while (sp.tiles == 0) sp = span_of<TILE>(p, ++s, 0);
         const int n = min(left, sp.tiles - k), rep = p.Hq / p.Hkv;
         Piece q;
         q.row0 = sp.row0;
@@ -301,7 +165,7 @@ struct Walk {  // (no constructors: it lies in shared memory)
         q.end = seq + n;
         q.flags = (k == 0 ? kBegins : 0) | (k + n == sp.tiles ? kEnds : 0);
         *out = q;
-        if (seg && q.flags != (kBegins | kEnds)) {
+        if (q.flags != (kBegins | kEnds)) {
             Seg g;
             g.row0 = q.row0;
             g.toks = q.toks;
@@ -319,7 +183,7 @@ struct Walk {  // (no constructors: it lies in shared memory)
                 part = 0;
                 if (++h == p.Hkv) {
                     h = 0;
-                    sp = span_of<TILE>(p, ++s, plane);
+                    sp = span_of<TILE>(p, ++s, 0);
                 }
             }
         }
@@ -472,9 +336,8 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     uint4* queries = reinterpret_cast<uint4*>(smem + SH::kSmem - SH::kQueryBytes);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int plane = blockIdx.x / p.ctas, cta = blockIdx.x % p.ctas;
-    Seg* seg = p.segs ? reinterpret_cast<Seg*>(p.segs) + ((long long)plane * p.ctas + cta) * 2
-                      : nullptr;
+    const int cta = blockIdx.x;
+    Seg* seg = reinterpret_cast<Seg*>(p.segs) + (long long)cta * 2;
 
     // every CTA finds its own run: the tiles of all sequences, then its share
     const int per = (p.S + kThreads - 1) / kThreads;
@@ -483,7 +346,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         for (int i = 0; i < per; ++i) {
             const int s = threadIdx.x * per + i;
             if (s >= p.S) break;
-            const Span sp = span_of<TILE>(p, s, plane);
+            const Span sp = span_of<TILE>(p, s, 0);
             sum += sp.tiles;
             if (sp.bad && blockIdx.x == 0) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
         }
@@ -514,7 +377,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         const long long vheads = (long long)p.Hkv * p.head_parts;
         const long long all = __shfl_sync(0xFFFFFFFFu, incl, 31) * vheads;
         const long long runs = all < p.ctas ? all : p.ctas;
-        if (seg && threadIdx.x == 0) seg[0].flags = seg[1].flags = -1;
+        if (threadIdx.x == 0) seg[0].flags = seg[1].flags = -1;
         if (cta >= runs) return;
         const long long u0 = cta * all / runs, u1 = (cta + 1) * all / runs;
         total = (int)(u1 - u0);
@@ -526,8 +389,8 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
             if (lane == 0) {
                 int i = owner * (kWarps + 1);  // the thread whose sequences the run starts in
                 while (at >= sums[i] * vheads) at -= sums[i++] * vheads;
-                walk.start(p, plane, i * per, at, total);
-                for (int n = 0; n < kPieces && walk.next(p, plane, &pieces[n], seg); ++n) {
+                walk.start(p, i * per, at, total);
+                for (int n = 0; n < kPieces && walk.next(p, &pieces[n], seg); ++n) {
                 }
             }
         }
@@ -844,7 +707,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         const float v_down = pow2_of(max(v_exp - 6, 1));  // 1 / v_up
         const bool whole = sp.flags == (kBegins | kEnds);
         float* part = p.partial +
-                      (((long long)plane * p.ctas + cta) * 2 + ((sp.flags & kBegins) ? 1 : 0)) *
+                      ((long long)cta * 2 + ((sp.flags & kBegins) ? 1 : 0)) *
                           SH::kPartialFloats;
 #pragma unroll 1
         for (int d0 = 0; d0 < D; d0 += kChunk) {
@@ -913,7 +776,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
             jparity ^= 1u;
         }
         // everyone is done with this piece: its place takes a later one
-        if (threadIdx.x == 0) walk.next(p, plane, &pieces[at_piece % kPieces], seg);
+        if (threadIdx.x == 0) walk.next(p, &pieces[at_piece % kPieces], seg);
     }
 }
 
@@ -929,10 +792,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParam
     __shared__ float row_inv[16], row_lse[16];
     __shared__ int last_piece;
     pdl_wait();
-    const int plane = blockIdx.x / p.ctas, cta = blockIdx.x % p.ctas;
-    const long long base = (long long)plane * p.ctas;
+    const int cta = blockIdx.x;
     const Seg* segs = reinterpret_cast<const Seg*>(p.segs);
-    const Seg g = segs[(base + cta) * 2 + 1];
+    const Seg g = segs[cta * 2 + 1];
     if (g.flags < 0 || !(g.flags & kBegins) || (g.flags & kEnds)) return;
     // after a wait that gave up the descriptors may be anything
     if (g.toks <= 0 || g.heads <= 0 || g.toks > tile_rows || g.heads > tile_rows ||
@@ -943,7 +805,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParam
     if (tid == 0) last_piece = p.ctas - 1;
     __syncthreads();
     for (int c = cta + 1 + tid; c < p.ctas; c += kJoinThreads) {
-        const int f = segs[(base + c) * 2].flags;
+        const int f = segs[c * 2].flags;
         if (f < 0 || (f & kEnds)) {
             atomicMin(&last_piece, c);
             break;
@@ -954,7 +816,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParam
     const long long stride = (long long)tile_rows * (D + 2);
     // piece 0 is the CTA's second, piece k the first of CTA cta + k
     auto piece = [&](int k) {
-        return p.partial + ((base + cta + k) * 2 + (k ? 0 : 1)) * stride;
+        return p.partial + ((cta + k) * 2LL + (k ? 0 : 1)) * stride;
     };
     for (int i = tid; i < n * rows; i += kJoinThreads)
         weight[i] = piece(i / rows)[2 * (i % rows)];
@@ -1029,10 +891,10 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     cudaError_t err = cudaFuncSetAttribute(kv_attn_kernel<D, G, KT>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kSmem);
     if (err != cudaSuccess) return err;
-    const unsigned grid = (unsigned)(p.planes * p.ctas);
+    const unsigned grid = (unsigned)p.ctas;
     kv_attn_kernel<D, G, KT><<<grid, SH::kThreads, SH::kSmem, stream>>>(p);
     err = cudaGetLastError();
-    if (err != cudaSuccess || !p.segs) return err;
+    if (err != cudaSuccess) return err;
     // the second kernel's blocks are placed as the first one's finish
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -1049,10 +911,10 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t kv_attn_seg_bytes(int planes, int ctas) { return (size_t)planes * ctas * 2 * sizeof(Seg); }
+size_t kv_attn_seg_bytes(int ctas) { return (size_t)ctas * 2 * sizeof(Seg); }
 
-size_t kv_attn_partial_bytes(int planes, int ctas, int tile_rows, int D) {
-    return (size_t)planes * ctas * 2 * tile_rows * (D + 2) * sizeof(float);
+size_t kv_attn_partial_bytes(int ctas, int tile_rows, int D) {
+    return (size_t)ctas * 2 * tile_rows * (D + 2) * sizeof(float);
 }
 
 int kv_attn_ctas_per_sm() { return Shape<128, 64, 1>::kCtas; }

@@ -1,0 +1,1057 @@
+// Attention of many query rows (prompts, chunks of them) over a paged 4-bit
+// key/value cache, on the 5th-generation tensor cores.
+//
+// The formulas are kv_attention.cu's; here keys and values become f16 numbers,
+// s q + b rounded once (11 bits), scaled by a power of two for each part of a
+// tile (64 or 32 tokens) that keeps them below one, and so do the queries (a
+// power of two for each row, exact) and the weights P (11 bits).  Products are
+// summed in fp32 in tensor memory; scores, maxima and sums are fp32.
+//
+// A row tile is up to 256 rows (128 for D = 256): all query heads of one
+// key/value head at 128 / heads tokens, once or twice.  A unit is (row tile,
+// 128 tokens); the units of all row tiles, in order, are cut into equal runs,
+// one per SM, as for few rows.  Roles of a CTA's 16 warps:
+//   0-3, 4-7  softmax of the first and second 128 rows, one row a thread:
+//             scores from tensor memory, maximum, weights back into tensor
+//             memory over the scores, and the output at the end
+//   8-11      codes -> f16 operands in shared memory (128-byte swizzle; keys
+//             along the values, values along the tokens)
+//   12, 13    the matrix instructions of one half each: Q K^T, then P V
+//   14        copies of page parts into a ring
+//   15        the list of the run's pieces; tensor memory
+// The two halves are independent chains (scores, weights, sum), so one half's
+// products run while the other half's softmax does.  For D = 256 there is one
+// half with two score buffers instead.  The running maximum is only moved when
+// a score exceeds it by 2^8; the output's sums in tensor memory are rescaled
+// then, by the softmax warps.
+// Bound by the tensor cores: 4 D flops per visible pair and head.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "kv_attn_common.cuh"
+
+namespace mxq {
+namespace {
+
+constexpr int kTile = 128;           // tokens of a unit
+constexpr int kThreads = 512;
+constexpr int kPieceRing = 8;
+constexpr int kMetaRing = 4;
+
+template <int D, int G>
+struct Shape {
+    static constexpr int MT = D == 256 ? 1 : 2;    // halves of 128 rows
+    static constexpr int SB = D == 256 ? 2 : 1;    // score buffers of a half
+    static constexpr int KB = D == 256 ? 1 : 2;    // key and value buffers
+    static constexpr int PT = D == 256 ? 32 : 64;  // tokens of a part
+    static constexpr int NP = kTile / PT;
+    static constexpr int kRows = 128 * MT;
+    static constexpr int kPartBytes = kv_block_bytes(D, G, PT) / 2;  // of keys or of values
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kOpBytes = kTile * D * 2;
+    static constexpr int kFixed = kQBytes + 2 * KB * kOpBytes;
+    static constexpr int kRoom = (232448 - 1024 - 3072 - kFixed) / kPartBytes;
+    static constexpr int kSlots = kRoom < 12 ? kRoom : 12;
+    static constexpr int kSmem = 1024 + kFixed + kSlots * kPartBytes;
+    static constexpr int kPartialFloats = kRows * (D + 2);
+};
+
+struct Piece {
+    int row0, toks, p0, head0, heads, s, h, head_tiles, tail, k0, count, flags;
+};
+
+// One row tile, in the workspace.
+struct Entry {
+    int s, row0, toks, p0, tiles, head_tiles, tail, pad;
+};
+
+struct Meta {
+    int state;     // bit i: tokens 16 i .. of the unit exist
+    int e[4];      // biased exponents of the parts: values are below 2^(e - 126)
+};
+
+__device__ __forceinline__ int unit_token(const Piece& q, int k) {
+    return (k < q.head_tiles ? k : q.tail + k - q.head_tiles) * kTile;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Instruction descriptor for kind::f16: f16 A and B, fp32 D, both K-major.
+__host__ __device__ constexpr uint32_t umma_idesc_f16(uint32_t M, uint32_t N) {
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t hfma2_f16(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t hsub2_f16(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The four pairs of a code word (nibbles 0 and 4, 1 and 5, ...) as s q + b in f16.
+// 0x64xx is 1024 + q, 0x54x0 is 64 + q; both differences are exact.
+__device__ __forceinline__ void dequant_word(uint32_t w, uint32_t s2, uint32_t b2,
+                                             uint32_t (&x)[4]) {
+    const uint32_t v = w >> 8;
+    x[0] = hfma2_f16(hsub2_f16((w & 0x000F000Fu) | 0x64006400u, 0x64006400u), s2, b2);
+    x[1] = hfma2_f16(hsub2_f16((w & 0x00F000F0u) | 0x54005400u, 0x54005400u), s2, b2);
+    x[2] = hfma2_f16(hsub2_f16((v & 0x000F000Fu) | 0x64006400u, 0x64006400u), s2, b2);
+    x[3] = hfma2_f16(hsub2_f16((v & 0x00F000F0u) | 0x54005400u, 0x54005400u), s2, b2);
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t a) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(a) : "memory");
+}
+
+// Barriers and small things that the warps share.
+template <int D, int G>
+struct Shared {
+    using SH = Shape<D, G>;
+    uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
+    uint64_t full[SH::kSlots], empty[SH::kSlots];
+    uint64_t k_full[SH::KB], k_empty[SH::KB], v_full[SH::KB], v_empty[SH::KB];
+    uint64_t q_full[SH::MT], s_full[2], p_full[SH::MT], pv_done[SH::MT], drained[SH::MT];
+    Piece pieces[kPieceRing];
+    Meta k_meta[kMetaRing], v_meta[kMetaRing];
+    int part_t0[SH::kSlots], part_state[SH::kSlots];
+    uint32_t tmem;
+};
+
+// The pieces of the run in order, for one warp.
+template <int D, int G>
+struct Pieces {
+    Shared<D, G>& sh;
+    long long budget;
+    int n;
+    __device__ Pieces(Shared<D, G>& s, long long b) : sh(s), budget(b), n(0) {}
+    // The next piece; null when a wait gave up.  count == 0: no more.
+    __device__ const Piece* next() {
+        if (!warp_wait(&sh.piece_full[n % kPieceRing], (uint32_t)(n / kPieceRing) & 1u, budget))
+            return nullptr;
+        return &sh.pieces[n % kPieceRing];
+    }
+    __device__ void done() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.piece_empty[n % kPieceRing]);
+        ++n;
+    }
+};
+
+// ---------------------------------------------------------------- pieces
+
+template <int D, int G>
+__device__ bool list_pieces(const KvAttnParams& p, Shared<D, G>& sh) {
+    const Entry* entries = reinterpret_cast<const Entry*>(p.entries);
+    const int* before = p.before;
+    const int n_entries = p.counts[0];
+    const long long vheads = (long long)p.Hkv * p.head_parts;
+    const long long all = p.counts[1] * vheads;
+    const long long runs = all < p.ctas ? all : p.ctas;
+    const int cta = blockIdx.x, rep = p.Hq / p.Hkv;
+    Seg* seg = reinterpret_cast<Seg*>(p.segs) + (long long)cta * 2;
+    seg[0].flags = seg[1].flags = -1;
+    long long left = 0;
+    int e = 0, k = 0, h = 0, part = 0;
+    Entry en{};
+    if (cta < runs) {
+        const long long u0 = cta * all / runs;
+        left = (cta + 1) * all / runs - u0;
+        int lo = 0, hi = n_entries - 1;  // the last entry that begins at or before u0
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (before[mid] * vheads <= u0) lo = mid;
+            else hi = mid - 1;
+        }
+        e = lo;
+        en = entries[e];
+        const long long at = u0 - before[e] * vheads;
+        const int vh = (int)(at / en.tiles);
+        k = (int)(at % en.tiles);
+        h = vh / p.head_parts;
+        part = vh % p.head_parts;
+    }
+    for (int n = 0;; ++n) {
+        const int slot = n % kPieceRing;
+        if (!mbar_wait(&sh.piece_empty[slot], ((uint32_t)(n / kPieceRing) & 1u) ^ 1u, p.wait_budget))
+            return false;
+        Piece q{};
+        if (left > 0) {
+            q.row0 = en.row0;
+            q.toks = en.toks;
+            q.p0 = en.p0;
+            q.head0 = h * rep + part * p.part_heads;
+            q.heads = min(p.part_heads, rep - part * p.part_heads);
+            q.s = en.s;
+            q.h = h;
+            q.head_tiles = en.head_tiles;
+            q.tail = en.tail;
+            q.k0 = k;
+            q.count = (int)(left < en.tiles - k ? left : en.tiles - k);
+            q.flags = (k == 0 ? kBegins : 0) | (k + q.count == en.tiles ? kEnds : 0);
+            if (q.flags != (kBegins | kEnds)) {
+                Seg g;
+                g.row0 = q.row0;
+                g.toks = q.toks;
+                g.head0 = q.head0;
+                g.heads = q.heads;
+                g.flags = q.flags;
+                seg[(q.flags & kBegins) ? 1 : 0] = g;
+            }
+            left -= q.count;
+            k += q.count;
+            if (k == en.tiles && left > 0) {
+                k = 0;
+                if (++part == p.head_parts) {
+                    part = 0;
+                    if (++h == p.Hkv) {
+                        h = 0;
+                        en = entries[++e];
+                    }
+                }
+            }
+        }
+        sh.pieces[slot] = q;
+        mbar_arrive(&sh.piece_full[slot]);
+        if (q.count == 0) return true;
+    }
+}
+
+// ---------------------------------------------------------------- copies
+
+// One warp.  The parts of a unit go into the ring in the order in which they are
+// converted: its keys, then its values.  Lane (part, i) looks after page i of
+// that part, or region i (codes, pairs) of its share of a longer page.
+template <int D, int G>
+__device__ bool copy_parts(const KvAttnParams& p, Shared<D, G>& sh, uint32_t ring, int lane) {
+    using SH = Shape<D, G>;
+    constexpr int PT = SH::PT, NP = SH::NP, NS = SH::kSlots;
+    const int page = p.page_size, size = min(page, PT);
+    const int each = page <= PT ? PT / page : 2;      // copies of a part
+    const int part = lane / each, i = lane % each;    // part: keys 0 .. NP - 1, then values
+    const long long block = kv_block_bytes(D, G, page);
+    const uint32_t bytes = page <= PT ? (uint32_t)(block / 2)
+                                      : (uint32_t)(i ? kv_pair_bytes(D, G, PT) : kv_code_bytes(D, PT));
+    const uint32_t dst = page <= PT ? i * (uint32_t)(block / 2) : i * (uint32_t)kv_code_bytes(D, PT);
+    const long long half = part >= NP ? block / 2 : 0;
+    Pieces<D, G> list(sh, p.wait_budget);
+    long long unit = 0;
+    bool ok = true;
+    while (ok) {
+        const Piece* q = list.next();
+        if (!q) ok = false;
+        if (!q || q->count == 0) break;
+        const int p1 = q->p0 + q->toks - 1;
+        const int32_t* row = p.table + (long long)q->s * p.max_pages;
+        for (int k = q->k0; k < q->k0 + q->count && ok; ++k) {
+            const int t0 = unit_token(*q, k);
+            const int t = t0 + (part % NP) * PT + (page <= PT ? i * page : 0);
+            int id = -2;
+            if (part < 2 * NP && t <= p1) id = __ldg(row + (t >> p.page_shift));
+            const bool good = (unsigned)id < (unsigned)p.n_pages;
+            if (!good && id != -2 && part < NP) {
+                const int te = min(t + size - 1, p1);  // a page that some row sees has to exist
+                if (!p.window || te > q->p0 - p.window || t < p.sinks)
+                    flag_status(p.status, MXQ_DEV_BAD_PAGE);
+            }
+            const uint32_t found = __ballot_sync(0xFFFFFFFFu, good);
+            const uint8_t* src = p.pages + half;
+            if (good) {
+                src += ((long long)id * p.Hkv + q->h) * block;
+                if (page > PT) {
+                    const int skip = t & (page - 1);
+                    src += i ? kv_code_bytes(D, page) + kv_pair_bytes(D, G, skip)
+                             : kv_code_bytes(D, skip);
+                }
+            }
+#pragma unroll 1
+            for (int u = 0; u < 2 * NP; ++u) {
+                const int slot = (int)(unit % NS);
+                if (!warp_wait(&sh.empty[slot], ((uint32_t)(unit / NS) & 1u) ^ 1u, p.wait_budget)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const uint32_t mine = (found >> (u * each)) & ((1u << each) - 1u);
+                    int state = 0;
+                    uint32_t sum = 0;
+                    if (page <= PT) {
+                        for (int j = 0; j < each; ++j)
+                            if ((mine >> j) & 1u) state |= ((1 << (size / 16)) - 1) << (j * (size / 16));
+                        sum = __popc(mine) * bytes;
+                    } else if (mine) {
+                        state = (1 << (PT / 16)) - 1;
+                        sum = SH::kPartBytes;
+                    }
+                    sh.part_t0[slot] = t0 + (u % NP) * PT;
+                    sh.part_state[slot] = state;
+                    mbar_expect_tx(&sh.full[slot], sum);
+                }
+                __syncwarp();
+                if (part == u && good)
+                    bulk_copy(ring + slot * SH::kPartBytes + dst, src, bytes, &sh.full[slot]);
+                ++unit;
+            }
+        }
+        list.done();
+    }
+    __syncwarp();
+    if (lane == 0 && !drain_ring(sh.full, NS, unit, NS)) ok = false;
+    return ok;
+}
+
+// ---------------------------------------------------------------- codes -> operands
+
+// Four warps convert each part together.
+template <int D, int G>
+__device__ bool convert(const KvAttnParams& p, Shared<D, G>& sh, const uint8_t* ring, uint32_t kbuf,
+                        uint32_t vbuf, int dw, int lane) {
+    using SH = Shape<D, G>;
+    constexpr int PT = SH::PT, NP = SH::NP, NS = SH::kSlots, KB = SH::KB;
+    constexpr int NG = D / G, U = D / 32;
+    const int r = lane >> 2, i4 = lane & 3;
+    const int size = min(p.page_size, PT);
+    const int whole = (kv_code_bytes(D, size) + kv_pair_bytes(D, G, size));
+    Pieces<D, G> list(sh, p.wait_budget);
+    long long unit = 0;
+    int jt = 0;
+    for (;;) {
+        const Piece* q = list.next();
+        if (!q) return false;
+        if (q->count == 0) return true;
+        const int p0 = q->p0, p1 = p0 + q->toks - 1;
+        for (int k = 0; k < q->count; ++k, ++jt) {
+            const int buf = jt % KB;
+            const uint32_t round = (uint32_t)(jt / KB) & 1u;
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t out = kv ? vbuf + buf * SH::kOpBytes : kbuf + buf * SH::kOpBytes;
+                Meta& meta = kv ? sh.v_meta[jt % kMetaRing] : sh.k_meta[jt % kMetaRing];
+                if (!warp_wait(kv ? &sh.v_empty[buf] : &sh.k_empty[buf], round ^ 1u, p.wait_budget))
+                    return false;
+                int states = 0;
+#pragma unroll 1
+                for (int part = 0; part < NP; ++part, ++unit) {
+                    const int slot = (int)(unit % NS);
+                    if (!warp_wait(&sh.full[slot], (uint32_t)(unit / NS) & 1u, p.wait_budget))
+                        return false;
+                    const uint8_t* at = ring + slot * SH::kPartBytes;
+                    const int t0 = sh.part_t0[slot], state = sh.part_state[slot];
+                    states |= state << (part * (PT / 16));
+                    // some token of the part is seen by no row: what it holds is not used
+                    const bool edge =
+                        state != (1 << (PT / 16)) - 1 || t0 + PT - 1 > p1 ||
+                        (p.window && t0 <= p0 - p.window && t0 + PT > p.sinks);
+                    auto unseen = [&](int t) {
+                        return !((state >> (t / 16)) & 1) || t0 + t > p1 ||
+                               (p.window && t0 + t <= p0 - p.window && t0 + t >= p.sinks);
+                    };
+                    auto pairs_of = [&](int t) {
+                        return at + t / size * whole + kv_code_bytes(D, size) + t % size * (NG * 4);
+                    };
+                    // a power of two above every |s q + b| of the part
+                    uint32_t big = 0;
+#pragma unroll
+                    for (int j = 0; j < PT / 32; ++j) {
+                        const int t = lane + 32 * j;
+                        uint32_t w[NG];
+                        load_pairs<NG>(pairs_of(t), w);
+                        const uint32_t keep = edge && unseen(t) ? 0u : 0x7FFF7FFFu;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) big = max_u16x2(big, w[g] & keep);
+                    }
+                    const int es = (int)(__reduce_max_sync(0xFFFFFFFFu, big & 0xFFFFu) >> 7) + 4;
+                    const int eb = (int)(__reduce_max_sync(0xFFFFFFFFu, big >> 16) >> 7);
+                    const int e = min(max(max(es, eb) + 1, 30), 250);
+                    const float dn = pow2_of(253 - e);  // 2^(126 - e)
+                    if (dw == 0 && lane == 0) meta.e[part] = e;
+                    // 8 tokens at a time
+#pragma unroll
+                    for (int j = 0; j < PT / 32; ++j) {
+                        const int tb = (dw + 4 * j) * 8;
+                        const uint8_t* codes = at + tb / size * whole + kv_code_bytes(D, tb % size) +
+                                               lane * (D == 64 ? 8 : 16);
+                        uint32_t w[U];
+                        load_words<U>(codes, w);
+                        const int tt = part * PT + tb;  // token within the unit
+                        if (kv == 0) {
+                            uint32_t pr[NG];
+                            load_pairs<NG>(pairs_of(tb + r), pr);
+                            if (edge && unseen(tb + r)) {
+#pragma unroll
+                                for (int g = 0; g < NG; ++g) pr[g] = 0u;
+                            }
+                            // odd tokens take the words of a pair in the other order: their
+                            // stores would meet the even ones' in the same banks
+                            const bool odd = r & 1;
+#pragma unroll
+                            for (int u = 0; u < U; u += 2) {
+                                const uint32_t a = w[u], b = w[u + 1];
+                                w[u] = odd ? b : a;
+                                w[u + 1] = odd ? a : b;
+                            }
+                            if (G == 32) {
+#pragma unroll
+                                for (int g = 0; g < NG; g += 2) {
+                                    const uint32_t a = pr[g], b = pr[g + 1];
+                                    pr[g] = odd ? b : a;
+                                    pr[g + 1] = odd ? a : b;
+                                }
+                            }
+                            uint32_t s2[NG], b2[NG];
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                const float s = __uint_as_float(pr[g] << 16) * dn;
+                                const float b = __uint_as_float(pr[g] & 0xFFFF0000u) * dn;
+                                s2[g] = cvt_f16x2(s, s);
+                                b2[g] = cvt_f16x2(b, b);
+                            }
+                            const uint32_t row = out + (tt + r) * 128;
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                uint32_t x[4];
+                                dequant_word(w[u], s2[u * 32 / G], b2[u * 32 / G], x);
+                                // values 32 u' + 8 i4 ..: 16 bytes of row tt + r
+                                const int chunk = (((u & 1) ^ (r & 1)) * 4 + i4) ^ r;
+                                sts128(row + (u / 2) * (kTile * 128) + chunk * 16, x[0], x[1], x[2],
+                                       x[3]);
+                            }
+                        } else {
+                            uint32_t pa[NG], pc[NG];
+                            load_pairs<NG>(pairs_of(tb + 2 * i4), pa);
+                            load_pairs<NG>(pairs_of(tb + 2 * i4 + 1), pc);
+                            if (edge) {
+#pragma unroll
+                                for (int g = 0; g < NG; ++g) {
+                                    if (unseen(tb + 2 * i4)) pa[g] = 0u;
+                                    if (unseen(tb + 2 * i4 + 1)) pc[g] = 0u;
+                                }
+                            }
+                            // values 32 u + r + 8 n of tokens 2 i4 and 2 i4 + 1
+                            const uint32_t row = out + (tt / 64) * (D * 128) + r * 128 +
+                                                 ((((tt % 64) / 8) ^ r) * 16) + i4 * 4;
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                const uint32_t s2 =
+                                    cvt_f16x2(__uint_as_float(pa[g] << 16) * dn,
+                                              __uint_as_float(pc[g] << 16) * dn);
+                                const uint32_t b2 =
+                                    cvt_f16x2(__uint_as_float(pa[g] & 0xFFFF0000u) * dn,
+                                              __uint_as_float(pc[g] & 0xFFFF0000u) * dn);
+#pragma unroll
+                                for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
+                                    uint32_t x[4];
+                                    dequant_word(w[u], s2, b2, x);
+#pragma unroll
+                                    for (int n = 0; n < 4; ++n)
+                                        sts32(row + (32 * u + 8 * n) * 128, x[n]);
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.empty[slot]);
+                }
+                if (dw == 0 && lane == 0) meta.state = states;
+                fence_proxy_async_smem();  // the tensor cores read what was written
+                __syncwarp();
+                if (lane == 0) mbar_arrive(kv ? &sh.v_full[buf] : &sh.k_full[buf]);
+            }
+        }
+        list.done();
+    }
+}
+
+// ---------------------------------------------------------------- matrix instructions
+
+// One warp issues the instructions of one half.
+template <int D, int G>
+__device__ bool issue_products(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t kbuf,
+                               uint32_t vbuf, uint32_t tmem, int m, int lane) {
+    using SH = Shape<D, G>;
+    constexpr int KB = SH::KB, SB = SH::SB;
+    constexpr uint32_t id_s = umma_idesc_f16(128, kTile), id_o = umma_idesc_f16(128, D);
+    const uint32_t o_col = tmem + 256 + m * D;
+    Pieces<D, G> list(sh, p.wait_budget);
+    int jt = 0;   // units so far: key and value buffers
+    int at = 0;   // units of this half so far: its score buffers
+    int nq = 0;   // pieces of this half so far
+    for (;;) {
+        const Piece* q = list.next();
+        if (!q) return false;
+        const int count = q->count;
+        if (count == 0) return true;
+        if (q->toks <= m * p.half_toks) {
+            // no rows in this half: only let the buffers go
+            for (int k = 0; k < count; ++k, ++jt) {
+                const int buf = jt % KB;
+                const uint32_t par = (uint32_t)(jt / KB) & 1u;
+                if (!warp_wait(&sh.k_full[buf], par, p.wait_budget)) return false;
+                if (lane == 0) mbar_arrive(&sh.k_empty[buf]);
+                if (!warp_wait(&sh.v_full[buf], par, p.wait_budget)) return false;
+                if (lane == 0) mbar_arrive(&sh.v_empty[buf]);
+            }
+            list.done();
+            continue;
+        }
+        if (!warp_wait(&sh.q_full[m], (uint32_t)nq & 1u, p.wait_budget)) return false;
+        ++nq;
+        // scores of unit k of the piece
+        auto scores = [&](int k) {
+            const int buf = (jt + k) % KB, a = at + k;
+            if (!warp_wait(&sh.k_full[buf], (uint32_t)((jt + k) / KB) & 1u, p.wait_budget)) return false;
+            // the buffer's earlier weights have been used
+            if (k >= SB && !warp_wait(&sh.pv_done[m], (uint32_t)(a - SB) & 1u, p.wait_budget)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t s_col = tmem + (SB == 1 ? m : (a & 1)) * kTile;
+#pragma unroll
+                for (int kb = 0; kb < D / 64; ++kb) {
+                    const uint64_t ad = umma_desc_sw128(qbuf + (m * (D / 64) + kb) * (128 * 128));
+                    const uint64_t bd =
+                        umma_desc_sw128(kbuf + buf * SH::kOpBytes + kb * (kTile * 128));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_bf16(s_col, ad + 2 * j, bd + 2 * j, id_s, kb | j ? 1u : 0u);
+                }
+                umma_commit(&sh.s_full[SB == 1 ? m : (a & 1)]);
+                umma_commit(&sh.k_empty[buf]);
+            }
+            __syncwarp();
+            return true;
+        };
+        if (SB == 2 && !scores(0)) return false;
+        for (int k = 0; k < count; ++k) {
+            if (SB == 1) {
+                if (!scores(k)) return false;
+            } else if (k + 1 < count) {
+                if (!scores(k + 1)) return false;
+            }
+            const int buf = (jt + k) % KB, a = at + k;
+            if (!warp_wait(&sh.v_full[buf], (uint32_t)((jt + k) / KB) & 1u, p.wait_budget) ||
+                !warp_wait(&sh.p_full[m], (uint32_t)a & 1u, p.wait_budget))
+                return false;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t p_col = tmem + (SB == 1 ? m : (a & 1)) * kTile;
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+                    const uint64_t bd = umma_desc_sw128(vbuf + buf * SH::kOpBytes + tb * (D * 128));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_bf16_tmem_a(o_col, p_col + (tb * 4 + j) * 8, bd + 2 * j, id_o,
+                                         k | tb | j ? 1u : 0u);
+                }
+                umma_commit(&sh.v_empty[buf]);
+                umma_commit(&sh.pv_done[m]);
+            }
+            __syncwarp();
+        }
+        jt += count;
+        at += count;
+        list.done();
+    }
+}
+
+// ---------------------------------------------------------------- softmax
+
+template <int D, int G>
+__device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tmem, int m,
+                        int quarter, int lane) {
+    using SH = Shape<D, G>;
+    constexpr int KB = SH::KB, SB = SH::SB, PT = SH::PT;
+    const int lr = quarter * 32 + lane;                 // row of the half
+    const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
+    const uint32_t o_at = tmem + t_lane + 256 + m * D;
+    Pieces<D, G> list(sh, p.wait_budget);
+    int jt = 0, at = 0;
+    for (;;) {
+        const Piece* q = list.next();
+        if (!q) return false;
+        const int count = q->count;
+        if (count == 0) return true;
+        const int heads = q->heads, tok0 = m * p.half_toks;
+        const int toks = min(p.half_toks, q->toks - tok0);
+        if (toks <= 0) {
+            jt += count;
+            list.done();
+            continue;
+        }
+        const bool in = lr < toks * heads;
+        const int tok = in ? lr / heads : 0, hh = in ? lr % heads : 0;
+        const int row = q->row0 + tok0 + tok;
+        const int first = q->p0 + tok0, last = first + toks - 1;  // positions of the half
+        const int pos = in ? first + tok : -1;
+        // ---- this thread's query row: f16, its largest value 2^13 .. 2^14
+        float unit;
+        {
+            const __nv_bfloat16* src = p.q + (long long)row * p.q_row_stride +
+                                       (long long)(q->head0 + hh) * p.q_head_stride;
+            uint32_t big = 0;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (in) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                big = max_u16x2(big, max_u16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
+                big = max_u16x2(big, max_u16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+            }
+            const int ex = max((int)(max(big & 0xFFFFu, big >> 16) >> 7), 16);
+            const float up = pow2_of(267 - ex);  // 2^(140 - ex)
+            unit = p.scale_log2 * pow2_of(ex - 13);
+            const uint32_t base = qbuf + m * (D / 64) * (128 * 128) + lr * 128;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (in) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = __uint_as_float(w[e] << 16) * up;
+                    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * up;
+                }
+                // in the order of a code word's pairs
+                sts128(base + (c / 8) * (128 * 128) + (((c % 8) ^ (lr % 8)) * 16),
+                       cvt_f16x2(x[0], x[4]), cvt_f16x2(x[1], x[5]), cvt_f16x2(x[2], x[6]),
+                       cvt_f16x2(x[3], x[7]));
+            }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();  // (the last piece's output has been read)
+        mbar_arrive(&sh.q_full[m]);
+
+        float mx = -INFINITY, mu = 0.f, l = 0.f;
+        int e_o = 30;  // the output's sums are of values over 2^(e_o - 126)
+        for (int k = 0; k < count; ++k, ++jt, ++at) {
+            const int sidx = SB == 1 ? m : (at & 1);
+            if (!warp_wait(&sh.s_full[sidx], (uint32_t)(at / SB) & 1u, p.wait_budget)) return false;
+            tc_fence_after();
+            const uint32_t s_at = tmem + t_lane + sidx * kTile;
+            const volatile Meta& km = sh.k_meta[jt % kMetaRing];
+            const int state = km.state;
+            const int t0 = unit_token(*q, q->k0 + k);
+            const bool edge = state != 0xFF || t0 + kTile - 1 > first ||
+                              (p.window && t0 <= last - p.window && t0 + kTile > p.sinks);
+            // what this row sees of columns c .. c + 31, as bits
+            auto sees = [&](int c) {
+                uint32_t bits = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int t = t0 + c + i;
+                    const bool s = t <= pos && (!p.window || t > pos - p.window || t < p.sinks) &&
+                                   ((state >> ((c + i) / 16)) & 1);
+                    bits |= (s ? 1u : 0u) << i;
+                }
+                return bits;
+            };
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+                uint32_t x[32];
+                tmem_ld32(s_at + c, x);
+                const float f = unit * pow2_of(km.e[c / PT] + 1);
+                tmem_ld_wait();
+                float t = -INFINITY;
+                if (!edge) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) t = fmaxf(t, __uint_as_float(x[i]));
+                } else {
+                    const uint32_t bits = sees(c);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        t = fmaxf(t, (bits >> i) & 1u ? __uint_as_float(x[i]) : -INFINITY);
+                }
+                if (t != -INFINITY) top = fmaxf(top, t * f);
+                __syncwarp();
+            }
+            // the values of this unit have been converted: their powers of two
+            if (!warp_wait(&sh.v_full[jt % KB], (uint32_t)(jt / KB) & 1u, p.wait_budget)) return false;
+            const volatile Meta& vm = sh.v_meta[jt % kMetaRing];
+            int e_new = e_o;
+#pragma unroll
+            for (int i = 0; i < SH::NP; ++i) e_new = max(e_new, vm.e[i]);
+            if (__any_sync(0xFFFFFFFFu, top > mx + 8.f) || e_new > e_o) {
+                const float mn = fmaxf(mx, top);
+                mu = mn == -INFINITY ? 0.f : mn;
+                const float a = exp2_approx(mx - mu);
+                mx = mn;
+                l *= a;
+                const float f = a * pow2_of(max(e_o - e_new + 127, 1));
+                e_o = e_new;
+                if (k > 0) {
+                    // the sums so far, once the last unit's products are in
+                    if (!warp_wait(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget)) return false;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t x[16];
+                        tmem_ld16(o_at + c, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                        tmem_st16(o_at + c, x);
+                    }
+                    tmem_st_wait();
+                }
+            }
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+                uint32_t x[32], y[16];
+                tmem_ld32(s_at + c, x);
+                const float f = unit * pow2_of(km.e[c / PT] + 1);
+                const int de = vm.e[c / PT] - e_o;  // at most 0
+                const float off = (float)(7 + de) - mu;
+                const uint32_t bits = edge ? sees(c) : 0xFFFFFFFFu;
+                tmem_ld_wait();
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float a = exp2_approx(fmaf(__uint_as_float(x[2 * i]), f, off));
+                    float b = exp2_approx(fmaf(__uint_as_float(x[2 * i + 1]), f, off));
+                    if (edge) {
+                        a = (bits >> (2 * i)) & 1u ? a : 0.f;
+                        b = (bits >> (2 * i + 1)) & 1u ? b : 0.f;
+                    }
+                    sum += a + b;
+                    y[i] = cvt_f16x2(a, b);
+                }
+                l = fmaf(sum, pow2_of(min(127 - de, 254)), l);
+                tmem_st16(s_at + c / 2, y);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sh.p_full[m]);
+        }
+        // ---- the row's result
+        if (!warp_wait(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget)) return false;
+        tc_fence_after();
+        const bool whole = q->flags == (kBegins | kEnds);
+        const float up = pow2_of(e_o + 1);  // 2^(e_o - 126)
+        l *= 0x1p-7f;
+        const float inv = whole ? (l > 0.f ? up * (0x1p-7f / l) : 0.f) : up * 0x1p-7f;
+        const long long to = (long long)row * p.Hq + q->head0 + hh;
+        float* part = p.partial + ((long long)blockIdx.x * 2 + ((q->flags & kBegins) ? 1 : 0)) *
+                                      SH::kPartialFloats;
+        const int dense = tok0 * heads + lr;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+            uint32_t x[16];
+            tmem_ld16(o_at + c, x);
+            tmem_ld_wait();
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(x[i]) * inv;
+            if (in && whole) {
+                uint4 a, b;
+                a.x = cvt_bf16x2(v[0], v[1]);
+                a.y = cvt_bf16x2(v[2], v[3]);
+                a.z = cvt_bf16x2(v[4], v[5]);
+                a.w = cvt_bf16x2(v[6], v[7]);
+                b.x = cvt_bf16x2(v[8], v[9]);
+                b.y = cvt_bf16x2(v[10], v[11]);
+                b.z = cvt_bf16x2(v[12], v[13]);
+                b.w = cvt_bf16x2(v[14], v[15]);
+                uint4* dst = reinterpret_cast<uint4*>(p.out + to * D + c);
+                dst[0] = a;
+                dst[1] = b;
+            } else if (in) {
+                float4* dst = reinterpret_cast<float4*>(part + 2 * SH::kRows + (long long)dense * D + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+            __syncwarp();
+        }
+        if (in) {
+            if (whole) {
+                if (p.lse) p.lse[to] = l > 0.f ? (mx + log2f(l)) * 0.69314718f : -INFINITY;
+            } else {
+                part[2 * dense] = mx;
+                part[2 * dense + 1] = l;
+            }
+        }
+        list.done();
+    }
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnParams p) {
+    using SH = Shape<D, G>;
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared<D, G> sh;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t qbuf = base, kbuf = qbuf + SH::kQBytes, vbuf = kbuf + SH::KB * SH::kOpBytes;
+    const uint32_t ring = vbuf + SH::KB * SH::kOpBytes;
+    const uint8_t* ring_ptr = raw + (ring - smem_u32(raw));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPieceRing; ++i) {
+            mbar_init(&sh.piece_full[i], 1);
+            mbar_init(&sh.piece_empty[i], 5 * SH::MT + 5);
+        }
+        for (int i = 0; i < SH::kSlots; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 4);
+        }
+        for (int i = 0; i < SH::KB; ++i) {
+            mbar_init(&sh.k_full[i], 4);
+            mbar_init(&sh.v_full[i], 4);
+            mbar_init(&sh.k_empty[i], SH::MT);
+            mbar_init(&sh.v_empty[i], SH::MT);
+        }
+        for (int i = 0; i < SH::MT; ++i) {
+            mbar_init(&sh.q_full[i], 128);
+            mbar_init(&sh.p_full[i], 128);
+            mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.drained[i], 1);
+        }
+        mbar_init(&sh.s_full[0], 1);
+        mbar_init(&sh.s_full[1], 1);
+        mbar_init_fence();
+    }
+    if (warp == 15) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    bool ok = true;
+    if (warp < 4 * SH::MT) {
+        ok = softmax<D, G>(p, sh, qbuf, tmem, warp / 4, warp % 4, lane);
+    } else if (warp >= 8 && warp < 12) {
+        ok = convert<D, G>(p, sh, ring_ptr, kbuf, vbuf, warp - 8, lane);
+    } else if (warp >= 12 && warp < 12 + SH::MT) {
+        ok = issue_products<D, G>(p, sh, qbuf, kbuf, vbuf, tmem, warp - 12, lane);
+        __syncwarp();
+        // no instruction may still be running when the CTA lets its memory go
+        if (elect_one()) umma_commit(&sh.drained[warp - 12]);
+        __syncwarp();
+        ok = warp_wait(&sh.drained[warp - 12], 0, kWaitBudgetCycles) && ok;
+    } else if (warp == 14) {
+        ok = copy_parts<D, G>(p, sh, ring, lane);
+    } else if (warp == 15) {
+        if (lane == 0) ok = list_pieces<D, G>(p, sh);
+    }
+    if (!ok) flag_status(p.status, MXQ_DEV_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 15) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- plan and join
+
+__device__ int block_scan(int x, int* total) {  // exclusive; 1024 threads
+    __shared__ int sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int w = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+        if (lane >= o) w += y;
+    }
+    *total = __shfl_sync(0xFFFFFFFFu, w, 31);
+    const int before = warp ? __shfl_sync(0xFFFFFFFFu, w, warp - 1) : 0;
+    __syncthreads();
+    return before + incl - x;
+}
+
+// The row tiles of all sequences and the units before each: one block.
+__global__ void __launch_bounds__(1024) kv_plan_kernel(const KvAttnParams p) {
+    Entry* entries = reinterpret_cast<Entry*>(p.entries);
+    int* starts = p.seq_tiles;  // first row tile of each sequence
+    int run = 0;
+    bool bad = false;
+    for (int s0 = 0; s0 < p.S; s0 += 1024) {
+        const int s = s0 + threadIdx.x;
+        int n = 0;
+        if (s < p.S) {
+            const Span sp = span_of<kTile>(p, s, 0);
+            bad |= sp.bad != 0;
+            if (sp.toks > 0) {
+                const int rows = p.q_starts ? __ldg(p.q_starts + s + 1) - __ldg(p.q_starts + s) : 1;
+                n = (rows + p.tile_toks - 1) / p.tile_toks;
+            }
+        }
+        int total;
+        const int at = run + block_scan(n, &total);
+        if (s < p.S) starts[s] = at;
+        run += total;
+    }
+    // rows that overlap (decreasing starts) can make more row tiles than there is room for
+    bad |= run > p.max_entries;
+    const int n_entries = min(run, p.max_entries);
+    if (bad) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
+    __syncthreads();
+    run = 0;
+    for (int e0 = 0; e0 < n_entries; e0 += 1024) {
+        const int e = e0 + threadIdx.x;
+        int tiles = 0;
+        if (e < n_entries) {
+            int lo = 0, hi = p.S - 1;  // the last sequence that starts at or before e
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (starts[mid] <= e) lo = mid;
+                else hi = mid - 1;
+            }
+            const Span sp = span_of<kTile>(p, lo, e - starts[lo]);
+            Entry en;
+            en.s = lo;
+            en.row0 = sp.row0;
+            en.toks = sp.toks;
+            en.p0 = sp.p0;
+            en.tiles = tiles = sp.tiles;
+            en.head_tiles = sp.head_tiles;
+            en.tail = sp.tail;
+            en.pad = 0;
+            entries[e] = en;
+        }
+        int total;
+        const int at = run + block_scan(tiles, &total);
+        if (e < n_entries) p.before[e] = at;
+        run += total;
+    }
+    if (threadIdx.x == 0) {
+        p.counts[0] = n_entries;
+        p.counts[1] = run;
+    }
+}
+
+// Joins the pieces of cut row tiles; blockIdx.y takes a share of the rows.
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_rows_kernel(const KvAttnParams p, int tile_rows) {
+    pdl_wait();
+    const int cta = blockIdx.x;
+    const Seg* segs = reinterpret_cast<const Seg*>(p.segs);
+    const Seg g = segs[cta * 2 + 1];
+    if (g.flags < 0 || !(g.flags & kBegins) || (g.flags & kEnds)) return;
+    // after a wait that gave up the descriptors may be anything
+    if (g.toks <= 0 || g.heads <= 0 || g.toks > tile_rows || g.heads > tile_rows ||
+        g.toks * g.heads > tile_rows || g.row0 < 0 || g.row0 > p.T - g.toks || g.head0 < 0 ||
+        g.head0 > p.Hq - g.heads)
+        return;
+    int last = cta;
+    while (last + 1 < p.ctas) {
+        ++last;
+        const int f = segs[last * 2].flags;
+        if (f < 0 || (f & kEnds)) break;
+    }
+    const int n = last - cta + 1, rows = g.toks * g.heads;
+    const long long stride = (long long)tile_rows * (D + 2);
+    auto piece = [&](int k) { return p.partial + ((cta + k) * 2LL + (k ? 0 : 1)) * stride; };
+    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < rows * (D / 4);
+         i += gridDim.y * blockDim.x) {
+        const int row = i / (D / 4), d = (i % (D / 4)) * 4;
+        float mm = -INFINITY;
+        for (int k = 0; k < n; ++k) mm = fmaxf(mm, piece(k)[2 * row]);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        float ll = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float* q = piece(k);
+            const float2 ml = *reinterpret_cast<const float2*>(q + 2 * row);
+            const float4 y =
+                *reinterpret_cast<const float4*>(q + 2 * tile_rows + (long long)row * D + d);
+            const float f = exp2_approx(ml.x - ref);
+            ll = fmaf(ml.y, f, ll);
+            o.x = fmaf(y.x, f, o.x);
+            o.y = fmaf(y.y, f, o.y);
+            o.z = fmaf(y.z, f, o.z);
+            o.w = fmaf(y.w, f, o.w);
+        }
+        const long long to = (long long)(g.row0 + row / g.heads) * p.Hq + g.head0 + row % g.heads;
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        uint2 v;
+        v.x = cvt_bf16x2(o.x * inv, o.y * inv);
+        v.y = cvt_bf16x2(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(p.out + to * D + d) = v;
+        if (p.lse && d == 0) p.lse[to] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718f : -INFINITY;
+    }
+}
+
+template <int D, int G>
+cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
+    using SH = Shape<D, G>;
+    cudaError_t err = cudaFuncSetAttribute(kv_prefill_kernel<D, G>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kSmem);
+    if (err != cudaSuccess) return err;
+    kv_plan_kernel<<<1, 1024, 0, stream>>>(p);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    kv_prefill_kernel<D, G><<<p.ctas, kThreads, SH::kSmem, stream>>>(p);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.ctas, 16);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_join_rows_kernel<D>, p, (int)SH::kRows);
+}
+
+}  // namespace
+
+int kv_prefill_rows(int D) { return D == 256 ? 128 : 256; }
+
+size_t kv_prefill_entry_bytes() { return sizeof(Entry); }
+
+cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, int G, cudaStream_t stream) {
+#define MXQ_KV_PREFILL(d, g) \
+    if (D == d && G == g) return launch<d, g>(p, stream);
+    MXQ_KV_PREFILL(64, 32)
+    MXQ_KV_PREFILL(64, 64)
+    MXQ_KV_PREFILL(128, 32)
+    MXQ_KV_PREFILL(128, 64)
+    MXQ_KV_PREFILL(128, 128)
+    MXQ_KV_PREFILL(256, 32)
+    MXQ_KV_PREFILL(256, 64)
+    MXQ_KV_PREFILL(256, 128)
+#undef MXQ_KV_PREFILL
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace mxq

@@ -177,8 +177,7 @@ cudaError_t launch_kv_append(const KvRowsParams& p, int D, int G, cudaStream_t s
 cudaError_t launch_kv_read(const KvRowsParams& p, int D, int G, cudaStream_t stream);
 
 // Attention over the cache.  A row tile is up to `tile_rows` rows, each one
-// (token, query head) of one sequence and key/value head; a plane is the row
-// tiles of one index over all sequences.
+// (token, query head) of one sequence and key/value head.
 struct KvAttnParams {
     const __nv_bfloat16* q;  // bf16 [T, Hq, D], strides in values
     long long q_row_stride, q_head_stride;
@@ -194,19 +193,32 @@ struct KvAttnParams {
     int head_parts;          // a key/value head's query heads, in so many row tiles ...
     int part_heads;          // ... of at most this many heads
     int tile_toks;           // tokens in a row tile
-    int planes, ctas;        // ctas per plane
+    int min_rows, max_rows;  // a sequence's rows, for it to be this kernel's
+    int ctas;
     int page_shift;          // log2(page_size)
     int* segs;               // workspace: 2 descriptors per CTA
     float* partial;          // workspace: 2 partial results per CTA
+    // many rows:
+    int half_toks;           // tokens in 128 rows
+    int* seq_tiles;          // workspace: first row tile of each sequence
+    void* entries;           // workspace: row tiles
+    int* before;             // workspace: units before each row tile
+    int* counts;             // workspace: row tiles, units
+    int max_entries;
     int32_t* status;
     long long wait_budget;
 };
 
 cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int G, int tile_rows,
                            cudaStream_t stream);
-// Workspace of launch_kv_attn: descriptors, then partial results.
-size_t kv_attn_seg_bytes(int planes, int ctas);
-size_t kv_attn_partial_bytes(int planes, int ctas, int tile_rows, int D);
+// Workspace of both: descriptors, then partial results.
+size_t kv_attn_seg_bytes(int ctas);
+size_t kv_attn_partial_bytes(int ctas, int tile_rows, int D);
 int kv_attn_ctas_per_sm();
+
+// Sequences with more rows than launch_kv_attn takes, on the tensor cores.
+cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, int G, cudaStream_t stream);
+int kv_prefill_rows(int D);          // rows of its row tiles
+size_t kv_prefill_entry_bytes();     // workspace of a row tile
 
 }  // namespace mxq

@@ -382,8 +382,8 @@ mxq_status mxq_kv_read(const void* pages, const int32_t* slots, void* k_out, voi
  *   row that sees nothing
  *   max_q_len: the most rows a sequence has, a host-side bound
  *   window: 0 for none; sinks: first tokens that stay visible
- *   workspace: mxq_kv_attention_workspace_bytes(Hq, Hkv, D, max_q_len) bytes,
- *   256-byte aligned, overwritten
+ *   workspace: mxq_kv_attention_workspace_bytes(T, S, Hq, Hkv, D, max_q_len)
+ *   bytes, 256-byte aligned, overwritten
  * A page number outside [0, n_pages) where a row sees it makes its tokens
  * invisible and is reported (MXQ_DEV_BAD_PAGE).  A length outside [0, max_pages
  * * page_size] is clamped to it; a sequence whose rows are not within [0, T],
@@ -399,7 +399,7 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
                             int group_size, int max_q_len, float scale, int window, int sinks,
                             void* workspace, size_t workspace_bytes, int32_t* dev_status,
                             void* stream);
-size_t mxq_kv_attention_workspace_bytes(int Hq, int Hkv, int D, int max_q_len);
+size_t mxq_kv_attention_workspace_bytes(int T, int S, int Hq, int Hkv, int D, int max_q_len);
 
 /* Static description of a status code. */
 const char* mxq_status_string(mxq_status status);

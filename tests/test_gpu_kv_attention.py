@@ -239,7 +239,7 @@ def test_same_bits_every_time_and_on_another_stream(rows):
     c = Case(ctx, [rows] * 3, 8, 2, 128, 64, 64, seed=16)
     first = c.run()[0]
     s = torch.cuda.Stream()
-    need = mxq.kv_attention_workspace_bytes(8, 2, 128, rows)
+    need = mxq.kv_attention_workspace_bytes(3 * rows, 3, 8, 2, 128, rows)
     for _ in range(3):
         ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda")
         out = torch.empty(c.q.shape, dtype=torch.bfloat16, device="cuda")
@@ -257,7 +257,7 @@ def test_captured_steps_follow_the_lengths():
     import affine_bit_matmul_gb300 as mxq
 
     c = Case([500, 64, 1], [1, 1, 1], 8, 2, 128, 64, 16, seed=17, extra_width=2)
-    ws = torch.empty(mxq.kv_attention_workspace_bytes(8, 2, 128, 1), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(mxq.kv_attention_workspace_bytes(3, 3, 8, 2, 128), dtype=torch.uint8, device="cuda")
     out = torch.zeros(3, 8, 128, dtype=torch.bfloat16, device="cuda")
 
     def step():

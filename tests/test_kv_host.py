@@ -98,10 +98,14 @@ def test_sizes(L):
     for D, G, page in ((64, 32, 16), (256, 128, 128)):
         assert L.mxq_kv_block_bytes(D, page, G) == ku.block_bytes(D, page, G)
     assert L.mxq_kv_block_bytes(128, 24, 64) == 0 and L.mxq_kv_block_bytes(96, 16, 32) == 0
-    assert L.mxq_kv_attention_workspace_bytes(8, 3, 128, 1) == 0
-    assert L.mxq_kv_attention_workspace_bytes(8, 2, 128, 0) == 0
-    assert 0 < L.mxq_kv_attention_workspace_bytes(8, 2, 128, 1)
-    assert L.mxq_kv_attention_workspace_bytes(64, 1, 256, 10 ** 6) < 1 << 31
+    assert L.mxq_kv_attention_workspace_bytes(4, 4, 8, 3, 128, 1) == 0
+    assert L.mxq_kv_attention_workspace_bytes(4, 4, 8, 2, 128, 0) == 0
+    assert 0 < L.mxq_kv_attention_workspace_bytes(4, 4, 8, 2, 128, 1)
+    # long prompts take no more than the partial results of one block per SM and a list
+    assert L.mxq_kv_attention_workspace_bytes(10 ** 6, 4, 64, 1, 256, 10 ** 6) < 1 << 28
+    # a bound above the rows there are is as good as their number
+    assert (L.mxq_kv_attention_workspace_bytes(40, 4, 8, 2, 128, 10 ** 6) ==
+            L.mxq_kv_attention_workspace_bytes(40, 4, 8, 2, 128, 40))
 
 
 def test_python_refusals():
