@@ -10,15 +10,15 @@
 // A row tile is up to 256 rows (128 for D = 256): all query heads of one
 // key/value head at 128 / heads tokens, once or twice.  A unit is (row tile,
 // 128 tokens); the units of all row tiles, in order, are cut into equal runs,
-// one per SM, as for few rows.  Roles of a CTA's 16 warps:
+// one per SM, as for few rows.  Roles of a CTA's 20 warps:
 //   0-3, 4-7  softmax of the first and second 128 rows, one row a thread:
 //             scores from tensor memory, maximum, weights back into tensor
 //             memory over the scores, and the output at the end
-//   8-11      codes -> f16 operands in shared memory (128-byte swizzle; keys
-//             along the values, values along the tokens)
-//   12, 13    the matrix instructions of one half each: Q K^T, then P V
-//   14        copies of page parts into a ring
-//   15        the list of the run's pieces; tensor memory
+//   8-15      codes -> f16 operands in shared memory (128-byte swizzle; keys
+//             along the values, values along the tokens), 32 tokens a warp
+//   16, 17    the matrix instructions of one half each: Q K^T, then P V
+//   18        copies of page parts into a ring
+//   19        the list of the run's pieces; tensor memory
 // The two halves are independent chains (scores, weights, sum), so one half's
 // products run while the other half's softmax does.  For D = 256 there is one
 // half with two score buffers instead.  The running maximum is only moved when
@@ -36,7 +36,7 @@ namespace mxq {
 namespace {
 
 constexpr int kTile = 128;           // tokens of a unit
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kPieceRing = 8;
 constexpr int kMetaRing = 4;
 
@@ -68,7 +68,7 @@ struct Entry {
 };
 
 struct Meta {
-    int state;     // bit i: tokens 16 i .. of the unit exist
+    int state[4];  // of each part, bit i: tokens 16 i .. of it exist
     int e[4];      // biased exponents of the parts: values are below 2^(e - 126)
 };
 
@@ -76,19 +76,57 @@ __device__ __forceinline__ int unit_token(const Piece& q, int k) {
     return (k < q.head_tiles ? k : q.tail + k - q.head_tiles) * kTile;
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// Waits for this thread's tensor-memory loads; the registers named are not used
+// before.
+__device__ __forceinline__ void tmem_ld_wait_of(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// 8 columns of this thread's lane.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
+          "=r"(r[7])
         : "r"(taddr)
         : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void parts_of(uint64_t p, float* a, float* b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t hmul2_f16(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // Instruction descriptor for kind::f16: f16 A and B, fp32 D, both K-major.
@@ -137,7 +175,7 @@ struct Shared {
     uint64_t q_full[SH::MT], s_full[2], p_full[SH::MT], pv_done[SH::MT], drained[SH::MT];
     Piece pieces[kPieceRing];
     Meta k_meta[kMetaRing], v_meta[kMetaRing];
-    int part_t0[SH::kSlots], part_state[SH::kSlots];
+    int part_unit[SH::kSlots], part_t0[SH::kSlots], part_state[SH::kSlots];
     uint32_t tmem;
 };
 
@@ -308,6 +346,7 @@ __device__ bool copy_parts(const KvAttnParams& p, Shared<D, G>& sh, uint32_t rin
                     }
                     sh.part_t0[slot] = t0 + (u % NP) * PT;
                     sh.part_state[slot] = state;
+                    *const_cast<volatile int*>(&sh.part_unit[slot]) = (int)unit;
                     mbar_expect_tx(&sh.full[slot], sum);
                 }
                 __syncwarp();
@@ -325,18 +364,36 @@ __device__ bool copy_parts(const KvAttnParams& p, Shared<D, G>& sh, uint32_t rin
 
 // ---------------------------------------------------------------- codes -> operands
 
-// Four warps convert each part together.
+// Waits, within the budget, until a slot holds part `n` of the run (whole warp).
+// The warps may be a round of the ring apart, and the parity of a phase alone
+// does not tell a round from the one two before it.
+__device__ __forceinline__ bool part_comes(const int* unit, int n, long long budget) {
+    const volatile int* u = unit;
+    bool ok = true;
+    if (*u != n) {
+        const long long since = clock64();
+        while (*u != n && ok) {
+            __nanosleep(20);
+            ok = clock64() - since <= budget;
+        }
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// Warp cw of eight converts 32 tokens of the keys or of the values of each unit.
 template <int D, int G>
 __device__ bool convert(const KvAttnParams& p, Shared<D, G>& sh, const uint8_t* ring, uint32_t kbuf,
-                        uint32_t vbuf, int dw, int lane) {
+                        uint32_t vbuf, int cw, int lane) {
     using SH = Shape<D, G>;
     constexpr int PT = SH::PT, NP = SH::NP, NS = SH::kSlots, KB = SH::KB;
     constexpr int NG = D / G, U = D / 32;
+    constexpr int kShare = PT / 32;                  // warps of a part
     const int r = lane >> 2, i4 = lane & 3;
+    const bool kv = cw / kShare >= NP;               // values
+    const int part = cw / kShare % NP, first = cw % kShare * 32;
     const int size = min(p.page_size, PT);
-    const int whole = (kv_code_bytes(D, size) + kv_pair_bytes(D, G, size));
+    const int whole = kv_code_bytes(D, size) + kv_pair_bytes(D, G, size);
     Pieces<D, G> list(sh, p.wait_budget);
-    long long unit = 0;
     int jt = 0;
     for (;;) {
         const Piece* q = list.next();
@@ -345,140 +402,132 @@ __device__ bool convert(const KvAttnParams& p, Shared<D, G>& sh, const uint8_t* 
         const int p0 = q->p0, p1 = p0 + q->toks - 1;
         for (int k = 0; k < q->count; ++k, ++jt) {
             const int buf = jt % KB;
-            const uint32_t round = (uint32_t)(jt / KB) & 1u;
-#pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint32_t out = kv ? vbuf + buf * SH::kOpBytes : kbuf + buf * SH::kOpBytes;
-                Meta& meta = kv ? sh.v_meta[jt % kMetaRing] : sh.k_meta[jt % kMetaRing];
-                if (!warp_wait(kv ? &sh.v_empty[buf] : &sh.k_empty[buf], round ^ 1u, p.wait_budget))
-                    return false;
-                int states = 0;
-#pragma unroll 1
-                for (int part = 0; part < NP; ++part, ++unit) {
-                    const int slot = (int)(unit % NS);
-                    if (!warp_wait(&sh.full[slot], (uint32_t)(unit / NS) & 1u, p.wait_budget))
-                        return false;
-                    const uint8_t* at = ring + slot * SH::kPartBytes;
-                    const int t0 = sh.part_t0[slot], state = sh.part_state[slot];
-                    states |= state << (part * (PT / 16));
-                    // some token of the part is seen by no row: what it holds is not used
-                    const bool edge =
-                        state != (1 << (PT / 16)) - 1 || t0 + PT - 1 > p1 ||
-                        (p.window && t0 <= p0 - p.window && t0 + PT > p.sinks);
-                    auto unseen = [&](int t) {
-                        return !((state >> (t / 16)) & 1) || t0 + t > p1 ||
-                               (p.window && t0 + t <= p0 - p.window && t0 + t >= p.sinks);
-                    };
-                    auto pairs_of = [&](int t) {
-                        return at + t / size * whole + kv_code_bytes(D, size) + t % size * (NG * 4);
-                    };
-                    // a power of two above every |s q + b| of the part
-                    uint32_t big = 0;
+            const uint32_t out = (kv ? vbuf : kbuf) + buf * SH::kOpBytes;
+            Meta& meta = kv ? sh.v_meta[jt % kMetaRing] : sh.k_meta[jt % kMetaRing];
+            const int unit = jt * 2 * NP + cw / kShare, slot = unit % NS;
+            if (!part_comes(&sh.part_unit[slot], unit, p.wait_budget) ||
+                !warp_wait(&sh.full[slot], (uint32_t)(unit / NS) & 1u, p.wait_budget))
+                return false;
+            const uint8_t* at = ring + slot * SH::kPartBytes;
+            const int t0 = sh.part_t0[slot], state = sh.part_state[slot];
+            // some token of the part is seen by no row: what it holds is not used
+            const bool edge = state != (1 << (PT / 16)) - 1 || t0 + PT - 1 > p1 ||
+                              (p.window && t0 <= p0 - p.window && t0 + PT > p.sinks);
+            auto unseen = [&](int t) {
+                return !((state >> (t / 16)) & 1) || t0 + t > p1 ||
+                       (p.window && t0 + t <= p0 - p.window && t0 + t >= p.sinks);
+            };
+            auto pairs_of = [&](int t) {
+                return at + t / size * whole + kv_code_bytes(D, size) + t % size * (NG * 4);
+            };
+            // a power of two above every |s q + b| of the part
+            uint32_t big = 0;
 #pragma unroll
-                    for (int j = 0; j < PT / 32; ++j) {
-                        const int t = lane + 32 * j;
-                        uint32_t w[NG];
-                        load_pairs<NG>(pairs_of(t), w);
-                        const uint32_t keep = edge && unseen(t) ? 0u : 0x7FFF7FFFu;
+            for (int j = 0; j < PT / 32; ++j) {
+                const int t = lane + 32 * j;
+                uint32_t w[NG];
+                load_pairs<NG>(pairs_of(t), w);
+                const uint32_t keep = edge && unseen(t) ? 0u : 0x7FFF7FFFu;
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) big = max_u16x2(big, w[g] & keep);
+                for (int g = 0; g < NG; ++g) big = max_u16x2(big, w[g] & keep);
+            }
+            const int es = (int)(__reduce_max_sync(0xFFFFFFFFu, big & 0xFFFFu) >> 7) + 4;
+            const int eb = (int)(__reduce_max_sync(0xFFFFFFFFu, big >> 16) >> 7);
+            const int e = min(max(max(es, eb) + 1, 30), 250);
+            const float dn = pow2_of(253 - e);  // 2^(126 - e)
+            if (!warp_wait(kv ? &sh.v_empty[buf] : &sh.k_empty[buf], ((uint32_t)(jt / KB) & 1u) ^ 1u,
+                           p.wait_budget))
+                return false;
+            // 8 tokens at a time
+            const uint8_t* base = at + first / size * whole + kv_code_bytes(D, first % size) +
+                                  lane * (D == 64 ? 8 : 16);
+            const int next16 = size == 16 ? whole : kv_code_bytes(D, 16);  // codes 16 tokens on
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int tb = first + 8 * j;
+                uint32_t w[U];
+                load_words<U>(base + (j / 2) * next16 + (j % 2) * (4 * D), w);
+                const int tt = part * PT + tb;  // token within the unit
+                if (!kv) {
+                    uint32_t pr[NG];
+                    load_pairs<NG>(pairs_of(tb + r), pr);
+                    if (edge && unseen(tb + r)) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) pr[g] = 0u;
                     }
-                    const int es = (int)(__reduce_max_sync(0xFFFFFFFFu, big & 0xFFFFu) >> 7) + 4;
-                    const int eb = (int)(__reduce_max_sync(0xFFFFFFFFu, big >> 16) >> 7);
-                    const int e = min(max(max(es, eb) + 1, 30), 250);
-                    const float dn = pow2_of(253 - e);  // 2^(126 - e)
-                    if (dw == 0 && lane == 0) meta.e[part] = e;
-                    // 8 tokens at a time
+                    // odd tokens take the words of a pair in the other order: their
+                    // stores would meet the even ones' in the same banks
+                    const bool odd = r & 1;
 #pragma unroll
-                    for (int j = 0; j < PT / 32; ++j) {
-                        const int tb = (dw + 4 * j) * 8;
-                        const uint8_t* codes = at + tb / size * whole + kv_code_bytes(D, tb % size) +
-                                               lane * (D == 64 ? 8 : 16);
-                        uint32_t w[U];
-                        load_words<U>(codes, w);
-                        const int tt = part * PT + tb;  // token within the unit
-                        if (kv == 0) {
-                            uint32_t pr[NG];
-                            load_pairs<NG>(pairs_of(tb + r), pr);
-                            if (edge && unseen(tb + r)) {
+                    for (int u = 0; u < U; u += 2) {
+                        const uint32_t a = w[u], b = w[u + 1];
+                        w[u] = odd ? b : a;
+                        w[u + 1] = odd ? a : b;
+                    }
+                    if (G == 32) {
 #pragma unroll
-                                for (int g = 0; g < NG; ++g) pr[g] = 0u;
-                            }
-                            // odd tokens take the words of a pair in the other order: their
-                            // stores would meet the even ones' in the same banks
-                            const bool odd = r & 1;
-#pragma unroll
-                            for (int u = 0; u < U; u += 2) {
-                                const uint32_t a = w[u], b = w[u + 1];
-                                w[u] = odd ? b : a;
-                                w[u + 1] = odd ? a : b;
-                            }
-                            if (G == 32) {
-#pragma unroll
-                                for (int g = 0; g < NG; g += 2) {
-                                    const uint32_t a = pr[g], b = pr[g + 1];
-                                    pr[g] = odd ? b : a;
-                                    pr[g + 1] = odd ? a : b;
-                                }
-                            }
-                            uint32_t s2[NG], b2[NG];
-#pragma unroll
-                            for (int g = 0; g < NG; ++g) {
-                                const float s = __uint_as_float(pr[g] << 16) * dn;
-                                const float b = __uint_as_float(pr[g] & 0xFFFF0000u) * dn;
-                                s2[g] = cvt_f16x2(s, s);
-                                b2[g] = cvt_f16x2(b, b);
-                            }
-                            const uint32_t row = out + (tt + r) * 128;
-#pragma unroll
-                            for (int u = 0; u < U; ++u) {
-                                uint32_t x[4];
-                                dequant_word(w[u], s2[u * 32 / G], b2[u * 32 / G], x);
-                                // values 32 u' + 8 i4 ..: 16 bytes of row tt + r
-                                const int chunk = (((u & 1) ^ (r & 1)) * 4 + i4) ^ r;
-                                sts128(row + (u / 2) * (kTile * 128) + chunk * 16, x[0], x[1], x[2],
-                                       x[3]);
-                            }
-                        } else {
-                            uint32_t pa[NG], pc[NG];
-                            load_pairs<NG>(pairs_of(tb + 2 * i4), pa);
-                            load_pairs<NG>(pairs_of(tb + 2 * i4 + 1), pc);
-                            if (edge) {
-#pragma unroll
-                                for (int g = 0; g < NG; ++g) {
-                                    if (unseen(tb + 2 * i4)) pa[g] = 0u;
-                                    if (unseen(tb + 2 * i4 + 1)) pc[g] = 0u;
-                                }
-                            }
-                            // values 32 u + r + 8 n of tokens 2 i4 and 2 i4 + 1
-                            const uint32_t row = out + (tt / 64) * (D * 128) + r * 128 +
-                                                 ((((tt % 64) / 8) ^ r) * 16) + i4 * 4;
-#pragma unroll
-                            for (int g = 0; g < NG; ++g) {
-                                const uint32_t s2 =
-                                    cvt_f16x2(__uint_as_float(pa[g] << 16) * dn,
-                                              __uint_as_float(pc[g] << 16) * dn);
-                                const uint32_t b2 =
-                                    cvt_f16x2(__uint_as_float(pa[g] & 0xFFFF0000u) * dn,
-                                              __uint_as_float(pc[g] & 0xFFFF0000u) * dn);
-#pragma unroll
-                                for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
-                                    uint32_t x[4];
-                                    dequant_word(w[u], s2, b2, x);
-#pragma unroll
-                                    for (int n = 0; n < 4; ++n)
-                                        sts32(row + (32 * u + 8 * n) * 128, x[n]);
-                                }
-                            }
+                        for (int g = 0; g < NG; g += 2) {
+                            const uint32_t a = pr[g], b = pr[g + 1];
+                            pr[g] = odd ? b : a;
+                            pr[g + 1] = odd ? a : b;
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.empty[slot]);
+                    uint32_t s2[NG], b2[NG];
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const float s = __uint_as_float(pr[g] << 16) * dn;
+                        const float b = __uint_as_float(pr[g] & 0xFFFF0000u) * dn;
+                        s2[g] = cvt_f16x2(s, s);
+                        b2[g] = cvt_f16x2(b, b);
+                    }
+                    const uint32_t row = out + (tt + r) * 128;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        uint32_t x[4];
+                        dequant_word(w[u], s2[u * 32 / G], b2[u * 32 / G], x);
+                        // values 32 u' + 8 i4 ..: 16 bytes of row tt + r
+                        const int chunk = (((u & 1) ^ (r & 1)) * 4 + i4) ^ r;
+                        sts128(row + (u / 2) * (kTile * 128) + chunk * 16, x[0], x[1], x[2], x[3]);
+                    }
+                } else {
+                    uint32_t pa[NG], pc[NG];
+                    load_pairs<NG>(pairs_of(tb + 2 * i4), pa);
+                    load_pairs<NG>(pairs_of(tb + 2 * i4 + 1), pc);
+                    if (edge) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            if (unseen(tb + 2 * i4)) pa[g] = 0u;
+                            if (unseen(tb + 2 * i4 + 1)) pc[g] = 0u;
+                        }
+                    }
+                    // values 32 u + r + 8 n of tokens 2 i4 and 2 i4 + 1
+                    const uint32_t row = out + (tt / 64) * (D * 128) + r * 128 +
+                                         ((((tt % 64) / 8) ^ r) * 16) + i4 * 4;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t s2 = cvt_f16x2(__uint_as_float(pa[g] << 16) * dn,
+                                                      __uint_as_float(pc[g] << 16) * dn);
+                        const uint32_t b2 = cvt_f16x2(__uint_as_float(pa[g] & 0xFFFF0000u) * dn,
+                                                      __uint_as_float(pc[g] & 0xFFFF0000u) * dn);
+#pragma unroll
+                        for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
+                            uint32_t x[4];
+                            dequant_word(w[u], s2, b2, x);
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) sts32(row + (32 * u + 8 * n) * 128, x[n]);
+                        }
+                    }
                 }
-                if (dw == 0 && lane == 0) meta.state = states;
-                fence_proxy_async_smem();  // the tensor cores read what was written
-                __syncwarp();
-                if (lane == 0) mbar_arrive(kv ? &sh.v_full[buf] : &sh.k_full[buf]);
+            }
+            if (lane == 0 && first == 0) {
+                meta.e[part] = e;
+                meta.state[part] = state;
+            }
+            fence_proxy_async_smem();  // the tensor cores read what was written
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.empty[slot]);
+                mbar_arrive(kv ? &sh.v_full[buf] : &sh.k_full[buf]);
             }
         }
         list.done();
@@ -650,50 +699,36 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
             if (!warp_wait(&sh.s_full[sidx], (uint32_t)(at / SB) & 1u, p.wait_budget)) return false;
             tc_fence_after();
             const uint32_t s_at = tmem + t_lane + sidx * kTile;
+            uint32_t xa[16], xb[16];
+            tmem_ld16(s_at, xa);
             const volatile Meta& km = sh.k_meta[jt % kMetaRing];
-            const int state = km.state;
+            const volatile Meta& vm = sh.v_meta[jt % kMetaRing];
+            int state = 0;
+#pragma unroll
+            for (int i = 0; i < SH::NP; ++i) state |= km.state[i] << (i * (PT / 16));
             const int t0 = unit_token(*q, q->k0 + k);
             const bool edge = state != 0xFF || t0 + kTile - 1 > first ||
                               (p.window && t0 <= last - p.window && t0 + kTile > p.sinks);
-            // what this row sees of columns c .. c + 31, as bits
+            // what this row sees of columns c .. c + 15, as bits
             auto sees = [&](int c) {
                 uint32_t bits = 0;
+                if (!((state >> (c / 16)) & 1)) return bits;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     const int t = t0 + c + i;
-                    const bool s = t <= pos && (!p.window || t > pos - p.window || t < p.sinks) &&
-                                   ((state >> ((c + i) / 16)) & 1);
+                    const bool s = t <= pos && (!p.window || t > pos - p.window || t < p.sinks);
                     bits |= (s ? 1u : 0u) << i;
                 }
                 return bits;
             };
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-                uint32_t x[32];
-                tmem_ld32(s_at + c, x);
-                const float f = unit * pow2_of(km.e[c / PT] + 1);
-                tmem_ld_wait();
-                float t = -INFINITY;
-                if (!edge) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) t = fmaxf(t, __uint_as_float(x[i]));
-                } else {
-                    const uint32_t bits = sees(c);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        t = fmaxf(t, (bits >> i) & 1u ? __uint_as_float(x[i]) : -INFINITY);
-                }
-                if (t != -INFINITY) top = fmaxf(top, t * f);
-                __syncwarp();
-            }
             // the values of this unit have been converted: their powers of two
             if (!warp_wait(&sh.v_full[jt % KB], (uint32_t)(jt / KB) & 1u, p.wait_budget)) return false;
-            const volatile Meta& vm = sh.v_meta[jt % kMetaRing];
             int e_new = e_o;
 #pragma unroll
             for (int i = 0; i < SH::NP; ++i) e_new = max(e_new, vm.e[i]);
-            if (__any_sync(0xFFFFFFFFu, top > mx + 8.f) || e_new > e_o) {
+            // Moves the maximum and the values' power of two: what has been summed, and
+            // the weights of this unit's first `c` columns, follow.
+            auto move = [&](float top, int c) {
                 const float mn = fmaxf(mx, top);
                 mu = mn == -INFINITY ? 0.f : mn;
                 const float a = exp2_approx(mx - mu);
@@ -701,47 +736,84 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                 l *= a;
                 const float f = a * pow2_of(max(e_o - e_new + 127, 1));
                 e_o = e_new;
+                tmem_st_wait();
+                const uint32_t a2 = cvt_f16x2(f, f);
+#pragma unroll 1
+                for (int i = 0; i < c / 2; i += 8) {
+                    uint32_t y[8];
+                    tmem_ld8(s_at + i, y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = hmul2_f16(y[j], a2);
+                    tmem_st8(s_at + i, y);
+                }
+                bool ok = true;
                 if (k > 0) {
                     // the sums so far, once the last unit's products are in
-                    if (!warp_wait(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget)) return false;
+                    ok = warp_wait(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t x[16];
-                        tmem_ld16(o_at + c, x);
-                        tmem_ld_wait();
+                    for (int i = 0; i < D; i += 8) {
+                        uint32_t y[8];
+                        tmem_ld8(o_at + i, y);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                        tmem_st16(o_at + c, x);
+                        for (int j = 0; j < 8; ++j)
+                            y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                        tmem_st8(o_at + i, y);
                     }
-                    tmem_st_wait();
                 }
-            }
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-                uint32_t x[32], y[16];
-                tmem_ld32(s_at + c, x);
-                const float f = unit * pow2_of(km.e[c / PT] + 1);
-                const int de = vm.e[c / PT] - e_o;  // at most 0
-                const float off = (float)(7 + de) - mu;
-                const uint32_t bits = edge ? sees(c) : 0xFFFFFFFFu;
-                tmem_ld_wait();
-                float sum = 0.f;
+                return ok;
+            };
+            // 16 columns: weights over the scores
+            auto weigh = [&](uint32_t (&x)[16], int c) {
+                const int part = c / PT;
+                // (never zero: a query of zeros still has -inf where it sees nothing)
+                const float f = fmaxf(unit * pow2_of(km.e[part] + 1), 0x1p-126f);
+                const uint32_t bits = edge ? sees(c) : 0xFFFFu;
+                float t = -INFINITY;
+                if (edge) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float a = exp2_approx(fmaf(__uint_as_float(x[2 * i]), f, off));
-                    float b = exp2_approx(fmaf(__uint_as_float(x[2 * i + 1]), f, off));
-                    if (edge) {
-                        a = (bits >> (2 * i)) & 1u ? a : 0.f;
-                        b = (bits >> (2 * i + 1)) & 1u ? b : 0.f;
-                    }
-                    sum += a + b;
+                    for (int i = 0; i < 16; ++i)
+                        if (!((bits >> i) & 1u)) x[i] = 0xFF800000u;  // -inf
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i += 2)
+                    t = fmaxf(t, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+                if (__any_sync(0xFFFFFFFFu, t * f > mx + 8.f) || e_new > e_o) {
+                    if (!move(t * f, c)) return false;
+                }
+                const int de = vm.e[part] - e_o;  // at most 0
+                const float off = (float)(7 + de) - mu;
+                const uint64_t f2 = pair_of(f, f), off2 = pair_of(off, off);
+                uint64_t sum = 0;
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float a, b;
+                    parts_of(fma_pair(pair_of(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                      f2, off2), &a, &b);
+                    a = exp2_approx(a);
+                    b = exp2_approx(b);
+                    sum = i ? add_pair(sum, pair_of(a, b)) : pair_of(a, b);
                     y[i] = cvt_f16x2(a, b);
                 }
-                l = fmaf(sum, pow2_of(min(127 - de, 254)), l);
-                tmem_st16(s_at + c / 2, y);
+                float a, b;
+                parts_of(sum, &a, &b);
+                l = fmaf(a + b, pow2_of(min(127 - de, 254)), l);
+                tmem_st8(s_at + c / 2, y);
+                return true;
+            };
+            bool ok = true;
+            tmem_ld_wait_of(xa);
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+                tmem_ld16(s_at + c + 16, xb);
+                ok = weigh(xa, c) && ok;
+                tmem_ld_wait_of(xb);
+                if (c + 32 < kTile) tmem_ld16(s_at + c + 32, xa);
+                ok = weigh(xb, c + 16) && ok;
+                tmem_ld_wait_of(xa);
             }
+            if (!ok) return false;
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sh.p_full[m]);
@@ -812,11 +884,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPieceRing; ++i) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], 5 * SH::MT + 5);
+            mbar_init(&sh.piece_empty[i], 5 * SH::MT + 9);
         }
         for (int i = 0; i < SH::kSlots; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 4);
+            mbar_init(&sh.empty[i], SH::PT / 32);
+            sh.part_unit[i] = -1;
         }
         for (int i = 0; i < SH::KB; ++i) {
             mbar_init(&sh.k_full[i], 4);
@@ -834,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         mbar_init(&sh.s_full[1], 1);
         mbar_init_fence();
     }
-    if (warp == 15) {
+    if (warp == 19) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
@@ -846,25 +919,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     bool ok = true;
     if (warp < 4 * SH::MT) {
         ok = softmax<D, G>(p, sh, qbuf, tmem, warp / 4, warp % 4, lane);
-    } else if (warp >= 8 && warp < 12) {
+    } else if (warp >= 8 && warp < 16) {
         ok = convert<D, G>(p, sh, ring_ptr, kbuf, vbuf, warp - 8, lane);
-    } else if (warp >= 12 && warp < 12 + SH::MT) {
-        ok = issue_products<D, G>(p, sh, qbuf, kbuf, vbuf, tmem, warp - 12, lane);
+    } else if (warp >= 16 && warp < 16 + SH::MT) {
+        ok = issue_products<D, G>(p, sh, qbuf, kbuf, vbuf, tmem, warp - 16, lane);
         __syncwarp();
         // no instruction may still be running when the CTA lets its memory go
-        if (elect_one()) umma_commit(&sh.drained[warp - 12]);
+        if (elect_one()) umma_commit(&sh.drained[warp - 16]);
         __syncwarp();
-        ok = warp_wait(&sh.drained[warp - 12], 0, kWaitBudgetCycles) && ok;
-    } else if (warp == 14) {
+        ok = warp_wait(&sh.drained[warp - 16], 0, kWaitBudgetCycles) && ok;
+    } else if (warp == 18) {
         ok = copy_parts<D, G>(p, sh, ring, lane);
-    } else if (warp == 15) {
+    } else if (warp == 19) {
         if (lane == 0) ok = list_pieces<D, G>(p, sh);
     }
     if (!ok) flag_status(p.status, MXQ_DEV_TIMEOUT);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 15) {
+    if (warp == 19) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

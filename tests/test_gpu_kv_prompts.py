@@ -30,3 +30,22 @@ def test_many_query_heads_in_a_prompt():
 def test_sixteen_rows_with_window(window, sinks):
     ctx = [16, 17, 90, 80, 400]
     Case(ctx, [16] * 5, 4, 2, 128, 64, 16, seed=16 + window).check(window, sinks)
+
+
+def test_queries_of_zeros():
+    # every visible key weighs the same, also for the first rows, which see little
+    import numpy as np
+
+    for rows in (1, 90):
+        c = Case([90], [rows], 2, 1, 128, 64, 16, seed=21)
+        c.q[:] = 0
+        c.q_d.zero_()
+        for window in (0, 5):
+            c.check(window=window)
+    c = Case([90], [90], 2, 1, 128, 64, 16, seed=22)
+    k = np.asarray(c.cache.k[:, :, :], dtype=np.float32) * np.float32(2.0 ** -90)
+    c.cache.write(np.arange(c.cache.n_pages * 16), k, np.asarray(c.cache.v, dtype=np.float32))
+    import torch
+
+    c.pages_d = torch.from_numpy(c.cache.bytes).cuda()
+    c.check()
