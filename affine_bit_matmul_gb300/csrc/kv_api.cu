@@ -278,14 +278,17 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     p.ctas = a.ctas;
     p.segs = reinterpret_cast<int*>(ws);
     p.partial = reinterpret_cast<float*>(ws + a.seg_bytes);
-    if (mxq::launch_kv_attn(p, D, group_size, a.tile_rows, s) != cudaSuccess) return MXQ_ERR_CUDA;
+    // where the others' rows cannot make up the total, every sequence has many
+    const bool all_many = T - (long long)(S - 1) * max_q_len > a.tile_toks;
+    if (!all_many && mxq::launch_kv_attn(p, D, group_size, a.tile_rows, s) != cudaSuccess)
+        return MXQ_ERR_CUDA;
     if (!a.many) return MXQ_OK;
     ws += a.few_bytes;
     p.head_parts = a.many_parts;
     p.part_heads = a.many_heads;
     p.tile_toks = a.many_toks;
     p.half_toks = a.half_toks;
-    p.min_rows = a.tile_toks + 1;
+    p.min_rows = all_many ? 0 : a.tile_toks + 1;
     p.max_rows = kMaxInt;
     p.ctas = a.many_ctas;
     p.max_entries = a.max_entries;

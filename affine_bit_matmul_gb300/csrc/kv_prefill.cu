@@ -2,23 +2,23 @@
 // key/value cache, on the 5th-generation tensor cores.
 //
 // The formulas are kv_attention.cu's; here keys and values become f16 numbers,
-// s q + b rounded once (11 bits), scaled by a power of two for each part of a
-// tile (64 or 32 tokens) that keeps them below one, and so do the queries (a
+// s q + b rounded once (11 bits), scaled by a power of two for each 32 tokens that
+// keeps them below one, and so do the queries (a
 // power of two for each row, exact) and the weights P (11 bits).  Products are
 // summed in fp32 in tensor memory; scores, maxima and sums are fp32.
 //
 // A row tile is up to 256 rows (128 for D = 256): all query heads of one
 // key/value head at 128 / heads tokens, once or twice.  A unit is (row tile,
 // 128 tokens); the units of all row tiles, in order, are cut into equal runs,
-// one per SM, as for few rows.  Roles of a CTA's 20 warps:
+// one per SM, as for few rows.  Roles of a CTA's 19 warps:
 //   0-3, 4-7  softmax of the first and second 128 rows, one row a thread:
 //             scores from tensor memory, maximum, weights back into tensor
 //             memory over the scores, and the output at the end
 //   8-15      codes -> f16 operands in shared memory (128-byte swizzle; keys
-//             along the values, values along the tokens), 32 tokens a warp
+//             along the values, values along the tokens): 32 tokens of the keys or
+//             of the values of a unit each, loaded a unit ahead into registers
 //   16, 17    the matrix instructions of one half each: Q K^T, then P V
-//   18        copies of page parts into a ring
-//   19        the list of the run's pieces; tensor memory
+//   18        the list of the run's pieces; tensor memory
 // The two halves are independent chains (scores, weights, sum), so one half's
 // products run while the other half's softmax does.  For D = 256 there is one
 // half with two score buffers instead.  The running maximum is only moved when
@@ -36,25 +36,21 @@ namespace mxq {
 namespace {
 
 constexpr int kTile = 128;           // tokens of a unit
-constexpr int kThreads = 640;
+constexpr int kThreads = 608;
 constexpr int kPieceRing = 8;
 constexpr int kMetaRing = 4;
+constexpr int kPart = 32;            // tokens that share a power of two
+constexpr int kParts = kTile / kPart;
 
 template <int D, int G>
 struct Shape {
     static constexpr int MT = D == 256 ? 1 : 2;    // halves of 128 rows
     static constexpr int SB = D == 256 ? 2 : 1;    // score buffers of a half
     static constexpr int KB = D == 256 ? 1 : 2;    // key and value buffers
-    static constexpr int PT = D == 256 ? 32 : 64;  // tokens of a part
-    static constexpr int NP = kTile / PT;
     static constexpr int kRows = 128 * MT;
-    static constexpr int kPartBytes = kv_block_bytes(D, G, PT) / 2;  // of keys or of values
     static constexpr int kQBytes = kRows * D * 2;
     static constexpr int kOpBytes = kTile * D * 2;
-    static constexpr int kFixed = kQBytes + 2 * KB * kOpBytes;
-    static constexpr int kRoom = (232448 - 1024 - 3072 - kFixed) / kPartBytes;
-    static constexpr int kSlots = kRoom < 12 ? kRoom : 12;
-    static constexpr int kSmem = 1024 + kFixed + kSlots * kPartBytes;
+    static constexpr int kSmem = 1024 + kQBytes + 2 * KB * kOpBytes;
     static constexpr int kPartialFloats = kRows * (D + 2);
 };
 
@@ -68,8 +64,8 @@ struct Entry {
 };
 
 struct Meta {
-    int state[4];  // of each part, bit i: tokens 16 i .. of it exist
-    int e[4];      // biased exponents of the parts: values are below 2^(e - 126)
+    int state[kParts];  // bit i: tokens 16 i .. of the part exist
+    int e[kParts];      // biased exponents: the part's values are below 2^(e - 126)
 };
 
 __device__ __forceinline__ int unit_token(const Piece& q, int k) {
@@ -170,12 +166,10 @@ template <int D, int G>
 struct Shared {
     using SH = Shape<D, G>;
     uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
-    uint64_t full[SH::kSlots], empty[SH::kSlots];
     uint64_t k_full[SH::KB], k_empty[SH::KB], v_full[SH::KB], v_empty[SH::KB];
     uint64_t q_full[SH::MT], s_full[2], p_full[SH::MT], pv_done[SH::MT], drained[SH::MT];
     Piece pieces[kPieceRing];
     Meta k_meta[kMetaRing], v_meta[kMetaRing];
-    int part_unit[SH::kSlots], part_t0[SH::kSlots], part_state[SH::kSlots];
     uint32_t tmem;
 };
 
@@ -203,6 +197,7 @@ struct Pieces {
 
 template <int D, int G>
 __device__ bool list_pieces(const KvAttnParams& p, Shared<D, G>& sh) {
+    pdl_wait();  // for the plan
     const Entry* entries = reinterpret_cast<const Entry*>(p.entries);
     const int* before = p.before;
     const int n_entries = p.counts[0];
@@ -278,261 +273,191 @@ __device__ bool list_pieces(const KvAttnParams& p, Shared<D, G>& sh) {
     }
 }
 
-// ---------------------------------------------------------------- copies
-
-// One warp.  The parts of a unit go into the ring in the order in which they are
-// converted: its keys, then its values.  Lane (part, i) looks after page i of
-// that part, or region i (codes, pairs) of its share of a longer page.
-template <int D, int G>
-__device__ bool copy_parts(const KvAttnParams& p, Shared<D, G>& sh, uint32_t ring, int lane) {
-    using SH = Shape<D, G>;
-    constexpr int PT = SH::PT, NP = SH::NP, NS = SH::kSlots;
-    const int page = p.page_size, size = min(page, PT);
-    const int each = page <= PT ? PT / page : 2;      // copies of a part
-    const int part = lane / each, i = lane % each;    // part: keys 0 .. NP - 1, then values
-    const long long block = kv_block_bytes(D, G, page);
-    const uint32_t bytes = page <= PT ? (uint32_t)(block / 2)
-                                      : (uint32_t)(i ? kv_pair_bytes(D, G, PT) : kv_code_bytes(D, PT));
-    const uint32_t dst = page <= PT ? i * (uint32_t)(block / 2) : i * (uint32_t)kv_code_bytes(D, PT);
-    const long long half = part >= NP ? block / 2 : 0;
-    Pieces<D, G> list(sh, p.wait_budget);
-    long long unit = 0;
-    bool ok = true;
-    while (ok) {
-        const Piece* q = list.next();
-        if (!q) ok = false;
-        if (!q || q->count == 0) break;
-        const int p1 = q->p0 + q->toks - 1;
-        const int32_t* row = p.table + (long long)q->s * p.max_pages;
-        for (int k = q->k0; k < q->k0 + q->count && ok; ++k) {
-            const int t0 = unit_token(*q, k);
-            const int t = t0 + (part % NP) * PT + (page <= PT ? i * page : 0);
-            int id = -2;
-            if (part < 2 * NP && t <= p1) id = __ldg(row + (t >> p.page_shift));
-            const bool good = (unsigned)id < (unsigned)p.n_pages;
-            if (!good && id != -2 && part < NP) {
-                const int te = min(t + size - 1, p1);  // a page that some row sees has to exist
-                if (!p.window || te > q->p0 - p.window || t < p.sinks)
-                    flag_status(p.status, MXQ_DEV_BAD_PAGE);
-            }
-            const uint32_t found = __ballot_sync(0xFFFFFFFFu, good);
-            const uint8_t* src = p.pages + half;
-            if (good) {
-                src += ((long long)id * p.Hkv + q->h) * block;
-                if (page > PT) {
-                    const int skip = t & (page - 1);
-                    src += i ? kv_code_bytes(D, page) + kv_pair_bytes(D, G, skip)
-                             : kv_code_bytes(D, skip);
-                }
-            }
-#pragma unroll 1
-            for (int u = 0; u < 2 * NP; ++u) {
-                const int slot = (int)(unit % NS);
-                if (!warp_wait(&sh.empty[slot], ((uint32_t)(unit / NS) & 1u) ^ 1u, p.wait_budget)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    const uint32_t mine = (found >> (u * each)) & ((1u << each) - 1u);
-                    int state = 0;
-                    uint32_t sum = 0;
-                    if (page <= PT) {
-                        for (int j = 0; j < each; ++j)
-                            if ((mine >> j) & 1u) state |= ((1 << (size / 16)) - 1) << (j * (size / 16));
-                        sum = __popc(mine) * bytes;
-                    } else if (mine) {
-                        state = (1 << (PT / 16)) - 1;
-                        sum = SH::kPartBytes;
-                    }
-                    sh.part_t0[slot] = t0 + (u % NP) * PT;
-                    sh.part_state[slot] = state;
-                    *const_cast<volatile int*>(&sh.part_unit[slot]) = (int)unit;
-                    mbar_expect_tx(&sh.full[slot], sum);
-                }
-                __syncwarp();
-                if (part == u && good)
-                    bulk_copy(ring + slot * SH::kPartBytes + dst, src, bytes, &sh.full[slot]);
-                ++unit;
-            }
-        }
-        list.done();
-    }
-    __syncwarp();
-    if (lane == 0 && !drain_ring(sh.full, NS, unit, NS)) ok = false;
-    return ok;
-}
-
 // ---------------------------------------------------------------- codes -> operands
 
-// Waits, within the budget, until a slot holds part `n` of the run (whole warp).
-// The warps may be a round of the ring apart, and the parity of a phase alone
-// does not tell a round from the one two before it.
-__device__ __forceinline__ bool part_comes(const int* unit, int n, long long budget) {
-    const volatile int* u = unit;
-    bool ok = true;
-    if (*u != n) {
-        const long long since = clock64();
-        while (*u != n && ok) {
-            __nanosleep(20);
-            ok = clock64() - since <= budget;
+// Warp cw of eight converts 32 tokens of the keys (0 .. 3) or of the values of
+// each unit.  Its loads run a unit ahead, the page numbers two.
+template <int D, int G>
+struct Convert {
+    using SH = Shape<D, G>;
+    static constexpr int KB = SH::KB, NG = D / G, U = D / 32;
+    const KvAttnParams& p;
+    Shared<D, G>& sh;
+    const int lane, part;
+    const bool kv;
+    // where the page numbers are looked up: unit at_k of piece at_n
+    int at_n, at_k;
+    bool at_end;
+    // looked up: pages of the 32 tokens' halves; -2: not needed
+    int id[2], look_t, look_p0, look_p1, look_h;
+    // loaded
+    uint32_t w[4][U], pr[NG];
+    int t0, p0, p1, state;
+
+    __device__ Convert(const KvAttnParams& p_, Shared<D, G>& sh_, int cw, int lane_)
+        : p(p_), sh(sh_), lane(lane_), part(cw % kParts), kv(cw >= kParts), at_n(0), at_k(-1),
+          at_end(false) {}
+
+    __device__ bool look() {
+        if (at_end) return true;
+        ++at_k;
+        if (at_k == 0 || at_k == sh.pieces[at_n % kPieceRing].count) {
+            if (at_k) ++at_n;
+            at_k = 0;
+            if (!warp_wait(&sh.piece_full[at_n % kPieceRing], (uint32_t)(at_n / kPieceRing) & 1u,
+                           p.wait_budget))
+                return false;
+        }
+        const Piece& q = sh.pieces[at_n % kPieceRing];
+        if (q.count == 0) {
+            at_end = true;
+            return true;
+        }
+        look_t = unit_token(q, q.k0 + at_k) + part * kPart;
+        look_p0 = q.p0;
+        look_p1 = q.p0 + q.toks - 1;
+        look_h = q.h;
+        const int32_t* row = p.table + (long long)q.s * p.max_pages;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = look_t + 16 * i;
+            id[i] = t <= look_p1 ? __ldg(row + (t >> p.page_shift)) : -2;
+        }
+        return true;
+    }
+    __device__ void load() {
+        t0 = look_t;
+        p0 = look_p0;
+        p1 = look_p1;
+        state = 0;
+        const int size = p.page_size;
+        const int half = kv_block_bytes(D, G, size) / 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 16 * i;
+            if ((unsigned)id[i] < (unsigned)p.n_pages) {
+                state |= 1 << i;
+                const uint8_t* src = p.pages + ((long long)id[i] * p.Hkv + look_h) * (2LL * half) +
+                                     (kv ? half : 0);
+                const int skip = t & (size - 1);
+                const uint8_t* codes = src + kv_code_bytes(D, skip) + lane * (D == 64 ? 8 : 16);
+                load_words<U>(codes, w[2 * i]);
+                load_words<U>(codes + 4 * D, w[2 * i + 1]);
+                // lane i's pairs are those of token t0 + i
+                if (lane / 16 == i)
+                    load_pairs<NG>(src + kv_code_bytes(D, size) + (skip + lane % 16) * (NG * 4), pr);
+            } else if (id[i] != -2 && !kv) {
+                // a page that some row sees has to exist
+                const int te = min(t + 15, p1);
+                if (!p.window || te > p0 - p.window || t < p.sinks)
+                    flag_status(p.status, MXQ_DEV_BAD_PAGE);
+            }
         }
     }
-    return __all_sync(0xFFFFFFFFu, ok);
-}
-
-// Warp cw of eight converts 32 tokens of the keys or of the values of each unit.
-template <int D, int G>
-__device__ bool convert(const KvAttnParams& p, Shared<D, G>& sh, const uint8_t* ring, uint32_t kbuf,
-                        uint32_t vbuf, int cw, int lane) {
-    using SH = Shape<D, G>;
-    constexpr int PT = SH::PT, NP = SH::NP, NS = SH::kSlots, KB = SH::KB;
-    constexpr int NG = D / G, U = D / 32;
-    constexpr int kShare = PT / 32;                  // warps of a part
-    const int r = lane >> 2, i4 = lane & 3;
-    const bool kv = cw / kShare >= NP;               // values
-    const int part = cw / kShare % NP, first = cw % kShare * 32;
-    const int size = min(p.page_size, PT);
-    const int whole = kv_code_bytes(D, size) + kv_pair_bytes(D, G, size);
-    Pieces<D, G> list(sh, p.wait_budget);
-    int jt = 0;
-    for (;;) {
-        const Piece* q = list.next();
-        if (!q) return false;
-        if (q->count == 0) return true;
-        const int p0 = q->p0, p1 = p0 + q->toks - 1;
-        for (int k = 0; k < q->count; ++k, ++jt) {
-            const int buf = jt % KB;
-            const uint32_t out = (kv ? vbuf : kbuf) + buf * SH::kOpBytes;
-            Meta& meta = kv ? sh.v_meta[jt % kMetaRing] : sh.k_meta[jt % kMetaRing];
-            const int unit = jt * 2 * NP + cw / kShare, slot = unit % NS;
-            if (!part_comes(&sh.part_unit[slot], unit, p.wait_budget) ||
-                !warp_wait(&sh.full[slot], (uint32_t)(unit / NS) & 1u, p.wait_budget))
-                return false;
-            const uint8_t* at = ring + slot * SH::kPartBytes;
-            const int t0 = sh.part_t0[slot], state = sh.part_state[slot];
-            // some token of the part is seen by no row: what it holds is not used
-            const bool edge = state != (1 << (PT / 16)) - 1 || t0 + PT - 1 > p1 ||
-                              (p.window && t0 <= p0 - p.window && t0 + PT > p.sinks);
-            auto unseen = [&](int t) {
-                return !((state >> (t / 16)) & 1) || t0 + t > p1 ||
-                       (p.window && t0 + t <= p0 - p.window && t0 + t >= p.sinks);
-            };
-            auto pairs_of = [&](int t) {
-                return at + t / size * whole + kv_code_bytes(D, size) + t % size * (NG * 4);
-            };
-            // a power of two above every |s q + b| of the part
-            uint32_t big = 0;
+    // The loaded unit into operand buffer `out`; its power of two.
+    __device__ int scale_bits() {
+        const int t = t0 + lane;
+        // what no row sees may hold anything
+        if (!((state >> (lane / 16)) & 1) || t > p1 ||
+            (p.window && t <= p0 - p.window && t >= p.sinks)) {
 #pragma unroll
-            for (int j = 0; j < PT / 32; ++j) {
-                const int t = lane + 32 * j;
-                uint32_t w[NG];
-                load_pairs<NG>(pairs_of(t), w);
-                const uint32_t keep = edge && unseen(t) ? 0u : 0x7FFF7FFFu;
+            for (int g = 0; g < NG; ++g) pr[g] = 0u;
+        }
+        uint32_t big = 0;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) big = max_u16x2(big, w[g] & keep);
+        for (int g = 0; g < NG; ++g) big = max_u16x2(big, pr[g] & 0x7FFF7FFFu);
+        const int es = (int)(__reduce_max_sync(0xFFFFFFFFu, big & 0xFFFFu) >> 7) + 4;
+        const int eb = (int)(__reduce_max_sync(0xFFFFFFFFu, big >> 16) >> 7);
+        return min(max(max(es, eb) + 1, 30), 250);
+    }
+    __device__ void store(uint32_t out, int e) {
+        const int r = lane >> 2, i4 = lane & 3;
+        const float dn = pow2_of(253 - e);  // 2^(126 - e)
+        // each lane's own token as f16 pairs (scale, bias)
+        uint32_t sb[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            sb[g] = cvt_f16x2(__uint_as_float(pr[g] << 16) * dn,
+                              __uint_as_float(pr[g] & 0xFFFF0000u) * dn);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // 8 tokens at a time
+            if (!kv) {
+                uint32_t s2[NG], b2[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const uint32_t x = __shfl_sync(0xFFFFFFFFu, sb[g], 8 * j + r);
+                    s2[g] = prmt(x, x, 0x1010u);
+                    b2[g] = prmt(x, x, 0x3232u);
+                }
+                const uint32_t row = out + (part * kPart + 8 * j + r) * 128;
+                // odd tokens take the words of a pair in the other order: their
+                // stores would meet the even ones' in the same banks
+                const bool odd = r & 1;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t word = odd ? w[j][u ^ 1] : w[j][u];
+                    const int g0 = u * 32 / G, g1 = (u ^ 1) * 32 / G;
+                    uint32_t x[4];
+                    dequant_word(word, g0 == g1 || !odd ? s2[g0] : s2[g1],
+                                 g0 == g1 || !odd ? b2[g0] : b2[g1], x);
+                    // values 32 u' + 8 i4 ..: 16 bytes of the token's row
+                    const int chunk = (((u & 1) ^ (r & 1)) * 4 + i4) ^ r;
+                    sts128(row + (u / 2) * (kTile * 128) + chunk * 16, x[0], x[1], x[2], x[3]);
+                }
+            } else {
+                // values 32 u + r + 8 n of tokens 2 i4 and 2 i4 + 1
+                const int tt = part * kPart + 8 * j;
+                const uint32_t row = out + (tt / 64) * (D * 128) + r * 128 +
+                                     ((((tt % 64) / 8) ^ r) * 16) + i4 * 4;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const uint32_t a = __shfl_sync(0xFFFFFFFFu, sb[g], 8 * j + 2 * i4);
+                    const uint32_t c = __shfl_sync(0xFFFFFFFFu, sb[g], 8 * j + 2 * i4 + 1);
+                    const uint32_t s2 = prmt(a, c, 0x5410u), b2 = prmt(a, c, 0x7632u);
+#pragma unroll
+                    for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
+                        uint32_t x[4];
+                        dequant_word(w[j][u], s2, b2, x);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) sts32(row + (32 * u + 8 * n) * 128, x[n]);
+                    }
+                }
             }
-            const int es = (int)(__reduce_max_sync(0xFFFFFFFFu, big & 0xFFFFu) >> 7) + 4;
-            const int eb = (int)(__reduce_max_sync(0xFFFFFFFFu, big >> 16) >> 7);
-            const int e = min(max(max(es, eb) + 1, 30), 250);
-            const float dn = pow2_of(253 - e);  // 2^(126 - e)
+        }
+    }
+    __device__ bool run(uint32_t kbuf, uint32_t vbuf) {
+        if (!look()) return false;
+        if (!at_end) load();
+        bool more = !at_end;
+        if (!look()) return false;
+        int n = 0, left = 0;  // piece of the loaded unit, its units left
+        for (int jt = 0; more; ++jt) {
+            if (left == 0) left = sh.pieces[n % kPieceRing].count;
+            const int buf = jt % KB;
+            const int e = scale_bits(), here = state;
             if (!warp_wait(kv ? &sh.v_empty[buf] : &sh.k_empty[buf], ((uint32_t)(jt / KB) & 1u) ^ 1u,
                            p.wait_budget))
                 return false;
-            // 8 tokens at a time
-            const uint8_t* base = at + first / size * whole + kv_code_bytes(D, first % size) +
-                                  lane * (D == 64 ? 8 : 16);
-            const int next16 = size == 16 ? whole : kv_code_bytes(D, 16);  // codes 16 tokens on
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int tb = first + 8 * j;
-                uint32_t w[U];
-                load_words<U>(base + (j / 2) * next16 + (j % 2) * (4 * D), w);
-                const int tt = part * PT + tb;  // token within the unit
-                if (!kv) {
-                    uint32_t pr[NG];
-                    load_pairs<NG>(pairs_of(tb + r), pr);
-                    if (edge && unseen(tb + r)) {
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) pr[g] = 0u;
-                    }
-                    // odd tokens take the words of a pair in the other order: their
-                    // stores would meet the even ones' in the same banks
-                    const bool odd = r & 1;
-#pragma unroll
-                    for (int u = 0; u < U; u += 2) {
-                        const uint32_t a = w[u], b = w[u + 1];
-                        w[u] = odd ? b : a;
-                        w[u + 1] = odd ? a : b;
-                    }
-                    if (G == 32) {
-#pragma unroll
-                        for (int g = 0; g < NG; g += 2) {
-                            const uint32_t a = pr[g], b = pr[g + 1];
-                            pr[g] = odd ? b : a;
-                            pr[g + 1] = odd ? a : b;
-                        }
-                    }
-                    uint32_t s2[NG], b2[NG];
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const float s = __uint_as_float(pr[g] << 16) * dn;
-                        const float b = __uint_as_float(pr[g] & 0xFFFF0000u) * dn;
-                        s2[g] = cvt_f16x2(s, s);
-                        b2[g] = cvt_f16x2(b, b);
-                    }
-                    const uint32_t row = out + (tt + r) * 128;
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        uint32_t x[4];
-                        dequant_word(w[u], s2[u * 32 / G], b2[u * 32 / G], x);
-                        // values 32 u' + 8 i4 ..: 16 bytes of row tt + r
-                        const int chunk = (((u & 1) ^ (r & 1)) * 4 + i4) ^ r;
-                        sts128(row + (u / 2) * (kTile * 128) + chunk * 16, x[0], x[1], x[2], x[3]);
-                    }
-                } else {
-                    uint32_t pa[NG], pc[NG];
-                    load_pairs<NG>(pairs_of(tb + 2 * i4), pa);
-                    load_pairs<NG>(pairs_of(tb + 2 * i4 + 1), pc);
-                    if (edge) {
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            if (unseen(tb + 2 * i4)) pa[g] = 0u;
-                            if (unseen(tb + 2 * i4 + 1)) pc[g] = 0u;
-                        }
-                    }
-                    // values 32 u + r + 8 n of tokens 2 i4 and 2 i4 + 1
-                    const uint32_t row = out + (tt / 64) * (D * 128) + r * 128 +
-                                         ((((tt % 64) / 8) ^ r) * 16) + i4 * 4;
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const uint32_t s2 = cvt_f16x2(__uint_as_float(pa[g] << 16) * dn,
-                                                      __uint_as_float(pc[g] << 16) * dn);
-                        const uint32_t b2 = cvt_f16x2(__uint_as_float(pa[g] & 0xFFFF0000u) * dn,
-                                                      __uint_as_float(pc[g] & 0xFFFF0000u) * dn);
-#pragma unroll
-                        for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
-                            uint32_t x[4];
-                            dequant_word(w[u], s2, b2, x);
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) sts32(row + (32 * u + 8 * n) * 128, x[n]);
-                        }
-                    }
-                }
-            }
-            if (lane == 0 && first == 0) {
+            store((kv ? vbuf : kbuf) + buf * SH::kOpBytes, e);
+            if (lane == 0) {
+                Meta& meta = kv ? sh.v_meta[jt % kMetaRing] : sh.k_meta[jt % kMetaRing];
                 meta.e[part] = e;
-                meta.state[part] = state;
+                meta.state[part] = here;
             }
             fence_proxy_async_smem();  // the tensor cores read what was written
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.empty[slot]);
-                mbar_arrive(kv ? &sh.v_full[buf] : &sh.k_full[buf]);
+            if (lane == 0) mbar_arrive(kv ? &sh.v_full[buf] : &sh.k_full[buf]);
+            more = !at_end;
+            if (more) load();
+            if (--left == 0) {
+                if (lane == 0) mbar_arrive(&sh.piece_empty[n % kPieceRing]);
+                ++n;
             }
+            if (more && !look()) return false;
         }
-        list.done();
+        return true;
     }
-}
+};
 
 // ---------------------------------------------------------------- matrix instructions
 
@@ -631,7 +556,7 @@ template <int D, int G>
 __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tmem, int m,
                         int quarter, int lane) {
     using SH = Shape<D, G>;
-    constexpr int KB = SH::KB, SB = SH::SB, PT = SH::PT;
+    constexpr int KB = SH::KB, SB = SH::SB;
     const int lr = quarter * 32 + lane;                 // row of the half
     const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
     const uint32_t o_at = tmem + t_lane + 256 + m * D;
@@ -705,7 +630,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
             const volatile Meta& vm = sh.v_meta[jt % kMetaRing];
             int state = 0;
 #pragma unroll
-            for (int i = 0; i < SH::NP; ++i) state |= km.state[i] << (i * (PT / 16));
+            for (int i = 0; i < kParts; ++i) state |= km.state[i] << (i * (kPart / 16));
             const int t0 = unit_token(*q, q->k0 + k);
             const bool edge = state != 0xFF || t0 + kTile - 1 > first ||
                               (p.window && t0 <= last - p.window && t0 + kTile > p.sinks);
@@ -725,7 +650,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
             if (!warp_wait(&sh.v_full[jt % KB], (uint32_t)(jt / KB) & 1u, p.wait_budget)) return false;
             int e_new = e_o;
 #pragma unroll
-            for (int i = 0; i < SH::NP; ++i) e_new = max(e_new, vm.e[i]);
+            for (int i = 0; i < kParts; ++i) e_new = max(e_new, vm.e[i]);
             // Moves the maximum and the values' power of two: what has been summed, and
             // the weights of this unit's first `c` columns, follow.
             auto move = [&](float top, int c) {
@@ -765,7 +690,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
             };
             // 16 columns: weights over the scores
             auto weigh = [&](uint32_t (&x)[16], int c) {
-                const int part = c / PT;
+                const int part = c / kPart;
                 // (never zero: a query of zeros still has -inf where it sees nothing)
                 const float f = fmaxf(unit * pow2_of(km.e[part] + 1), 0x1p-126f);
                 const uint32_t bits = edge ? sees(c) : 0xFFFFu;
@@ -877,19 +802,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     __shared__ Shared<D, G> sh;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t qbuf = base, kbuf = qbuf + SH::kQBytes, vbuf = kbuf + SH::KB * SH::kOpBytes;
-    const uint32_t ring = vbuf + SH::KB * SH::kOpBytes;
-    const uint8_t* ring_ptr = raw + (ring - smem_u32(raw));
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPieceRing; ++i) {
             mbar_init(&sh.piece_full[i], 1);
-            mbar_init(&sh.piece_empty[i], 5 * SH::MT + 9);
-        }
-        for (int i = 0; i < SH::kSlots; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], SH::PT / 32);
-            sh.part_unit[i] = -1;
+            mbar_init(&sh.piece_empty[i], 5 * SH::MT + 8);
         }
         for (int i = 0; i < SH::KB; ++i) {
             mbar_init(&sh.k_full[i], 4);
@@ -907,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         mbar_init(&sh.s_full[1], 1);
         mbar_init_fence();
     }
-    if (warp == 19) {
+    if (warp == 18) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
@@ -920,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     if (warp < 4 * SH::MT) {
         ok = softmax<D, G>(p, sh, qbuf, tmem, warp / 4, warp % 4, lane);
     } else if (warp >= 8 && warp < 16) {
-        ok = convert<D, G>(p, sh, ring_ptr, kbuf, vbuf, warp - 8, lane);
+        ok = Convert<D, G>(p, sh, warp - 8, lane).run(kbuf, vbuf);
     } else if (warp >= 16 && warp < 16 + SH::MT) {
         ok = issue_products<D, G>(p, sh, qbuf, kbuf, vbuf, tmem, warp - 16, lane);
         __syncwarp();
@@ -929,15 +847,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         __syncwarp();
         ok = warp_wait(&sh.drained[warp - 16], 0, kWaitBudgetCycles) && ok;
     } else if (warp == 18) {
-        ok = copy_parts<D, G>(p, sh, ring, lane);
-    } else if (warp == 19) {
         if (lane == 0) ok = list_pieces<D, G>(p, sh);
     }
     if (!ok) flag_status(p.status, MXQ_DEV_TIMEOUT);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 19) {
+    if (warp == 18) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -970,6 +886,7 @@ __device__ int block_scan(int x, int* total) {  // exclusive; 1024 threads
 
 // The row tiles of all sequences and the units before each: one block.
 __global__ void __launch_bounds__(1024) kv_plan_kernel(const KvAttnParams p) {
+    pdl_launch_dependents();
     Entry* entries = reinterpret_cast<Entry*>(p.entries);
     int* starts = p.seq_tiles;  // first row tile of each sequence
     int run = 0;
@@ -1091,18 +1008,22 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     kv_plan_kernel<<<1, 1024, 0, stream>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    kv_prefill_kernel<D, G><<<p.ctas, kThreads, SH::kSmem, stream>>>(p);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.ctas, 16);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
+    // each kernel's blocks are placed while the one before it finishes
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = SH::kSmem;
+    cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D, G>, p);
+    if (err != cudaSuccess) return err;
+    cfg.gridDim = dim3((unsigned)p.ctas, 16);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, kv_join_rows_kernel<D>, p, (int)SH::kRows);
 }
 
