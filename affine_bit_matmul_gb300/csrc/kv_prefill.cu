@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <type_traits>
 
 #include "kv_attn_common.cuh"
 
@@ -63,9 +64,10 @@ struct Entry {
     int s, row0, toks, p0, tiles, head_tiles, tail, pad;
 };
 
+// Of each part of a unit, one byte: the biased exponent e of the keys' and of the
+// values' power of two (they are below 2^(e - 126)), and which 16 tokens exist.
 struct Meta {
-    int state[kParts];  // bit i: tokens 16 i .. of the part exist
-    int e[kParts];      // biased exponents: the part's values are below 2^(e - 126)
+    uint8_t k_exp[kParts], v_exp[kParts], there[kParts];
 };
 
 __device__ __forceinline__ int unit_token(const Piece& q, int k) {
@@ -169,7 +171,7 @@ struct Shared {
     uint64_t k_full[SH::KB], k_empty[SH::KB], v_full[SH::KB], v_empty[SH::KB];
     uint64_t q_full[SH::MT], s_full[2], p_full[SH::MT], pv_done[SH::MT], drained[SH::MT];
     Piece pieces[kPieceRing];
-    Meta k_meta[kMetaRing], v_meta[kMetaRing];
+    Meta meta[kMetaRing];
     uint32_t tmem;
 };
 
@@ -182,7 +184,7 @@ struct Pieces {
     __device__ Pieces(Shared<D, G>& s, long long b) : sh(s), budget(b), n(0) {}
     // The next piece; null when a wait gave up.  count == 0: no more.
     __device__ const Piece* next() {
-        if (!warp_wait(&sh.piece_full[n % kPieceRing], (uint32_t)(n / kPieceRing) & 1u, budget))
+        if (!warp_wait_sleep(&sh.piece_full[n % kPieceRing], (uint32_t)(n / kPieceRing) & 1u, budget))
             return nullptr;
         return &sh.pieces[n % kPieceRing];
     }
@@ -229,7 +231,7 @@ __device__ bool list_pieces(const KvAttnParams& p, Shared<D, G>& sh) {
     }
     for (int n = 0;; ++n) {
         const int slot = n % kPieceRing;
-        if (!mbar_wait(&sh.piece_empty[slot], ((uint32_t)(n / kPieceRing) & 1u) ^ 1u, p.wait_budget))
+        if (!mbar_wait_sleep(&sh.piece_empty[slot], ((uint32_t)(n / kPieceRing) & 1u) ^ 1u, p.wait_budget))
             return false;
         Piece q{};
         if (left > 0) {
@@ -304,7 +306,7 @@ struct Convert {
         if (at_k == 0 || at_k == sh.pieces[at_n % kPieceRing].count) {
             if (at_k) ++at_n;
             at_k = 0;
-            if (!warp_wait(&sh.piece_full[at_n % kPieceRing], (uint32_t)(at_n / kPieceRing) & 1u,
+            if (!warp_wait_sleep(&sh.piece_full[at_n % kPieceRing], (uint32_t)(at_n / kPieceRing) & 1u,
                            p.wait_budget))
                 return false;
         }
@@ -435,14 +437,14 @@ struct Convert {
             if (left == 0) left = sh.pieces[n % kPieceRing].count;
             const int buf = jt % KB;
             const int e = scale_bits(), here = state;
-            if (!warp_wait(kv ? &sh.v_empty[buf] : &sh.k_empty[buf], ((uint32_t)(jt / KB) & 1u) ^ 1u,
+            if (!warp_wait_sleep(kv ? &sh.v_empty[buf] : &sh.k_empty[buf], ((uint32_t)(jt / KB) & 1u) ^ 1u,
                            p.wait_budget))
                 return false;
             store((kv ? vbuf : kbuf) + buf * SH::kOpBytes, e);
             if (lane == 0) {
-                Meta& meta = kv ? sh.v_meta[jt % kMetaRing] : sh.k_meta[jt % kMetaRing];
-                meta.e[part] = e;
-                meta.state[part] = here;
+                Meta& meta = sh.meta[jt % kMetaRing];
+                (kv ? meta.v_exp : meta.k_exp)[part] = (uint8_t)e;
+                if (!kv) meta.there[part] = (uint8_t)here;
             }
             fence_proxy_async_smem();  // the tensor cores read what was written
             __syncwarp();
@@ -483,22 +485,22 @@ __device__ bool issue_products(const KvAttnParams& p, Shared<D, G>& sh, uint32_t
             for (int k = 0; k < count; ++k, ++jt) {
                 const int buf = jt % KB;
                 const uint32_t par = (uint32_t)(jt / KB) & 1u;
-                if (!warp_wait(&sh.k_full[buf], par, p.wait_budget)) return false;
+                if (!warp_wait_sleep(&sh.k_full[buf], par, p.wait_budget)) return false;
                 if (lane == 0) mbar_arrive(&sh.k_empty[buf]);
-                if (!warp_wait(&sh.v_full[buf], par, p.wait_budget)) return false;
+                if (!warp_wait_sleep(&sh.v_full[buf], par, p.wait_budget)) return false;
                 if (lane == 0) mbar_arrive(&sh.v_empty[buf]);
             }
             list.done();
             continue;
         }
-        if (!warp_wait(&sh.q_full[m], (uint32_t)nq & 1u, p.wait_budget)) return false;
+        if (!warp_wait_sleep(&sh.q_full[m], (uint32_t)nq & 1u, p.wait_budget)) return false;
         ++nq;
         // scores of unit k of the piece
         auto scores = [&](int k) {
             const int buf = (jt + k) % KB, a = at + k;
-            if (!warp_wait(&sh.k_full[buf], (uint32_t)((jt + k) / KB) & 1u, p.wait_budget)) return false;
+            if (!warp_wait_sleep(&sh.k_full[buf], (uint32_t)((jt + k) / KB) & 1u, p.wait_budget)) return false;
             // the buffer's earlier weights have been used
-            if (k >= SB && !warp_wait(&sh.pv_done[m], (uint32_t)(a - SB) & 1u, p.wait_budget)) return false;
+            if (k >= SB && !warp_wait_sleep(&sh.pv_done[m], (uint32_t)(a - SB) & 1u, p.wait_budget)) return false;
             tc_fence_after();
             if (elect_one()) {
                 const uint32_t s_col = tmem + (SB == 1 ? m : (a & 1)) * kTile;
@@ -525,8 +527,8 @@ __device__ bool issue_products(const KvAttnParams& p, Shared<D, G>& sh, uint32_t
                 if (!scores(k + 1)) return false;
             }
             const int buf = (jt + k) % KB, a = at + k;
-            if (!warp_wait(&sh.v_full[buf], (uint32_t)((jt + k) / KB) & 1u, p.wait_budget) ||
-                !warp_wait(&sh.p_full[m], (uint32_t)a & 1u, p.wait_budget))
+            if (!warp_wait_sleep(&sh.v_full[buf], (uint32_t)((jt + k) / KB) & 1u, p.wait_budget) ||
+                !warp_wait_sleep(&sh.p_full[m], (uint32_t)a & 1u, p.wait_budget))
                 return false;
             tc_fence_after();
             if (elect_one()) {
@@ -579,39 +581,56 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
         const int row = q->row0 + tok0 + tok;
         const int first = q->p0 + tok0, last = first + toks - 1;  // positions of the half
         const int pos = in ? first + tok : -1;
-        // ---- this thread's query row: f16, its largest value 2^13 .. 2^14
+        // ---- the warp's 32 query rows, D / 8 lanes a row: f16, the largest value of each
+        // row 2^13 .. 2^14
         float unit;
         {
-            const __nv_bfloat16* src = p.q + (long long)row * p.q_row_stride +
-                                       (long long)(q->head0 + hh) * p.q_head_stride;
-            uint32_t big = 0;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (in) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-                big = max_u16x2(big, max_u16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
-                big = max_u16x2(big, max_u16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-            }
-            const int ex = max((int)(max(big & 0xFFFFu, big >> 16) >> 7), 16);
-            const float up = pow2_of(267 - ex);  // 2^(140 - ex)
-            unit = p.scale_log2 * pow2_of(ex - 13);
-            const uint32_t base = qbuf + m * (D / 64) * (128 * 128) + lr * 128;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (in) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                float x[8];
+            constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+            const int c = lane % kLanes;
+            const uint32_t base = qbuf + m * (D / 64) * (128 * 128) + (c / 8) * (128 * 128);
+            int my_ex = 16;
+            constexpr int kBatch = 8;
+            const int rows = toks * heads;
+#pragma unroll 1
+            for (int i0 = 0; i0 < kLanes; i0 += kBatch) {
+                uint4 v[kBatch];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[2 * e] = __uint_as_float(w[e] << 16) * up;
-                    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * up;
+                for (int i = 0; i < kBatch; ++i) {
+                    // (rows past the last repeat it; their scores are not used)
+                    const int at_row = min(quarter * 32 + (i0 + i) * kAtOnce + lane / kLanes, rows - 1);
+                    v[i] = __ldg(reinterpret_cast<const uint4*>(
+                                     p.q + (long long)(q->row0 + tok0 + at_row / heads) * p.q_row_stride +
+                                     (long long)(q->head0 + at_row % heads) * p.q_head_stride) +
+                                 c);
                 }
-                // in the order of a code word's pairs
-                sts128(base + (c / 8) * (128 * 128) + (((c % 8) ^ (lr % 8)) * 16),
-                       cvt_f16x2(x[0], x[4]), cvt_f16x2(x[1], x[5]), cvt_f16x2(x[2], x[6]),
-                       cvt_f16x2(x[3], x[7]));
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int at_row = quarter * 32 + (i0 + i) * kAtOnce + lane / kLanes;
+                    uint32_t big = max_u16x2(max_u16x2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                             max_u16x2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+                    big = max(big & 0xFFFFu, big >> 16);
+#pragma unroll
+                    for (int o = 1; o < kLanes; o <<= 1)
+                        big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+                    const int ex = max((int)(big >> 7), 16);
+                    // the lane whose row this is keeps the exponent
+                    const int mine = __shfl_sync(0xFFFFFFFFu, ex, lane % kAtOnce * kLanes);
+                    if (lane / kAtOnce == i0 + i) my_ex = mine;
+                    const float up = pow2_of(267 - ex);  // 2^(140 - ex)
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[2 * e] = __uint_as_float(w[e] << 16) * up;
+                        x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u) * up;
+                    }
+                    // in the order of a code word's pairs
+                    sts128(base + at_row * 128 + (((c % 8) ^ (at_row % 8)) * 16),
+                           cvt_f16x2(x[0], x[4]), cvt_f16x2(x[1], x[5]), cvt_f16x2(x[2], x[6]),
+                           cvt_f16x2(x[3], x[7]));
+                }
             }
+            unit = p.scale_log2 * pow2_of(my_ex - 13);
         }
         fence_proxy_async_smem();
         tc_fence_before();  // (the last piece's output has been read)
@@ -621,16 +640,17 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
         int e_o = 30;  // the output's sums are of values over 2^(e_o - 126)
         for (int k = 0; k < count; ++k, ++jt, ++at) {
             const int sidx = SB == 1 ? m : (at & 1);
-            if (!warp_wait(&sh.s_full[sidx], (uint32_t)(at / SB) & 1u, p.wait_budget)) return false;
+            if (!warp_wait_sleep(&sh.s_full[sidx], (uint32_t)(at / SB) & 1u, p.wait_budget)) return false;
             tc_fence_after();
             const uint32_t s_at = tmem + t_lane + sidx * kTile;
             uint32_t xa[16], xb[16];
             tmem_ld16(s_at, xa);
-            const volatile Meta& km = sh.k_meta[jt % kMetaRing];
-            const volatile Meta& vm = sh.v_meta[jt % kMetaRing];
-            int state = 0;
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) state |= km.state[i] << (i * (kPart / 16));
+            const volatile uint32_t* meta =
+                reinterpret_cast<const volatile uint32_t*>(&sh.meta[jt % kMetaRing]);
+            const uint32_t k_exp = meta[0];
+            uint32_t state = meta[2];
+            state |= state >> 6;            // 2 bits of each byte, together
+            state = (state | state >> 12) & 0xFFu;
             const int t0 = unit_token(*q, q->k0 + k);
             const bool edge = state != 0xFF || t0 + kTile - 1 > first ||
                               (p.window && t0 <= last - p.window && t0 + kTile > p.sinks);
@@ -647,10 +667,10 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                 return bits;
             };
             // the values of this unit have been converted: their powers of two
-            if (!warp_wait(&sh.v_full[jt % KB], (uint32_t)(jt / KB) & 1u, p.wait_budget)) return false;
-            int e_new = e_o;
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) e_new = max(e_new, vm.e[i]);
+            if (!warp_wait_sleep(&sh.v_full[jt % KB], (uint32_t)(jt / KB) & 1u, p.wait_budget)) return false;
+            const uint32_t v_exp = meta[1];
+            const uint32_t two = __vmaxu4(v_exp, v_exp >> 16), e_top = max(two & 0xFFu, (two >> 8) & 0xFFu);
+            const int e_new = max(e_o, (int)e_top);
             // Moves the maximum and the values' power of two: what has been summed, and
             // the weights of this unit's first `c` columns, follow.
             auto move = [&](float top, int c) {
@@ -674,7 +694,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                 bool ok = true;
                 if (k > 0) {
                     // the sums so far, once the last unit's products are in
-                    ok = warp_wait(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget);
+                    ok = warp_wait_sleep(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget);
                     tc_fence_after();
 #pragma unroll 1
                     for (int i = 0; i < D; i += 8) {
@@ -688,63 +708,79 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                 }
                 return ok;
             };
-            // 16 columns: weights over the scores
-            auto weigh = [&](uint32_t (&x)[16], int c) {
-                const int part = c / kPart;
-                // (never zero: a query of zeros still has -inf where it sees nothing)
-                const float f = fmaxf(unit * pow2_of(km.e[part] + 1), 0x1p-126f);
-                const uint32_t bits = edge ? sees(c) : 0xFFFFu;
-                float t = -INFINITY;
-                if (edge) {
+            // 16 columns: weights over the scores.  f: the scores' factor, off: what is
+            // added to them (with the maximum), back: the factor of the weights' sum.
+            auto weigh = [&](uint32_t (&x)[16], int c, float f, float shift, float back, auto masked) {
+                if constexpr (decltype(masked)::value) {
+                    const uint32_t bits = sees(c);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (!((bits >> i) & 1u)) x[i] = 0xFF800000u;  // -inf
                 }
+                float t = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 16; i += 2)
                     t = fmaxf(t, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-                if (__any_sync(0xFFFFFFFFu, t * f > mx + 8.f) || e_new > e_o) {
-                    if (!move(t * f, c)) return false;
-                }
-                const int de = vm.e[part] - e_o;  // at most 0
-                const float off = (float)(7 + de) - mu;
-                const uint64_t f2 = pair_of(f, f), off2 = pair_of(off, off);
-                uint64_t sum = 0;
+                const bool over = __any_sync(0xFFFFFFFFu, t * f > mx + 8.f);
                 uint32_t y[8];
+                float sum;
+                auto weights = [&]() {
+                    const float off = shift - mu;
+                    const uint64_t f2 = pair_of(f, f), off2 = pair_of(off, off);
+                    uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 8; ++i) {
+                        float a, b;
+                        parts_of(fma_pair(pair_of(__uint_as_float(x[2 * i]),
+                                                  __uint_as_float(x[2 * i + 1])),
+                                          f2, off2), &a, &b);
+                        a = exp2_approx(a);
+                        b = exp2_approx(b);
+                        uint64_t& s = i & 1 ? s1 : s0;
+                        s = i > 1 ? add_pair(s, pair_of(a, b)) : pair_of(a, b);
+                        y[i] = cvt_f16x2(a, b);
+                    }
                     float a, b;
-                    parts_of(fma_pair(pair_of(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
-                                      f2, off2), &a, &b);
-                    a = exp2_approx(a);
-                    b = exp2_approx(b);
-                    sum = i ? add_pair(sum, pair_of(a, b)) : pair_of(a, b);
-                    y[i] = cvt_f16x2(a, b);
+                    parts_of(add_pair(s0, s1), &a, &b);
+                    sum = a + b;
+                };
+                weights();  // most often the maximum stays, and this has not waited for the vote
+                if (over) {
+                    if (!move(t * f, c)) return false;
+                    weights();
                 }
-                float a, b;
-                parts_of(sum, &a, &b);
-                l = fmaf(a + b, pow2_of(min(127 - de, 254)), l);
+                l = fmaf(sum, back, l);
                 tmem_st8(s_at + c / 2, y);
                 return true;
             };
             bool ok = true;
-            tmem_ld_wait_of(xa);
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-                tmem_ld16(s_at + c + 16, xb);
-                ok = weigh(xa, c) && ok;
-                tmem_ld_wait_of(xb);
-                if (c + 32 < kTile) tmem_ld16(s_at + c + 32, xa);
-                ok = weigh(xb, c + 16) && ok;
+            if (e_new > e_o) ok = move(-INFINITY, 0);
+            auto all_columns = [&](auto masked) {
                 tmem_ld_wait_of(xa);
-            }
+#pragma unroll 1
+                for (int c = 0; c < kTile; c += 32) {
+                    tmem_ld16(s_at + c + 16, xb);
+                    const int ek = (k_exp >> (c / 4)) & 0xFF, de = ((v_exp >> (c / 4)) & 0xFF) - e_o;
+                    // (never zero: a query of zeros still has -inf where it sees nothing)
+                    const float f = fmaxf(unit * pow2_of(ek + 1), 0x1p-126f);
+                    const float shift = (float)(7 + de);  // de <= 0
+                    const float back = pow2_of(min(127 - de, 254));
+                    ok = weigh(xa, c, f, shift, back, masked) && ok;
+                    tmem_ld_wait_of(xb);
+                    if (c + 32 < kTile) tmem_ld16(s_at + c + 32, xa);
+                    ok = weigh(xb, c + 16, f, shift, back, masked) && ok;
+                    tmem_ld_wait_of(xa);
+                }
+            };
+            if (edge) all_columns(std::true_type());
+            else all_columns(std::false_type());
             if (!ok) return false;
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sh.p_full[m]);
         }
         // ---- the row's result
-        if (!warp_wait(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget)) return false;
+        if (!warp_wait_sleep(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget)) return false;
         tc_fence_after();
         const bool whole = q->flags == (kBegins | kEnds);
         const float up = pow2_of(e_o + 1);  // 2^(e_o - 126)
@@ -754,32 +790,44 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
         float* part = p.partial + ((long long)blockIdx.x * 2 + ((q->flags & kBegins) ? 1 : 0)) *
                                       SH::kPartialFloats;
         const int dense = tok0 * heads + lr;
+        // A finished row goes through this half's query buffer, which is not needed any
+        // more, so that the warp writes whole rows at a time.
+        const uint32_t stage = qbuf + m * (D / 64) * (128 * 128);
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
             uint32_t x[16];
             tmem_ld16(o_at + c, x);
-            tmem_ld_wait();
+            tmem_ld_wait_of(x);
             float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(x[i]) * inv;
-            if (in && whole) {
-                uint4 a, b;
-                a.x = cvt_bf16x2(v[0], v[1]);
-                a.y = cvt_bf16x2(v[2], v[3]);
-                a.z = cvt_bf16x2(v[4], v[5]);
-                a.w = cvt_bf16x2(v[6], v[7]);
-                b.x = cvt_bf16x2(v[8], v[9]);
-                b.y = cvt_bf16x2(v[10], v[11]);
-                b.z = cvt_bf16x2(v[12], v[13]);
-                b.w = cvt_bf16x2(v[14], v[15]);
-                uint4* dst = reinterpret_cast<uint4*>(p.out + to * D + c);
-                dst[0] = a;
-                dst[1] = b;
+            if (whole) {
+                const uint32_t row_at = stage + (c / 64) * (128 * 128) + lr * 128;
+                sts128(row_at + ((((c % 64) / 8) ^ (lr % 8)) * 16), cvt_bf16x2(v[0], v[1]),
+                       cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+                sts128(row_at + ((((c % 64) / 8 + 1) ^ (lr % 8)) * 16), cvt_bf16x2(v[8], v[9]),
+                       cvt_bf16x2(v[10], v[11]), cvt_bf16x2(v[12], v[13]),
+                       cvt_bf16x2(v[14], v[15]));
             } else if (in) {
                 float4* dst = reinterpret_cast<float4*>(part + 2 * SH::kRows + (long long)dense * D + c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+            __syncwarp();
+        }
+        if (whole) {
+            constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+            const int c = lane % kLanes;
+#pragma unroll 4
+            for (int i = 0; i < kLanes; ++i) {
+                const int at_row = quarter * 32 + i * kAtOnce + lane / kLanes;
+                const uint4 v = ld_shared_v4(stage + (c / 8) * (128 * 128) + at_row * 128 +
+                                             (((c % 8) ^ (at_row % 8)) * 16));
+                if (at_row < toks * heads)
+                    *(reinterpret_cast<uint4*>(
+                          p.out + ((long long)(q->row0 + tok0 + at_row / heads) * p.Hq + q->head0 +
+                                   at_row % heads) * D) + c) = v;
             }
             __syncwarp();
         }
@@ -845,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         // no instruction may still be running when the CTA lets its memory go
         if (elect_one()) umma_commit(&sh.drained[warp - 16]);
         __syncwarp();
-        ok = warp_wait(&sh.drained[warp - 16], 0, kWaitBudgetCycles) && ok;
+        ok = warp_wait_sleep(&sh.drained[warp - 16], 0, kWaitBudgetCycles) && ok;
     } else if (warp == 18) {
         if (lane == 0) ok = list_pieces<D, G>(p, sh);
     }
