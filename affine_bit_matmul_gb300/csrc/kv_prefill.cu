@@ -137,21 +137,22 @@ __device__ __forceinline__ uint32_t hfma2_f16(uint32_t a, uint32_t b, uint32_t c
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-__device__ __forceinline__ uint32_t hsub2_f16(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
+// The four pairs of a code word (nibbles 0 and 4, 1 and 5, ...) as s q + b in f16.
+// As f16 numbers the masked codes are 2^-24 and 2^-20 times their values (both
+// subnormal): s is 2^24 times what it is, and 2^20 for the odd ones.
+__device__ __forceinline__ void dequant_word(uint32_t w, uint32_t s_even, uint32_t s_odd,
+                                             uint32_t b2, uint32_t (&x)[4]) {
+    const uint32_t v = w >> 8;
+    x[0] = hfma2_f16(w & 0x000F000Fu, s_even, b2);
+    x[1] = hfma2_f16(w & 0x00F000F0u, s_odd, b2);
+    x[2] = hfma2_f16(v & 0x000F000Fu, s_even, b2);
+    x[3] = hfma2_f16(v & 0x00F000F0u, s_odd, b2);
 }
 
-// The four pairs of a code word (nibbles 0 and 4, 1 and 5, ...) as s q + b in f16.
-// 0x64xx is 1024 + q, 0x54x0 is 64 + q; both differences are exact.
-__device__ __forceinline__ void dequant_word(uint32_t w, uint32_t s2, uint32_t b2,
-                                             uint32_t (&x)[4]) {
-    const uint32_t v = w >> 8;
-    x[0] = hfma2_f16(hsub2_f16((w & 0x000F000Fu) | 0x64006400u, 0x64006400u), s2, b2);
-    x[1] = hfma2_f16(hsub2_f16((w & 0x00F000F0u) | 0x54005400u, 0x54005400u), s2, b2);
-    x[2] = hfma2_f16(hsub2_f16((v & 0x000F000Fu) | 0x64006400u, 0x64006400u), s2, b2);
-    x[3] = hfma2_f16(hsub2_f16((v & 0x00F000F0u) | 0x54005400u, 0x54005400u), s2, b2);
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
@@ -356,7 +357,8 @@ struct Convert {
             }
         }
     }
-    // The loaded unit into operand buffer `out`; its power of two.
+    // The biased exponent e of a power of two above the unit's values: they are below
+    // 2^(e - 126).
     __device__ int scale_bits() {
         const int t = t0 + lane;
         // what no row sees may hold anything
@@ -370,25 +372,30 @@ struct Convert {
         for (int g = 0; g < NG; ++g) big = max_u16x2(big, pr[g] & 0x7FFF7FFFu);
         const int es = (int)(__reduce_max_sync(0xFFFFFFFFu, big & 0xFFFFu) >> 7) + 4;
         const int eb = (int)(__reduce_max_sync(0xFFFFFFFFu, big >> 16) >> 7);
-        return min(max(max(es, eb) + 1, 30), 250);
+        return min(max(max(es, eb) + 1, 30), 247);
     }
+    // The loaded unit into operand buffer `out`.
     __device__ void store(uint32_t out, int e) {
         const int r = lane >> 2, i4 = lane & 3;
-        const float dn = pow2_of(253 - e);  // 2^(126 - e)
+        // Values come out below 2^-5, so that 2^24 times a scale, which is at most 2^-5 of
+        // the largest value, is an f16 number.
+        const float dn = pow2_of(248 - e);  // 2^(121 - e)
         // each lane's own token as f16 pairs (scale, bias)
         uint32_t sb[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g)
-            sb[g] = cvt_f16x2(__uint_as_float(pr[g] << 16) * dn,
+            sb[g] = cvt_f16x2(__uint_as_float(pr[g] << 16) * dn * 0x1p24f,
                               __uint_as_float(pr[g] & 0xFFFF0000u) * dn);
+        constexpr uint32_t sixteenth = 0x2C002C00u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // 8 tokens at a time
             if (!kv) {
-                uint32_t s2[NG], b2[NG];
+                uint32_t s2[NG], t2[NG], b2[NG];
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const uint32_t x = __shfl_sync(0xFFFFFFFFu, sb[g], 8 * j + r);
                     s2[g] = prmt(x, x, 0x1010u);
+                    t2[g] = hmul2_f16(s2[g], sixteenth);
                     b2[g] = prmt(x, x, 0x3232u);
                 }
                 const uint32_t row = out + (part * kPart + 8 * j + r) * 128;
@@ -400,8 +407,9 @@ struct Convert {
                     const uint32_t word = odd ? w[j][u ^ 1] : w[j][u];
                     const int g0 = u * 32 / G, g1 = (u ^ 1) * 32 / G;
                     uint32_t x[4];
-                    dequant_word(word, g0 == g1 || !odd ? s2[g0] : s2[g1],
-                                 g0 == g1 || !odd ? b2[g0] : b2[g1], x);
+                    const bool other = g0 != g1 && odd;
+                    dequant_word(word, other ? s2[g1] : s2[g0], other ? t2[g1] : t2[g0],
+                                 other ? b2[g1] : b2[g0], x);
                     // values 32 u' + 8 i4 ..: 16 bytes of the token's row
                     const int chunk = (((u & 1) ^ (r & 1)) * 4 + i4) ^ r;
                     sts128(row + (u / 2) * (kTile * 128) + chunk * 16, x[0], x[1], x[2], x[3]);
@@ -416,10 +424,11 @@ struct Convert {
                     const uint32_t a = __shfl_sync(0xFFFFFFFFu, sb[g], 8 * j + 2 * i4);
                     const uint32_t c = __shfl_sync(0xFFFFFFFFu, sb[g], 8 * j + 2 * i4 + 1);
                     const uint32_t s2 = prmt(a, c, 0x5410u), b2 = prmt(a, c, 0x7632u);
+                    const uint32_t t2 = hmul2_f16(s2, sixteenth);
 #pragma unroll
                     for (int u = g * G / 32; u < (g + 1) * G / 32; ++u) {
                         uint32_t x[4];
-                        dequant_word(w[j][u], s2, b2, x);
+                        dequant_word(w[j][u], s2, t2, b2, x);
 #pragma unroll
                         for (int n = 0; n < 4; ++n) sts32(row + (32 * u + 8 * n) * 128, x[n]);
                     }
@@ -717,10 +726,10 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                     for (int i = 0; i < 16; ++i)
                         if (!((bits >> i) & 1u)) x[i] = 0xFF800000u;  // -inf
                 }
-                float t = -INFINITY;
+                float t = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-                for (int i = 0; i < 16; i += 2)
-                    t = fmaxf(t, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+                for (int i = 2; i < 16; i += 2)
+                    t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                 const bool over = __any_sync(0xFFFFFFFFu, t * f > mx + 8.f);
                 uint32_t y[8];
                 float sum;
@@ -762,7 +771,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                     tmem_ld16(s_at + c + 16, xb);
                     const int ek = (k_exp >> (c / 4)) & 0xFF, de = ((v_exp >> (c / 4)) & 0xFF) - e_o;
                     // (never zero: a query of zeros still has -inf where it sees nothing)
-                    const float f = fmaxf(unit * pow2_of(ek + 1), 0x1p-126f);
+                    const float f = fmaxf(unit * pow2_of(ek + 6), 0x1p-126f);  // 2^(e - 121)
                     const float shift = (float)(7 + de);  // de <= 0
                     const float back = pow2_of(min(127 - de, 254));
                     ok = weigh(xa, c, f, shift, back, masked) && ok;
@@ -783,7 +792,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
         if (!warp_wait_sleep(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget)) return false;
         tc_fence_after();
         const bool whole = q->flags == (kBegins | kEnds);
-        const float up = pow2_of(e_o + 1);  // 2^(e_o - 126)
+        const float up = pow2_of(e_o + 1) * 32.f;  // 2^(e_o - 121)
         l *= 0x1p-7f;
         const float inv = whole ? (l > 0.f ? up * (0x1p-7f / l) : 0.f) : up * 0x1p-7f;
         const long long to = (long long)row * p.Hq + q->head0 + hh;
