@@ -183,30 +183,53 @@ def _check(status: int, what: str):
 
 # ---------------------------------------------------------------- torch level
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
+class _Here:
+    """A context that does nothing: the tensors' device is the current one."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_CTX = _Here()
+
+
 def _launch_on(device, stream):
     """The device context and raw stream handle for a call on ``device``.
 
     The library launches on the CUDA device that is current when it is
-    called, so every wrapper makes the tensors' device current for the call;
-    ``stream`` (default: that device's current stream) must belong to the
-    same device, else the launch would pair one device's pointers with
-    another device's stream."""
+    called, so every wrapper makes the tensors' device current for the call
+    (nothing is to be done where it is); ``stream`` (default: that device's
+    current stream) must belong to the same device, else the launch would pair
+    one device's pointers with another device's stream."""
     torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError("stream is on %s but the tensors are on %s" % (stream.device, device))
-    return torch.cuda.device(device), ctypes.c_void_p(stream.cuda_stream)
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        return _HERE_CTX, handle
+    return torch.cuda.device(device), handle
 
 
 def _require(t, name, dtypes, device=None):
@@ -575,31 +598,52 @@ def gather_qmm_gateup(x, w_gate, s_gate, b_gate, w_up, s_up, b_up, expert_ids, r
 
 # ------------------------------------------------- 4-bit key/value cache
 
-def _heads(t, name, device=None, out=False):
+def _heads(t, name, index=None, out=False):
     """Checks a bf16 [T, heads, D] tensor whose heads are contiguous; returns
-    its (row, head) strides in values."""
+    its (row, head) strides in values.  ``index``: the device it has to be on."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
+    on = t.get_device()
+    if on < 0:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype is not torch.bfloat16:
         raise TypeError("%s has dtype %s, expected torch.bfloat16" % (name, t.dtype))
     if t.dim() != 3:
         raise ValueError("%s must be 3-D [T, heads, D]" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    (n, h, d), (rs, hs, vs) = t.shape, t.stride()
+    if index is not None and on != index:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, index))
+    n, h, d = t.shape
+    rs, hs, vs = t.stride()
     if vs != 1 and d > 1:
         raise ValueError("the values of a head of %s must be contiguous" % name)
-    hs = hs if h > 1 else d
-    rs = rs if n > 1 else h * d
+    if h <= 1:
+        hs = d
+    if n <= 1:
+        rs = h * d
     if rs % 8 or hs % 8:
         raise ValueError("the strides of %s must be multiples of 8 values" % name)
     if out and ((h > 1 and hs < d) or (n > 1 and rs < d) or
                 (n > 1 and h > 1 and rs < h * hs and hs < n * rs)):
         raise ValueError("the rows of %s overlap" % name)
     return rs, hs
+
+
+def _flat(t, name, dtype, index=None):
+    """Checks a contiguous tensor of ``dtype`` on device ``index``; its address."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    on = t.get_device()
+    if on < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if index is not None and on != index:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, index))
+    return t.data_ptr()
 
 
 def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling=None, factor: float = 1.0,
@@ -674,48 +718,58 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     torch = _torch()
     q_rs, q_hs = _heads(q, "q")
     dev = q.device
+    on = dev.index
     T, Hq, D = q.shape
-    Hk = k_rs = k_hs = k_ors = k_ohs = 0
+    Hk = k_rs = k_hs = k_ors = k_ohs = rot = 0
+    k_at = k_out_at = pos_at = freq_at = qw_at = kw_at = None
     if k is not None:
-        k_rs, k_hs = _heads(k, "k", dev)
+        k_rs, k_hs = _heads(k, "k", on)
         Hk = k.shape[1]
         if k.shape[0] != T or k.shape[2] != D:
             raise ValueError("k has shape %s, expected [%d, heads, %d]" % (tuple(k.shape), T, D))
+        k_at = k.data_ptr()
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    rot = 0
     if inv_freq is not None:
-        _require(inv_freq, "inv_freq", (torch.float32,), dev)
+        freq_at = _flat(inv_freq, "inv_freq", torch.float32, on)
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _require(positions, "positions", (torch.int32,), dev)
+        pos_at = _flat(positions, "positions", torch.int32, on)
         if positions.numel() != T:
             raise ValueError("positions must have T entries")
         rot = 2 * inv_freq.numel()
         if inv_freq.dim() != 1 or rot == 0:
             raise ValueError("inv_freq must be 1-D [rot_dim/2]")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _require(w, name, (torch.bfloat16,), dev)
-            if tuple(w.shape) != (D,):
-                raise ValueError("%s has shape %s, expected %s" % (name, tuple(w.shape), (D,)))
+    if q_weight is not None:
+        qw_at = _flat(q_weight, "q_weight", torch.bfloat16, on)
+        if q_weight.dim() != 1 or q_weight.numel() != D:
+            raise ValueError("q_weight must be [D]")
+    if k_weight is not None:
+        kw_at = _flat(k_weight, "k_weight", torch.bfloat16, on)
+        if k_weight.dim() != 1 or k_weight.numel() != D:
+            raise ValueError("k_weight must be [D]")
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    if k is not None and k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
-    for o, i, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if o is not None and o.shape != i.shape:
-            raise ValueError("%s has shape %s, expected %s" % (name, tuple(o.shape), tuple(i.shape)))
-    q_ors, q_ohs = _heads(q_out, "q_out", dev, out=True)
+        q_ors, q_ohs = Hq * D, D
+    else:
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        q_ors, q_ohs = _heads(q_out, "q_out", on, out=True)
     if k is not None:
-        k_ors, k_ohs = _heads(k_out, "k_out", dev, out=True)
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
+            k_ors, k_ohs = Hk * D, D
+        else:
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have the shape of k")
+            k_ors, k_ohs = _heads(k_out, "k_out", on, out=True)
+        k_out_at = k_out.data_ptr()
     ctx, st = _launch_on(dev, stream)
     with ctx:
         _check(lib().mxq_qk_norm_rope(
-            _ptr(q), q_rs, q_hs, _ptr(k), k_rs, k_hs, _ptr(positions) if rot else None,
-            _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(q_out), q_ors, q_ohs,
-            _ptr(k_out), k_ors, k_ohs, T, Hq, Hk, D, rot, int(interleaved), eps, weight_offset,
-            rope_scale, st), "mxq_qk_norm_rope")
+            q.data_ptr(), q_rs, q_hs, k_at, k_rs, k_hs, pos_at, freq_at, qw_at, kw_at,
+            q_out.data_ptr(), q_ors, q_ohs, k_out_at, k_ors, k_ohs, T, Hq, Hk, D, rot,
+            1 if interleaved else 0, eps, weight_offset, rope_scale, st), "mxq_qk_norm_rope")
     return q_out, k_out
 
 
@@ -729,10 +783,9 @@ def kv_block_bytes(head_dim: int, page_size: int, group_size: int = 64) -> int:
     return n
 
 
-def _cache(pages, head_dim, group_size, device, kv_heads=None):
-    """Checks a cache tensor and returns (n_pages, kv_heads, page_size)."""
-    torch = _torch()
-    _require(pages, "pages", (torch.uint8,), device)
+def _cache(pages, head_dim, group_size, index, kv_heads=None):
+    """Checks a cache tensor and returns (address, n_pages, kv_heads, page_size)."""
+    at = _flat(pages, "pages", _torch().uint8, index)
     if pages.dim() != 3:
         raise ValueError("pages must be [n_pages, kv_heads, block bytes]")
     n, h, block = pages.shape
@@ -744,7 +797,7 @@ def _cache(pages, head_dim, group_size, device, kv_heads=None):
     if block % per or block // per not in (16, 32, 64, 128):
         raise ValueError("a block of %d bytes is no page of head_dim %d, group_size %d" % (
             block, head_dim, group_size))
-    return n, h, block // per
+    return at, n, h, block // per
 
 
 def kv_append(k, v, pages, slots, group_size: int = 64, dev_status=None, stream=None):
@@ -753,21 +806,22 @@ def kv_append(k, v, pages, slots, group_size: int = 64, dev_status=None, stream=
     page_size + token; negative: skipped) of the cache ``pages``."""
     torch = _torch()
     k_rs, k_hs = _heads(k, "k")
-    v_rs, v_hs = _heads(v, "v", k.device)
+    dev = k.device
+    on = dev.index
+    v_rs, v_hs = _heads(v, "v", on)
     if v.shape != k.shape:
         raise ValueError("v has shape %s, expected %s" % (tuple(v.shape), tuple(k.shape)))
     T, H, D = k.shape
-    n_pages, _, page_size = _cache(pages, D, group_size, k.device, H)
-    _require(slots, "slots", (torch.int32,), k.device)
+    at, n_pages, _, page_size = _cache(pages, D, group_size, on, H)
+    slots_at = _flat(slots, "slots", torch.int32, on)
     if slots.numel() != T:
         raise ValueError("slots must have T entries")
-    if dev_status is not None:
-        _require(dev_status, "dev_status", (torch.int32,), k.device)
-    ctx, st = _launch_on(k.device, stream)
+    status = None if dev_status is None else _flat(dev_status, "dev_status", torch.int32, on)
+    ctx, st = _launch_on(dev, stream)
     with ctx:
-        _check(lib().mxq_kv_append(_ptr(k), k_rs, k_hs, _ptr(v), v_rs, v_hs, _ptr(pages),
-                                   _ptr(slots), T, H, D, n_pages, page_size, group_size,
-                                   _ptr(dev_status), st), "mxq_kv_append")
+        _check(lib().mxq_kv_append(k.data_ptr(), k_rs, k_hs, v.data_ptr(), v_rs, v_hs, at, slots_at,
+                                   T, H, D, n_pages, page_size, group_size, status, st),
+               "mxq_kv_append")
     return pages
 
 
@@ -776,27 +830,28 @@ def kv_read(pages, slots, head_dim: int, group_size: int = 64, k_out=None, v_out
     """The rows of ``slots`` (int32 [T]) out of the cache: (k, v) bf16 [T,
     kv_heads, head_dim]; zeros for a negative slot."""
     torch = _torch()
-    n_pages, H, page_size = _cache(pages, head_dim, group_size, None)
+    at, n_pages, H, page_size = _cache(pages, head_dim, group_size, None)
     dev = pages.device
-    _require(slots, "slots", (torch.int32,), dev)
+    on = dev.index
+    slots_at = _flat(slots, "slots", torch.int32, on)
     T = slots.numel()
-    outs = []
-    for o, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if o is None:
-            o = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=dev)
-        _require(o, name, (torch.bfloat16,), dev)
-        if tuple(o.shape) != (T, H, head_dim):
-            raise ValueError("%s has shape %s, expected %s" % (name, tuple(o.shape),
-                                                               (T, H, head_dim)))
-        outs.append(o)
-    if dev_status is not None:
-        _require(dev_status, "dev_status", (torch.int32,), dev)
+    shape = (T, H, head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    elif tuple(k_out.shape) != shape:
+        raise ValueError("k_out has shape %s, expected %s" % (tuple(k_out.shape), shape))
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    elif tuple(v_out.shape) != shape:
+        raise ValueError("v_out has shape %s, expected %s" % (tuple(v_out.shape), shape))
+    k_at = _flat(k_out, "k_out", torch.bfloat16, on)
+    v_at = _flat(v_out, "v_out", torch.bfloat16, on)
+    status = None if dev_status is None else _flat(dev_status, "dev_status", torch.int32, on)
     ctx, st = _launch_on(dev, stream)
     with ctx:
-        _check(lib().mxq_kv_read(_ptr(pages), _ptr(slots), _ptr(outs[0]), _ptr(outs[1]), T, H,
-                                 head_dim, n_pages, page_size, group_size, _ptr(dev_status), st),
-               "mxq_kv_read")
-    return outs[0], outs[1]
+        _check(lib().mxq_kv_read(at, slots_at, k_at, v_at, T, H, head_dim, n_pages, page_size,
+                                 group_size, status, st), "mxq_kv_read")
+    return k_out, v_out
 
 
 def kv_attention_workspace_bytes(rows: int, seqs: int, heads: int, kv_heads: int, head_dim: int,
@@ -821,48 +876,52 @@ def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int =
     torch = _torch()
     q_rs, q_hs = _heads(q, "q")
     dev = q.device
+    on = dev.index
     T, Hq, D = q.shape
-    n_pages, Hkv, page_size = _cache(pages, D, group_size, dev)
-    if Hq == 0 or Hq % Hkv:
+    at, n_pages, Hkv, page_size = _cache(pages, D, group_size, on)
+    if Hq == 0 or Hkv == 0 or Hq % Hkv:
         raise ValueError("%d query heads do not divide over %d key/value heads" % (Hq, Hkv))
-    _require(page_table, "page_table", (torch.int32,), dev)
+    table_at = _flat(page_table, "page_table", torch.int32, on)
     if page_table.dim() != 2:
         raise ValueError("page_table must be 2-D [S, max_pages]")
     S, max_pages = page_table.shape
-    _require(ctx_lens, "ctx_lens", (torch.int32,), dev)
+    lens_at = _flat(ctx_lens, "ctx_lens", torch.int32, on)
     if ctx_lens.numel() != S:
         raise ValueError("ctx_lens must have S entries")
+    starts_at = lse_at = status = None
     if q_starts is not None:
-        _require(q_starts, "q_starts", (torch.int32,), dev)
+        starts_at = _flat(q_starts, "q_starts", torch.int32, on)
         if q_starts.numel() != S + 1:
             raise ValueError("q_starts must have S + 1 entries")
     elif T != S or max_q_len != 1:
         raise ValueError("without q_starts every sequence has one row: T must be S, max_q_len 1")
     if out is None:
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    _require(out, "out", (torch.bfloat16,), dev)
-    if tuple(out.shape) != (T, Hq, D):
-        raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), (T, Hq, D)))
+        out_at = out.data_ptr()
+    else:
+        out_at = _flat(out, "out", torch.bfloat16, on)
+        if tuple(out.shape) != (T, Hq, D):
+            raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), (T, Hq, D)))
     if lse is not None:
-        _require(lse, "lse", (torch.float32,), dev)
+        lse_at = _flat(lse, "lse", torch.float32, on)
         if tuple(lse.shape) != (T, Hq):
             raise ValueError("lse has shape %s, expected %s" % (tuple(lse.shape), (T, Hq)))
     if dev_status is not None:
-        _require(dev_status, "dev_status", (torch.int32,), dev)
+        status = _flat(dev_status, "dev_status", torch.int32, on)
     if max_q_len <= 0:
         raise ValueError("max_q_len must be positive")
+    L = lib()
     if workspace is None:
-        need = kv_attention_workspace_bytes(T, S, Hq, Hkv, D, max_q_len)
-        workspace = torch.empty((need,),
-                                dtype=torch.uint8, device=dev)
-    _require(workspace, "workspace", (torch.uint8,), dev)
+        need = L.mxq_kv_attention_workspace_bytes(T, S, Hq, Hkv, D, max_q_len)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    ws_at = _flat(workspace, "workspace", torch.uint8, on)
     ctx, st = _launch_on(dev, stream)
     with ctx:
-        _check(lib().mxq_kv_attention(
-            _ptr(q), q_rs, q_hs, _ptr(pages), _ptr(page_table), _ptr(ctx_lens), _ptr(q_starts),
-            _ptr(out), _ptr(lse), T, S, Hq, Hkv, D, n_pages, max_pages, page_size, group_size,
-            max_q_len, D ** -0.5 if scale is None else scale, window, sinks, _ptr(workspace),
-            workspace.numel(), _ptr(dev_status), st), "mxq_kv_attention")
+        _check(L.mxq_kv_attention(
+            q.data_ptr(), q_rs, q_hs, at, table_at, lens_at, starts_at, out_at, lse_at, T, S, Hq,
+            Hkv, D, n_pages, max_pages, page_size, group_size, max_q_len,
+            D ** -0.5 if scale is None else scale, window, sinks, ws_at, workspace.numel(), status,
+            st), "mxq_kv_attention")
     return out
 
 

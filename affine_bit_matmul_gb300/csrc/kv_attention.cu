@@ -888,8 +888,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParam
 template <int D, int G, int KT>
 cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     using SH = Shape<D, G, KT>;
-    cudaError_t err = cudaFuncSetAttribute(kv_attn_kernel<D, G, KT>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kSmem);
+    static std::atomic<uint64_t> asked{0};  // devices on which the kernel may take its memory
+    cudaError_t err = allow_shared(kv_attn_kernel<D, G, KT>, SH::kSmem, asked);
     if (err != cudaSuccess) return err;
     const unsigned grid = (unsigned)p.ctas;
     kv_attn_kernel<D, G, KT><<<grid, SH::kThreads, SH::kSmem, stream>>>(p);

@@ -2,6 +2,7 @@
 // descriptors of its pieces, and small helpers.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -139,6 +140,19 @@ __device__ __forceinline__ void load_pairs(const uint8_t* at, uint32_t (&w)[NG])
             w[4 * i + 3] = v.w;
         }
     }
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device.
+template <typename K>
+cudaError_t allow_shared(K* kernel, int bytes, std::atomic<uint64_t>& asked) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (asked.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess) asked.fetch_or(bit, std::memory_order_release);
+    return err;
 }
 
 }  // namespace

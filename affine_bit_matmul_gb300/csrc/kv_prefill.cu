@@ -1059,8 +1059,8 @@ __global__ void __launch_bounds__(256) kv_join_rows_kernel(const KvAttnParams p,
 template <int D, int G>
 cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     using SH = Shape<D, G>;
-    cudaError_t err = cudaFuncSetAttribute(kv_prefill_kernel<D, G>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kSmem);
+    static std::atomic<uint64_t> asked{0};  // devices on which the kernel may take its memory
+    cudaError_t err = allow_shared(kv_prefill_kernel<D, G>, SH::kSmem, asked);
     if (err != cudaSuccess) return err;
     kv_plan_kernel<<<1, 1024, 0, stream>>>(p);
     err = cudaGetLastError();
