@@ -37,6 +37,7 @@
 // moved when a score exceeds it by 2^8, so most tiles have no reductions across
 // lanes at all.
 // Bound by HBM for long contexts: 2 (D / 2 + 4 D / G) bytes per token and head.
+#include <climits>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,8 +47,11 @@
 namespace mxq {
 namespace {
 
-constexpr int kChunk = 64;                      // values joined at a time
-constexpr int kRowPad = kChunk + 8;
+// What the end of a row tile costs a CTA (joining its warps, the next queries), in
+// tiles: the runs are cut equal with so many tiles that do nothing after each row
+// tile.  Measured for 64 sequences of 1024 to 8192 tokens, where the CTAs of short
+// ones took 81 us and those of long ones 52 us without it.
+constexpr int kEndTiles = 4;
 
 // Sizes of a kernel for row tiles of 4 KT rows: tokens of a tile, compute warps,
 // CTAs per SM, tiles in the ring.
@@ -63,9 +67,11 @@ struct Shape {
     static constexpr int kQueryBytes = kQueryShared ? kColumns * D * 16 : 0;
     static constexpr int kWarps = KT == 4 ? 3 : D == 256 ? 5 : 7;
     static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kChunk = KT == 1 && D > 64 ? 128 : 64;  // values joined at a time
+    static constexpr int kRowPad = kChunk + 8;
     static constexpr int kJoinBytes = kWarps * kRows * kRowPad * 4;
     static constexpr int kStatBytes = kWarps * kRows * 8;
-    static constexpr int kRoom = 109 * 1024 - kJoinBytes - kStatBytes - kQueryBytes;
+    static constexpr int kRoom = 107 * 1024 - kJoinBytes - kStatBytes - kQueryBytes;
     static constexpr int kSlots = kRoom / kStageBytes < 24 ? kRoom / kStageBytes : 24;
     static constexpr int kRingBytes = kSlots * kStageBytes;
     static constexpr int kSmem = kRingBytes + kJoinBytes + kStatBytes + kQueryBytes;
@@ -120,11 +126,18 @@ struct Piece {
     int head_tiles, tail;     // which tiles its units are (Span)
     int k0, seq0, end;        // first unit; numbers of its units in the run
     int flags;                // kBegins, kEnds
+    int last;                 // no piece: the run is over
 };
-constexpr int kPieces = 32;   // pieces of the run that are known ahead
+// Pieces of the run that are known ahead: the copying warp looks up to two rounds of
+// its ring (24 tiles at most) ahead of the unit that is being worked on.
+constexpr int kPieces = 64;
 
 // One thread: lists the pieces of the CTA's run, the first kPieces at once and
-// one more whenever the warps are done with one.
+// one more whenever the warps are done with one; then one marked `last`.
+__device__ __forceinline__ int units_of(const Span& sp) {
+    return sp.tiles ? sp.tiles + kEndTiles : 0;
+}
+
 template <int TILE>
 struct Walk {  // (no constructors: it lies in shared memory)
     int s, h, part, k, seq, left;
@@ -135,59 +148,72 @@ struct Walk {  // (no constructors: it lies in shared memory)
         s = s_;
         sp = span_of<TILE>(p, s, 0);
         const long long vheads = (long long)p.Hkv * p.head_parts;
-        while (at >= sp.tiles * vheads) {
-            at -= sp.tiles * vheads;
+        while (at >= units_of(sp) * vheads) {
+            at -= units_of(sp) * vheads;
             sp = span_of<TILE>(p, ++s, 0);
         }
-        const int vh = (int)(at / sp.tiles);
-        k = (int)(at % sp.tiles);
+        const unsigned first = (unsigned)at;  // below 2^31 units a sequence
+        const int vh = (int)(first / (unsigned)units_of(sp));
+        k = (int)(first % (unsigned)units_of(sp));
         h = vh / p.head_parts;
         part = vh % p.head_parts;
         seq = 0;
         left = units;
     }
     __device__ bool next(const KvAttnParams& p, Piece* out, Seg* seg) {
-        if (left == 0) return false;
-        while (sp.tiles == 0) sp = span_of<TILE>(p, ++s, 0);
-        const int n = min(left, sp.tiles - k), rep = p.Hq / p.Hkv;
-        Piece q;
-        q.row0 = sp.row0;
-        q.toks = sp.toks;
-        q.p0 = sp.p0;
-        q.head0 = h * rep + part * p.part_heads;
-        q.heads = min(p.part_heads, rep - part * p.part_heads);
-        q.s = s;
-        q.h = h;
-        q.head_tiles = sp.head_tiles;
-        q.tail = sp.tail;
-        q.k0 = k;
-        q.seq0 = seq;
-        q.end = seq + n;
-        q.flags = (k == 0 ? kBegins : 0) | (k + n == sp.tiles ? kEnds : 0);
-        *out = q;
-        if (q.flags != (kBegins | kEnds)) {
-            Seg g;
-            g.row0 = q.row0;
-            g.toks = q.toks;
-            g.head0 = q.head0;
-            g.heads = q.heads;
-            g.flags = q.flags;
-            seg[(q.flags & kBegins) ? 1 : 0] = g;
-        }
-        seq += n;
-        left -= n;
-        k += n;
-        if (k == sp.tiles && left) {
-            k = 0;
-            if (++part == p.head_parts) {
-                part = 0;
-                if (++h == p.Hkv) {
-                    h = 0;
-                    sp = span_of<TILE>(p, ++s, 0);
+        bool found = false;
+        while (left && !found) {
+            while (sp.tiles == 0) sp = span_of<TILE>(p, ++s, 0);
+            const int units = units_of(sp), n = min(left, units - k);
+            const int tiles = min(k + n, sp.tiles) - k;  // the others are the row tile's end
+            if (tiles > 0) {
+                const int rep = p.Hq / p.Hkv;
+                Piece q;
+                q.row0 = sp.row0;
+                q.toks = sp.toks;
+                q.p0 = sp.p0;
+                q.head0 = h * rep + part * p.part_heads;
+                q.heads = min(p.part_heads, rep - part * p.part_heads);
+                q.s = s;
+                q.h = h;
+                q.head_tiles = sp.head_tiles;
+                q.tail = sp.tail;
+                q.k0 = k;
+                q.seq0 = seq;
+                q.end = seq + tiles;
+                q.flags = (k == 0 ? kBegins : 0) | (k + tiles == sp.tiles ? kEnds : 0);
+                q.last = 0;
+                *out = q;
+                if (q.flags != (kBegins | kEnds)) {
+                    Seg g;
+                    g.row0 = q.row0;
+                    g.toks = q.toks;
+                    g.head0 = q.head0;
+                    g.heads = q.heads;
+                    g.flags = q.flags;
+                    seg[(q.flags & kBegins) ? 1 : 0] = g;
+                }
+                seq += tiles;
+                found = true;
+            }
+            left -= n;
+            k += n;
+            if (k == units && left) {
+                k = 0;
+                if (++part == p.head_parts) {
+                    part = 0;
+                    if (++h == p.Hkv) {
+                        h = 0;
+                        sp = span_of<TILE>(p, ++s, 0);
+                    }
                 }
             }
         }
-        return true;
+        if (!found) {
+            out->end = 1 << 30;
+            out->last = 1;  // no piece: the run is over
+        }
+        return found;
     }
 };
 
@@ -219,7 +245,7 @@ __device__ __forceinline__ bool unit_comes(const int* unit, int n, long long bud
 // most a tile are copied whole, of longer ones the four regions of the tile's
 // part.
 template <int D, int G, int TILE, int SLOTS>
-__device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int total, int lane,
+__device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int lane,
                            uint32_t ring, Tile* tiles, uint64_t* full, uint64_t* empty) {
     constexpr int kMost = TILE / 16;
     constexpr uint32_t cb = kv_code_bytes(D, TILE), pb = kv_pair_bytes(D, G, TILE);
@@ -228,16 +254,20 @@ __device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int total
     const uint32_t slot = ring + lane * kv_block_bytes(D, G, TILE);
     int n = lane, end = 0, piece = -1;
     uint32_t parity = 1;  // the first wait passes at once
-    bool work = lane < SLOTS && n < total;
+    bool work = lane < SLOTS;
     int t0 = 0, id[kMost];
     Piece q;
 
-    auto look = [&]() {  // the pages of unit n
+    auto look = [&]() {  // the pages of unit n, if there is one
         if (n >= end) {
             do ++piece;
             while (n >= pieces[piece % kPieces].end);
             q = pieces[piece % kPieces];
             end = q.end;
+            if (q.last) {
+                work = false;
+                return;
+            }
         }
         const int k = q.k0 + n - q.seq0;
         t0 = (k < q.head_tiles ? k : q.tail + k - q.head_tiles) * TILE;
@@ -297,8 +327,7 @@ __device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int total
             }
             parity ^= 1u;
             n += SLOTS;
-            work = n < total;
-            if (work) look();
+            look();
         }
         if (__any_sync(0xFFFFFFFFu, ready)) {
             since = clock64();
@@ -320,12 +349,13 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     using SH = Shape<D, G, KT>;
     constexpr int TILE = SH::kTile, SUB = TILE / 16;  // a warp takes 16 tokens at a time
     constexpr int kWarps = SH::kWarps, kThreads = SH::kThreads, kSlots = SH::kSlots;
+    constexpr int kChunk = SH::kChunk, kRowPad = SH::kRowPad;
     constexpr int NG = D / G;          // groups
     constexpr int U = D / 32;          // code words of a lane per 8 tokens
     constexpr int MT = D / 16;         // output tiles of 16 values
     constexpr int VT = SH::kColumns;   // tiles of 8 columns
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[kSlots], empty[kSlots], joined;
+    __shared__ uint64_t full[kSlots], empty[kSlots], joined, freed, queried;
     __shared__ Tile tiles[kSlots];
     __shared__ Piece pieces[kPieces];
     __shared__ Walk<TILE> walk;  // thread 0's
@@ -347,7 +377,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
             const int s = threadIdx.x * per + i;
             if (s >= p.S) break;
             const Span sp = span_of<TILE>(p, s, 0);
-            sum += sp.tiles;
+            sum += units_of(sp);
             if (sp.bad && blockIdx.x == 0) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
         }
         sums[threadIdx.x] = sum;
@@ -359,11 +389,12 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
             tiles[i].unit = -1;
         }
         mbar_init(&joined, kWarps);
+        mbar_init(&freed, kWarps);
+        mbar_init(&queried, kWarps);
         mbar_init_fence();
     }
     __syncthreads();
     // scan of the threads' sums, in every warp
-    int total;           // units of this CTA's run
     {
         long long mine = 0;
 #pragma unroll
@@ -379,8 +410,11 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         const long long runs = all < p.ctas ? all : p.ctas;
         if (threadIdx.x == 0) seg[0].flags = seg[1].flags = -1;
         if (cta >= runs) return;
-        const long long u0 = cta * all / runs, u1 = (cta + 1) * all / runs;
-        total = (int)(u1 - u0);
+        // the first `all % runs` runs have one unit more
+        const long long each = all <= INT_MAX ? (int)all / (int)runs : all / runs;
+        const int more = (int)(all - each * runs);
+        const long long u0 = cta * each + min(cta, more);
+        const int total = (int)each + (cta < more ? 1 : 0);
         if (warp == 0) {
             const uint32_t here = __ballot_sync(0xFFFFFFFFu, u0 >= (incl - mine) * vheads &&
                                                                  u0 < incl * vheads);
@@ -398,7 +432,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     __syncthreads();
 
     if (warp == kWarps) {
-        copy_tiles<D, G, TILE, kSlots>(p, pieces, total, lane, smem_u32(smem), tiles, full, empty);
+        copy_tiles<D, G, TILE, kSlots>(p, pieces, lane, smem_u32(smem), tiles, full, empty);
         return;
     }
 
@@ -416,14 +450,14 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     auto pairs_at = [&](int b) {
         return kv_code_bytes(D, piece) + r * NG * 4 + (b & 1) * pairs_1 + (b >> 1) * pairs_2;
     };
-    uint32_t jparity = 0;
     int n = warp;  // this warp's units: those whose number in the run is warp modulo kWarps
     auto gave_up = [&](bool ok) {
         if (!ok && lane == 0) flag_status(p.status, MXQ_DEV_TIMEOUT);
         return !ok;
     };
 
-    for (int at_piece = 0, done = 0; done < total; ++at_piece) {
+    int joins = 0;
+    for (int at_piece = 0; !pieces[at_piece % kPieces].last; ++at_piece) {
         const Piece& sp = pieces[at_piece % kPieces];
         const int heads = sp.heads, rows = sp.toks * heads, head0 = sp.head0;
         const int p0 = sp.p0, p1 = p0 + sp.toks - 1, end = sp.end;
@@ -508,9 +542,8 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         }
         if (SH::kQueryShared) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&joined);
-            if (gave_up(warp_wait(&joined, jparity, p.wait_budget))) return;
-            jparity ^= 1u;
+            if (lane == 0) mbar_arrive(&queried);
+            if (gave_up(warp_wait(&queried, (uint32_t)at_piece & 1u, p.wait_budget))) return;
         }
 
         for (; n < end; n += kWarps) {
@@ -694,9 +727,10 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
         }
-        done = end;
 
-        // ---- the warps' results of this row tile become one
+        // ---- the warps' results of this row tile become one, once those of the last
+        // have been read
+        if (joins && gave_up(warp_wait(&freed, (uint32_t)(joins - 1) & 1u, p.wait_budget))) return;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             const float x = sum_rows(l[kt]);
@@ -711,6 +745,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                           SH::kPartialFloats;
 #pragma unroll 1
         for (int d0 = 0; d0 < D; d0 += kChunk) {
+            if (d0 && gave_up(warp_wait(&freed, (uint32_t)(joins - 1) & 1u, p.wait_budget))) return;
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 if (t / (kChunk / 16) != d0 / kChunk) continue;
@@ -728,8 +763,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&joined);
-            if (gave_up(warp_wait(&joined, jparity, p.wait_budget))) return;
-            jparity ^= 1u;
+            if (gave_up(warp_wait(&joined, (uint32_t)joins & 1u, p.wait_budget))) return;
             for (int e = threadIdx.x; e < SH::kRows * (kChunk / 4); e += kThreads - 32) {
                 const int row = e / (kChunk / 4), d = (e % (kChunk / 4)) * 4;
                 if (row >= rows) break;
@@ -771,12 +805,12 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&joined);
-            if (gave_up(warp_wait(&joined, jparity, p.wait_budget))) return;
-            jparity ^= 1u;
+            if (lane == 0) mbar_arrive(&freed);
+            ++joins;
         }
-        // everyone is done with this piece: its place takes a later one
-        if (threadIdx.x == 0) walk.next(p, &pieces[at_piece % kPieces], seg);
+        // everyone is done with the piece before this one: its place takes a later one
+        if (threadIdx.x == 0 && at_piece > 0)
+            walk.next(p, &pieces[(at_piece - 1) % kPieces], seg);
     }
 }
 

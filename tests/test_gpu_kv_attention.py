@@ -346,3 +346,9 @@ def test_long_runs_of_tiles(heads, page):
                 E = np.asarray(D ** -0.5 * (np.abs(k) @ np.abs(q[i, a])).max())
                 A = np.repeat(7.5 * (w @ V[1].astype(np.float64)), G)
                 assert (np.abs(o[i, a] - ref) <= ku.tolerance(ref, A, w @ np.abs(v), E, False)).all()
+
+
+def test_many_row_tiles_in_a_block():
+    # more one-tile sequences and heads to a block than its list of them holds
+    ctx = [1 + i % 3 for i in range(3000)]
+    Case(ctx, [1] * 3000, 8, 8, 64, 64, 16, seed=23).check(q_starts=None)
