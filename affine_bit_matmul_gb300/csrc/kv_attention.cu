@@ -48,17 +48,21 @@ namespace mxq {
 namespace {
 
 // What the end of a row tile costs a CTA (joining its warps, the next queries), in
-// tiles: the runs are cut equal with so many tiles that do nothing after each row
-// tile.  Measured for 64 sequences of 1024 to 8192 tokens, where the CTAs of short
-// ones took 81 us and those of long ones 52 us without it.
-constexpr int kEndTiles = 4;
+// tokens: the runs are cut equal with so many tokens that take no work after each
+// row tile.  64 sequences of 1024 to 8192 tokens take 88 us without it (the CTAs of
+// short ones 81 us, those of long ones 52), 78 with 128 tokens, 76 with 256, 74 with
+// 512.
+constexpr int kEndTokens = 512;
 
 // Sizes of a kernel for row tiles of 4 KT rows: tokens of a tile, compute warps,
-// CTAs per SM, tiles in the ring.
+// CTAs per SM, tiles in the ring.  Warps: as many as their registers allow, 16 an SM
+// with 128 registers each (D <= 128, up to 8 rows), 12 with 168, 8 with 255.  16 rows:
+// tiles of 32 tokens, which take 31 us for 32 sequences with a window of 1024 and 115
+// for 32 of 8192 tokens (64 tokens: 40 and 109).
 template <int D, int G, int KT>
 struct Shape {
     static constexpr int kRows = 4 * KT;
-    static constexpr int kTile = D == 256 ? 32 : 64;
+    static constexpr int kTile = D == 256 || KT == 4 ? 32 : 64;
     static constexpr int kCtas = 2;
     static constexpr int kStageBytes = kv_block_bytes(D, G, kTile);
     // the queries lie in shared memory where they would take 32 registers or more
@@ -134,8 +138,9 @@ constexpr int kPieces = 64;
 
 // One thread: lists the pieces of the CTA's run, the first kPieces at once and
 // one more whenever the warps are done with one; then one marked `last`.
+template <int TILE>
 __device__ __forceinline__ int units_of(const Span& sp) {
-    return sp.tiles ? sp.tiles + kEndTiles : 0;
+    return sp.tiles ? sp.tiles + kEndTokens / TILE : 0;
 }
 
 template <int TILE>
@@ -148,13 +153,13 @@ struct Walk {  // (no constructors: it lies in shared memory)
         s = s_;
         sp = span_of<TILE>(p, s, 0);
         const long long vheads = (long long)p.Hkv * p.head_parts;
-        while (at >= units_of(sp) * vheads) {
-            at -= units_of(sp) * vheads;
+        while (at >= units_of<TILE>(sp) * vheads) {
+            at -= units_of<TILE>(sp) * vheads;
             sp = span_of<TILE>(p, ++s, 0);
         }
         const unsigned first = (unsigned)at;  // below 2^31 units a sequence
-        const int vh = (int)(first / (unsigned)units_of(sp));
-        k = (int)(first % (unsigned)units_of(sp));
+        const int vh = (int)(first / (unsigned)units_of<TILE>(sp));
+        k = (int)(first % (unsigned)units_of<TILE>(sp));
         h = vh / p.head_parts;
         part = vh % p.head_parts;
         seq = 0;
@@ -164,7 +169,7 @@ struct Walk {  // (no constructors: it lies in shared memory)
         bool found = false;
         while (left && !found) {
             while (sp.tiles == 0) sp = span_of<TILE>(p, ++s, 0);
-            const int units = units_of(sp), n = min(left, units - k);
+            const int units = units_of<TILE>(sp), n = min(left, units - k);
             const int tiles = min(k + n, sp.tiles) - k;  // the others are the row tile's end
             if (tiles > 0) {
                 const int rep = p.Hq / p.Hkv;
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
             const int s = threadIdx.x * per + i;
             if (s >= p.S) break;
             const Span sp = span_of<TILE>(p, s, 0);
-            sum += units_of(sp);
+            sum += units_of<TILE>(sp);
             if (sp.bad && blockIdx.x == 0) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
         }
         sums[threadIdx.x] = sum;
