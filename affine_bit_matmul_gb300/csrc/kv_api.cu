@@ -22,6 +22,10 @@ bool cache_shape(int D, int G, int page_size) {
     return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128;
 }
 
+int page_shift_of(int page_size) {
+    return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+}
+
 bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 
 // How an attention call is cut into row tiles and CTAs.  Sequences whose rows
@@ -144,7 +148,8 @@ mxq_status mxq_kv_append(const void* k, long long k_row_stride, long long k_head
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pages, 16) || !aligned(slots, 4) ||
         !aligned(dev_status, 4))
         return MXQ_ERR_MISALIGNED;
-    const mxq_status st = mxq::check_current_device(nullptr);
+    int sms = 0;
+    const mxq_status st = mxq::check_current_device(&sms);
     if (st != MXQ_OK) return st;
     if (2LL * T * Hkv > (long long)kMaxInt * 4) return MXQ_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -165,8 +170,9 @@ mxq_status mxq_kv_append(const void* k, long long k_row_stride, long long k_head
     p.H = Hkv;
     p.n_pages = n_pages;
     p.page_size = page_size;
+    p.page_shift = page_shift_of(page_size);
     p.status = dev_status;
-    const cudaError_t err = mxq::launch_kv_append(p, D, group_size, s);
+    const cudaError_t err = mxq::launch_kv_append(p, D, group_size, sms, s);
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
@@ -179,7 +185,8 @@ mxq_status mxq_kv_read(const void* pages, const int32_t* slots, void* k_out, voi
     if (!aligned(pages, 16) || !aligned(slots, 4) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
         !aligned(dev_status, 4))
         return MXQ_ERR_MISALIGNED;
-    const mxq_status st = mxq::check_current_device(nullptr);
+    int sms = 0;
+    const mxq_status st = mxq::check_current_device(&sms);
     if (st != MXQ_OK) return st;
     if (2LL * T * Hkv > (long long)kMaxInt * 4) return MXQ_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -196,8 +203,9 @@ mxq_status mxq_kv_read(const void* pages, const int32_t* slots, void* k_out, voi
     p.H = Hkv;
     p.n_pages = n_pages;
     p.page_size = page_size;
+    p.page_shift = page_shift_of(page_size);
     p.status = dev_status;
-    const cudaError_t err = mxq::launch_kv_read(p, D, group_size, s);
+    const cudaError_t err = mxq::launch_kv_read(p, D, group_size, sms, s);
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
@@ -266,7 +274,7 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     p.window = window < kMaxInt ? window : kMaxInt;
     p.sinks = sinks < kMaxInt ? sinks : kMaxInt;
     p.scale_log2 = (float)(scale * 1.4426950408889634);
-    p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    p.page_shift = page_shift_of(page_size);
     p.status = dev_status;
     p.wait_budget = mxq::wait_budget_cycles();
     uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -170,11 +170,12 @@ struct KvRowsParams {
     uint8_t* pages;
     const int32_t* slots;
     int T, H, n_pages, page_size;
+    int page_shift;          // log2(page_size)
     int32_t* status;
 };
 
-cudaError_t launch_kv_append(const KvRowsParams& p, int D, int G, cudaStream_t stream);
-cudaError_t launch_kv_read(const KvRowsParams& p, int D, int G, cudaStream_t stream);
+cudaError_t launch_kv_append(const KvRowsParams& p, int D, int G, int sms, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvRowsParams& p, int D, int G, int sms, cudaStream_t stream);
 
 // Attention over the cache.  A row tile is up to `tile_rows` rows, each one
 // (token, query head) of one sequence and key/value head.

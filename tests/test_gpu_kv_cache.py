@@ -61,6 +61,41 @@ def test_append_and_read_bit_for_bit(D, G, page, T, H):
     assert np.array_equal(host(ko), ku.bf16(want.k[slots])) and np.array_equal(host(vo), ku.bf16(want.v[slots]))
 
 
+@pytest.mark.parametrize("T", [5, 700])  # below and above the size from which a warp takes 8 tokens
+def test_codes_halfway_next_to_halfway_and_of_every_size(T):
+    """Quotients that are halfway between two codes, one unit of the difference's last place from
+    it, and values from the smallest to the largest exponents: the codes are those of the
+    formula's subtraction and division in binary32."""
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    H, D, G, page = 2, 128, 32, 16
+    rng = np.random.default_rng(T)
+    x = rng.integers(0, 31, (2, T, H, D // G, G)).astype(np.float64) / 2  # codes and the halves between
+    x[..., 0], x[..., 1] = 0, 15
+    scale = rng.choice([1.0, 1.25, 1.5, 1.75], (2, T, H, D // G, 1)) * 2.0 ** rng.integers(-20, 20, (2, T, H, D // G, 1))
+    x = x * scale
+    low = rng.integers(0, 16, (2, T, H, D // G, 1)) / 2 * scale  # bias -low; tiny values differ from it by low and a bit
+    tiny = rng.random(x.shape) < 0.3
+    x = np.where(tiny, rng.choice([-1.0, 1.0], x.shape) * 2.0 ** rng.integers(-26, -16, x.shape) * scale, x - low)
+    x[..., 0], x[..., 1] = -low[..., 0], 15 * scale[..., 0] - low[..., 0]
+    wide = rng.random((2, T, H)) < 0.3
+    far = rng.choice([-1.0, 1.0], x.shape) * (1 + rng.random(x.shape)) * 2.0 ** rng.integers(-140, 126, x.shape)
+    spread = 2.0 ** rng.integers(-150, 1, (2, T, H, 1, 1))  # some groups all small
+    x = np.where(wide[..., None, None], far * np.where(far < 1, spread, 1), x)
+    small = rng.random((2, T, H)) < 0.1
+    x = np.where(small[..., None, None], rng.integers(-9, 9, x.shape) * 2.0 ** -133.0, x)  # the type's last places
+    k, v = (ku.bf16(a.reshape(T, H, D)) for a in x)
+    n_pages = T // page + 2
+    slots = np.arange(7, 7 + T).astype(np.int32)
+    want = ku.Cache(n_pages, H, D, page, G)
+    want.write(slots, k, v)
+    pages = torch.zeros(want.bytes.shape, dtype=torch.uint8, device="cuda")
+    mxq.kv_append(dev_bf16(k), dev_bf16(v), pages, i32(slots), group_size=G)
+    assert np.array_equal(pages.cpu().numpy(), want.bytes)
+
+
 def test_strided_rows_padding_and_bad_slots():
     import torch
 
