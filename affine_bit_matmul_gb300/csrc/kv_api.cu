@@ -31,8 +31,11 @@ bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 // How an attention call is cut into row tiles and CTAs.  Sequences whose rows
 // times query heads of a key/value head are at most 16 go through the kernel for
 // few rows (bound by the cache's bytes), the others through the tensor cores'
-// (bound by their products).  Measured for 8 query heads to a key head over 8192
-// tokens: 2 rows 16, 3 rows 24 of the products' 128.
+// (bound by their products).  32 sequences of 8192 tokens, 8 key/value heads of 128
+// values: the first takes 113 us for 16 rows, the second 277 for 20 rows and 284 for
+// 128; of 64 values 80 and 240, of 256 242 and 400.  Two row tiles of the first
+// would win up to 32 rows, but its weights are rounded against a group's range, not
+// against the values: more than a prompt's first rows, which see few tokens, bear.
 struct AttnPlan {
     int head_parts, part_heads, tile_rows, tile_toks, ctas;  // few rows
     int many, many_parts, many_heads, half_toks, many_toks, many_ctas, max_entries;

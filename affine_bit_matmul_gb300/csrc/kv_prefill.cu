@@ -49,7 +49,10 @@ constexpr int kParts = kTile / kPart;
 template <int D, int G>
 struct Shape {
     static constexpr int MT = D == 256 ? 1 : 2;    // halves of 128 rows
-    static constexpr int SB = D == 256 ? 2 : 1;    // score buffers of a half
+    // Tokens of one score tile; two of them in turn for each half, so that the tensor
+    // cores work on the next while one is weighed.
+    static constexpr int kCols = D == 256 ? 128 : 64;
+    static constexpr int kSubs = kTile / kCols;
     static constexpr int KB = D == 256 ? 1 : 2;    // key and value buffers
     static constexpr int kRows = 128 * MT;
     static constexpr int kQBytes = kRows * D * 2;
@@ -173,7 +176,7 @@ struct Shared {
     using SH = Shape<D, G>;
     uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
     uint64_t k_full[SH::KB], k_empty[SH::KB], v_full[SH::KB], v_empty[SH::KB];
-    uint64_t q_full[SH::MT], s_full[2], p_full[SH::MT], pv_done[SH::MT], drained[SH::MT];
+    uint64_t q_full[SH::MT], s_full[2 * SH::MT], p_full[2 * SH::MT], pv_done[SH::MT], drained[SH::MT];
     Piece pieces[kPieceRing];
     Meta meta[kMetaRing];
     uint32_t tmem;
@@ -484,12 +487,12 @@ template <int D, int G>
 __device__ bool issue_products(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t kbuf,
                                uint32_t vbuf, uint32_t tmem, int m, int lane) {
     using SH = Shape<D, G>;
-    constexpr int KB = SH::KB, SB = SH::SB;
-    constexpr uint32_t id_s = umma_idesc_f16(128, kTile), id_o = umma_idesc_f16(128, D);
-    const uint32_t o_col = tmem + 256 + m * D;
+    constexpr int KB = SH::KB, kCols = SH::kCols, kSubs = SH::kSubs;
+    constexpr uint32_t id_s = umma_idesc_f16(128, kCols), id_o = umma_idesc_f16(128, D);
+    const uint32_t o_col = tmem + 256 + m * D, s_cols = tmem + m * kTile;
     Pieces<D, G> list(sh, p.wait_budget);
     int jt = 0;   // units so far: key and value buffers
-    int at = 0;   // units of this half so far: its score buffers
+    int at = 0;   // score tiles of this half so far
     int nq = 0;   // pieces of this half so far
     for (;;) {
         const Piece* q = list.next();
@@ -511,59 +514,57 @@ __device__ bool issue_products(const KvAttnParams& p, Shared<D, G>& sh, uint32_t
         }
         if (!warp_wait_sleep(&sh.q_full[m], (uint32_t)nq & 1u, p.wait_budget)) return false;
         ++nq;
-        // scores of unit k of the piece
-        auto scores = [&](int k) {
-            const int buf = (jt + k) % KB, a = at + k;
-            if (!warp_wait_sleep(&sh.k_full[buf], (uint32_t)((jt + k) / KB) & 1u, p.wait_budget)) return false;
+        // scores of tile i of the piece
+        auto scores = [&](int i) {
+            const int j = jt + i / kSubs, sub = i % kSubs, buf = j % KB, a = at + i;
+            if (!warp_wait_sleep(&sh.k_full[buf], (uint32_t)(j / KB) & 1u, p.wait_budget)) return false;
             // the buffer's earlier weights have been used
-            if (k >= SB && !warp_wait_sleep(&sh.pv_done[m], (uint32_t)(a - SB) & 1u, p.wait_budget)) return false;
+            if (i >= 2 && !warp_wait_sleep(&sh.pv_done[m], (uint32_t)a & 1u, p.wait_budget)) return false;
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t s_col = tmem + (SB == 1 ? m : (a & 1)) * kTile;
+                const uint32_t s_col = s_cols + (a & 1) * kCols;
 #pragma unroll
                 for (int kb = 0; kb < D / 64; ++kb) {
                     const uint64_t ad = umma_desc_sw128(qbuf + (m * (D / 64) + kb) * (128 * 128));
-                    const uint64_t bd =
-                        umma_desc_sw128(kbuf + buf * SH::kOpBytes + kb * (kTile * 128));
+                    const uint64_t bd = umma_desc_sw128(kbuf + buf * SH::kOpBytes +
+                                                        (kb * kTile + sub * kCols) * 128);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        umma_bf16(s_col, ad + 2 * j, bd + 2 * j, id_s, kb | j ? 1u : 0u);
+                    for (int j4 = 0; j4 < 4; ++j4)
+                        umma_bf16(s_col, ad + 2 * j4, bd + 2 * j4, id_s, kb | j4 ? 1u : 0u);
                 }
-                umma_commit(&sh.s_full[SB == 1 ? m : (a & 1)]);
-                umma_commit(&sh.k_empty[buf]);
+                umma_commit(&sh.s_full[2 * m + (a & 1)]);
+                if (sub == kSubs - 1) umma_commit(&sh.k_empty[buf]);
             }
             __syncwarp();
             return true;
         };
-        if (SB == 2 && !scores(0)) return false;
-        for (int k = 0; k < count; ++k) {
-            if (SB == 1) {
-                if (!scores(k)) return false;
-            } else if (k + 1 < count) {
-                if (!scores(k + 1)) return false;
-            }
-            const int buf = (jt + k) % KB, a = at + k;
-            if (!warp_wait_sleep(&sh.v_full[buf], (uint32_t)((jt + k) / KB) & 1u, p.wait_budget) ||
-                !warp_wait_sleep(&sh.p_full[m], (uint32_t)a & 1u, p.wait_budget))
+        const int n_tiles = count * kSubs;
+        if (!scores(0)) return false;
+        for (int i = 0; i < n_tiles; ++i) {
+            if (i + 1 < n_tiles && !scores(i + 1)) return false;
+            const int j = jt + i / kSubs, sub = i % kSubs, buf = j % KB, a = at + i;
+            if (!warp_wait_sleep(&sh.v_full[buf], (uint32_t)(j / KB) & 1u, p.wait_budget) ||
+                !warp_wait_sleep(&sh.p_full[2 * m + (a & 1)], (uint32_t)(a >> 1) & 1u, p.wait_budget))
                 return false;
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t p_col = tmem + (SB == 1 ? m : (a & 1)) * kTile;
+                const uint32_t p_col = s_cols + (a & 1) * kCols;
 #pragma unroll
-                for (int tb = 0; tb < 2; ++tb) {
-                    const uint64_t bd = umma_desc_sw128(vbuf + buf * SH::kOpBytes + tb * (D * 128));
+                for (int tb = 0; tb < kCols / 64; ++tb) {
+                    const uint64_t bd = umma_desc_sw128(vbuf + buf * SH::kOpBytes +
+                                                        (sub * (kCols / 64) + tb) * (D * 128));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        umma_bf16_tmem_a(o_col, p_col + (tb * 4 + j) * 8, bd + 2 * j, id_o,
-                                         k | tb | j ? 1u : 0u);
+                    for (int j4 = 0; j4 < 4; ++j4)
+                        umma_bf16_tmem_a(o_col, p_col + (tb * 4 + j4) * 8, bd + 2 * j4, id_o,
+                                         i | tb | j4 ? 1u : 0u);
                 }
-                umma_commit(&sh.v_empty[buf]);
+                if (sub == kSubs - 1) umma_commit(&sh.v_empty[buf]);
                 umma_commit(&sh.pv_done[m]);
             }
             __syncwarp();
         }
         jt += count;
-        at += count;
+        at += n_tiles;
         list.done();
     }
 }
@@ -574,7 +575,7 @@ template <int D, int G>
 __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tmem, int m,
                         int quarter, int lane) {
     using SH = Shape<D, G>;
-    constexpr int KB = SH::KB, SB = SH::SB;
+    constexpr int KB = SH::KB, kCols = SH::kCols, kSubs = SH::kSubs;
     const int lr = quarter * 32 + lane;                 // row of the half
     const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
     const uint32_t o_at = tmem + t_lane + 256 + m * D;
@@ -588,7 +589,10 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
         const int heads = q->heads, tok0 = m * p.half_toks;
         const int toks = min(p.half_toks, q->toks - tok0);
         if (toks <= 0) {
-            jt += count;
+            // (the phases are passed one by one: a parity does not tell one from the next but one)
+            for (int k = 0; k < count; ++k, ++jt)
+                if (!warp_wait_sleep(&sh.v_full[jt % KB], (uint32_t)(jt / KB) & 1u, p.wait_budget))
+                    return false;
             list.done();
             continue;
         }
@@ -654,152 +658,158 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
 
         float mx = -INFINITY, mu = 0.f, l = 0.f;
         int e_o = 30;  // the output's sums are of values over 2^(e_o - 126)
-        for (int k = 0; k < count; ++k, ++jt, ++at) {
-            const int sidx = SB == 1 ? m : (at & 1);
-            const uint32_t s_at = tmem + t_lane + sidx * kTile;
-            const int t0 = unit_token(*q, q->k0 + k);
-            const bool inside = t0 + kTile - 1 <= first &&
-                                (!p.window || t0 > last - p.window || t0 + kTile <= p.sinks);
+        for (int k = 0; k < count; ++k, ++jt) {
             const volatile uint32_t* meta =
                 reinterpret_cast<const volatile uint32_t*>(&sh.meta[jt % kMetaRing]);
             // the values of this unit have been converted: their powers of two
             if (!warp_wait_sleep(&sh.v_full[jt % KB], (uint32_t)(jt / KB) & 1u, p.wait_budget))
                 return false;
-            const uint32_t v_exp = meta[1];
-            const uint32_t two = __vmaxu4(v_exp, v_exp >> 16), e_top = max(two & 0xFFu, (two >> 8) & 0xFFu);
-            const int e_new = max(e_o, (int)e_top);
-            if (!warp_wait_sleep(&sh.s_full[sidx], (uint32_t)(at / SB) & 1u, p.wait_budget))
-                return false;
-            tc_fence_after();
-            uint32_t xa[16], xb[16];
-            tmem_ld16(s_at, xa);
-            const uint32_t k_exp = meta[0];
-            uint32_t state = meta[2];
-            state |= state >> 6;            // 2 bits of each byte, together
-            state = (state | state >> 12) & 0xFFu;
-            const bool edge = state != 0xFF || !inside;
-            // what this row sees of columns c .. c + 15, as bits
-            auto sees = [&](int c) {
-                uint32_t bits = 0;
-                if (!((state >> (c / 16)) & 1)) return bits;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = t0 + c + i;
-                    const bool s = t <= pos && (!p.window || t > pos - p.window || t < p.sinks);
-                    bits |= (s ? 1u : 0u) << i;
-                }
-                return bits;
-            };
-            // Moves the maximum and the values' power of two: what has been summed, and
-            // the weights of this unit's first `c` columns, follow.
-            auto move = [&](float top, int c) {
-                const float mn = fmaxf(mx, top);
-                mu = mn == -INFINITY ? 0.f : mn;
-                const float a = exp2_approx(mx - mu);
-                mx = mn;
-                l *= a;
-                const float f = a * pow2_of(max(e_o - e_new + 127, 1));
-                e_o = e_new;
-                tmem_st_wait();
-                const uint32_t a2 = cvt_f16x2(f, f);
+            const uint32_t v_exps = meta[1];
+            const uint32_t two = __vmaxu4(v_exps, v_exps >> 16);
+            const int e_new = max(e_o, (int)max(two & 0xFFu, (two >> 8) & 0xFFu));
 #pragma unroll 1
-                for (int i = 0; i < c / 2; i += 8) {
-                    uint32_t y[8];
-                    tmem_ld8(s_at + i, y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = hmul2_f16(y[j], a2);
-                    tmem_st8(s_at + i, y);
-                }
-                bool ok = true;
-                if (k > 0) {
-                    // the sums so far, once the last unit's products are in
-                    ok = warp_wait_sleep(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget);
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int i = 0; i < D; i += 8) {
-                        uint32_t y[8];
-                        tmem_ld8(o_at + i, y);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                        tmem_st8(o_at + i, y);
+            for (int sub = 0; sub < kSubs; ++sub, ++at) {
+                const uint32_t s_at = tmem + t_lane + m * kTile + (at & 1) * kCols;
+                const int t0 = unit_token(*q, q->k0 + k) + sub * kCols;
+                const bool inside = t0 + kCols - 1 <= first &&
+                                    (!p.window || t0 > last - p.window || t0 + kCols <= p.sinks);
+                if (!warp_wait_sleep(&sh.s_full[2 * m + (at & 1)], (uint32_t)(at >> 1) & 1u, p.wait_budget))
+                    return false;
+                tc_fence_after();
+                uint32_t xa[16], xb[16];
+                tmem_ld16(s_at, xa);
+                // (the keys' part is complete now that there are scores)
+                const uint32_t k_exp = meta[0] >> (sub * kCols / 4), v_exp = v_exps >> (sub * kCols / 4);
+                uint32_t state = meta[2];
+                state |= state >> 6;              // 2 bits of each byte, together
+                state = ((state | state >> 12) & 0xFFu) >> (sub * kCols / 16);
+                constexpr uint32_t kThere = (1u << (kCols / 16)) - 1u;
+                const bool edge = (state & kThere) != kThere || !inside;
+                // what this row sees of columns c .. c + 15, as bits
+                auto sees = [&](int c) {
+                    uint32_t bits = 0;
+                    if (!((state >> (c / 16)) & 1)) return bits;
+    #pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int t = t0 + c + i;
+                        const bool s = t <= pos && (!p.window || t > pos - p.window || t < p.sinks);
+                        bits |= (s ? 1u : 0u) << i;
                     }
-                }
-                return ok;
-            };
-            // 16 columns: weights over the scores.  f: the scores' factor, off: what is
-            // added to them (with the maximum), back: the factor of the weights' sum.
-            auto weigh = [&](uint32_t (&x)[16], int c, float f, float shift, float back, auto masked) {
-                if constexpr (decltype(masked)::value) {
-                    const uint32_t bits = sees(c);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!((bits >> i) & 1u)) x[i] = 0xFF800000u;  // -inf
-                }
-                float t = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-#pragma unroll
-                for (int i = 2; i < 16; i += 2)
-                    t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                const bool over = __any_sync(0xFFFFFFFFu, t * f > mx + 8.f);
-                uint32_t y[8];
-                float sum;
-                auto weights = [&]() {
-                    const float off = shift - mu;
-                    const uint64_t f2 = pair_of(f, f), off2 = pair_of(off, off);
-                    uint64_t s0 = 0, s1 = 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float a, b;
-                        parts_of(fma_pair(pair_of(__uint_as_float(x[2 * i]),
-                                                  __uint_as_float(x[2 * i + 1])),
-                                          f2, off2), &a, &b);
-                        a = exp2_approx(a);
-                        b = exp2_approx(b);
-                        uint64_t& s = i & 1 ? s1 : s0;
-                        s = i > 1 ? add_pair(s, pair_of(a, b)) : pair_of(a, b);
-                        y[i] = cvt_f16x2(a, b);
-                    }
-                    float a, b;
-                    parts_of(add_pair(s0, s1), &a, &b);
-                    sum = a + b;
+                    return bits;
                 };
-                weights();  // most often the maximum stays, and this has not waited for the vote
-                if (over) {
-                    if (!move(t * f, c)) return false;
-                    weights();
-                }
-                l = fmaf(sum, back, l);
-                tmem_st8(s_at + c / 2, y);
-                return true;
-            };
-            bool ok = true;
-            if (e_new > e_o) ok = move(-INFINITY, 0);
-            auto all_columns = [&](auto masked) {
-                tmem_ld_wait_of(xa);
-#pragma unroll 1
-                for (int c = 0; c < kTile; c += 32) {
-                    tmem_ld16(s_at + c + 16, xb);
-                    const int ek = (k_exp >> (c / 4)) & 0xFF, de = ((v_exp >> (c / 4)) & 0xFF) - e_o;
-                    // (never zero: a query of zeros still has -inf where it sees nothing)
-                    const float f = fmaxf(unit * pow2_of(ek + 6), 0x1p-126f);  // 2^(e - 121)
-                    const float shift = (float)(7 + de);  // de <= 0
-                    const float back = pow2_of(min(127 - de, 254));
-                    ok = weigh(xa, c, f, shift, back, masked) && ok;
-                    tmem_ld_wait_of(xb);
-                    if (c + 32 < kTile) tmem_ld16(s_at + c + 32, xa);
-                    ok = weigh(xb, c + 16, f, shift, back, masked) && ok;
+                // Moves the maximum and the values' power of two: what has been summed, and
+                // the weights of this unit's first `c` columns, follow.
+                auto move = [&](float top, int c) {
+                    const float mn = fmaxf(mx, top);
+                    mu = mn == -INFINITY ? 0.f : mn;
+                    const float a = exp2_approx(mx - mu);
+                    mx = mn;
+                    l *= a;
+                    const float f = a * pow2_of(max(e_o - e_new + 127, 1));
+                    e_o = e_new;
+                    tmem_st_wait();
+                    const uint32_t a2 = cvt_f16x2(f, f);
+    #pragma unroll 1
+                    for (int i = 0; i < c / 2; i += 8) {
+                        uint32_t y[8];
+                        tmem_ld8(s_at + i, y);
+    #pragma unroll
+                        for (int j = 0; j < 8; ++j) y[j] = hmul2_f16(y[j], a2);
+                        tmem_st8(s_at + i, y);
+                    }
+                    bool ok = true;
+                    if (k + sub > 0) {
+                        // the sums so far, once the last tile's products are in
+                        ok = warp_wait_sleep(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget);
+                        tc_fence_after();
+    #pragma unroll 1
+                        for (int i = 0; i < D; i += 8) {
+                            uint32_t y[8];
+                            tmem_ld8(o_at + i, y);
+    #pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                            tmem_st8(o_at + i, y);
+                        }
+                    }
+                    return ok;
+                };
+                // 16 columns: weights over the scores.  f: the scores' factor, off: what is
+                // added to them (with the maximum), back: the factor of the weights' sum.
+                auto weigh = [&](uint32_t (&x)[16], int c, float f, float shift, float back, auto masked) {
+                    if constexpr (decltype(masked)::value) {
+                        const uint32_t bits = sees(c);
+    #pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (!((bits >> i) & 1u)) x[i] = 0xFF800000u;  // -inf
+                    }
+                    float t = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    #pragma unroll
+                    for (int i = 2; i < 16; i += 2)
+                        t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                    const bool over = __any_sync(0xFFFFFFFFu, t * f > mx + 8.f);
+                    uint32_t y[8];
+                    float sum;
+                    auto weights = [&]() {
+                        const float off = shift - mu;
+                        const uint64_t f2 = pair_of(f, f), off2 = pair_of(off, off);
+                        uint64_t s0 = 0, s1 = 0;
+    #pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float a, b;
+                            parts_of(fma_pair(pair_of(__uint_as_float(x[2 * i]),
+                                                      __uint_as_float(x[2 * i + 1])),
+                                              f2, off2), &a, &b);
+                            a = exp2_approx(a);
+                            b = exp2_approx(b);
+                            uint64_t& s = i & 1 ? s1 : s0;
+                            s = i > 1 ? add_pair(s, pair_of(a, b)) : pair_of(a, b);
+                            y[i] = cvt_f16x2(a, b);
+                        }
+                        float a, b;
+                        parts_of(add_pair(s0, s1), &a, &b);
+                        sum = a + b;
+                    };
+                    weights();  // most often the maximum stays, and this has not waited for the vote
+                    if (over) {
+                        if (!move(t * f, c)) return false;
+                        weights();
+                    }
+                    l = fmaf(sum, back, l);
+                    tmem_st8(s_at + c / 2, y);
+                    return true;
+                };
+                bool ok = true;
+                if (e_new > e_o) ok = move(-INFINITY, 0);
+                auto all_columns = [&](auto masked) {
                     tmem_ld_wait_of(xa);
-                }
-            };
-            if (edge) all_columns(std::true_type());
-            else all_columns(std::false_type());
-            if (!ok) return false;
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&sh.p_full[m]);
+    #pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        tmem_ld16(s_at + c + 16, xb);
+                        const int ek = (k_exp >> (c / 4)) & 0xFF, de = ((v_exp >> (c / 4)) & 0xFF) - e_o;
+                        // (never zero: a query of zeros still has -inf where it sees nothing)
+                        const float f = fmaxf(unit * pow2_of(ek + 6), 0x1p-126f);  // 2^(e - 121)
+                        const float shift = (float)(7 + de);  // de <= 0
+                        const float back = pow2_of(min(127 - de, 254));
+                        ok = weigh(xa, c, f, shift, back, masked) && ok;
+                        tmem_ld_wait_of(xb);
+                        if (c + 32 < kCols) tmem_ld16(s_at + c + 32, xa);
+                        ok = weigh(xb, c + 16, f, shift, back, masked) && ok;
+                        tmem_ld_wait_of(xa);
+                    }
+                };
+                if (edge) all_columns(std::true_type());
+                else all_columns(std::false_type());
+                if (!ok) return false;
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[2 * m + (at & 1)]);
+            }
         }
-        // ---- the row's result
-        if (!warp_wait_sleep(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget)) return false;
+        // ---- the row's result, once the products of the last two tiles are in
+        if ((count * kSubs > 1 && !warp_wait_sleep(&sh.pv_done[m], (uint32_t)at & 1u, p.wait_budget)) ||
+            !warp_wait_sleep(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget))
+            return false;
         tc_fence_after();
         const bool whole = q->flags == (kBegins | kEnds);
         const float up = pow2_of(e_o + 1) * 32.f;  // 2^(e_o - 121)
@@ -884,12 +894,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         }
         for (int i = 0; i < SH::MT; ++i) {
             mbar_init(&sh.q_full[i], 128);
-            mbar_init(&sh.p_full[i], 128);
             mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.drained[i], 1);
         }
-        mbar_init(&sh.s_full[0], 1);
-        mbar_init(&sh.s_full[1], 1);
+        for (int i = 0; i < 2 * SH::MT; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 128);  // (a warp may be a tile ahead of the others)
+        }
         mbar_init_fence();
     }
     if (warp == 18) {
