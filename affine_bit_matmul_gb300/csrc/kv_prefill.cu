@@ -170,13 +170,16 @@ __device__ __forceinline__ void sts32(uint32_t at, uint32_t a) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(a) : "memory");
 }
 
-// Barriers and small things that the warps share.
+// Barriers and small things that the warps share.  A wait names a phase by its parity, so
+// each is placed where the phase before has ended and the one after cannot end without
+// the waiting warp.  Those of the score tiles are two for each half, used in turn: the
+// softmax warps may be a tile apart.
 template <int D, int G>
 struct Shared {
     using SH = Shape<D, G>;
     uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
     uint64_t k_full[SH::KB], k_empty[SH::KB], v_full[SH::KB], v_empty[SH::KB];
-    uint64_t q_full[SH::MT], s_full[2 * SH::MT], p_full[2 * SH::MT], pv_done[SH::MT], drained[SH::MT];
+    uint64_t q_full[SH::MT], s_full[2 * SH::MT], p_full[2 * SH::MT], pv_done[2 * SH::MT], drained[SH::MT];
     Piece pieces[kPieceRing];
     Meta meta[kMetaRing];
     uint32_t tmem;
@@ -519,7 +522,8 @@ __device__ bool issue_products(const KvAttnParams& p, Shared<D, G>& sh, uint32_t
             const int j = jt + i / kSubs, sub = i % kSubs, buf = j % KB, a = at + i;
             if (!warp_wait_sleep(&sh.k_full[buf], (uint32_t)(j / KB) & 1u, p.wait_budget)) return false;
             // the buffer's earlier weights have been used
-            if (i >= 2 && !warp_wait_sleep(&sh.pv_done[m], (uint32_t)a & 1u, p.wait_budget)) return false;
+            if (i >= 2 && !warp_wait_sleep(&sh.pv_done[2 * m + (a & 1)], (uint32_t)((a >> 1) - 1) & 1u, p.wait_budget))
+                return false;
             tc_fence_after();
             if (elect_one()) {
                 const uint32_t s_col = s_cols + (a & 1) * kCols;
@@ -559,7 +563,7 @@ __device__ bool issue_products(const KvAttnParams& p, Shared<D, G>& sh, uint32_t
                                          i | tb | j4 ? 1u : 0u);
                 }
                 if (sub == kSubs - 1) umma_commit(&sh.v_empty[buf]);
-                umma_commit(&sh.pv_done[m]);
+                umma_commit(&sh.pv_done[2 * m + (a & 1)]);
             }
             __syncwarp();
         }
@@ -589,10 +593,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
         const int heads = q->heads, tok0 = m * p.half_toks;
         const int toks = min(p.half_toks, q->toks - tok0);
         if (toks <= 0) {
-            // (the phases are passed one by one: a parity does not tell one from the next but one)
-            for (int k = 0; k < count; ++k, ++jt)
-                if (!warp_wait_sleep(&sh.v_full[jt % KB], (uint32_t)(jt / KB) & 1u, p.wait_budget))
-                    return false;
+            jt += count;
             list.done();
             continue;
         }
@@ -658,6 +659,11 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
 
         float mx = -INFINITY, mu = 0.f, l = 0.f;
         int e_o = 30;  // the output's sums are of values over 2^(e_o - 126)
+        // The first scores come after the values of all units before this piece, of which
+        // a half without rows has not waited for any: a parity does not tell a phase from
+        // the next but one.
+        if (!warp_wait_sleep(&sh.s_full[2 * m + (at & 1)], (uint32_t)(at >> 1) & 1u, p.wait_budget))
+            return false;
         for (int k = 0; k < count; ++k, ++jt) {
             const volatile uint32_t* meta =
                 reinterpret_cast<const volatile uint32_t*>(&sh.meta[jt % kMetaRing]);
@@ -689,7 +695,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                 auto sees = [&](int c) {
                     uint32_t bits = 0;
                     if (!((state >> (c / 16)) & 1)) return bits;
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int t = t0 + c + i;
                         const bool s = t <= pos && (!p.window || t > pos - p.window || t < p.sinks);
@@ -709,24 +715,24 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                     e_o = e_new;
                     tmem_st_wait();
                     const uint32_t a2 = cvt_f16x2(f, f);
-    #pragma unroll 1
+#pragma unroll 1
                     for (int i = 0; i < c / 2; i += 8) {
                         uint32_t y[8];
                         tmem_ld8(s_at + i, y);
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < 8; ++j) y[j] = hmul2_f16(y[j], a2);
                         tmem_st8(s_at + i, y);
                     }
                     bool ok = true;
                     if (k + sub > 0) {
                         // the sums so far, once the last tile's products are in
-                        ok = warp_wait_sleep(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget);
+                        ok = warp_wait_sleep(&sh.pv_done[2 * m + ((at - 1) & 1)], (uint32_t)((at - 1) >> 1) & 1u, p.wait_budget);
                         tc_fence_after();
-    #pragma unroll 1
+#pragma unroll 1
                         for (int i = 0; i < D; i += 8) {
                             uint32_t y[8];
                             tmem_ld8(o_at + i, y);
-    #pragma unroll
+#pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
                             tmem_st8(o_at + i, y);
@@ -739,12 +745,12 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                 auto weigh = [&](uint32_t (&x)[16], int c, float f, float shift, float back, auto masked) {
                     if constexpr (decltype(masked)::value) {
                         const uint32_t bits = sees(c);
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (!((bits >> i) & 1u)) x[i] = 0xFF800000u;  // -inf
                     }
                     float t = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-    #pragma unroll
+#pragma unroll
                     for (int i = 2; i < 16; i += 2)
                         t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                     const bool over = __any_sync(0xFFFFFFFFu, t * f > mx + 8.f);
@@ -754,7 +760,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                         const float off = shift - mu;
                         const uint64_t f2 = pair_of(f, f), off2 = pair_of(off, off);
                         uint64_t s0 = 0, s1 = 0;
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             float a, b;
                             parts_of(fma_pair(pair_of(__uint_as_float(x[2 * i]),
@@ -783,7 +789,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                 if (e_new > e_o) ok = move(-INFINITY, 0);
                 auto all_columns = [&](auto masked) {
                     tmem_ld_wait_of(xa);
-    #pragma unroll 1
+#pragma unroll 1
                     for (int c = 0; c < kCols; c += 32) {
                         tmem_ld16(s_at + c + 16, xb);
                         const int ek = (k_exp >> (c / 4)) & 0xFF, de = ((v_exp >> (c / 4)) & 0xFF) - e_o;
@@ -806,9 +812,8 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
                 mbar_arrive(&sh.p_full[2 * m + (at & 1)]);
             }
         }
-        // ---- the row's result, once the products of the last two tiles are in
-        if ((count * kSubs > 1 && !warp_wait_sleep(&sh.pv_done[m], (uint32_t)at & 1u, p.wait_budget)) ||
-            !warp_wait_sleep(&sh.pv_done[m], (uint32_t)(at - 1) & 1u, p.wait_budget))
+        // ---- the row's result, once the products of the last tile, and so of all, are in
+        if (!warp_wait_sleep(&sh.pv_done[2 * m + ((at - 1) & 1)], (uint32_t)((at - 1) >> 1) & 1u, p.wait_budget))
             return false;
         tc_fence_after();
         const bool whole = q->flags == (kBegins | kEnds);
@@ -894,12 +899,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         }
         for (int i = 0; i < SH::MT; ++i) {
             mbar_init(&sh.q_full[i], 128);
-            mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.drained[i], 1);
         }
         for (int i = 0; i < 2 * SH::MT; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], 128);  // (a warp may be a tile ahead of the others)
+            mbar_init(&sh.pv_done[i], 1);
         }
         mbar_init_fence();
     }
