@@ -598,6 +598,18 @@ def gather_qmm_gateup(x, w_gate, s_gate, b_gate, w_up, s_up, b_up, expert_ids, r
 
 # ------------------------------------------------- 4-bit key/value cache
 
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on ``stream``, out of that stream's memory: what was freed on the
+    current one may still be in use there, and a workspace goes when the call returns."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if stream.device != device:
+        raise ValueError("stream is on %s but the tensors are on %s" % (stream.device, device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _heads(t, name, index=None, out=False):
     """Checks a bf16 [T, heads, D] tensor whose heads are contiguous; returns
     its (row, head) strides in values.  ``index``: the device it has to be on."""
@@ -749,7 +761,7 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
         if k_weight.dim() != 1 or k_weight.numel() != D:
             raise ValueError("k_weight must be [D]")
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        q_out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
         q_ors, q_ohs = Hq * D, D
     else:
         if q_out.shape != q.shape:
@@ -757,7 +769,7 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
         q_ors, q_ohs = _heads(q_out, "q_out", on, out=True)
     if k is not None:
         if k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
+            k_out = _empty((T, Hk, D), torch.bfloat16, dev, stream)
             k_ors, k_ohs = Hk * D, D
         else:
             if k_out.shape != k.shape:
@@ -837,11 +849,11 @@ def kv_read(pages, slots, head_dim: int, group_size: int = 64, k_out=None, v_out
     T = slots.numel()
     shape = (T, H, head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        k_out = _empty(shape, torch.bfloat16, dev, stream)
     elif tuple(k_out.shape) != shape:
         raise ValueError("k_out has shape %s, expected %s" % (tuple(k_out.shape), shape))
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        v_out = _empty(shape, torch.bfloat16, dev, stream)
     elif tuple(v_out.shape) != shape:
         raise ValueError("v_out has shape %s, expected %s" % (tuple(v_out.shape), shape))
     k_at = _flat(k_out, "k_out", torch.bfloat16, on)
@@ -896,7 +908,7 @@ def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int =
     elif T != S or max_q_len != 1:
         raise ValueError("without q_starts every sequence has one row: T must be S, max_q_len 1")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
         out_at = out.data_ptr()
     else:
         out_at = _flat(out, "out", torch.bfloat16, on)
@@ -913,7 +925,7 @@ def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int =
     L = lib()
     if workspace is None:
         need = L.mxq_kv_attention_workspace_bytes(T, S, Hq, Hkv, D, max_q_len)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty((need,), torch.uint8, dev, stream)
     ws_at = _flat(workspace, "workspace", torch.uint8, on)
     ctx, st = _launch_on(dev, stream)
     with ctx:

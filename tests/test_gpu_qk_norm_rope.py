@@ -112,3 +112,23 @@ def test_zero_rows_of_values_and_no_tokens():
     none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
     qo, ko = mxq.qk_norm_rope(none, none, q_weight=w, k_weight=w)
     assert qo.shape == (0, 2, 64) and ko.shape == (0, 2, 64)
+
+
+def test_memory_for_a_call_on_another_stream():
+    """What a call on a stream allocates is not what was just freed on the current one, which
+    may still be at work there."""
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    q = torch.randn((1024, 8, 128), device="cuda").bfloat16()
+    w = torch.ones(128, device="cuda").bfloat16()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    freed = torch.empty_like(q)
+    at = freed.data_ptr()
+    del freed
+    got, _ = mxq.qk_norm_rope(q, None, q_weight=w, stream=s)
+    torch.cuda.synchronize()
+    assert got.data_ptr() != at
+    assert torch.equal(got, mxq.qk_norm_rope(q, None, q_weight=w)[0])
