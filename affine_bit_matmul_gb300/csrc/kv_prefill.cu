@@ -19,12 +19,15 @@
 //             of the values of a unit each, loaded a unit ahead into registers
 //   16, 17    the matrix instructions of one half each: Q K^T, then P V
 //   18        the list of the run's pieces; tensor memory
-// The two halves are independent chains (scores, weights, sum), so one half's
-// products run while the other half's softmax does.  For D = 256 there is one
-// half with two score buffers instead.  The running maximum is only moved when
-// a score exceeds it by 2^8; the output's sums in tensor memory are rescaled
-// then, by the softmax warps.
-// Bound by the tensor cores: 4 D flops per visible pair and head.
+// The two halves are independent chains (scores, weights, sum), and each has two
+// score tiles in turn (of 64 tokens; D = 256 has one half with two tiles of 128), so that
+// products run while the softmax warps work.  The running maximum is only moved when
+// a score exceeds it by 2^8; the output's sums in tensor memory are rescaled then, by
+// the softmax warps.
+//   4 D flops per visible pair and head: a chunk of 2048 tokens that ends at 8192, 32 query
+// heads of 128 values, takes 288 us, 830 TFLOP/s (score tiles of 128 tokens, one a half:
+// 333 us); a whole prompt of 8192, 800 us.  Bound by the softmax warps' instructions:
+// the schedulers issue in 60% of the cycles, the tensor cores work in 36 to 48%.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -967,7 +970,8 @@ __device__ int block_scan(int x, int* total) {  // exclusive; 1024 threads
     return before + incl - x;
 }
 
-// The row tiles of all sequences and the units before each: one block.
+// The row tiles of all sequences and the units before each: one block, 3.5 us, most of
+// it the chain of three scans.
 __global__ void __launch_bounds__(1024) kv_plan_kernel(const KvAttnParams p) {
     pdl_launch_dependents();
     Entry* entries = reinterpret_cast<Entry*>(p.entries);
@@ -1030,7 +1034,8 @@ __global__ void __launch_bounds__(1024) kv_plan_kernel(const KvAttnParams p) {
     }
 }
 
-// Joins the pieces of cut row tiles; blockIdx.y takes a share of the rows.
+// Joins the pieces of cut row tiles; blockIdx.y takes a share of the rows.  13 us for
+// 151 cut tiles of 256 rows of 128 values (40 MB of fp32 sums, in L2).
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_rows_kernel(const KvAttnParams p, int tile_rows) {
     pdl_wait();
