@@ -27,7 +27,8 @@
 // call, in order, are cut into equal runs, one per CTA, whatever the lengths
 // of the sequences.  A run that begins or ends inside a row tile leaves its
 // (max, sum, weighted sum) in the workspace and a second kernel joins them in
-// order, so the result does not depend on timing.
+// order, so the result does not depend on timing.  Short calls whose row tiles can have
+// a CTA each are not cut.
 //
 // A CTA's warps take the units of its run in turn, each with a softmax state of
 // its own; they are joined at the end of a row tile.  One more warp fills the
@@ -40,8 +41,8 @@
 // sequences of 65536 to 131072 tokens, 5 query heads to a key head of 128 values,
 // 163 us, 5.9 TB/s; 64 of 1024 to 8192 tokens, 4 query heads, 74 us, 4.6 TB/s with the
 // ends of the row tiles.  From 16 rows on by the instructions around the products: 32
-// sequences of 8192 tokens 113 us, 2.6 TB/s.  One sequence of 573 tokens takes 11 us: two
-// kernels, each with its chain of loads (lengths, pages, tiles; pieces).
+// sequences of 8192 tokens 113 us, 2.6 TB/s.  One sequence of 573 tokens takes 7.6 us: a
+// chain of loads (length, pages, tiles) and two rounds of tiles in each warp.
 //   The matrix instructions' fp32 sums round towards zero.  Codes and weights are not
 // negative, so the sums of all weights times codes, of which the biases then take most
 // away again, are low by up to 2^-23 of themselves for each 16 tokens that a warp
@@ -174,6 +175,15 @@ struct Walk {  // (no constructors: it lies in shared memory)
         part = vh % p.head_parts;
         seq = 0;
         left = units;
+    }
+    // the run is one row tile
+    __device__ void whole(const KvAttnParams& p, int s_, int vh, const Span& span) {
+        s = s_;
+        sp = span;
+        h = vh / p.head_parts;
+        part = vh % p.head_parts;
+        k = seq = 0;
+        left = sp.tiles;
     }
     __device__ bool next(const KvAttnParams& p, Piece* out, Seg* seg) {
         bool found = false;
@@ -384,9 +394,10 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     const int cta = blockIdx.x;
     Seg* seg = reinterpret_cast<Seg*>(p.segs) + (long long)cta * 2;
 
-    // every CTA finds its own run: the tiles of all sequences, then its share
+    // every CTA finds its own run: the tiles of all sequences, then its share (or its
+    // row tile)
     const int per = (p.S + kThreads - 1) / kThreads;
-    {
+    if (!p.whole) {
         int sum = 0;
         for (int i = 0; i < per; ++i) {
             const int s = threadIdx.x * per + i;
@@ -409,8 +420,16 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         mbar_init_fence();
     }
     __syncthreads();
-    // scan of the threads' sums, in every warp
-    {
+    if (p.whole) {
+        if (threadIdx.x == 0) {
+            const int vheads = p.Hkv * p.head_parts, s = cta / vheads, vh = cta % vheads;
+            const Span sp = span_of<TILE>(p, s, 0);
+            if (sp.bad && vh == 0) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
+            walk.whole(p, s, vh, sp);
+            if (walk.next(p, &pieces[0], seg)) walk.next(p, &pieces[1], seg);
+        }
+    } else {
+        // scan of the threads' sums, in every warp
         long long mine = 0;
 #pragma unroll
         for (int i = 0; i < kWarps + 1; ++i) mine += sums[lane * (kWarps + 1) + i];
@@ -445,6 +464,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         }
     }
     __syncthreads();
+    if (pieces[0].last) return;
 
     if (warp == kWarps) {
         copy_tiles<D, G, TILE, kSlots>(p, pieces, lane, smem_u32(smem), tiles, full, empty);
@@ -942,6 +962,24 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> asked{0};  // devices on which the kernel may take its memory
     cudaError_t err = allow_shared(kv_attn_kernel<D, G, KT>, SH::kSmem, asked);
     if (err != cudaSuccess) return err;
+    // Where each CTA can have a row tile of its own and the longest is little longer than
+    // an equal share, by up to 2 tiles a warp, nothing is cut and no second kernel
+    // needed.  (The lengths are not known here, only how many pages or which window they
+    // are in.)  1 sequence of 573 tokens: 11.1 us cut, 7.6 whole; 32 of 4 rows with a
+    // window of 1024: 30.8 cut, 23.3 whole.
+    long long most = ((long long)p.max_pages * p.page_size + SH::kTile - 1) / SH::kTile;
+    if (p.window) {
+        const long long seen = ((long long)p.window + p.tile_toks - 2) / SH::kTile + 2 +
+                               ((long long)p.sinks + SH::kTile - 1) / SH::kTile;
+        most = most < seen ? most : seen;
+    }
+    const long long row_tiles = (long long)p.S * p.Hkv * p.head_parts;
+    if (row_tiles <= p.ctas && most * (p.ctas - row_tiles) <= 2LL * SH::kWarps * p.ctas) {
+        KvAttnParams one = p;
+        one.whole = 1;
+        kv_attn_kernel<D, G, KT><<<(unsigned)row_tiles, SH::kThreads, SH::kSmem, stream>>>(one);
+        return cudaGetLastError();
+    }
     const unsigned grid = (unsigned)p.ctas;
     kv_attn_kernel<D, G, KT><<<grid, SH::kThreads, SH::kSmem, stream>>>(p);
     err = cudaGetLastError();

@@ -196,6 +196,7 @@ struct KvAttnParams {
     int tile_toks;           // tokens in a row tile
     int min_rows, max_rows;  // a sequence's rows, for it to be this kernel's
     int ctas;
+    int whole;               // few rows: a CTA takes one row tile, all of it
     int page_shift;          // log2(page_size)
     int* segs;               // workspace: 2 descriptors per CTA
     float* partial;          // workspace: 2 partial results per CTA

@@ -352,3 +352,16 @@ def test_many_row_tiles_in_a_block():
     # more one-tile sequences and heads to a block than its list of them holds
     ctx = [1 + i % 3 for i in range(3000)]
     Case(ctx, [1] * 3000, 8, 8, 64, 64, 16, seed=23).check(q_starts=None)
+
+
+@pytest.mark.parametrize("D,G", SHAPES)
+@pytest.mark.parametrize("heads,rows", [(4, 1), (8, 1), (4, 4)])
+def test_tables_much_wider_than_the_sequences(D, G, heads, rows):
+    # as far as the call can know the sequences are long, so it cuts them over many blocks
+    import torch
+
+    c = Case([577, rows, 64, 300], [rows] * 4, heads, 1, D, G, 64, seed=D + G + heads + rows)
+    wide = torch.full((4, 600), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.table_d.shape[1]] = c.table_d
+    c.table_d = wide
+    c.check()
