@@ -24,6 +24,7 @@ group 64"):
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 __all__ = [
@@ -167,6 +168,28 @@ def lib():
         L.mxq_debug_set_wait_budget.restype = ctypes.c_longlong
         _lib_handle = L
     return _lib_handle
+
+
+_calls_module = None
+
+
+def _direct():
+    """The module that reads and checks the cache operators' tensors (``csrc/torch_calls.cpp``),
+    with the library's functions; raises if it is not built."""
+    global _calls_module
+    if _calls_module is None:
+        L = lib()
+        _torch()
+        try:
+            module = importlib.import_module("._calls", __name__)
+        except ImportError as e:
+            raise RuntimeError("_calls.so is not built; run affine_bit_matmul_gb300.build.build() "
+                               "before using the cache operators") from e
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.mxq_qk_norm_rope, L.mxq_kv_append, L.mxq_kv_read, L.mxq_kv_attention,
+            L.mxq_kv_attention_workspace_bytes)))
+        _calls_module = module
+    return _calls_module
 
 
 def _status_string(status: int) -> str:
@@ -727,6 +750,11 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     ``q`` bf16 [T, Hq, D] and ``k`` bf16 [T, Hk, D] or None may be slices of
     one projection's output (heads contiguous, strides multiples of 8);
     ``q_out``/``k_out`` may be ``q``/``k`` themselves.  Returns (q_out, k_out)."""
+    if stream is None:
+        done = _direct().qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, weight_offset,
+                                     interleaved, rope_scale, q_out, k_out)
+        if done is not None:
+            return done
     torch = _torch()
     q_rs, q_hs = _heads(q, "q")
     dev = q.device
@@ -816,6 +844,8 @@ def kv_append(k, v, pages, slots, group_size: int = 64, dev_status=None, stream=
     """Encodes the rows ``k``, ``v`` (bf16 [T, kv_heads, D], heads contiguous)
     to 4 bits and writes row t to slot ``slots[t]`` (int32 [T], page *
     page_size + token; negative: skipped) of the cache ``pages``."""
+    if stream is None and _direct().kv_append(k, v, pages, slots, group_size, dev_status) is not None:
+        return pages
     torch = _torch()
     k_rs, k_hs = _heads(k, "k")
     dev = k.device
@@ -841,6 +871,10 @@ def kv_read(pages, slots, head_dim: int, group_size: int = 64, k_out=None, v_out
             dev_status=None, stream=None):
     """The rows of ``slots`` (int32 [T]) out of the cache: (k, v) bf16 [T,
     kv_heads, head_dim]; zeros for a negative slot."""
+    if stream is None:
+        done = _direct().kv_read(pages, slots, head_dim, group_size, k_out, v_out, dev_status)
+        if done is not None:
+            return done
     torch = _torch()
     at, n_pages, H, page_size = _cache(pages, head_dim, group_size, None)
     dev = pages.device
@@ -885,6 +919,11 @@ def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int =
     tokens up to its own and the first ``sinks``.  ``scale`` defaults to
     D^-1/2.  ``lse`` (fp32 [T, heads]) receives the log sum exp.  Returns out
     bf16 [T, heads, D]; a row that sees nothing is 0."""
+    if stream is None:
+        done = _direct().kv_attention(q, pages, page_table, ctx_lens, q_starts, max_q_len, group_size, scale,
+                                     window, sinks, out, lse, workspace, dev_status)
+        if done is not None:
+            return done
     torch = _torch()
     q_rs, q_hs = _heads(q, "q")
     dev = q.device

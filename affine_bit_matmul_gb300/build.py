@@ -1,8 +1,9 @@
 """Compile the CUDA library ``libmxq.so`` for sm_103a, in-tree.
 
 Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into
-``affine_bit_matmul_gb300/libmxq.so`` (static CUDA runtime).  Rebuilds only
-when a source or header is newer than the library.
+``affine_bit_matmul_gb300/libmxq.so`` (static CUDA runtime).  ``csrc/torch_calls.cpp``
+becomes the Python module ``_calls.so`` beside it, which reads the tensors of the small
+calls.  Rebuilds only when a source or header is newer than what it makes.
 """
 
 from __future__ import annotations
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxq.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -36,16 +38,41 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def calls_source():
+    return os.path.join(CSRC, "torch_calls.cpp")
+
+
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
+    return sources() + [calls_source()] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
         os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _build_calls(cuda: str):
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    libs = os.path.join(home, "lib")
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "g++", "-O2", "-shared", "-fPIC", "-std=c++17",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           calls_source(), "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath," + libs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s%s" % (calls_source(), r.stdout, r.stderr))
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -66,7 +93,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_build_calls, os.path.dirname(os.path.dirname(os.path.realpath(cc))))
         objs = list(ex.map(compile_one, sources()))
+        calls.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -179,3 +179,88 @@ def test_pages_past_four_gigabytes():
     o = mxq.kv_attention(dev_bf16(q), pages, i32(table), i32([70]), group_size=G)
     ref, _, A, B, E = ku.attention(q, want, [[0, 1]], [70], [0, 1], D ** -0.5)
     assert (np.abs(host(o) - ref) <= ku.tolerance(ref, A, B, E, False)).all()
+
+
+def layer_calls(mxq, stream, given=False):
+    """All four operators on slices of one projection's output; what they return."""
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rows = torch.randn((37, 12, 128), generator=gen, device="cuda").bfloat16()
+    q, k, v = rows[:, :8], rows[:, 8:10], rows[:, 10:]
+    w = torch.rand(128, generator=gen, device="cuda").bfloat16()
+    freq, scale = mxq.rope_inv_freq(64, device="cuda")
+    pos, slots = i32(np.arange(37)), i32(np.r_[np.arange(32, 64), np.arange(5)])
+    pages = torch.zeros((2, 2, mxq.kv_block_bytes(128, 32, 32)), dtype=torch.uint8, device="cuda")
+    empty = dict(device="cuda", dtype=torch.bfloat16)
+    out = [torch.empty((37, h, 128), **empty) for h in (8, 2, 2, 2, 8)] if given else [None] * 5
+    lse = torch.empty((37, 8), device="cuda") if given else None
+    status = i32([7]) if given else None
+    qr, kr = mxq.qk_norm_rope(q, k, pos, freq, w, w, weight_offset=1.0, interleaved=True, rope_scale=scale,
+                              q_out=out[0], k_out=out[1], stream=stream)
+    assert mxq.kv_append(kr, v, pages, slots, group_size=32, dev_status=status, stream=stream) is pages
+    k4, v4 = mxq.kv_read(pages, slots, 128, group_size=32, k_out=out[2], v_out=out[3], stream=stream)
+    o = mxq.kv_attention(qr, pages, i32([[1, 0]]), i32([37]), i32([0, 37]), 37, group_size=32, window=20, sinks=2,
+                         out=out[4], lse=lse, dev_status=status, stream=stream)
+    torch.cuda.synchronize()
+    if given:
+        assert qr is out[0] and kr is out[1] and k4 is out[2] and v4 is out[3] and o is out[4]
+        assert int(status.item()) == 0 and bool(lse.isfinite().all())
+    return qr, kr, pages, k4, v4, o
+
+
+def test_the_same_on_a_given_stream_and_with_given_outputs():
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    first = layer_calls(mxq, None)
+    for got in (layer_calls(mxq, None, True), layer_calls(mxq, torch.cuda.current_stream()),
+                layer_calls(mxq, torch.cuda.current_stream(), True)):
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_refusals_of_tensors_on_the_device():
+    import torch
+
+    import affine_bit_matmul_gb300 as mxq
+
+    q = torch.zeros((4, 8, 128), device="cuda").bfloat16()
+    k = torch.zeros((4, 2, 128), device="cuda").bfloat16()
+    pages = torch.full((2, 2, mxq.kv_block_bytes(128, 16, 64)), 3, dtype=torch.uint8, device="cuda")
+    slots, table, lens = i32([0, 1, 2, 3]), i32([[0], [1], [0], [1]]), i32([1, 1, 1, 1])
+    pos, freq = i32([0, 1, 2, 3]), mxq.rope_inv_freq(128, device="cuda")[0]
+    one = torch.zeros((4, 1, 128), device="cuda").bfloat16()
+    calls = [
+        (ValueError, lambda: mxq.qk_norm_rope(q, k[:3], pos, freq)),
+        (ValueError, lambda: mxq.qk_norm_rope(q, k, pos[:3], freq)),
+        (ValueError, lambda: mxq.qk_norm_rope(q, k, pos.cpu(), freq)),
+        (ValueError, lambda: mxq.qk_norm_rope(q, None, pos, freq, k_out=k)),
+        (ValueError, lambda: mxq.qk_norm_rope(q, k, pos, freq, q_out=one.expand(4, 8, 128))),
+        (TypeError, lambda: mxq.qk_norm_rope(q, k, pos.long(), freq)),
+        (TypeError, lambda: mxq.qk_norm_rope(q.float(), k, pos, freq)),
+        (ValueError, lambda: mxq.kv_append(k, q, pages, slots)),
+        (ValueError, lambda: mxq.kv_append(k, k, pages, slots[:3])),
+        (ValueError, lambda: mxq.kv_append(q, q, pages, slots)),
+        (ValueError, lambda: mxq.kv_append(k, k, pages, slots, group_size=16)),
+        (ValueError, lambda: mxq.kv_append(k.transpose(1, 2).contiguous().transpose(1, 2), k, pages, slots)),
+        (TypeError, lambda: mxq.kv_append(k, k, pages.int(), slots)),
+        (ValueError, lambda: mxq.kv_read(pages, slots, 96)),
+        (ValueError, lambda: mxq.kv_read(pages, slots, 128, k_out=q)),
+        (TypeError, lambda: mxq.kv_read(pages, slots.float(), 128)),
+        (ValueError, lambda: mxq.kv_attention(q[:3], pages, table, lens)),
+        (ValueError, lambda: mxq.kv_attention(q[:, :7], pages, table, lens)),
+        (ValueError, lambda: mxq.kv_attention(q, pages, table[0], lens)),
+        (ValueError, lambda: mxq.kv_attention(q, pages, table, lens, max_q_len=0)),
+        (ValueError, lambda: mxq.kv_attention(q, pages, table, lens, lse=torch.zeros(4, 7, device="cuda"))),
+        (TypeError, lambda: mxq.kv_attention(q, pages, table, lens, out=q.float())),
+        (RuntimeError, lambda: mxq.kv_attention(q, pages, table, lens, scale=float("nan"))),
+        (RuntimeError, lambda: mxq.kv_attention(q, pages, table, lens, window=-1)),
+        (RuntimeError, lambda: mxq.kv_attention(q, pages, table, lens,
+                                                workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))),
+    ]
+    for error, f in calls:
+        with pytest.raises(error):
+            f()
+    torch.cuda.synchronize()
+    assert bool((pages == 3).all())
