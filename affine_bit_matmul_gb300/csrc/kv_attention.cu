@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     __shared__ Piece pieces[kPieces];
     __shared__ Walk<TILE> walk;  // thread 0's
     __shared__ int sums[kThreads];
-    pdl_launch_dependents();  // the joining kernel waits for this one's end by itself
+    // the joining kernel waits for this one's end by itself; what else follows may not
+    if (!p.whole) pdl_launch_dependents();
     float* join = reinterpret_cast<float*>(smem + SH::kRingBytes);
     float2* stat = reinterpret_cast<float2*>(smem + SH::kRingBytes + SH::kJoinBytes);
     uint4* queries = reinterpret_cast<uint4*>(smem + SH::kSmem - SH::kQueryBytes);
