@@ -13,8 +13,8 @@
 //      the low half, token 2 i + 1 in the high half.
 // So a lane's operands of 8 tokens are one 16-byte load without bank
 // conflicts, a K word's nibbles pair up along the values (0 with 4, 1 with 5,
-// ...) and a V word's along the tokens, and either pair becomes two bf16
-// numbers 16 + q with one shift and one three-input logic operation.
+// ...) and a V word's along the tokens, and four masks and one shift make the
+// pairs of a word four registers of f16 operands.
 #pragma once
 
 #include <cstdint>
