@@ -25,7 +25,7 @@
 // a score exceeds it by 2^8; the output's sums in tensor memory are rescaled then, by
 // the softmax warps.
 //   4 D flops per visible pair and head: a chunk of 2048 tokens that ends at 8192, 32 query
-// heads of 128 values, takes 288 us, 830 TFLOP/s (score tiles of 128 tokens, one a half:
+// heads of 128 values, takes 285 us, 840 TFLOP/s (score tiles of 128 tokens, one a half:
 // 333 us); a whole prompt of 8192, 800 us.  Bound by the softmax warps' instructions:
 // the schedulers issue in 60% of the cycles, the tensor cores work in 36 to 48%.
 #include <cstdint>
@@ -44,8 +44,10 @@ constexpr int kThreads = 608;
 constexpr int kPieceRing = 8;
 constexpr int kMetaRing = 4;
 // What the ends of a row tile cost (queries in, output out), in units, while the runs
-// are cut: 15000 cycles against 6200 of a unit.
-constexpr int kEndUnits = 2;
+// are cut.  8 whole prompts of 2048 tokens, 32 query heads of 128 values: 782, 625, 538,
+// 469, 449, 460, 483 us with 0, 1, 2, 3, 4, 5, 8; 16 of 300: 110, 86, 85, 87, 81, 82, 87;
+// the longest calls do not care.
+constexpr int kEndUnits = 4;
 constexpr int kPart = 32;            // tokens that share a power of two
 constexpr int kParts = kTile / kPart;
 
