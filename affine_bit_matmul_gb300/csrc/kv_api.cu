@@ -32,8 +32,8 @@ bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 // times query heads of a key/value head are at most 16 go through the kernel for
 // few rows (bound by the cache's bytes), the others through the tensor cores'
 // (bound by their products).  32 sequences of 8192 tokens, 8 key/value heads of 128
-// values: the first takes 113 us for 16 rows, the second 277 for 20 rows and 284 for
-// 128; of 64 values 80 and 240, of 256 242 and 400.  Two row tiles of the first
+// values: the first takes 113 us for 16 rows, the second 260 for 20 rows and 267 for
+// 128; of 64 values 82 and 242, of 256 242 and 406.  Two row tiles of the first
 // would win up to 32 rows, but its weights are rounded against a group's range, not
 // against the values: more than a prompt's first rows, which see few tokens, bear.
 struct AttnPlan {

@@ -26,7 +26,7 @@
 // the softmax warps.
 //   4 D flops per visible pair and head: a chunk of 2048 tokens that ends at 8192, 32 query
 // heads of 128 values, takes 285 us, 840 TFLOP/s (score tiles of 128 tokens, one a half:
-// 333 us); a whole prompt of 8192, 800 us.  Bound by the softmax warps' instructions:
+// 333 us); a whole prompt of 8192, 642 us.  Bound by the softmax warps' instructions:
 // the schedulers issue in 60% of the cycles, the tensor cores work in 36 to 48%.
 #include <cstdint>
 #include <cuda_bf16.h>
