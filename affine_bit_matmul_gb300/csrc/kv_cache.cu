@@ -244,8 +244,9 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const KvRowsPara
 #pragma unroll
         for (int o = 1; o < G / 8; o <<= 1)
             ends = bf16x2_min(ends, __shfl_xor_sync(0xFFFFFFFFu, ends, o));
-        const float b = __fadd_rn(value_of(ends, 0), 0.f);  // -0 -> +0
-        const float range = __fsub_rn(-value_of(ends, 1), b);
+        // -0 -> +0 at both ends: a range of -0 would be stored as a scale of -0
+        const float b = __fadd_rn(value_of(ends, 0), 0.f);
+        const float range = __fsub_rn(__fadd_rn(-value_of(ends, 1), 0.f), b);
         const float s = bf16_round(__fdiv_rn(range, 15.f));
         const uint32_t word = codes_of(x[i], s, b);
         const uint32_t halves = w.is_v ? halves_of(word) : 0u;
