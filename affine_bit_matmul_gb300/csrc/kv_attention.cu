@@ -679,10 +679,21 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                 over |= top[kt] > m[kt] + 8.f;
             }
             if (__any_sync(0xFFFFFFFFu, over)) {
-                // (a scale with its sign set comes here every time)
-                uint32_t big = __reduce_max_sync(0xFFFFFFFFu, scales & 0x7FFFu);
-                if (scales > 0x7FFFu) big = 0x7F00u;
-                big = __reduce_max_sync(0xFFFFFFFFu, big);
+                uint32_t big = __reduce_max_sync(0xFFFFFFFFu, scales);
+                if (big > 0x7FFFu) {
+                    // a scale with its sign set, which comes here every time: only the sizes count
+                    uint32_t size = 0;
+#pragma unroll 1
+                    for (int b = 0; b < SUB; ++b) {
+                        uint32_t pr0[NG], pr1[NG];
+                        load_pairs<NG>(at + v_off + pairs_at(b), pr0);
+                        load_pairs<NG>(at + v_off + pairs_at(b) + 8 * NG * 4, pr1);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+                            size = max(size, max(pr0[g] & 0x7FFFu, pr1[g] & 0x7FFFu));
+                    }
+                    big = __reduce_max_sync(0xFFFFFFFFu, size);
+                }
                 const int e_new = max(v_exp, min((int)(big >> 7), 254));
                 const float fv = pow2_of(max(v_exp - e_new + 127, 1));
                 v_exp = e_new;

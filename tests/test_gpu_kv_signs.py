@@ -1,4 +1,5 @@
-"""Signs in the paged 4-bit key/value cache: groups of negative zeros going in."""
+"""Signs in the paged 4-bit key/value cache: groups of negative zeros going in, and
+pairs whose scale is negative in what the attention reads."""
 
 import numpy as np
 import pytest
@@ -73,4 +74,44 @@ def test_attention_after_a_token_of_negative_zeros(D, G, rows):
     c.cache = fresh
     c.pages_d = torch.full(fresh.bytes.shape, 0xFF, dtype=torch.uint8, device="cuda")
     mxq.kv_append(dev_bf16(k[held]), dev_bf16(v[held]), c.pages_d, i32(held), group_size=G)
+    c.check()
+
+
+def turned(cache, slots, which):
+    """Gives the groups `which` [slots, H, D/G] of the values at `slots` a negative scale: the same
+    codes count down from the group's maximum."""
+    D, G, page = cache.D, cache.group, cache.page
+    half = cache.bytes.shape[-1] // 2
+    for row, slot in enumerate(slots):
+        p, t = slot // page, slot % page
+        for h in range(cache.H):
+            first = half + page * D // 2 + t * (D // G) * 4
+            pairs = cache.bytes[p, h, first:first + D // G * 4].view(np.uint16).reshape(-1, 2)
+            s = (pairs[:, 0].astype(np.uint32) << 16).view(np.float32)
+            b = (pairs[:, 1].astype(np.uint32) << 16).view(np.float32)
+            top = ku.bf16(b + 15 * s)
+            m = which[row, h]
+            q = (cache.v[slot, h].reshape(-1, G) - b[:, None].astype(np.float64)) / np.where(s == 0, 1, s)[:, None]
+            now = top[:, None] - s[:, None].astype(np.float64) * np.rint(q)
+            cache.v[slot, h] = np.where(m[:, None], now, cache.v[slot, h].reshape(-1, G)).reshape(-1)
+            pairs[m, 0] ^= 0x8000
+            pairs[m, 1] = ku.bf16_bits(top)[m]
+
+
+@pytest.mark.parametrize("D,G", SHAPES)
+@pytest.mark.parametrize("heads,rows", [(4, 1), (8, 1), (4, 4), (4, 40)])
+def test_values_with_negative_scales(D, G, heads, rows):
+    import torch
+
+    c = Case([330, 90, 17], [rows, rows, min(rows, 17)], heads, 1, D, G, 32, seed=D + heads + rows)
+    rng = np.random.default_rng(G)
+    slots = np.flatnonzero((c.cache.v != 0).any((1, 2)))
+    turned(c.cache, slots, rng.random((len(slots), 1, D // G)) < 0.1)
+    c.pages_d = torch.from_numpy(c.cache.bytes).cuda()
+    c.check()
+    # and all of them
+    c = Case([200, 90], [rows, rows], heads, 1, D, G, 16, seed=D + heads + rows)
+    slots = np.flatnonzero((c.cache.v != 0).any((1, 2)))
+    turned(c.cache, slots, np.ones((len(slots), 1, D // G), dtype=bool))
+    c.pages_d = torch.from_numpy(c.cache.bytes).cuda()
     c.check()
