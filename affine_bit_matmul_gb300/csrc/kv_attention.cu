@@ -44,10 +44,14 @@
 // sequences of 8192 tokens 113 us, 2.6 TB/s.  One sequence of 573 tokens takes 7.6 us: a
 // chain of loads (length, pages, tiles) and two rounds of tiles in each warp.
 //   The matrix instructions' fp32 sums round towards zero.  Codes and weights are not
-// negative, so the sums of all weights times codes, of which the biases then take most
-// away again, are low by up to 2^-23 of themselves for each 16 tokens that a warp
-// adds: over 100000 tokens of values around zero the result is off by 1.4e-3 of its norm,
-// a little less than its rounding to bf16 (1.7e-3).
+// negative, so their products add up to sums of which the biases then take most away
+// again, and what a long chain of them loses is a good part of a small result: of 40 sequences of
+// 131072 tokens of values around zero 1.2e-2 of the norm for 4 rows, 5.9e-2 for 16, where the
+// rounding to bf16 is 1.7e-3.  The values of a group share most of that sum.  So every 512
+// tokens a warp moves a group's mean from the sums to the biases': what stays is no larger
+// than the result, and a chain loses parts of 512 tokens' products only.  The same
+// calls are off by 1.8e-3 in all, the rest beside the rounding being the weights' 11 bits; 256 tokens
+// gain 1e-5 more.  Time: none at 4 rows, 2% at 16.
 #include <climits>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -57,6 +61,10 @@
 
 namespace mxq {
 namespace {
+
+// Tokens whose value products a warp adds before it takes out what the values of a group
+// have in common.
+constexpr int kChainTokens = 512;
 
 // What the end of a row tile costs a CTA (joining its warps, the next queries), in
 // tokens: the runs are cut equal with so many tokens that take no work after each
@@ -502,7 +510,6 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         uint4 qf[VT][SH::kQueryShared ? 1 : U];
         float qsum[KT][NG];    // sum of a row's values over a group, in the products' unit
         float unit[KT];        // the factor that makes scores (times log2 e) of the sums
-        int pos[KT];
         float acc[VT][MT][4];
         float pb[KT][NG], l[KT], m[KT], mu[KT];
         int v_exp = 20;        // the values' scales are below 2^(v_exp - 126) ...
@@ -568,8 +575,6 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                 l[kt] = 0.f;
                 m[kt] = -INFINITY;
                 mu[kt] = 0.f;
-                const int row = kt * 4 + i4;
-                pos[kt] = row < rows ? p0 + row / heads : -1;
             }
 #pragma unroll
             for (int t = 0; t < MT; ++t)
@@ -583,6 +588,29 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         }
 
         for (; n < end; n += kWarps) {
+            if (n / kWarps % (kChainTokens / TILE) == kChainTokens / TILE - 1) {
+                // ---- the mean of a row's sums over a group goes to where its biases are summed,
+                // an eighth in each of the column's lanes
+                const float down = pow2_of(max(v_exp - 6, 1));
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    const int vt = kt / 2, c = kt & 1;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        float x = 0.f;
+#pragma unroll
+                        for (int t = g * G / 16; t < (g + 1) * G / 16; ++t)
+                            x += fmaf(acc[vt][t][2 + c], 0.0625f, acc[vt][t][c]);
+                        x = sum_rows(x) * (1.f / G);
+#pragma unroll
+                        for (int t = g * G / 16; t < (g + 1) * G / 16; ++t) {
+                            acc[vt][t][c] -= x;
+                            acc[vt][t][2 + c] = fmaf(x, -16.f, acc[vt][t][2 + c]);
+                        }
+                        pb[kt][g] = fmaf(x * down, 0x1p21f, pb[kt][g]);
+                    }
+                }
+            }
             const int slot = n % kSlots;
             if (gave_up(unit_comes(&tiles[slot].unit, n, p.wait_budget) &&
                         warp_wait_sleep(&full[slot], (uint32_t)(n / kSlots) & 1u, p.wait_budget)))
@@ -633,6 +661,12 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
             }
             if (!(tile.state & kAll)) {
                 // some row does not see some token; what no row sees may hold anything
+                int pos[KT];
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    const int row = kt * 4 + i4;
+                    pos[kt] = row < rows ? p0 + row / heads : -1;
+                }
 #pragma unroll
                 for (int b = 0; b < SUB; ++b) {
 #pragma unroll
