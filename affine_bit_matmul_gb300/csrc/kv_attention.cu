@@ -73,6 +73,13 @@ constexpr int kChainTokens = 512;
 // 512.
 constexpr int kEndTokens = 512;
 
+// A call is left uncut only if none of its row tiles can have more tiles than this: however
+// ragged the batch, the others then do not wait long for the block of the longest.  38
+// sequences, 8 key heads of 128 values, one as long as possible and the others of 64 tokens,
+// uncut and cut: 4 rows 12.2 and 14.5 us for 32 tiles, 19.6 and 15.3 for 64, 242 and 27 for
+// 1024; 16 rows 17.1 and 19.2 for 32, 25.4 and 20.5 for 64.
+constexpr int kUncutTiles = 40;
+
 // Sizes of a kernel for row tiles of 4 KT rows: tokens of a tile, compute warps,
 // CTAs per SM, tiles in the ring.  Warps: as many as their registers allow, 16 an SM
 // with 128 registers each (D <= 128, up to 8 rows), 12 with 168, 8 with 255.  16 rows:
@@ -1008,11 +1015,11 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> asked{0};  // devices on which the kernel may take its memory
     cudaError_t err = allow_shared(kv_attn_kernel<D, G, KT>, SH::kSmem, asked);
     if (err != cudaSuccess) return err;
-    // Where each CTA can have a row tile of its own and the longest is little longer than
-    // an equal share, by up to 2 tiles a warp, nothing is cut and no second kernel
-    // needed.  (The lengths are not known here, only how many pages or which window they
-    // are in.)  1 sequence of 573 tokens: 11.1 us cut, 7.6 whole; 32 of 4 rows with a
-    // window of 1024: 30.8 cut, 23.3 whole.
+    // Where each CTA can have a row tile of its own and the longest possible one is short, and
+    // longer than an equal share of row tiles like it by at most 2 tiles a warp, nothing is
+    // cut and no second kernel needed.  (The lengths are not known here, only how many
+    // pages or which window they are in.)  1 sequence of 573 tokens: 11.1 us cut, 7.6
+    // whole; 32 of 4 rows with a window of 1024: 30.8 cut, 23.3 whole.
     long long most = ((long long)p.max_pages * p.page_size + SH::kTile - 1) / SH::kTile;
     if (p.window) {
         const long long seen = ((long long)p.window + p.tile_toks - 2) / SH::kTile + 2 +
@@ -1020,7 +1027,8 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
         most = most < seen ? most : seen;
     }
     const long long row_tiles = (long long)p.S * p.Hkv * p.head_parts;
-    if (row_tiles <= p.ctas && most * (p.ctas - row_tiles) <= 2LL * SH::kWarps * p.ctas) {
+    if (row_tiles <= p.ctas && most <= kUncutTiles &&
+        most * (p.ctas - row_tiles) <= 2LL * SH::kWarps * p.ctas) {
         KvAttnParams one = p;
         one.whole = 1;
         kv_attn_kernel<D, G, KT><<<(unsigned)row_tiles, SH::kThreads, SH::kSmem, stream>>>(one);
