@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                     v.y = cvt_bf16x2(o.z * inv, o.w * inv);
                     *reinterpret_cast<uint2*>(p.out + to * D + d0 + d) = v;
                     if (p.lse && d0 + d == 0)
-                        p.lse[to] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718f : -INFINITY;
+                        p.lse[to] = log_sum_of(mm, ll);
                 } else {
                     *reinterpret_cast<float4*>(part + 2 * SH::kRows + row * D + d0 + d) = o;
                     if (d0 + d == 0) {
@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParam
         for (int o = 16; o; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o);
         if (lane == 0) {
             row_inv[row] = ll > 0.f ? 1.f / ll : 0.f;
-            row_lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718f : -INFINITY;
+            row_lse[row] = log_sum_of(mm, ll);
         }
     }
     __syncthreads();

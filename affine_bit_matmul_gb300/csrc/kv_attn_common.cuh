@@ -95,6 +95,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// Log sum exp of a row: m its largest score times log2 e, l its sum.  -inf for a row that
+// sees nothing; not a number where its scores are none.
+__device__ __forceinline__ float log_sum_of(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+}
+
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
     asm volatile(

@@ -872,7 +872,7 @@ __device__ bool softmax(const KvAttnParams& p, Shared<D, G>& sh, uint32_t qbuf, 
         }
         if (in) {
             if (whole) {
-                if (p.lse) p.lse[to] = l > 0.f ? (mx + log2f(l)) * 0.69314718f : -INFINITY;
+                if (p.lse) p.lse[to] = log_sum_of(mx, l);
             } else {
                 part[2 * dense] = mx;
                 part[2 * dense + 1] = l;
@@ -1086,7 +1086,7 @@ __global__ void __launch_bounds__(256) kv_join_rows_kernel(const KvAttnParams p,
         v.x = cvt_bf16x2(o.x * inv, o.y * inv);
         v.y = cvt_bf16x2(o.z * inv, o.w * inv);
         *reinterpret_cast<uint2*>(p.out + to * D + d) = v;
-        if (p.lse && d == 0) p.lse[to] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718f : -INFINITY;
+        if (p.lse && d == 0) p.lse[to] = log_sum_of(mm, ll);
     }
 }
 
