@@ -813,10 +813,16 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     return q_out, k_out
 
 
+def _int32(x):
+    """A count for the C functions, which take 32 bits and would be given the lowest ones: what is
+    past them stays past every length there is."""
+    return max(min(x, 2 ** 31 - 1), -2 ** 31)
+
+
 def kv_block_bytes(head_dim: int, page_size: int, group_size: int = 64) -> int:
     """Bytes of one page of the 4-bit cache for one key/value head: a cache is
     a uint8 tensor ``[n_pages, kv_heads, kv_block_bytes(...)]``."""
-    n = int(lib().mxq_kv_block_bytes(head_dim, page_size, group_size))
+    n = int(lib().mxq_kv_block_bytes(_int32(head_dim), _int32(page_size), _int32(group_size)))
     if n == 0:
         raise ValueError("no cache of head_dim %s, page_size %s, group_size %s" % (
             head_dim, page_size, group_size))
@@ -904,7 +910,7 @@ def kv_attention_workspace_bytes(rows: int, seqs: int, heads: int, kv_heads: int
                                  max_q_len: int = 1) -> int:
     """Workspace bytes for kv_attention of ``rows`` query rows in ``seqs`` sequences."""
     return int(lib().mxq_kv_attention_workspace_bytes(rows, seqs, heads, kv_heads, head_dim,
-                                                      max_q_len))
+                                                      _int32(max_q_len)))
 
 
 def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int = 1,
@@ -961,6 +967,7 @@ def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int =
         status = _flat(dev_status, "dev_status", torch.int32, on)
     if max_q_len <= 0:
         raise ValueError("max_q_len must be positive")
+    max_q_len, window, sinks = _int32(max_q_len), _int32(window), _int32(sinks)
     L = lib()
     if workspace is None:
         need = L.mxq_kv_attention_workspace_bytes(T, S, Hq, Hkv, D, max_q_len)
