@@ -95,13 +95,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
         calls = ex.submit(_build_calls, os.path.dirname(os.path.dirname(os.path.realpath(cc))))
         objs = list(ex.map(compile_one, sources()))
-        calls.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    # the library does not need torch: it is there also where the module cannot be built
+    try:
+        calls.result()
+    except Exception as e:
+        raise RuntimeError("%s is built, but not the module %s: %s" % (LIB, CALLS, e)) from e
     return LIB
 
 
