@@ -183,8 +183,9 @@ def _direct():
         try:
             module = importlib.import_module("._calls", __name__)
         except ImportError as e:
-            raise RuntimeError("_calls.so is not built; run affine_bit_matmul_gb300.build.build() "
-                               "before using the cache operators") from e
+            raise RuntimeError("_calls.so is not built, or not for this Python and torch (%s); run "
+                               "affine_bit_matmul_gb300.build.build() before using the cache "
+                               "operators" % e) from e
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.mxq_qk_norm_rope, L.mxq_kv_append, L.mxq_kv_read, L.mxq_kv_attention,
             L.mxq_kv_attention_workspace_bytes)))

@@ -3,7 +3,8 @@
 Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into
 ``affine_bit_matmul_gb300/libmxq.so`` (static CUDA runtime).  ``csrc/torch_calls.cpp``
 becomes the Python module ``_calls.so`` beside it, which reads the tensors of the small
-calls.  Rebuilds only when a source or header is newer than what it makes.
+calls.  Rebuilds what is older than a source or header of it, and the module also when
+Python or torch is another one than it was built for.
 """
 
 from __future__ import annotations
@@ -42,16 +43,53 @@ def calls_source():
     return os.path.join(CSRC, "torch_calls.cpp")
 
 
-def _inputs():
-    return sources() + [calls_source()] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
-        os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+def _headers():
+    return glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+        os.path.join(INCLUDE, "*.h"))
+
+
+def _newer(made: str, inputs) -> bool:
+    if not os.path.exists(made):
+        return False
+    t = os.path.getmtime(made)
+    return all(os.path.getmtime(p) <= t for p in inputs)
+
+
+def _versions() -> str:
+    """What ``_calls.so`` has to be built for: it loads into this Python and this torch only."""
+    import importlib.metadata
+    import sys
+
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch as module
+
+        torch = module.__version__
+    return "python %s, torch %s\n" % (sys.version, torch)
+
+
+def _calls_for() -> str:
+    """The file that says what ``_calls.so`` was built for."""
+    return os.path.join(BUILD, "calls_versions.txt")
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, sources() + _headers())
+
+
+def calls_up_to_date() -> bool:
+    if not _newer(CALLS, [calls_source()] + _headers()):
+        return False
+    try:
+        with open(_calls_for()) as f:
+            return f.read() == _versions()
+    except OSError:
+        return False
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    return library_up_to_date() and calls_up_to_date()
 
 
 def _build_calls(cuda: str):
@@ -73,6 +111,8 @@ def _build_calls(cuda: str):
     if r.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s%s" % (calls_source(), r.stdout, r.stderr))
     os.replace(tmp, CALLS)
+    with open(_calls_for(), "w") as f:
+        f.write(_versions())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -80,7 +120,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
-    objs = []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -93,17 +132,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        calls = ex.submit(_build_calls, os.path.dirname(os.path.dirname(os.path.realpath(cc))))
-        objs = list(ex.map(compile_one, sources()))
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
-    os.replace(tmp, LIB)
+        calls = None
+        if force or not calls_up_to_date():
+            calls = ex.submit(_build_calls, os.path.dirname(os.path.dirname(os.path.realpath(cc))))
+        if force or not library_up_to_date():
+            objs = list(ex.map(compile_one, sources()))
+            tmp = LIB + ".tmp%d" % os.getpid()
+            cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
+            os.replace(tmp, LIB)
     # the library does not need torch: it is there also where the module cannot be built
     try:
-        calls.result()
+        if calls is not None:
+            calls.result()
     except Exception as e:
         raise RuntimeError("%s is built, but not the module %s: %s" % (LIB, CALLS, e)) from e
     return LIB
