@@ -38,7 +38,8 @@ bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 // against the values: more than a prompt's first rows, which see few tokens, bear.
 struct AttnPlan {
     int head_parts, part_heads, tile_rows, tile_toks, ctas;  // few rows
-    int many, many_parts, many_heads, half_toks, many_toks, many_ctas, max_entries;
+    int many, many_parts, many_heads, half_toks, many_toks, many_ctas;
+    long long max_entries;
     size_t seg_bytes, few_bytes;
     size_t many_seg_bytes, many_partial_bytes, seq_bytes, entry_bytes, before_bytes, many_bytes;
     size_t bytes;
@@ -64,7 +65,7 @@ AttnPlan plan_attn(int T, int S, int Hq, int Hkv, int D, int max_q, int sms) {
         const int tile_rows = mxq::kv_prefill_rows(D);
         a.many_toks = a.half_toks * (tile_rows / 128);
         a.many_ctas = sms;
-        a.max_entries = T / a.many_toks + S;
+        a.max_entries = (long long)T / a.many_toks + S;
         a.many_seg_bytes = align_up(mxq::kv_attn_seg_bytes(a.many_ctas), 256);
         a.many_partial_bytes =
             align_up(mxq::kv_attn_partial_bytes(a.many_ctas, tile_rows, D), 256);
@@ -76,6 +77,20 @@ AttnPlan plan_attn(int T, int S, int Hq, int Hkv, int D, int max_q, int sms) {
         a.bytes += a.many_bytes;
     }
     return a;
+}
+
+// The kernels count units (a row tile and a tile of the tokens that it sees) in 32 bits: of a few
+// rows' sequences in a thread and in a CTA's run, of all prompts' row tiles for one head.  True
+// where the counts fit for any lengths in pages of `tokens` tokens.
+bool countable(const AttnPlan& a, int S, int Hkv, long long tokens) {
+    constexpr long long kMost = (1LL << 30) - 64;
+    const long long vheads = (long long)Hkv * a.head_parts, few = tokens / 32 + 32;
+    if ((S / 128 + 1) * few > kMost || few * vheads > kMost || S * few > kMost / vheads * a.ctas)
+        return false;
+    if (!a.many) return true;
+    const long long many_vheads = (long long)Hkv * a.many_parts, units = tokens / 128 + 16;
+    if (a.max_entries > 2 * kMost || a.max_entries * units > 2 * kMost) return false;
+    return a.max_entries * units <= kMost / many_vheads * a.many_ctas;
 }
 
 }  // namespace
@@ -243,6 +258,9 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
         !aligned(dev_status, 4) || !aligned(workspace, 256))
         return MXQ_ERR_MISALIGNED;
     if (max_q_len > T && T > 0) max_q_len = T;  // no sequence has more rows than there are
+    const long long tokens = (long long)max_pages * page_size;
+    if (!countable(plan_attn(T, S, Hq, Hkv, D, max_q_len, kMaxSms), S, Hkv, tokens))
+        return MXQ_ERR_UNSUPPORTED;
     if (T > 0 && S > 0 &&
         (!workspace ||
          workspace_bytes < mxq_kv_attention_workspace_bytes(T, S, Hq, Hkv, D, max_q_len)))
@@ -250,11 +268,12 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     int sms = 0;
     const mxq_status st = mxq::check_current_device(&sms);
     if (st != MXQ_OK) return st;
+    const AttnPlan a = plan_attn(T, S, Hq, Hkv, D, max_q_len, sms < kMaxSms ? sms : kMaxSms);
+    if (!countable(a, S, Hkv, tokens)) return MXQ_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dev_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess)
         return MXQ_ERR_CUDA;
     if (T == 0 || S == 0) return MXQ_OK;
-    const AttnPlan a = plan_attn(T, S, Hq, Hkv, D, max_q_len, sms < kMaxSms ? sms : kMaxSms);
     mxq::KvAttnParams p;
     std::memset(&p, 0, sizeof p);
     p.q = static_cast<const __nv_bfloat16*>(q);
@@ -302,7 +321,7 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     p.min_rows = all_many ? 0 : a.tile_toks + 1;
     p.max_rows = kMaxInt;
     p.ctas = a.many_ctas;
-    p.max_entries = a.max_entries;
+    p.max_entries = (int)a.max_entries;
     p.segs = reinterpret_cast<int*>(ws);
     ws += a.many_seg_bytes;
     p.partial = reinterpret_cast<float*>(ws);

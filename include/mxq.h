@@ -391,7 +391,11 @@ mxq_status mxq_kv_read(const void* pages, const int32_t* slots, void* k_out, voi
  * both are reported (MXQ_DEV_BAD_SEQUENCE).  Rows that belong to no sequence
  * are not written.  No invalid entry makes the kernels read or write out of
  * bounds.  The result is deterministic for given arguments.
- * Requirements: Hq % Hkv == 0; scale positive; q, pages, out 16-byte aligned.  */
+ * Requirements: Hq % Hkv == 0; scale positive; q, pages, out 16-byte aligned;
+ * max_pages * page_size at most 2^30 tokens.  Calls are counted in units of one
+ * row tile and 32 to 128 tokens, in 32 bits; one that could have more of them for
+ * its T, S and max_pages is refused (MXQ_ERR_UNSUPPORTED): some 10^13 rows times
+ * tokens.                                                                     */
 mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_head_stride,
                             const void* pages, const int32_t* page_table, const int32_t* ctx_lens,
                             const int32_t* q_starts, void* out, float* lse, int T, int S, int Hq,
