@@ -342,7 +342,7 @@ static bool many_rows(const KvRowsParams& p, int sms) {
 }
 
 static unsigned row_blocks(const KvRowsParams& p, int rows) {
-    const long long warps = 2LL * ((p.T + rows - 1) / rows) * p.H;
+    const long long warps = 2LL * (((long long)p.T + rows - 1) / rows) * p.H;
     return (unsigned)((warps + kRowThreads / 32 - 1) / (kRowThreads / 32));
 }
 
