@@ -124,3 +124,30 @@ def test_long_contexts_are_as_good_as_the_output_type(seqs, heads, D, G):
             off += float((o[i, h * rep:(h + 1) * rep] - ref).pow(2).sum())
             norm += float(ref.pow(2).sum())
     assert (off / norm) ** 0.5 <= MOST, "%.3e of the norm" % (off / norm) ** 0.5
+
+
+def test_rows_of_sequences_beside_one_whose_rows_decrease():
+    import affine_bit_matmul_gb300 as mxq
+
+    c = Case([100, 60, 30], [3, 2, 4], 4, 2, 128, 64, 16, seed=13)
+    c.starts_d[1], c.starts_d[2] = 5, 3   # sequence 0 has 5 rows, 1 has -2, 2 has 6: rows 3 and 4 are of both
+    o, _, status = c.run(max_q_len=6)
+    assert status == mxq.DEV_BAD_SEQUENCE
+    for i, n, a, b, rows in ((0, 100, 0, 5, [0, 1, 2]), (2, 30, 3, 9, [5, 6, 7, 8])):
+        table, starts = c.table[i:i + 1], [a, b]
+        ref, tol = few_rows(c.q, c.cache, table, [n], starts)
+        assert (np.abs(o - ref)[rows] <= tol[rows]).all()
+    # a bound that leaves all of them out writes nothing
+    o, _, status = c.run(max_q_len=4)
+    assert status == mxq.DEV_BAD_SEQUENCE and np.isnan(o).all()
+
+
+@pytest.mark.parametrize("heads", [129, 160])
+def test_more_query_heads_to_a_key_head_than_a_row_tile_holds(heads):
+    # single rows, in parts of at most 16 heads; a prompt, in parts of at most 128
+    c = Case([90, 33], [1, 1], heads, 1, 64, 64, 32, seed=heads)
+    c.check()
+    o, _, _ = c.run()
+    ref, tol = few_rows(c.q, c.cache, c.table, c.ctx, c.starts)
+    assert (np.abs(o - ref) <= tol).all()
+    Case([90, 150], [3, 40], heads, 1, 64, 64, 32, seed=heads).check()
