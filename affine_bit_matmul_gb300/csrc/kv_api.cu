@@ -32,10 +32,12 @@ bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 // times query heads of a key/value head are at most 16 go through the kernel for
 // few rows (bound by the cache's bytes), the others through the tensor cores'
 // (bound by their products).  32 sequences of 8192 tokens, 8 key/value heads of 128
-// values: the first takes 113 us for 16 rows, the second 260 for 20 rows and 267 for
-// 128; of 64 values 82 and 242, of 256 242 and 406.  Two row tiles of the first
-// would win up to 32 rows, but its weights are rounded against a group's range, not
-// against the values: more than a prompt's first rows, which see few tokens, bear.
+// values: the first takes 117 us for 16 rows, the second 262 for 20 rows and 270 for
+// 128; of 64 values 87 and 243, of 256 272 and 409.  Two row tiles of the first took
+// 226 for 17 to 32 rows; they are not used: a prompt's first rows, which see few tokens,
+// would then have weights times scales of 11 bits, rounded against a group's range, as rows
+// of up to 16 have, and not weights and values of 11 bits each, which is what rows of this
+// number are held to.
 struct AttnPlan {
     int head_parts, part_heads, tile_rows, tile_toks, ctas;  // few rows
     int many, many_parts, many_heads, half_toks, many_toks, many_ctas;

@@ -39,9 +39,9 @@
 // lanes at all.
 // Bound by HBM for long contexts, 2 (D / 2 + 4 D / G) bytes per token and head: 8
 // sequences of 65536 to 131072 tokens, 5 query heads to a key head of 128 values,
-// 163 us, 5.9 TB/s; 64 of 1024 to 8192 tokens, 4 query heads, 74 us, 4.6 TB/s with the
+// 164 us, 5.8 TB/s; 64 of 1024 to 8192 tokens, 4 query heads, 71 us, 4.8 TB/s with the
 // ends of the row tiles.  From 16 rows on by the instructions around the products: 32
-// sequences of 8192 tokens 113 us, 2.6 TB/s.  One sequence of 573 tokens takes 7.6 us: a
+// sequences of 8192 tokens 117 us, 2.6 TB/s.  One sequence of 573 tokens takes 7.6 us: a
 // chain of loads (length, pages, tiles) and two rounds of tiles in each warp.
 //   The matrix instructions' fp32 sums round towards zero.  Codes and weights are not
 // negative, so their products add up to sums of which the biases then take most away
@@ -162,13 +162,14 @@ struct Piece {
 // its ring (24 tiles at most) ahead of the unit that is being worked on.
 constexpr int kPieces = 64;
 
-// One thread: lists the pieces of the CTA's run, the first kPieces at once and
-// one more whenever the warps are done with one; then one marked `last`.
+// A row tile's units: its tiles of tokens, and what its end costs.
 template <int TILE>
 __device__ __forceinline__ int units_of(const Span& sp) {
     return sp.tiles ? sp.tiles + kEndTokens / TILE : 0;
 }
 
+// One thread: lists the pieces of the CTA's run, the first kPieces at once and
+// one more whenever the warps are done with one; then one marked `last`.
 template <int TILE>
 struct Walk {  // (no constructors: it lies in shared memory)
     int s, h, part, k, seq, left;

@@ -21,8 +21,10 @@
 // takes one token and several heads and computes each angle once.
 // HBM-bound at large sizes, every value being read and written once: 4584 tokens of
 // 48 heads of 128 values in 19.5 us (5.8 TB/s) interleaved, 26.0 (4.3 TB/s) in the half
-// layout; about 130 instructions for 256 values keep it from the memory's rate.  A
-// decode step's rows (16 tokens) take 2.8 us, a launch and three dependent loads.
+// layout.  Both execute 12 M warp instructions there, and neither fills the issue slots
+// (61% and 49% of the cycles) or the memory: the half layout's twice as many loads and stores
+// of 8 bytes take 78 registers, so an SM holds 18 warps instead of 27 to wait with.  A
+// decode step's rows (16 tokens) take 2.9 us, a launch and three dependent loads.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -34,8 +36,6 @@ namespace mxq {
 namespace {
 
 constexpr int kRopeThreads = 256;
-// Warps an SM is given before a warp takes more than one round of heads: 512 tokens of 48
-// heads take 5.0 us with 16, 6.0 with 32; the largest calls do not care.
 // Warps an SM is given before a warp takes more than one round of heads: 512 tokens of 48
 // heads take 5.0 us with 16, 6.0 with 32; the largest calls do not care.
 constexpr int kWarps = 16;
