@@ -46,6 +46,8 @@ __all__ = [
     "kv_read",
     "kv_attention",
     "kv_attention_workspace_bytes",
+    "kv_attention_shared",
+    "kv_attention_shared_workspace_bytes",
     "set_wait_budget",
     "NOALLOC_SCRATCH_BYTES",
     "MxqError",
@@ -99,6 +101,8 @@ EXPORTED_SYMBOLS = (
     "mxq_kv_read",
     "mxq_kv_attention",
     "mxq_kv_attention_workspace_bytes",
+    "mxq_kv_attention_shared",
+    "mxq_kv_attention_shared_workspace_bytes",
     "mxq_status_string",
     "mxq_version",
     "mxq_debug_set_wait_budget",
@@ -159,6 +163,10 @@ def lib():
         L.mxq_kv_attention.restype = I
         L.mxq_kv_attention_workspace_bytes.argtypes = [I, I, I, I, I, I]
         L.mxq_kv_attention_workspace_bytes.restype = Z
+        L.mxq_kv_attention_shared.argtypes = [P, J, J] + [P] * 9 + [I] * 13 + [F, P, Z, P, P]
+        L.mxq_kv_attention_shared.restype = I
+        L.mxq_kv_attention_shared_workspace_bytes.argtypes = [I] * 8
+        L.mxq_kv_attention_shared_workspace_bytes.restype = Z
         L.mxq_gather_workspace_bytes.argtypes = [I, I, I, I]
         L.mxq_gather_workspace_bytes.restype = Z
         L.mxq_status_string.argtypes = [I]
@@ -981,6 +989,100 @@ def kv_attention(q, pages, page_table, ctx_lens, q_starts=None, max_q_len: int =
             Hkv, D, n_pages, max_pages, page_size, group_size, max_q_len,
             D ** -0.5 if scale is None else scale, window, sinks, ws_at, workspace.numel(), status,
             st), "mxq_kv_attention")
+    return out
+
+
+def kv_attention_shared_workspace_bytes(rows: int, seqs: int, groups: int, heads: int, kv_heads: int,
+                                        head_dim: int, max_q_len: int = 1, max_group=None) -> int:
+    """Workspace bytes for kv_attention_shared of ``rows`` query rows in ``seqs`` sequences and
+    ``groups`` groups of at most ``max_group`` sequences (default: all of them)."""
+    return int(lib().mxq_kv_attention_shared_workspace_bytes(
+        rows, seqs, groups, heads, kv_heads, head_dim, _int32(max_q_len),
+        max(seqs, 1) if max_group is None else _int32(max_group)))
+
+
+def kv_attention_shared(q, pages, prefix_table, prefix_lens, page_table, ctx_lens, group_starts=None,
+                        q_starts=None, max_q_len: int = 1, max_group=None, group_size: int = 64,
+                        scale=None, out=None, lse=None, workspace=None, dev_status=None, stream=None):
+    """Attention of ``q`` (bf16 [T, heads, D]) over a 4-bit paged cache for groups of sequences
+    that begin with the same tokens, which are read once for a group.
+
+    Group g shares the ``prefix_lens[g]`` tokens (int32 [N]) in the pages ``prefix_table[g]``
+    (int32 [N, max_prefix_pages]); its sequences are ``group_starts[g]:group_starts[g+1]`` (int32
+    [N+1], at most ``max_group`` each, default all; None: S / N each).  Sequence i has
+    ``ctx_lens[i]`` tokens of its own in the pages ``page_table[i]`` (int32 [S, max_pages]); its
+    query rows ``q_starts[i]:q_starts[i+1]`` (int32 [S+1], at most ``max_q_len`` each; None: one
+    row per sequence) are the last of them: row j of n sees the whole prefix and the own tokens up
+    to ``ctx_lens[i] - n + j``.  ``scale`` defaults to D^-1/2.  ``lse`` (fp32 [T, heads]) receives
+    the log sum exp.  Returns out bf16 [T, heads, D]; a row that sees nothing is 0."""
+    torch = _torch()
+    q_rs, q_hs = _heads(q, "q")
+    dev = q.device
+    on = dev.index
+    T, Hq, D = q.shape
+    at, n_pages, Hkv, page_size = _cache(pages, D, group_size, on)
+    if Hq == 0 or Hkv == 0 or Hq % Hkv:
+        raise ValueError("%d query heads do not divide over %d key/value heads" % (Hq, Hkv))
+    prefix_at = _flat(prefix_table, "prefix_table", torch.int32, on)
+    if prefix_table.dim() != 2 or prefix_table.shape[0] == 0:
+        raise ValueError("prefix_table must be 2-D [N, max_prefix_pages]")
+    N, max_prefix_pages = prefix_table.shape
+    prefix_lens_at = _flat(prefix_lens, "prefix_lens", torch.int32, on)
+    if prefix_lens.numel() != N:
+        raise ValueError("prefix_lens must have N entries")
+    table_at = _flat(page_table, "page_table", torch.int32, on)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D [S, max_pages]")
+    S, max_pages = page_table.shape
+    lens_at = _flat(ctx_lens, "ctx_lens", torch.int32, on)
+    if ctx_lens.numel() != S:
+        raise ValueError("ctx_lens must have S entries")
+    groups_at = starts_at = lse_at = status = None
+    if group_starts is not None:
+        groups_at = _flat(group_starts, "group_starts", torch.int32, on)
+        if group_starts.numel() != N + 1:
+            raise ValueError("group_starts must have N + 1 entries")
+        max_group = max(S, 1) if max_group is None else max_group
+    elif S % N:
+        raise ValueError("without group_starts the %d sequences must divide over the %d groups" % (S, N))
+    else:
+        max_group = max(S // N, 1) if max_group is None else max_group
+        if max_group < S // N:
+            raise ValueError("max_group must be at least the %d sequences of a group" % (S // N))
+    if q_starts is not None:
+        starts_at = _flat(q_starts, "q_starts", torch.int32, on)
+        if q_starts.numel() != S + 1:
+            raise ValueError("q_starts must have S + 1 entries")
+    elif T != S or max_q_len != 1:
+        raise ValueError("without q_starts every sequence has one row: T must be S, max_q_len 1")
+    if out is None:
+        out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
+        out_at = out.data_ptr()
+    else:
+        out_at = _flat(out, "out", torch.bfloat16, on)
+        if tuple(out.shape) != (T, Hq, D):
+            raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), (T, Hq, D)))
+    if lse is not None:
+        lse_at = _flat(lse, "lse", torch.float32, on)
+        if tuple(lse.shape) != (T, Hq):
+            raise ValueError("lse has shape %s, expected %s" % (tuple(lse.shape), (T, Hq)))
+    if dev_status is not None:
+        status = _flat(dev_status, "dev_status", torch.int32, on)
+    if max_q_len <= 0 or max_group <= 0:
+        raise ValueError("max_q_len and max_group must be positive")
+    max_q_len, max_group = _int32(max_q_len), _int32(max_group)
+    L = lib()
+    if workspace is None:
+        need = L.mxq_kv_attention_shared_workspace_bytes(T, S, N, Hq, Hkv, D, max_q_len, max_group)
+        workspace = _empty((need,), torch.uint8, dev, stream)
+    ws_at = _flat(workspace, "workspace", torch.uint8, on)
+    ctx, st = _launch_on(dev, stream)
+    with ctx:
+        _check(L.mxq_kv_attention_shared(
+            q.data_ptr(), q_rs, q_hs, at, prefix_at, prefix_lens_at, groups_at, table_at, lens_at,
+            starts_at, out_at, lse_at, T, S, N, Hq, Hkv, D, n_pages, max_prefix_pages, max_pages,
+            page_size, group_size, max_q_len, max_group, D ** -0.5 if scale is None else scale, ws_at,
+            workspace.numel(), status, st), "mxq_kv_attention_shared")
     return out
 
 

@@ -95,6 +95,74 @@ bool countable(const AttnPlan& a, int S, int Hkv, long long tokens) {
     return a.max_entries * units <= kMost / many_vheads * a.many_ctas;
 }
 
+// How one part of a call over shared prefixes is cut (KvSharedParams): row tiles, CTAs, and its
+// share of the workspace.
+struct SharedPart {
+    int head_parts, part_heads, tile_rows, tile_toks, half_toks, ctas;
+    long long planes, most_planes;  // row tiles of one head: with rows that do not overlap, at all
+    size_t before_bytes, bytes;
+};
+
+SharedPart shared_part(long long items, long long rows, long long T, int rep, int Hkv, int D, int sms) {
+    SharedPart a;
+    a.head_parts = (rep + 15) / 16;
+    a.part_heads = (rep + a.head_parts - 1) / a.head_parts;
+    const long long all = rows * a.part_heads;
+    a.tile_rows = all <= 4 ? 4 : all <= 8 ? 8 : 16;
+    a.tile_toks = a.tile_rows / a.part_heads;
+    a.half_toks = 0;
+    a.ctas = sms * mxq::kv_attn_ctas_per_sm();
+    a.most_planes = items * ((rows + a.tile_toks - 1) / a.tile_toks);
+    a.planes = a.most_planes;
+    return a;
+}
+
+struct SharedPlan {
+    SharedPart prefix, own;
+    size_t bytes;
+};
+
+// The groups' rows are taken by the kernel for few rows up to kFewPrefixRows, above by the
+// tensor cores'.
+constexpr int kFewPrefixRows = 32;
+
+SharedPlan plan_shared(int T, int S, int N, int Hq, int Hkv, int D, int max_q, int max_group, int sms) {
+    SharedPlan a;
+    const int rep = Hq / Hkv;
+    a.own = shared_part(S, max_q, T, rep, Hkv, D, sms);
+    const long long all = (long long)max_group * max_q, rows = all < T ? all : T;
+    SharedPart& p = a.prefix;
+    p = shared_part(N, rows, T, rep, Hkv, D, sms);
+    if (rows * p.part_heads > kFewPrefixRows) {
+        p.head_parts = (rep + 127) / 128;
+        p.part_heads = (rep + p.head_parts - 1) / p.head_parts;
+        p.tile_rows = mxq::kv_prefill_rows(D);
+        p.half_toks = 128 / p.part_heads;
+        p.tile_toks = p.half_toks * (p.tile_rows / 128);
+        p.ctas = sms;
+        p.most_planes = N * ((rows + p.tile_toks - 1) / p.tile_toks);
+    }
+    // the groups have all rows between them
+    p.planes = T / p.tile_toks + (long long)N;
+    if (p.planes > p.most_planes) p.planes = p.most_planes;
+    a.bytes = 0;
+    for (SharedPart* x : {&a.prefix, &a.own}) {
+        x->before_bytes = align_up((size_t)(x == &a.own ? S : N) * sizeof(int2), 256) + 256;
+        const size_t places = (size_t)x->planes * Hkv * x->head_parts + x->ctas;
+        x->bytes = x->before_bytes + align_up(places * x->tile_rows * (D + 2) * sizeof(float), 256);
+        a.bytes += x->bytes;
+    }
+    return a;
+}
+
+// As for AttnPlan: units of one head and of a run, and places, fit 32 bits.
+bool countable(const SharedPart& a, int Hkv, long long tokens) {
+    constexpr long long kMost = (1LL << 30) - 64;
+    const long long units = tokens / (a.tile_rows > 16 ? 128 : 32) + 32, vheads = (long long)Hkv * a.head_parts;
+    if (a.most_planes > kMost / units || a.most_planes > kMost / vheads - a.ctas) return false;
+    return a.most_planes * units <= kMost / vheads * a.ctas;
+}
+
 }  // namespace
 
 extern "C" {
@@ -336,6 +404,110 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     ws += a.before_bytes;
     p.counts = reinterpret_cast<int*>(ws);
     const cudaError_t err = mxq::launch_kv_prefill(p, D, group_size, s);
+    return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+}
+
+size_t mxq_kv_attention_shared_workspace_bytes(int T, int S, int N, int Hq, int Hkv, int D,
+                                               int max_q_len, int max_group) {
+    if (T < 0 || S < 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_q_len <= 0 ||
+        max_group <= 0)
+        return 0;
+    if (max_q_len > T) max_q_len = T > 0 ? T : 1;
+    if (max_group > S) max_group = S > 0 ? S : 1;
+    return plan_shared(T, S, N, Hq, Hkv, D, max_q_len, max_group, kMaxSms).bytes;
+}
+
+mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long long q_head_stride,
+                                   const void* pages, const int32_t* prefix_table,
+                                   const int32_t* prefix_lens, const int32_t* group_starts,
+                                   const int32_t* page_table, const int32_t* ctx_lens,
+                                   const int32_t* q_starts, void* out, float* lse, int T, int S, int N,
+                                   int Hq, int Hkv, int D, int n_pages, int max_prefix_pages,
+                                   int max_pages, int page_size, int group_size, int max_q_len,
+                                   int max_group, float scale, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, void* stream) {
+    if (T < 0 || S < 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || n_pages <= 0 ||
+        max_pages <= 0 || max_prefix_pages <= 0 || !cache_shape(D, group_size, page_size))
+        return MXQ_ERR_INVALID_ARG;
+    if (max_q_len <= 0 || max_group <= 0 || !(scale > 0.f) || scale - scale != 0.f)
+        return MXQ_ERR_INVALID_ARG;
+    if (!q_starts && (T != S || max_q_len != 1)) return MXQ_ERR_INVALID_ARG;
+    if (!group_starts && (S % N != 0 || S / N > max_group)) return MXQ_ERR_INVALID_ARG;
+    if (!pages || (T > 0 && S > 0 &&
+                   (!q || !prefix_table || !prefix_lens || !page_table || !ctx_lens || !out)))
+        return MXQ_ERR_INVALID_ARG;
+    if (!stride_ok(q_row_stride) || !stride_ok(q_head_stride)) return MXQ_ERR_INVALID_ARG;
+    const long long tokens[2] = {(long long)max_prefix_pages * page_size, (long long)max_pages * page_size};
+    if (tokens[0] > kMaxInt || tokens[1] > kMaxInt || T > kMaxInt || S > kMaxInt || N > kMaxInt)
+        return MXQ_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(pages, 16) || !aligned(out, 16) || !aligned(prefix_table, 4) ||
+        !aligned(prefix_lens, 4) || !aligned(group_starts, 4) || !aligned(page_table, 4) ||
+        !aligned(ctx_lens, 4) || !aligned(q_starts, 4) || !aligned(lse, 4) ||
+        !aligned(dev_status, 4) || !aligned(workspace, 256))
+        return MXQ_ERR_MISALIGNED;
+    if (max_q_len > T && T > 0) max_q_len = T;
+    if (max_group > S && S > 0) max_group = S;
+    const SharedPlan most = plan_shared(T, S, N, Hq, Hkv, D, max_q_len, max_group, kMaxSms);
+    if (!countable(most.prefix, Hkv, tokens[0]) || !countable(most.own, Hkv, tokens[1]))
+        return MXQ_ERR_UNSUPPORTED;
+    if (T > 0 && S > 0 && (!workspace || workspace_bytes < most.bytes)) return MXQ_ERR_WORKSPACE;
+    int sms = 0;
+    const mxq_status st = mxq::check_current_device(&sms);
+    if (st != MXQ_OK) return st;
+    const SharedPlan a =
+        plan_shared(T, S, N, Hq, Hkv, D, max_q_len, max_group, sms < kMaxSms ? sms : kMaxSms);
+    if (!countable(a.prefix, Hkv, tokens[0]) || !countable(a.own, Hkv, tokens[1]))
+        return MXQ_ERR_UNSUPPORTED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dev_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess)
+        return MXQ_ERR_CUDA;
+    if (T == 0 || S == 0) return MXQ_OK;
+    mxq::KvSharedParams p[2];
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    for (int i = 0; i < 2; ++i) {
+        mxq::KvSharedParams& x = p[i];
+        const SharedPart& part = i ? a.own : a.prefix;
+        x = mxq::KvSharedParams();
+        x.q = static_cast<const __nv_bfloat16*>(q);
+        x.q_row_stride = q_row_stride;
+        x.q_head_stride = q_head_stride;
+        x.pages = static_cast<const uint8_t*>(pages);
+        x.table = i ? page_table : prefix_table;
+        x.max_pages = i ? max_pages : max_prefix_pages;
+        x.ctx_lens = ctx_lens;
+        x.q_starts = q_starts;
+        x.out = static_cast<__nv_bfloat16*>(out);
+        x.lse = lse;
+        x.T = T;
+        x.S = S;
+        x.n_pages = n_pages;
+        x.Hq = Hq;
+        x.Hkv = Hkv;
+        x.page_size = page_size;
+        x.page_shift = page_shift_of(page_size);
+        x.max_q = max_q_len;
+        x.scale_log2 = (float)(scale * 1.4426950408889634);
+        x.status = dev_status;
+        x.wait_budget = mxq::wait_budget_cycles();
+        x.head_parts = part.head_parts;
+        x.part_heads = part.part_heads;
+        x.tile_toks = part.tile_toks;
+        x.half_toks = part.half_toks;
+        x.ctas = part.ctas;
+        x.prefix = !i;
+        x.groups_n = N;
+        x.max_group = max_group;
+        x.groups = group_starts;
+        x.prefix_lens = prefix_lens;
+        x.max_planes = (int)part.planes;
+        x.tile_rows = part.tile_rows;
+        x.totals = reinterpret_cast<long long*>(ws);
+        x.before = reinterpret_cast<int2*>(ws + 256);
+        x.partial = reinterpret_cast<float*>(ws + part.before_bytes);
+        ws += part.bytes;
+        if (mxq::launch_kv_shared_part(x, D, group_size, i == 1, s) != cudaSuccess) return MXQ_ERR_CUDA;
+    }
+    const cudaError_t err = mxq::launch_kv_shared_join(p[0], p[1], D, s);
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 

@@ -180,6 +180,7 @@ cudaError_t launch_kv_read(const KvRowsParams& p, int D, int G, int sms, cudaStr
 // Attention over the cache.  A row tile is up to `tile_rows` rows, each one
 // (token, query head) of one sequence and key/value head.
 struct KvAttnParams {
+    static constexpr bool kShared = false;
     const __nv_bfloat16* q;  // bf16 [T, Hq, D], strides in values
     long long q_row_stride, q_head_stride;
     const uint8_t* pages;
@@ -217,6 +218,31 @@ cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int G, int tile_rows,
 size_t kv_attn_seg_bytes(int ctas);
 size_t kv_attn_partial_bytes(int ctas, int tile_rows, int D);
 int kv_attn_ctas_per_sm();
+
+// One of the two parts of an attention call over shared prefixes: each group's rows over its
+// prefix, or each sequence's rows over its own tokens.  `table` and `max_pages` are that part's,
+// `ctx_lens` the sequences' own lengths.
+struct KvSharedParams : KvAttnParams {
+    static constexpr bool kShared = true;
+    int prefix;                  // which part
+    int groups_n, max_group;     // groups, the most sequences of one
+    const int32_t* groups;       // int32 [groups_n + 1], or null: S / groups_n sequences each
+    const int32_t* prefix_lens;  // int32 [groups_n]
+    int max_planes;              // row tiles of one head for which `partial` has places
+    // For each item (group or sequence): units and row tiles of one head before it; and units
+    // of a run.  Written by the part's kernel for the one that joins.
+    int2* before;
+    long long* totals;
+    int tile_rows, tile_tokens, end_units;  // of the part's kernel
+};
+
+// Rows of one part by the kernel for few rows (tile_rows as for launch_kv_attn) or on the tensor
+// cores (tile_rows > 16), without the joining; `dependent`: beside the kernel before it.
+cudaError_t launch_kv_shared_part(KvSharedParams& p, int D, int G, bool dependent,
+                                  cudaStream_t stream);
+cudaError_t launch_kv_shared_many(KvSharedParams& p, int D, int G, cudaStream_t stream);
+cudaError_t launch_kv_shared_join(const KvSharedParams& prefix, const KvSharedParams& own, int D,
+                                  cudaStream_t stream);
 
 // Sequences with more rows than launch_kv_attn takes, on the tensor cores.
 cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, int G, cudaStream_t stream);

@@ -414,6 +414,48 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
                             void* stream);
 size_t mxq_kv_attention_workspace_bytes(int T, int S, int Hq, int Hkv, int D, int max_q_len);
 
+/* Attention over the cache for groups of sequences that begin with the same
+ * tokens (several continuations of one prompt, conversations after one
+ * instruction text): the keys and values of a group's prefix are read and
+ * multiplied for all of its rows at once.
+ *   Group g is the sequences group_starts[g] .. group_starts[g + 1] - 1 (NULL:
+ * S / N each) and shares the prefix_lens[g] tokens in the pages prefix_table[g,
+ * 0 ...].  Sequence i has ctx_lens[i] tokens of its own after them (its new ones
+ * already appended), in the pages page_table[i, 0 ...], and the query rows
+ * q_starts[i] .. q_starts[i + 1] - 1: row j of n sees its group's whole prefix
+ * and the own tokens t <= ctx_lens[i] - n + j.  A sequence of no group has no
+ * prefix.  A prefix need not end with a page: the own tokens begin in a page of
+ * their own.
+ *   out, lse, q, scale, pages, dev_status, workspace: as for mxq_kv_attention,
+ *   mxq_kv_attention_shared_workspace_bytes(...) bytes; a row that sees nothing
+ *   is 0 with lse -inf
+ *   prefix_table: int32 [N, max_prefix_pages]; page_table: int32 [S, max_pages];
+ *   group_starts: int32 [N + 1] or NULL; q_starts: int32 [S + 1], or NULL: one row
+ *   per sequence (T == S)
+ *   max_q_len, max_group: the most rows of a sequence and the most sequences of
+ *   a group, host-side bounds; max_group decides which kernel takes the prefixes
+ * Invalid entries as for mxq_kv_attention: pages outside [0, n_pages) are
+ * invisible (MXQ_DEV_BAD_PAGE), lengths are clamped, a sequence or group whose
+ * rows or sequences are out of range, decrease or exceed the bounds is left out
+ * with its rows of out, and the whole call where groups overlap so that their rows
+ * are more than T (MXQ_DEV_BAD_SEQUENCE).  The result is deterministic for given
+ * arguments.
+ * Accuracy: that of mxq_kv_attention for few rows in the own tokens and in
+ * prefixes of up to 32 rows (times query heads to a key/value head) in a group,
+ * that for more rows in the other prefixes.  There are no windows: a layer with
+ * one reads few tokens of each sequence anyway.                              */
+mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long long q_head_stride,
+                                   const void* pages, const int32_t* prefix_table,
+                                   const int32_t* prefix_lens, const int32_t* group_starts,
+                                   const int32_t* page_table, const int32_t* ctx_lens,
+                                   const int32_t* q_starts, void* out, float* lse, int T, int S, int N,
+                                   int Hq, int Hkv, int D, int n_pages, int max_prefix_pages,
+                                   int max_pages, int page_size, int group_size, int max_q_len,
+                                   int max_group, float scale, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, void* stream);
+size_t mxq_kv_attention_shared_workspace_bytes(int T, int S, int N, int Hq, int Hkv, int D,
+                                               int max_q_len, int max_group);
+
 /* Static description of a status code. */
 const char* mxq_status_string(mxq_status status);
 
