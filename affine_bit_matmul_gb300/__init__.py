@@ -48,6 +48,8 @@ __all__ = [
     "kv_attention_workspace_bytes",
     "kv_attention_shared",
     "kv_attention_shared_workspace_bytes",
+    "beam_select",
+    "kv_reorder",
     "set_wait_budget",
     "NOALLOC_SCRATCH_BYTES",
     "MxqError",
@@ -103,6 +105,10 @@ EXPORTED_SYMBOLS = (
     "mxq_kv_attention_workspace_bytes",
     "mxq_kv_attention_shared",
     "mxq_kv_attention_shared_workspace_bytes",
+    "mxq_beam_select",
+    "mxq_beam_select_workspace_bytes",
+    "mxq_kv_reorder",
+    "mxq_kv_reorder_workspace_bytes",
     "mxq_status_string",
     "mxq_version",
     "mxq_debug_set_wait_budget",
@@ -167,6 +173,14 @@ def lib():
         L.mxq_kv_attention_shared.restype = I
         L.mxq_kv_attention_shared_workspace_bytes.argtypes = [I] * 8
         L.mxq_kv_attention_shared_workspace_bytes.restype = Z
+        L.mxq_beam_select.argtypes = [P, J, I, P, P, P, P, P, P, I, I, I, I, I, P, Z, P]
+        L.mxq_beam_select.restype = I
+        L.mxq_beam_select_workspace_bytes.argtypes = [I] * 5
+        L.mxq_beam_select_workspace_bytes.restype = Z
+        L.mxq_kv_reorder.argtypes = [P] * 7 + [I] * 9 + [P, Z, P, P]
+        L.mxq_kv_reorder.restype = I
+        L.mxq_kv_reorder_workspace_bytes.argtypes = [I]
+        L.mxq_kv_reorder_workspace_bytes.restype = Z
         L.mxq_gather_workspace_bytes.argtypes = [I, I, I, I]
         L.mxq_gather_workspace_bytes.restype = Z
         L.mxq_status_string.argtypes = [I]
@@ -196,7 +210,9 @@ def _direct():
                                "operators" % e) from e
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.mxq_qk_norm_rope, L.mxq_kv_append, L.mxq_kv_read, L.mxq_kv_attention,
-            L.mxq_kv_attention_workspace_bytes)))
+            L.mxq_kv_attention_workspace_bytes, L.mxq_kv_attention_shared,
+            L.mxq_kv_attention_shared_workspace_bytes, L.mxq_beam_select, L.mxq_beam_select_workspace_bytes,
+            L.mxq_kv_reorder, L.mxq_kv_reorder_workspace_bytes)))
         _calls_module = module
     return _calls_module
 
@@ -1015,6 +1031,12 @@ def kv_attention_shared(q, pages, prefix_table, prefix_lens, page_table, ctx_len
     row per sequence) are the last of them: row j of n sees the whole prefix and the own tokens up
     to ``ctx_lens[i] - n + j``.  ``scale`` defaults to D^-1/2.  ``lse`` (fp32 [T, heads]) receives
     the log sum exp.  Returns out bf16 [T, heads, D]; a row that sees nothing is 0."""
+    if stream is None:
+        done = _direct().kv_attention_shared(q, pages, prefix_table, prefix_lens, page_table, ctx_lens, group_starts,
+                                             q_starts, max_q_len, max_group, group_size, scale, out, lse, workspace,
+                                             dev_status)
+        if done is not None:
+            return done
     torch = _torch()
     q_rs, q_hs = _heads(q, "q")
     dev = q.device
@@ -1084,6 +1106,143 @@ def kv_attention_shared(q, pages, prefix_table, prefix_lens, page_table, ctx_len
             page_size, group_size, max_q_len, max_group, D ** -0.5 if scale is None else scale, ws_at,
             workspace.numel(), status, st), "mxq_kv_attention_shared")
     return out
+
+
+# ------------------------------------------------- beams
+
+def beam_select(logits, scores, k=None, done=None, end_token: int = 0, scores_out=None, parents_out=None,
+                tokens_out=None, done_out=None, workspace=None, stream=None):
+    """The ``k`` best continuations (default: as many as beams) of N prompts with W beams each:
+    ``scores[w] + log_softmax(logits[w])[v]`` over a prompt's beams and tokens, the best first,
+    equal ones in the order of w V + v.
+
+    ``logits`` bf16 or fp32 [N, W, V] or [N W, V] (tokens contiguous, rows at equal distances), ``scores`` fp32
+    [N, W]; -inf is a beam that is not in use, a -inf logit a token that is not allowed.  ``done``
+    (bool [N, W]): beams that have ended; one has the single candidate ``end_token``, with its score
+    as it is.  Returns (scores fp32, parents int32, tokens int32), each [N, k], and with ``done``
+    a fourth, bool: the parent had ended or the token is ``end_token``."""
+    if stream is None:
+        found = _direct().beam_select(logits, scores, k, done, end_token, scores_out, parents_out, tokens_out,
+                                      done_out, workspace)
+        if found is not None:
+            return found
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("logits has dtype %s, expected bfloat16 or float32" % logits.dtype)
+    dev = logits.device
+    on = dev.index
+    scores_at = _flat(scores, "scores", torch.float32, on)
+    if scores.dim() != 2:
+        raise ValueError("scores must be 2-D [N, W]")
+    N, W = scores.shape
+    if logits.dim() not in (2, 3) or tuple(logits.shape[:-1]) != ((N * W,) if logits.dim() == 2 else (N, W)):
+        raise ValueError("logits has shape %s, expected [%d, %d, V] or [%d, V]" % (tuple(logits.shape), N, W, N * W))
+    V = logits.shape[-1]
+    row = logits.stride(-2) if logits.shape[-2] > 1 else logits.stride(0)
+    if V > 1 and logits.stride(-1) != 1:
+        raise ValueError("the tokens of a row of logits must be contiguous")
+    if logits.dim() == 3 and N > 1 and W > 1 and logits.stride(0) != W * row:
+        raise ValueError("the rows of logits must be at equal distances")
+    k = W if k is None else k
+    if not 0 < k <= min(64, W * V) or W > 64:
+        raise ValueError("%d of %d beams times %d tokens: at most 64 beams and 64 of them" % (k, W, V))
+    done_at = done_out_at = None
+    if done is not None:
+        done_at = _flat(done, "done", torch.bool, on)
+        if tuple(done.shape) != (N, W):
+            raise ValueError("done has shape %s, expected %s" % (tuple(done.shape), (N, W)))
+    elif done_out is not None:
+        raise ValueError("done_out needs done")
+    if done is not None and not 0 <= end_token < V:
+        raise ValueError("end_token %d is none of %d tokens" % (end_token, V))
+    outs = []
+    for t, name, dtype in ((scores_out, "scores_out", torch.float32), (parents_out, "parents_out", torch.int32),
+                           (tokens_out, "tokens_out", torch.int32), (done_out, "done_out", torch.bool)):
+        if name == "done_out" and done is None:
+            break
+        if t is None:
+            t = _empty((N, k), dtype, dev, stream)
+        _flat(t, name, dtype, on)
+        if tuple(t.shape) != (N, k):
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (N, k)))
+        outs.append(t)
+    if done is not None:
+        done_out_at = outs[3].data_ptr()
+    fp32 = 1 if logits.dtype is torch.float32 else 0
+    L = lib()
+    if workspace is None:
+        workspace = _empty((L.mxq_beam_select_workspace_bytes(N, W, V, k, fp32),), torch.uint8, dev, stream)
+    ws_at = _flat(workspace, "workspace", torch.uint8, on)
+    ctx, st = _launch_on(dev, stream)
+    with ctx:
+        _check(L.mxq_beam_select(logits.data_ptr(), row, fp32, scores_at, done_at, outs[0].data_ptr(),
+                                 outs[1].data_ptr(), outs[2].data_ptr(), done_out_at, N, W, V, k,
+                                 end_token if done is not None else 0, ws_at, workspace.numel(), st),
+               "mxq_beam_select")
+    return tuple(outs)
+
+
+def kv_reorder(pages, page_table, home_table, ctx_lens, parents, head_dim: int, group_size: int = 64,
+               table_out=None, lens_out=None, workspace=None, dev_status=None, stream=None):
+    """The cache after a selection of beams: sequence i of a group goes on from sequence
+    ``parents[i]`` of it (int32 [N, W], as beam_select gives them; groups of W sequences in a row).
+
+    ``home_table`` (int32 [S, max_pages]) are the pages that each sequence was given; ``page_table``
+    starts as a copy of it.  Full pages come to be shared, the page that is being written stays with
+    the lowest sequence that goes on from it, and each other one gets one of the group's own pages
+    of that column that nobody uses, into which the tokens are copied.  ``pages``: the cache, uint8
+    [n_pages, kv_heads, block] or [layers, n_pages, kv_heads, block] for layers with one table.
+    Returns (table, lens), the page table and ``ctx_lens`` (int32 [S]) of the sequences as they go
+    on; ``table_out`` and ``lens_out`` may be ``page_table`` and ``ctx_lens`` themselves."""
+    if stream is None:
+        found = _direct().kv_reorder(pages, page_table, home_table, ctx_lens, parents, head_dim, group_size,
+                                     table_out, lens_out, workspace, dev_status)
+        if found is not None:
+            return found
+    torch = _torch()
+    at = _flat(pages, "pages", torch.uint8)
+    dev = pages.device
+    on = dev.index
+    if pages.dim() not in (3, 4):
+        raise ValueError("pages must be [n_pages, kv_heads, block bytes] or [layers, n_pages, kv_heads, block bytes]")
+    layers = pages.shape[0] if pages.dim() == 4 else 1
+    if layers == 0:
+        raise ValueError("pages hold no layers")
+    _, n_pages, H, page_size = _cache(pages[0] if pages.dim() == 4 else pages, head_dim, group_size, on)
+    table_at = _flat(page_table, "page_table", torch.int32, on)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D [S, max_pages]")
+    S, max_pages = page_table.shape
+    home_at = _flat(home_table, "home_table", torch.int32, on)
+    if tuple(home_table.shape) != (S, max_pages):
+        raise ValueError("home_table has shape %s, expected %s" % (tuple(home_table.shape), (S, max_pages)))
+    lens_at = _flat(ctx_lens, "ctx_lens", torch.int32, on)
+    parents_at = _flat(parents, "parents", torch.int32, on)
+    if ctx_lens.numel() != S or parents.numel() != S or parents.dim() != 2 or not 0 < parents.shape[1] <= 64:
+        raise ValueError("ctx_lens must have S entries and parents be [N, W], N W = S, W up to 64")
+    if table_out is None:
+        table_out = _empty((S, max_pages), torch.int32, dev, stream)
+    if lens_out is None:
+        lens_out = _empty((S,), torch.int32, dev, stream)
+    table_out_at = _flat(table_out, "table_out", torch.int32, on)
+    lens_out_at = _flat(lens_out, "lens_out", torch.int32, on)
+    if tuple(table_out.shape) != (S, max_pages) or lens_out.numel() != S:
+        raise ValueError("table_out must be [S, max_pages] and lens_out have S entries")
+    status = None if dev_status is None else _flat(dev_status, "dev_status", torch.int32, on)
+    L = lib()
+    if workspace is None:
+        workspace = _empty((L.mxq_kv_reorder_workspace_bytes(S),), torch.uint8, dev, stream)
+    ws_at = _flat(workspace, "workspace", torch.uint8, on)
+    ctx, st = _launch_on(dev, stream)
+    with ctx:
+        _check(L.mxq_kv_reorder(at, table_at, home_at, lens_at, parents_at, table_out_at, lens_out_at, S,
+                                parents.shape[1], layers, n_pages, H, head_dim, max_pages, page_size, group_size,
+                                ws_at, workspace.numel(), status, st), "mxq_kv_reorder")
+    return table_out, lens_out
 
 
 def set_wait_budget(cycles: int) -> int:

@@ -511,4 +511,54 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
+size_t mxq_kv_reorder_workspace_bytes(int S) {
+    return S < 0 ? 0 : align_up((size_t)S * mxq::kv_reorder_move_bytes(), 256);
+}
+
+mxq_status mxq_kv_reorder(void* pages, const int32_t* page_table, const int32_t* home_table,
+                          const int32_t* ctx_lens, const int32_t* parents, int32_t* table_out,
+                          int32_t* lens_out, int S, int W, int layers, int n_pages, int Hkv, int D,
+                          int max_pages, int page_size, int group_size, void* workspace,
+                          size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    if (S < 0 || W <= 0 || W > 64 || S % W != 0 || layers <= 0 || n_pages <= 0 || Hkv <= 0 ||
+        max_pages <= 0 || !cache_shape(D, group_size, page_size))
+        return MXQ_ERR_INVALID_ARG;
+    if (!pages || (S > 0 && (!page_table || !home_table || !ctx_lens || !parents || !table_out || !lens_out)))
+        return MXQ_ERR_INVALID_ARG;
+    if (S > 0 && (table_out == home_table || lens_out == parents)) return MXQ_ERR_INVALID_ARG;
+    if (!aligned(pages, 16) || !aligned(page_table, 4) || !aligned(home_table, 4) || !aligned(ctx_lens, 4) ||
+        !aligned(parents, 4) || !aligned(table_out, 4) || !aligned(lens_out, 4) || !aligned(dev_status, 4) ||
+        !aligned(workspace, 256))
+        return MXQ_ERR_MISALIGNED;
+    if ((long long)max_pages * page_size > kMaxInt || S > kMaxInt || (long long)layers * Hkv > kMaxInt)
+        return MXQ_ERR_UNSUPPORTED;
+    if (S > 0 && (!workspace || workspace_bytes < mxq_kv_reorder_workspace_bytes(S)))
+        return MXQ_ERR_WORKSPACE;
+    const mxq_status st = mxq::check_current_device(nullptr);
+    if (st != MXQ_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dev_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess)
+        return MXQ_ERR_CUDA;
+    if (S == 0) return MXQ_OK;
+    mxq::KvReorderParams p;
+    p.pages = static_cast<uint8_t*>(pages);
+    p.table = page_table;
+    p.home = home_table;
+    p.lens = ctx_lens;
+    p.parents = parents;
+    p.table_out = table_out;
+    p.lens_out = lens_out;
+    p.moves = workspace;
+    p.S = S;
+    p.W = W;
+    p.layers = layers;
+    p.n_pages = n_pages;
+    p.H = Hkv;
+    p.max_pages = max_pages;
+    p.page_size = page_size;
+    p.status = dev_status;
+    const cudaError_t err = mxq::launch_kv_reorder(p, D, group_size, s);
+    return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+}
+
 }  // extern "C"

@@ -249,4 +249,16 @@ cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, int G, cudaStream_t 
 int kv_prefill_rows(int D);          // rows of its row tiles
 size_t kv_prefill_entry_bytes();     // workspace of a row tile
 
+// Reordering of the sequences of a paged cache, groups of W of them.
+struct KvReorderParams {
+    uint8_t* pages;          // [layers, n_pages, H, block]
+    const int32_t *table, *home, *lens, *parents;
+    int32_t *table_out, *lens_out;
+    void* moves;             // workspace: what is copied, for each sequence
+    int S, W, layers, n_pages, H, max_pages, page_size;
+    int32_t* status;
+};
+cudaError_t launch_kv_reorder(const KvReorderParams& p, int D, int G, cudaStream_t stream);
+size_t kv_reorder_move_bytes();
+
 }  // namespace mxq

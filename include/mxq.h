@@ -456,6 +456,64 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
 size_t mxq_kv_attention_shared_workspace_bytes(int T, int S, int N, int Hq, int Hkv, int D,
                                                int max_q_len, int max_group);
 
+/* The best continuations of N prompts with W beams each (beam search):
+ *   cand(w, v) = scores[w] + x[w, v] - log sum_u exp x[w, u]
+ * over a prompt's W beams and V tokens, x their logits; the K best, the best
+ * first, equal ones in the order of w V + v.
+ *   logits: bf16 or (fp32 != 0) fp32 [N W, V], row_stride values from row to row
+ *   (>= 0), any alignment of its type; scores: fp32 [N, W]
+ *   done: uint8 [N, W] or NULL: beams that have ended; such a one has the single
+ *   candidate end_token with its score as it is, and its logits are not read
+ *   out_scores: fp32, parents (w): int32, tokens (v): int32, all [N, K]
+ *   out_done: uint8 [N, K] or NULL: the parent had ended or the token is end_token
+ *   workspace: mxq_beam_select_workspace_bytes(N, W, V, K, fp32) bytes, 256-byte
+ *   aligned, overwritten
+ * A beam whose score is not finite is not in use: all its candidates, and any that
+ * are not a number (a row with a logit that is +inf or not a number has no
+ * others), count as -inf, which is a score like another: where there are fewer than K
+ * above it the lowest w V + v of those follow.  -inf logits are tokens that are not
+ * allowed.
+ * Candidates are compared in 64 bits; sums over a row are fp32 in chunks, which are
+ * added in 64 bits (scores are within 2^-18 and their rounding).  The result is
+ * deterministic, and equal rows with equal scores have equal candidates.
+ * Requirements: 1 <= W <= 64, 1 <= K <= 64, K <= W V; V > 0, W V < 2^31 - 65536;
+ * 0 <= end_token < V where done or out_done is given.                        */
+mxq_status mxq_beam_select(const void* logits, long long row_stride, int fp32, const float* scores,
+                           const uint8_t* done, float* out_scores, int32_t* parents, int32_t* tokens,
+                           uint8_t* out_done, int N, int W, int V, int K, int end_token, void* workspace,
+                           size_t workspace_bytes, void* stream);
+size_t mxq_beam_select_workspace_bytes(int N, int W, int V, int K, int fp32);
+
+/* The cache after a selection of beams.  Sequences g W .. g W + W - 1 are group g;
+ * sequence i of a group goes on from sequence parents[i] of it (0 .. W - 1), the
+ * tokens of a prefix that the group shares (mxq_kv_attention_shared) aside.
+ *   Every sequence has pages of its own, home_table int32 [S, max_pages], which
+ * never changes; page_table starts as a copy of it, and in each column holds
+ * pages out of the group's W home pages of that column.  Pages that are full are
+ * then shared by the sequences that go on from them; the page that is being written
+ * and those after it stay with the lowest of those sequences, and each other one
+ * gets the lowest home page (in the order of the group's sequences) that nobody
+ * keeps, into which the tokens are copied, in whole slabs of 8.
+ *   pages: uint8 [layers, n_pages, Hkv, block bytes]: layers whose caches have the
+ *   same page numbers are copied together
+ *   page_table, ctx_lens -> table_out int32 [S, max_pages], lens_out int32 [S],
+ *   which may be page_table and ctx_lens themselves; table_out[i, c], lens_out[i]
+ *   are those of the sequence it goes on from but for the pages above
+ *   parents: int32 [S]
+ *   workspace: mxq_kv_reorder_workspace_bytes(S) bytes, 256-byte aligned
+ * Sequences of a group may have different lengths.  A group with a parent outside
+ * 0 .. W - 1 or a length outside its pages stays as it is (MXQ_DEV_BAD_SEQUENCE),
+ * a column with pages that are not the group's home pages, or are outside the cache
+ * where tokens are copied, likewise (MXQ_DEV_BAD_PAGE).  Columns in which no sequence
+ * of a group has been given a page (negative in home_table) stay as they are.
+ * Requirements: 1 <= W <= 64, S % W == 0; pages 16-byte aligned.             */
+mxq_status mxq_kv_reorder(void* pages, const int32_t* page_table, const int32_t* home_table,
+                          const int32_t* ctx_lens, const int32_t* parents, int32_t* table_out,
+                          int32_t* lens_out, int S, int W, int layers, int n_pages, int Hkv, int D,
+                          int max_pages, int page_size, int group_size, void* workspace,
+                          size_t workspace_bytes, int32_t* dev_status, void* stream);
+size_t mxq_kv_reorder_workspace_bytes(int S);
+
 /* Static description of a status code. */
 const char* mxq_status_string(mxq_status status);
 
