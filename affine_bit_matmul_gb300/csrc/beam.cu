@@ -2,47 +2,65 @@
 //
 //   cand(w, v) = score[w] + x[w, v] - log sum_u exp x[w, u]
 //
-// A row's candidates are in the order of its logits x, so each CTA takes a chunk of one row,
-// keeps it in registers, and gives the K largest logits of it with their tokens, the
-// chunk's largest logit m and sum exp(x - m).  A second kernel, one CTA a prompt, adds the
-// sums to the rows' logarithms in 64 bits, turns the lists' logits into candidates and takes
-// the best K of all.
-//   Selecting without sorting: the largest logits of groups of threads are known, and at
-// least K logits are at or above the K-th largest of those; it is found bit by bit (16 bits
-// are enough), and what is not below it, little more than K logits, goes to shared memory,
-// where each counts how many are ahead of it.  Keys are (value, ~token), so no two are equal and
-// the order of arrival does not matter.  Where too many are level (rows of equal logits) the
-// K largest are taken one by one.
-//   Candidates are compared in 64 bits: two beams' are sums of different scores.  The chunks
-// of a row begin at the same tokens whatever the row's alignment, so that equal rows have equal
-// sums, and equal candidates of equal beams go to the lowest beam.
+// A row's candidates are in the order of its logits x, so each warp takes parts of rows, on
+// its own: it reads a part once, keeps the K largest logits with their tokens, the largest one
+// m and sum exp(x - m).  Then one CTA a prompt adds the sums to the rows' logarithms in 64 bits,
+// turns the lists' logits into candidates and takes the best K of all: the first of the prompt's
+// cluster where all prompts' clusters run at once, else a second kernel's.
+//   Selecting without sorting: a lane's vectors at one place of all steps are a slot, 128 of
+// them a warp, whose largest logits are known in the end.  At least K logits are at or above the K-th
+// largest of those, and a number a little below that is found bit by bit.  Only the slots that
+// reach it, few more than K, are looked at again, and what is not below it goes to shared memory, where
+// each of those logits counts how many are ahead of it.  Keys are (value, ~token), so no two are
+// equal.  When there are too many (level logits) the K best stay, and equal logits with later
+// tokens than all that were there cannot come in.
+//   Candidates are compared in 48 bits: two beams' are sums of different scores.  All rows are
+// cut at the same tokens, whatever their alignment, so that equal rows have equal sums, and equal
+// candidates of equal beams go to the lowest beam.
+//   A lane copies what it will look at (and its neighbour, where a row does not begin at 16
+// bytes) with asynchronous 16-byte copies two steps ahead; nothing in the loop waits for another
+// warp.
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "kv_attn_common.cuh"
 #include "mxq_internal.h"
 #include "tc_common.cuh"
 
 namespace mxq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRoom = 512;   // keys that are compared with each other
 constexpr int kMostK = 64;
 constexpr int kMostW = 64;
+constexpr int kMostCtas = 8;   // of a cluster
+constexpr int kMostClusters = 32;  // that run at once
+constexpr int kVecs = 4;       // 16-byte vectors of a lane in a step
+constexpr int kRoom = 96;      // keys of a warp: K and those of one look at 32 lanes
+constexpr int kStages = 3;
+constexpr int kFewK = 16;      // found one by one
+constexpr int kLook = 2;       // vectors of a lane that are looked at again at once
+constexpr int kPieces = kVecs * 32;              // of 16 bytes in a step
+constexpr int kStageBytes = (kPieces + 1) * 16;  // and one more, where rows are not aligned
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kSmem = kRingBytes + kWarps * (kRoom * 8 + kPieces);
+
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct BeamParams {
-    const void* logits;
+    const uint8_t* logits;
     long long row_stride;  // in bytes
     const float* scores;
     const uint8_t* done;
     float* out_scores;
     int32_t *parents, *tokens;
     uint8_t* out_done;
-    int N, W, V, K, chunks, end;
-    float2* stats;         // workspace: [row][chunk] largest logit, sum
-    unsigned long long* lists;  // workspace: [row][chunk][K] keys, 0 where there is none
+    int N, W, V, K, ctas, steps, parts, end;
+    float2* stats;              // workspace: [prompt][row in use][part] largest logit, sum
+    unsigned long long* lists;  // workspace: [prompt][row in use][part][K] keys, 0 where there is none
 };
 
 // Whether x orders before y as fp32 numbers is whether these order so as unsigned ones.
@@ -53,12 +71,18 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float from_ordered(uint32_t u) {
     return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
-__device__ __forceinline__ unsigned long long ordered(double x) {
-    const unsigned long long u = (unsigned long long)__double_as_longlong(x);
-    return u ^ ((unsigned long long)((long long)u >> 63) | 0x8000000000000000ull);
-}
-__device__ __forceinline__ double from_ordered(unsigned long long u) {
-    return __longlong_as_double((long long)(u ^ ((u >> 63) ? 0x8000000000000000ull : ~0ull)));
+// A candidate, logit and a row's offset (two fp32 numbers, the second within half a step of the
+// first), as a key: the sum in 48 bits, an fp32 number and what its rounding left.
+__device__ __forceinline__ unsigned long long sum_key(float x, float2 off) {
+    float s = x + off.x, e = 0.f;
+    if (fabsf(s) < INFINITY) {
+        const float y = s - x;
+        e = (x - (s - y)) + (off.x - y) + off.y;
+        const float t = s + e;
+        e = e - (t - s);
+        s = t;
+    }
+    return (unsigned long long)ordered(s + 0.f) << 32 | ordered(e + 0.f);
 }
 
 // A logit as a candidate's first key: -0 as +0, what is not a number as -inf.
@@ -70,10 +94,24 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
-__device__ __forceinline__ float exp2_of(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void parts_of(uint64_t p, float* a, float* b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
 // 16 bytes of a row, in registers.
@@ -85,8 +123,11 @@ struct Vec {
         if constexpr (F32) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
     }
-    __device__ __forceinline__ void none() {
-        w[0] = w[1] = w[2] = w[3] = F32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+    // the same, where i is not known to the compiler
+    __device__ __forceinline__ float any(int i) const {
+        const int k = F32 ? i : i / 2;
+        const uint32_t x = k < 2 ? (k ? w[1] : w[0]) : k == 2 ? w[2] : w[3];
+        return __uint_as_float(F32 ? x : i & 1 ? x & 0xFFFF0000u : x << 16);
     }
     // the largest that is a number
     __device__ __forceinline__ float most() const {
@@ -97,37 +138,48 @@ struct Vec {
             return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
         }
     }
-    // values v .. of a row of V at `row`; -inf past the end
+    // values past the first n: -inf
+    __device__ __forceinline__ void cut(int n) {
+#pragma unroll
+        for (int i = 0; i < kSize; ++i) {
+            if (i < n) continue;
+            if constexpr (F32) w[i] = 0xFF800000u;
+            else w[i / 2] = i & 1 ? (w[i / 2] & 0xFFFFu) | 0xFF800000u : (w[i / 2] & 0xFFFF0000u) | 0xFF80u;
+        }
+    }
+    // values v .. of a row of V in memory, v < V
     __device__ __forceinline__ void load(const uint8_t* row, int v, int V) {
         const uint8_t* at = row + (long long)v * kBytes;
         const int off = (int)(reinterpret_cast<uintptr_t>(at) & 15);
         if (off == 0 && v + kSize <= V) {
             const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
             w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-        } else if (v > 0 && v + 2 * kSize - off / kBytes <= V) {
-            // between two aligned pieces, both within the row
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(at - off));
-            const uint4 y = __ldg(reinterpret_cast<const uint4*>(at - off) + 1);
-            const int bits = (off & 3) * 8;
-            const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            switch (off >> 2) {
-                case 0: shift<0>(u, bits); break;
-                case 1: shift<1>(u, bits); break;
-                case 2: shift<2>(u, bits); break;
-                default: shift<3>(u, bits);
-            }
-        } else {
-            none();
+            return;
+        }
+        w[0] = w[1] = w[2] = w[3] = 0;
 #pragma unroll
-            for (int i = 0; i < kSize; ++i) {
-                if (v + i >= V) continue;
-                if constexpr (F32) {
-                    w[i] = __ldg(reinterpret_cast<const uint32_t*>(at) + i);
-                } else {
-                    const uint32_t x = __ldg(reinterpret_cast<const uint16_t*>(at) + i);
-                    w[i / 2] = i & 1 ? (w[i / 2] & 0xFFFFu) | x << 16 : (w[i / 2] & 0xFFFF0000u) | x;
-                }
-            }
+        for (int i = 0; i < kSize; ++i) {
+            if (v + i >= V) continue;
+            if constexpr (F32) w[i] = __ldg(reinterpret_cast<const uint32_t*>(at) + i);
+            else w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(at) + i) << (i & 1 ? 16 : 0);
+        }
+        cut(V - v);
+    }
+    // from two aligned pieces in shared memory, `off` bytes into the first
+    __device__ __forceinline__ void load(uint32_t at, int off) {
+        const uint4 x = ld_shared_v4(at);
+        if (off == 0) {
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            return;
+        }
+        const uint4 y = ld_shared_v4(at + 16);
+        const int bits = (off & 3) * 8;
+        const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        switch (off >> 2) {
+            case 0: shift<0>(u, bits); break;
+            case 1: shift<1>(u, bits); break;
+            case 2: shift<2>(u, bits); break;
+            default: shift<3>(u, bits);
         }
     }
 
@@ -139,39 +191,54 @@ private:
     }
 };
 
-// The groups' largest values of a block, in shared memory, and from them the largest and a
-// lower bound of the K-th largest of all: 2^SHIFT below it at most.
-template <int SHIFT>
-__device__ __forceinline__ uint32_t bound_of(const uint32_t* groups, int n, int K, uint32_t* top) {
-    const int lane = threadIdx.x & 31;
-    uint32_t x[kThreads / 32];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-        x[i] = i * 32 < n ? groups[i * 32 + lane] : 0u;
-        m = max(m, x[i]);
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
+    const uint32_t x = max(a, b);
+    b = min(a, b);
+    a = x;
+}
+
+// The K-th largest of four values of each lane, taken away from the top; for small K.
+__device__ __forceinline__ uint32_t kth_of(uint32_t (&x)[4], int K) {
+    order(x[0], x[1]);
+    order(x[2], x[3]);
+    order(x[0], x[2]);
+    order(x[1], x[3]);
+    order(x[1], x[2]);
+    for (;;) {
+        const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, x[0]);
+        const bool mine = x[0] == t;
+        K -= __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        if (K <= 0 || t == 0) return t;
+        if (mine) {
+            x[0] = x[1];
+            x[1] = x[2];
+            x[2] = x[3];
+            x[3] = 0;
+        }
     }
-    *top = __reduce_max_sync(0xFFFFFFFFu, m);
-    uint32_t t = 0;
-#pragma unroll 1
-    for (int bit = 31; bit >= SHIFT; --bit) {
+}
+
+// From N values of each lane a lower bound of the K-th largest of all that K of them are not below.
+template <int N>
+__device__ __forceinline__ uint32_t bound_in(const uint32_t (&x)[N], int K) {
+    uint32_t both = ~0u, any = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        both &= x[i];
+        any |= x[i];
+    }
+    any = __reduce_or_sync(0xFFFFFFFFu, any);
+    const int high = 31 - __clz(any & ~__reduce_and_sync(0xFFFFFFFFu, both));  // -1: all are equal
+    uint32_t t = high < 0 ? any : high == 31 ? 0u : any >> (high + 1) << (high + 1);
+    for (int bit = high; bit >= 0; --bit) {
         const uint32_t c = t | 1u << bit;
         int count = 0;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i)
-            if (i * 32 < n) count += __popc(__ballot_sync(0xFFFFFFFFu, x[i] >= c));
+        for (int i = 0; i < N; ++i) count += __popc(__ballot_sync(0xFFFFFFFFu, x[i] >= c));
         if (count >= K) t = c;
+        if (count == K) break;
     }
     return t;
-}
-
-// How many threads make a group, of 256: the K-th largest of their maxima is then not far
-// below the K-th largest of all.
-__device__ __forceinline__ int group_threads(int K) { return K <= 10 ? 8 : K <= 40 ? 2 : 1; }
-
-__device__ __forceinline__ uint32_t group_max(uint32_t x, int threads) {
-    for (int o = 1; o < threads; o <<= 1) x = max(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-    return x;
 }
 
 struct Key {
@@ -201,259 +268,547 @@ __device__ __forceinline__ Key block_first(Key k, Key* room) {
     return best;
 }
 
-// One chunk of a row, NV vectors a thread.
-//   Bound by the memory.
-template <bool F32, int NV>
-__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams p) {
-    using V4 = Vec<F32>;
-    __shared__ uint32_t groups[kThreads];
-    __shared__ unsigned long long keys[kRoom];
-    __shared__ float sums[kWarps];
-    __shared__ Key room[kWarps];
-    __shared__ int count;
-    pdl_launch_dependents();
-    const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    // a beam that has ended, or that is not in use, has no candidates here
-    const float score = __ldg(p.scores + row);
-    if (!(fabsf(score) < INFINITY) || (p.done && __ldg(p.done + row))) return;
-    const uint8_t* x = static_cast<const uint8_t*>(p.logits) + row * p.row_stride;
-    const int first = (chunk * NV * kThreads + (int)threadIdx.x) * V4::kSize;
-    auto token = [&](int i) { return first + i * kThreads * V4::kSize; };
-    if (threadIdx.x == 0) count = 0;
-    V4 v[NV];
-    if (((reinterpret_cast<uintptr_t>(x) & 15) == 0) &&
-        (chunk + 1) * NV * kThreads * V4::kSize <= p.V) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const uint4 y = __ldg(reinterpret_cast<const uint4*>(x + (long long)token(i) * V4::kBytes));
-            v[i].w[0] = y.x, v[i].w[1] = y.y, v[i].w[2] = y.z, v[i].w[3] = y.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (token(i) < p.V) v[i].load(x, token(i), p.V);
-            else v[i].none();
-        }
-    }
-    float most = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) most = fmaxf(most, v[i].most());
-    const int each = group_threads(p.K), n_groups = kThreads / each;
-    const uint32_t g = group_max(value_key(most), each);
-    if (threadIdx.x % each == 0) groups[threadIdx.x / each] = g;
-    __syncthreads();
-    uint32_t top;
-    const uint32_t bound = bound_of<16>(groups, n_groups, p.K, &top);
-    // ---- sum of exponentials
-    const float m = from_ordered(top), ref = m == -INFINITY ? 0.f : m;
-    float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < V4::kSize; e += 2) {
-            l0 += exp2_of((v[i].at(e) - ref) * 1.4426950408889634f);
-            l1 += exp2_of((v[i].at(e + 1) - ref) * 1.4426950408889634f);
-        }
-    float l = l0 + l1;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    if (lane == 0) sums[warp] = l;
-    // ---- keys at or above the bound
-    auto key_of = [&](float y, int t) {
-        return (unsigned long long)value_key(y) << 32 | (uint32_t)~t;
-    };
-    if (value_key(most) >= bound) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (value_key(v[i].most()) < bound) continue;
-#pragma unroll
-            for (int e = 0; e < V4::kSize; ++e) {
-                if (value_key(v[i].at(e)) >= bound && token(i) + e < p.V) {
-                    const int at = atomicAdd(&count, 1);
-                    if (at < kRoom) keys[at] = key_of(v[i].at(e), token(i) + e);
-                }
-            }
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float sum = 0.f;
-        for (int i = 0; i < kWarps; ++i) sum += sums[i];
-        p.stats[blockIdx.x] = make_float2(m, sum);
-    }
-    unsigned long long* out = p.lists + (long long)blockIdx.x * p.K;
-    const int n = count;
-    if (n <= kRoom) {
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const unsigned long long k = keys[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += keys[j] > k;
-            if (rank < p.K) out[rank] = k;
-        }
-        for (int i = n + threadIdx.x; i < p.K; i += kThreads) out[i] = 0;
-        return;
-    }
-    // level logits: the largest, the next one, ...
-    Key last{~0ull, 0};
-    for (int r = 0; r < p.K; ++r) {
-        Key k{0, 0};
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < V4::kSize; ++e)
-                if (token(i) + e < p.V) {
-                    const unsigned long long y = key_of(v[i].at(e), token(i) + e);
-                    if (y < last.value && y > k.value) k.value = y;
-                }
-        last = block_first(k, room);
-        if (threadIdx.x == 0) out[r] = last.value;
-    }
+struct Rows {
+    float2 offset[kMostW];
+    float top[kMostW];
+    unsigned long long sum[kMostW];
+    int8_t place[kMostW];   // of a row: its number among those in use; -1: ended or without a score
+    uint8_t row[kMostW];    // and back
+    int live, parts, steps; // rows in use; parts of a row, steps of a part
+    long long place0;       // of the prompt's parts
+};
+constexpr int kClusterWarps = kMostCtas * kWarps;
+constexpr int kClusterPlaces = kClusterWarps + kMostW;
+
+// Whether beam `row` of all has logits that count.
+__device__ __forceinline__ bool in_use(const BeamParams& p, long long row) {
+    return fabsf(__ldg(p.scores + row)) < INFINITY && !(p.done && __ldg(p.done + row));
 }
 
-// One prompt: the best K of the lists of its rows.
-__global__ void __launch_bounds__(kThreads) beam_best_kernel(const BeamParams p) {
-    __shared__ double offset[kMostW];
-    __shared__ uint8_t live[kMostW];
-    __shared__ uint32_t groups[kThreads];
-    __shared__ Key keys[kRoom];
-    __shared__ Key room[kWarps];
-    __shared__ int count;
-    const int prompt = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int row0 = prompt * p.W, each_row = max(p.chunks * p.K, p.K + 1), all = p.W * each_row;
-    if (threadIdx.x == 0) count = 0;
-    pdl_wait();
+// A prompt's rows in use, by one warp: beams that have ended, or have no score, have no candidates
+// in their logits.
+__device__ __forceinline__ int find_rows(const BeamParams& p, Rows& r, long long row0) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kMostW; i += 32) {
+        const int w = i + lane;
+        const bool in = w < p.W && in_use(p, row0 + w);
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, in);
+        const int at = n + __popc(live & ((1u << lane) - 1u));
+        if (w < p.W) r.place[w] = in ? at : -1;
+        if (in) r.row[at] = w;
+        n += __popc(live);
+    }
+    if (lane == 0) r.live = n;
+    return n;
+}
+
+// What the first CTA selects with, where the ring was.
+struct Best {
+    static constexpr int kKeys = 1024;
+    Key keys[kKeys];
+    uint32_t groups[kThreads / 2];
+    Key first[kWarps];
+    int count;
+};
+
+// The best K candidates of a prompt out of its rows' lists; one CTA.
+__device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Best& s, int prompt) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, row0 = prompt * p.W, parts = r.parts;
+    // entries: the lists of the rows in use, and K + 1 of each row, for those that have no other ones
+    const int each_row = parts * p.K, in_lists = r.live * each_row, all = in_lists + p.W * (p.K + 1);
+    auto entry = [&](int i) {
+        if (i >= in_lists) return 0ull;
+        const int n = i / each_row;
+        return __ldcg(p.lists + (r.place0 + r.place[r.row[n]] * parts) * p.K + (i - n * each_row));
+    };
+    constexpr int kHeld = 2;  // entries that a thread keeps
+    unsigned long long held[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = tid + i * kThreads < all ? entry(tid + i * kThreads) : 0;
     // ---- the rows' logarithms
+    if (tid == 0) s.count = 0;
     for (int w = warp; w < p.W; w += kWarps) {
-        const float score = __ldg(p.scores + row0 + w);
-        const bool in = fabsf(score) < INFINITY && !(p.done && __ldg(p.done + row0 + w));
-        double off = 0.0;
-        bool ok = in;
-        if (in) {
-            const float2* st = p.stats + (long long)(row0 + w) * p.chunks;
-            float m = -INFINITY;
-            for (int c = lane; c < p.chunks; c += 32) m = fmaxf(m, __ldcg(st + c).x);
+        if (r.place[w] < 0) continue;
+        const float2* st = p.stats + r.place0 + r.place[w] * parts;
+        const float2 x = lane < parts ? __ldcg(st + lane) : make_float2(-INFINITY, 0.f);
+        float m = x.x;  // in powers of two
+        for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, __ldcg(st + i).x);
+        m = from_ordered(__reduce_max_sync(0xFFFFFFFFu, ordered(m)));
+        // the parts' sums in units of 2^-31, which are added without rounding (there are less than
+        // 2^31 terms of at most 1; a part of -inf has the sum 0)
+        bool ok = true;
+        auto scaled = [&](float2 y) {
+            const float l = y.x == -INFINITY ? y.y : y.y * exp2_approx(y.x - m);
+            ok = ok && l < INFINITY;  // (a number)
+            return ok ? (unsigned long long)((double)l * 0x1p31) : 0ull;
+        };
+        unsigned long long l = scaled(x);
+        for (int i = lane + 32; i < parts; i += 32) l += scaled(__ldcg(st + i));
 #pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            double l = 0.0;
-            for (int c = lane; c < p.chunks; c += 32) {
-                const float2 s = __ldcg(st + c);
-                // (a chunk of -inf has the sum 0)
-                l += s.x == -INFINITY ? (double)s.y : (double)s.y * exp((double)s.x - (double)m);
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-            off = (double)score - ((double)m + log(l));
-            ok = off - off == 0.0;  // a number: some logit is finite, none is +inf or not a number
-        }
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (lane == 0) {
-            offset[w] = off;
-            live[w] = ok;
+            r.top[w] = m;
+            r.sum[w] = ok ? l : 0;
         }
     }
     __syncthreads();
-    // candidate e of row w
-    auto candidate = [&](int w, int e) {
-        Key k{0, 0};
-        if (live[w]) {
-            if (e >= p.chunks * p.K) return k;
-            const unsigned long long x = __ldcg(p.lists + (long long)(row0 + w) * p.chunks * p.K + e);
-            if (x == 0) return k;
-            k.value = ordered((double)from_ordered((uint32_t)(x >> 32)) + offset[w]);
-            k.back = ~((uint32_t)w * (uint32_t)p.V + ~(uint32_t)x);
-        } else if (e <= p.K) {
-            // a beam that has ended: its end token as it stands; then, as for one without
-            // candidates, the lowest tokens at -inf
-            const float score = __ldg(p.scores + row0 + w);
-            const bool ended = p.done && __ldg(p.done + row0 + w) && fabsf(score) < INFINITY;
-            int t = e - 1;
-            double x = -INFINITY;
-            if (e == 0) {
-                if (!ended) return k;
-                t = p.end;
-                x = (double)score;
-            } else if (t >= p.V || (ended && t == p.end)) {
-                return k;
-            }
-            k.value = ordered(x);
-            k.back = ~((uint32_t)w * (uint32_t)p.V + (uint32_t)t);
+    for (int w = tid; w < p.W; w += kThreads) {
+        // in 64 bits, as two fp32 numbers; not a number where no logit is finite, or one is +inf
+        // or not a number
+        float2 off = make_float2(NAN, 0.f);
+        if (r.place[w] >= 0 && r.sum[w]) {
+            // (the powers of two are of products with log2 e as an fp32 number)
+            const double x = (double)__ldg(p.scores + row0 + w) -
+                             ((double)r.top[w] * (1.0 / (double)kLog2e) + (log((double)r.sum[w]) - 21.487562597358306));  // 31 ln 2
+            off.x = (float)x;
+            off.y = (float)(x - (double)off.x);
         }
+        r.offset[w] = off;
+    }
+    __syncthreads();
+    // what entry i, x in a list, is as a candidate
+    auto candidate = [&](int i, unsigned long long x) {
+        Key k{0, 0};
+        if (i < in_lists) {
+            const int w = r.row[i / each_row];
+            const float2 off = r.offset[w];
+            if (x == 0 || off.x - off.x != 0.f) return k;
+            k.value = sum_key(from_ordered((uint32_t)(x >> 32)), off);
+            k.back = ~((uint32_t)w * (uint32_t)p.V + ~(uint32_t)x);
+            return k;
+        }
+        // a beam that has ended: its end token as it stands; then, as for one without
+        // candidates, the lowest tokens at -inf
+        const int w = (i - in_lists) / (p.K + 1), e = (i - in_lists) - w * (p.K + 1);
+        const float off = r.offset[w].x;
+        if (off - off == 0.f) return k;
+        const float score = __ldg(p.scores + row0 + w);
+        const bool ended = p.done && __ldg(p.done + row0 + w) && fabsf(score) < INFINITY;
+        int t = e - 1;
+        float y = -INFINITY;
+        if (e == 0) {
+            if (!ended) return k;
+            t = p.end;
+            y = score;
+        } else if (t >= p.V || (ended && t == p.end)) {
+            return k;
+        }
+        k.value = sum_key(y, make_float2(0.f, 0.f));
+        k.back = ~((uint32_t)w * (uint32_t)p.V + (uint32_t)t);
         return k;
     };
+    auto nth = [&](int i) { return candidate(i, entry(i)); };
+    Key mine[kHeld];
     uint32_t most = 0;
-    for (int i = threadIdx.x; i < all; i += kThreads)
-        most = max(most, (uint32_t)(candidate(i / each_row, i % each_row).value >> 32));
-    const int each = group_threads(p.K), n_groups = kThreads / each;
-    const uint32_t g = group_max(most, each);
-    if (threadIdx.x % each == 0) groups[threadIdx.x / each] = g;
-    __syncthreads();
-    uint32_t top;
-    const uint32_t bound = bound_of<0>(groups, n_groups, p.K, &top);
-    for (int i = threadIdx.x; i < all; i += kThreads) {
-        const Key k = candidate(i / each_row, i % each_row);
-        if (k.value != 0 && (uint32_t)(k.value >> 32) >= bound) {
-            const int at = atomicAdd(&count, 1);
-            if (at < kRoom) keys[at] = k;
-        }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        mine[i] = Key{0, 0};
+        if (tid + i * kThreads < all) mine[i] = candidate(tid + i * kThreads, held[i]);
+        most = max(most, (uint32_t)(mine[i].value >> 32));
     }
+    for (int i = tid + kHeld * kThreads; i < all; i += kThreads) most = max(most, (uint32_t)(nth(i).value >> 32));
+    // groups of 4 or 2 threads
+    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+    if (p.K <= 40) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+    const int each = p.K <= 40 ? 4 : 2;
+    if (tid % each == 0) s.groups[tid / each] = most;
+    __syncthreads();
+    uint32_t bound;
+    if (p.K <= 40) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = s.groups[i * 32 + lane];
+        bound = p.K <= kFewK ? kth_of(x, p.K) : bound_in(x, p.K);
+    } else {
+        uint32_t x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = s.groups[i * 32 + lane];
+        bound = bound_in(x, p.K);
+    }
+    auto take = [&](const Key& k) {
+        if (k.value == 0 || (uint32_t)(k.value >> 32) < bound) return;
+        const int at = atomicAdd(&s.count, 1);
+        if (at < Best::kKeys) s.keys[at] = k;
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) take(mine[i]);
+    for (int i = tid + kHeld * kThreads; i < all; i += kThreads) take(nth(i));
     __syncthreads();
     auto give = [&](int rank, const Key& k) {
         const uint32_t flat = ~k.back;
         const int w = (int)(flat / (uint32_t)p.V), t = (int)(flat % (uint32_t)p.V);
         const long long to = (long long)prompt * p.K + rank;
-        p.out_scores[to] = (float)from_ordered(k.value);
+        p.out_scores[to] = from_ordered((uint32_t)(k.value >> 32));
         p.parents[to] = w;
         p.tokens[to] = t;
-        if (p.out_done) p.out_done[to] = (p.done && p.done[row0 + w]) || t == p.end;
+        if (p.out_done) p.out_done[to] = (p.done && __ldg(p.done + row0 + w)) || t == p.end;
     };
-    const int n = count;
-    if (n <= kRoom) {
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const Key k = keys[i];
+    const int n = s.count;
+    if (n <= Best::kKeys) {
+        for (int i = tid; i < n; i += kThreads) {
+            const Key k = s.keys[i];
             int rank = 0;
-            for (int j = 0; j < n; ++j) rank += ahead(keys[j], k);
+            for (int j = 0; j < n; ++j) rank += ahead(s.keys[j], k);
             if (rank < p.K) give(rank, k);
         }
         return;
     }
+    // level candidates: the best, the next one, ...
     Key last{~0ull, ~0u};
-    for (int r = 0; r < p.K; ++r) {
+    for (int rank = 0; rank < p.K; ++rank) {
         Key k{0, 0};
-        for (int i = threadIdx.x; i < all; i += kThreads) {
-            const Key y = candidate(i / each_row, i % each_row);
+        for (int i = tid; i < all; i += kThreads) {
+            const Key y = nth(i);
             if (ahead(last, y) && ahead(y, k)) k = y;
         }
-        last = block_first(k, room);
-        if (threadIdx.x == 0) give(r, last);
+        last = block_first(k, s.first);
+        if (tid == 0) give(rank, last);
     }
 }
 
-// Vectors of a thread: as many as leave four CTAs for each SM, up to 8.
-struct Cut {
-    int vectors, chunks;
-};
-Cut cut_of(long long rows, int V, int fp32) {
-    Cut c{8, 1};
-    for (;; c.vectors /= 2) {
-        const int size = c.vectors * kThreads * (fp32 ? 4 : 8);
-        c.chunks = (V - 1) / size + 1;
-        if (c.vectors == 1 || rows * c.chunks >= 4 * 152) return c;
+// The best K of a warp's n keys (at most kRoom), in order where `to` is.
+__device__ __forceinline__ void rank_keys(const unsigned long long* keys, int n, int K, unsigned long long* to) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long k[kRoom / 32];
+    int rank[kRoom / 32];
+#pragma unroll
+    for (int i = 0; i < kRoom / 32; ++i) {
+        k[i] = i * 32 + lane < n ? keys[i * 32 + lane] : 0;
+        rank[i] = 0;
     }
+    for (int j = 0; j < n; ++j) {
+        const unsigned long long x = keys[j];
+#pragma unroll
+        for (int i = 0; i < kRoom / 32; ++i) rank[i] += x > k[i];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kRoom / 32; ++i)
+        if (k[i] && rank[i] < K) to[rank[i]] = k[i];
+    __syncwarp();
+}
+
+// CLUSTER: a prompt's CTAs take its parts, and its first one the best of them.
+//   Bound by the memory.
+template <bool F32, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
+    using V4 = Vec<F32>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ Rows rows;
+    const int prompt = CLUSTER ? (int)blockIdx.x / p.ctas : 0, cta = CLUSTER ? (int)blockIdx.x % p.ctas : (int)blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    const long long row0 = (long long)prompt * p.W;
+    const int all_steps = (p.V - 1) / (kPieces * V4::kSize) + 1;
+    if constexpr (CLUSTER) {
+        if (warp == 0) {
+            const int n = find_rows(p, rows, row0);
+            if (lane == 0) {
+                // a part for each warp of the cluster, if it is a step at least
+                const int most = p.ctas * kWarps / max(n, 1);
+                const int steps = (all_steps - 1) / max(1, min(most, all_steps)) + 1;
+                rows.steps = steps;
+                rows.parts = (all_steps - 1) / steps + 1;
+                rows.place0 = (long long)prompt * kClusterPlaces;
+            }
+        }
+        __syncthreads();
+    } else {
+        pdl_launch_dependents();
+    }
+    const int parts = CLUSTER ? rows.parts : p.parts, part_steps = CLUSTER ? rows.steps : p.steps;
+    // this warp's parts: every so many of all rows
+    const long long items = CLUSTER ? (long long)rows.live * parts : (long long)p.N * p.W * parts;
+    const int stride = (CLUSTER ? p.ctas : (int)gridDim.x) * kWarps;
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
+    unsigned long long* keys = reinterpret_cast<unsigned long long*>(smem + kRingBytes) + warp * kRoom;
+    uint8_t* slots = smem + kRingBytes + kWarps * kRoom * 8 + warp * kPieces;
+    // Steps one after the other: of a part of the row at x, from step0 to `end`.
+    struct At {
+        long long item;
+        int step0, step, end;
+        const uint8_t* x;
+    };
+    auto begin = [&](At& a, long long item) {
+        for (a.item = item; a.item < items; a.item += stride) {
+            const long long i = a.item / parts;
+            if (!CLUSTER && !in_use(p, i)) continue;
+            a.x = p.logits + (CLUSTER ? row0 + rows.row[i] : i) * p.row_stride;
+            a.step = a.step0 = (int)(a.item - i * parts) * part_steps;
+            a.end = min(a.step + part_steps, all_steps);
+            return;
+        }
+    };
+    auto next = [&](At& a) {
+        if (++a.step == a.end) begin(a, a.item + stride);
+    };
+    // the copies of a step's pieces that are within its row
+    At ahead_at{};
+    int to_stage = 0;
+    auto issue = [&]() {
+        if (ahead_at.item < items) {
+            const uint8_t* row = ahead_at.x;
+            const uint8_t* end = row + (long long)p.V * V4::kBytes;
+            const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+            const uint32_t to = ring + to_stage * kStageBytes;
+            const uint8_t* from = row - off + (long long)ahead_at.step * (kPieces * 16);
+            auto piece = [&](int i) {
+                const uint8_t* at = from + i * 16;
+                if (at >= end) return;
+                if (at >= row) {
+                    const long long left = end - at;
+                    cp_async_16(to + i * 16, at, left < 16 ? (uint32_t)left : 16u);
+                } else {
+                    // what is before the row is not read
+                    for (int b = off; b < 16 && at + b < end; b += V4::kBytes) {
+                        if constexpr (F32)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + i * 16 + b),
+                                         "r"(__ldg(reinterpret_cast<const uint32_t*>(at + b)))
+                                         : "memory");
+                        else
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + i * 16 + b),
+                                         "h"(__ldg(reinterpret_cast<const uint16_t*>(at + b)))
+                                         : "memory");
+                    }
+                }
+            };
+            if (off == 0 && from + kPieces * 16 <= end) {
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) cp_async_16(to + (i * 32 + lane) * 16, from + (i * 32 + lane) * 16, 16u);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kVecs; ++i) piece(i * 32 + lane);
+                if (lane == 0 && off) piece(kPieces);
+            }
+            if (++to_stage == kStages) to_stage = 0;
+            next(ahead_at);
+        }
+        cp_async_commit();
+    };
+    begin(ahead_at, cta * kWarps + warp);
+    At at = ahead_at;
+    issue();
+    issue();
+    int stage = 0;
+    float m = -INFINITY, l = 0.f;
+    float so_far[kVecs];  // largest logits of the slots
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) so_far[i] = -INFINITY;
+    while (at.item < items) {
+        cp_async_wait<1>();
+        __syncwarp();
+        issue();
+        const int off = (int)(reinterpret_cast<uintptr_t>(at.x) & 15);
+        const uint32_t from = ring + stage * kStageBytes + lane * 16;
+        if (++stage == kStages) stage = 0;
+        const int token0 = (at.step * kPieces + lane) * V4::kSize;
+        auto token = [&](int i) { return token0 + i * (32 * V4::kSize); };
+        V4 v[kVecs];
+        float top[kVecs], most = -INFINITY;
+        if (off == 0 && at.step + 1 < all_steps) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) v[i].load(from + i * 512, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                v[i].load(from + i * 512, off);
+                if (token(i) + V4::kSize > p.V) v[i].cut(p.V - token(i));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            top[i] = v[i].most();
+            most = fmaxf(most, top[i]);
+        }
+        // ---- sum of exponentials
+        // exp x as 2^(x log2 e - m), where m is the largest x log2 e, rounded
+        const float was = m;
+        m = fmaxf(m, most * kLog2e);
+        const float ref = m == -INFINITY ? 0.f : m;
+        l *= exp2_approx(was - ref);
+        const uint64_t ref2 = pair_of(-ref, -ref), log2 = pair_of(kLog2e, kLog2e);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            uint64_t sum = 0;
+#pragma unroll
+            for (int j = 0; j < V4::kSize; j += 2) {
+                float a, b;
+                parts_of(fma_pair(pair_of(v[i].at(j), v[i].at(j + 1)), log2, ref2), &a, &b);
+                const uint64_t e = pair_of(exp2_approx(a), exp2_approx(b));
+                sum = j ? add_pair(sum, e) : e;
+            }
+            float a, b;
+            parts_of(sum, &a, &b);
+            l += a + b;
+        }
+        // ---- keys at or above the bound
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) so_far[i] = fmaxf(so_far[i], top[i]);
+        const At was_at = at;
+        next(at);
+        if (at.item == was_at.item) continue;
+        // ---- the part is done: a bound of its K best logits
+        uint32_t slot_key[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) slot_key[i] = value_key(so_far[i]);
+        const uint32_t t = p.K <= kFewK ? kth_of(slot_key, p.K) : bound_in(slot_key, p.K);
+        // (what is left of the bits of -inf may be no number)
+        float bound = from_ordered(max(t, ordered(-INFINITY)));
+        // the slots that reach it, in order
+        int n_slots = 0;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, so_far[i] >= bound);
+            if ((who >> lane) & 1u) slots[n_slots + __popc(who & ((1u << lane) - 1u))] = (uint8_t)(i * 32 + lane);
+            n_slots += __popc(who);
+        }
+        __syncwarp();
+        // their vectors of all steps, by token
+        const int step0 = was_at.step0, n_vecs = n_slots * (was_at.end - step0);
+        int have = 0;  // keys
+        for (int q0 = 0; q0 < n_vecs; q0 += 32 * kLook) {
+            // the loads of several then take the time of one
+            V4 x[kLook];
+            int first_token[kLook];
+            uint32_t mine[kLook];
+#pragma unroll
+            for (int i = 0; i < kLook; ++i) {
+                const int q = q0 + i * 32 + lane, step = q / n_slots;
+                first_token[i] = q < n_vecs ? ((step0 + step) * kPieces + slots[q - step * n_slots]) * V4::kSize : p.V;
+                if (first_token[i] < p.V) x[i].load(was_at.x, first_token[i], p.V);
+            }
+#pragma unroll
+            for (int i = 0; i < kLook; ++i) {
+                mine[i] = 0;
+#pragma unroll
+                for (int j = 0; j < V4::kSize; ++j)
+                    mine[i] |= (first_token[i] + j < p.V && x[i].at(j) >= bound ? 1u : 0u) << j;
+            }
+#pragma unroll
+            for (int i = 0; i < kLook; ++i) {
+                bool full = false;  // the bound is a key's
+                for (uint32_t any = __reduce_or_sync(0xFFFFFFFFu, mine[i]); any; any &= any - 1) {
+                    const int j = __ffs(any) - 1;
+                    const float y = x[i].any(j);
+                    const bool take = ((mine[i] >> j) & 1u) && y >= bound;
+                    uint32_t who = __ballot_sync(0xFFFFFFFFu, take);
+                    if (have + __popc(who) > kRoom) {
+                        rank_keys(keys, have, p.K, keys);
+                        have = p.K;
+                        bound = from_ordered((uint32_t)(keys[p.K - 1] >> 32));
+                        full = true;
+                        who = __ballot_sync(0xFFFFFFFFu, take && y >= bound);
+                    }
+                    if ((who >> lane) & 1u)
+                        keys[have + __popc(who & ((1u << lane) - 1u))] =
+                            (unsigned long long)value_key(y) << 32 | (uint32_t)~(first_token[i] + j);
+                    have += __popc(who);
+                    __syncwarp();
+                }
+                // tokens only grow from here on: equal values are not ahead of any of K keys
+                if (full) bound = from_ordered(min(ordered(bound) + 1u, ordered(INFINITY)));
+            }
+        }
+        const long long place = (CLUSTER ? rows.place0 : 0) + was_at.item;
+        unsigned long long* list = p.lists + place * p.K;
+        rank_keys(keys, have, p.K, list);
+        for (int i = have + lane; i < p.K; i += 32) list[i] = 0ull;
+        const float mw = from_ordered(__reduce_max_sync(0xFFFFFFFFu, ordered(m)));
+        l *= exp2_approx(m - (mw == -INFINITY ? 0.f : mw));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (lane == 0) p.stats[place] = make_float2(mw, l);
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) so_far[i] = -INFINITY;
+    }
+    cp_async_wait<0>();
+    if constexpr (CLUSTER) {
+        if (p.ctas > 1) cluster_sync();
+        else __syncthreads();
+        if (cta == 0) best_of_prompt(p, rows, *reinterpret_cast<Best*>(smem), prompt);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) beam_best_kernel(const BeamParams p) {
+    __shared__ Rows rows;
+    __shared__ Best best;
+    if (threadIdx.x < 32) {
+        find_rows(p, rows, (long long)blockIdx.x * p.W);
+        if (threadIdx.x == 0) {
+            rows.parts = p.parts;
+            rows.place0 = (long long)blockIdx.x * p.W * p.parts;
+        }
+        // every row has places, in use or not
+        __syncwarp();
+        for (int w = threadIdx.x; w < p.W; w += 32)
+            if (rows.place[w] >= 0) rows.place[w] = w;
+    }
+    __syncthreads();
+    pdl_wait();
+    best_of_prompt(p, rows, best, blockIdx.x);
+}
+
+// How a call is cut: CTAs of a prompt's cluster (0: no clusters), steps of a part of a row, its
+// parts (of clusters: told on the device, where the rows in use are known).  Each warp that runs at
+// once has one part, if it is a step at least.
+struct Cut {
+    int ctas, steps, parts;
+    long long places;
+};
+constexpr int kSms = 152;
+Cut cut_of(int N, int W, int V, int fp32) {
+    const int steps = (V - 1) / (kPieces * (fp32 ? 4 : 8)) + 1;
+    Cut c{};
+    if (N <= kMostClusters) {
+        for (c.ctas = 1; c.ctas < kMostCtas && c.ctas * kWarps < (long long)W * steps;) c.ctas *= 2;
+        c.places = (long long)N * kClusterPlaces;
+    } else {
+        const long long rows = (long long)N * W, warps = 2 * kSms * kWarps;
+        c.parts = warps / rows < 1 ? 1 : warps / rows < steps ? (int)(warps / rows) : steps;
+        c.steps = (steps - 1) / c.parts + 1;
+        c.parts = (steps - 1) / c.steps + 1;
+        c.places = rows * c.parts;
+    }
+    return c;
 }
 
 template <bool F32>
-cudaError_t launch_rows(const BeamParams& p, int vectors, cudaStream_t s) {
-    const unsigned grid = (unsigned)((long long)p.N * p.W * p.chunks);
-    switch (vectors) {
-        case 8: beam_rows_kernel<F32, 8><<<grid, kThreads, 0, s>>>(p); break;
-        case 4: beam_rows_kernel<F32, 4><<<grid, kThreads, 0, s>>>(p); break;
-        case 2: beam_rows_kernel<F32, 2><<<grid, kThreads, 0, s>>>(p); break;
-        default: beam_rows_kernel<F32, 1><<<grid, kThreads, 0, s>>>(p);
+cudaError_t launch_of(const BeamParams& p, cudaStream_t s) {
+    static std::atomic<uint64_t> asked[2] = {};  // devices on which the kernels may take their memory
+    cudaError_t err = p.ctas ? allow_shared(beam_kernel<F32, true>, kSmem, asked[1])
+                             : allow_shared(beam_kernel<F32, false>, kSmem, asked[0]);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (p.ctas) {
+        cfg.gridDim = dim3((unsigned)(p.N * p.ctas));
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)p.ctas;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        return cudaLaunchKernelEx(&cfg, beam_kernel<F32, true>, p);
     }
-    return cudaGetLastError();
+    const long long ctas = ((long long)p.N * p.W * p.parts - 1) / kWarps + 1;
+    beam_kernel<F32, false><<<(unsigned)(ctas < 2 * kSms ? ctas : 2 * kSms), kThreads, kSmem, s>>>(p);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    // the second kernel's blocks are placed while the first one finishes
+    cfg.gridDim = dim3((unsigned)p.N);
+    cfg.dynamicSmemBytes = 0;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, beam_best_kernel, p);
 }
 
-size_t stat_bytes(long long rows, int chunks) { return ((size_t)rows * chunks * sizeof(float2) + 255) / 256 * 256; }
+size_t stat_bytes(const Cut& c) { return ((size_t)c.places * sizeof(float2) + 255) / 256 * 256; }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -468,9 +823,8 @@ extern "C" {
 
 size_t mxq_beam_select_workspace_bytes(int N, int W, int V, int K, int fp32) {
     if (!mxq::shape_ok(N, W, V, K)) return 0;
-    const long long rows = (long long)N * W;
-    const mxq::Cut c = mxq::cut_of(rows, V, fp32);
-    return mxq::stat_bytes(rows, c.chunks) + (size_t)rows * c.chunks * K * sizeof(unsigned long long);
+    const mxq::Cut c = mxq::cut_of(N, W, V, fp32);
+    return mxq::stat_bytes(c) + (size_t)c.places * K * sizeof(unsigned long long);
 }
 
 mxq_status mxq_beam_select(const void* logits, long long row_stride, int fp32, const float* scores,
@@ -483,19 +837,17 @@ mxq_status mxq_beam_select(const void* logits, long long row_stride, int fp32, c
     if (!mxq::aligned(logits, fp32 ? 4 : 2) || !mxq::aligned(scores, 4) || !mxq::aligned(out_scores, 4) ||
         !mxq::aligned(parents, 4) || !mxq::aligned(tokens, 4) || !mxq::aligned(workspace, 256))
         return MXQ_ERR_MISALIGNED;
-    const long long rows = (long long)N * W;
-    const mxq::Cut c = mxq::cut_of(rows, V, fp32);
-    // tokens are counted in 32 bits, over a prompt's beams too; CTAs as well
-    if ((long long)W * V > 0x7FFFFFFF - 65536 || rows * c.chunks > 0x7FFFFFFF ||
-        (long long)W * c.chunks * K > 0x7FFFFFFF)
-        return MXQ_ERR_UNSUPPORTED;
+    const mxq::Cut c = mxq::cut_of(N, W, V, fp32);
+    // tokens are counted in 32 bits, over a prompt's beams too, and CTAs
+    if ((long long)W * V > 0x7FFFFFFF - 65536 || N > 0x7FFFFFFF / 8 ||
+        (long long)W * (c.parts + 1) * (K + 1) > 0x7FFFFFFF) return MXQ_ERR_UNSUPPORTED;
     if (N > 0 && (!workspace || workspace_bytes < mxq_beam_select_workspace_bytes(N, W, V, K, fp32)))
         return MXQ_ERR_WORKSPACE;
     const mxq_status st = mxq::check_current_device(nullptr);
     if (st != MXQ_OK) return st;
     if (N == 0) return MXQ_OK;
     mxq::BeamParams p;
-    p.logits = logits;
+    p.logits = static_cast<const uint8_t*>(logits);
     p.row_stride = row_stride * (fp32 ? 4 : 2);
     p.scores = scores;
     p.done = done;
@@ -507,25 +859,15 @@ mxq_status mxq_beam_select(const void* logits, long long row_stride, int fp32, c
     p.W = W;
     p.V = V;
     p.K = K;
-    p.chunks = c.chunks;
+    p.ctas = c.ctas;
+    p.steps = c.steps;
+    p.parts = c.parts;
     p.end = end_token;
     p.stats = static_cast<float2*>(workspace);
     p.lists = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) +
-                                                    mxq::stat_bytes(rows, c.chunks));
+                                                    mxq::stat_bytes(c));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t err = fp32 ? mxq::launch_rows<true>(p, c.vectors, s) : mxq::launch_rows<false>(p, c.vectors, s);
-    if (err != cudaSuccess) return MXQ_ERR_CUDA;
-    // the second kernel's blocks are placed while the first one finishes
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)N);
-    cfg.blockDim = dim3(mxq::kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, mxq::beam_best_kernel, p);
+    const cudaError_t err = fp32 ? mxq::launch_of<true>(p, s) : mxq::launch_of<false>(p, s);
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 

@@ -473,7 +473,7 @@ size_t mxq_kv_attention_shared_workspace_bytes(int T, int S, int N, int Hq, int 
  * others), count as -inf, which is a score like another: where there are fewer than K
  * above it the lowest w V + v of those follow.  -inf logits are tokens that are not
  * allowed.
- * Candidates are compared in 64 bits; sums over a row are fp32 in chunks, which are
+ * Candidates are compared in 48 bits; sums over a row are fp32 in parts, which are
  * added in 64 bits (scores are within 2^-18 and their rounding).  The result is
  * deterministic, and equal rows with equal scores have equal candidates.
  * Requirements: 1 <= W <= 64, 1 <= K <= 64, K <= W V; V > 0, W V < 2^31 - 65536;

@@ -55,7 +55,7 @@ def select(L, x=FAKE, scores=FAKE, done=None, so=FAKE, po=FAKE, to=FAKE, do=None
     (dict(W=2, V=3, K=7, stride=3), 1), (dict(stride=-1), 1), (dict(done=FAKE, end=-1), 1), (dict(done=FAKE, end=1000), 1),
     (dict(do=FAKE, end=1000), 1), (dict(x=None), 1), (dict(scores=None), 1), (dict(so=None), 1), (dict(po=None), 1), (dict(to=None), 1),
     (dict(x=ODD1), 2), (dict(x=ODD2, fp32=1), 2), (dict(scores=ODD2), 2), (dict(so=ODD2), 2), (dict(po=ODD2), 2), (dict(to=ODD2), 2),
-    (dict(ws=ODD), 2), (dict(W=64, V=1 << 25), 3), (dict(N=1 << 26, V=1 << 20, wsb=1 << 62), 3), (dict(ws=None), 6), (dict(wsb=64), 6)])
+    (dict(ws=ODD), 2), (dict(W=64, V=1 << 25), 3), (dict(ws=None), 6), (dict(wsb=64), 6)])
 def test_select_argument_checks(L, kw, code):
     assert select(L, **kw) == code
 
