@@ -95,24 +95,24 @@ bool countable(const AttnPlan& a, int S, int Hkv, long long tokens) {
     return a.max_entries * units <= kMost / many_vheads * a.many_ctas;
 }
 
-// How one part of a call over shared prefixes is cut (KvSharedParams): row tiles, CTAs, and its
-// share of the workspace.
+// How one part of a call over shared prefixes is cut (KvSharedParams): row tiles, runners (warps, or
+// CTAs on the tensor cores), and its share of the workspace.
 struct SharedPart {
-    int head_parts, part_heads, tile_rows, tile_toks, half_toks, ctas;
+    int head_parts, part_heads, tile_rows, tensor_cores;
+    long long runners;
     long long planes, most_planes;  // row tiles of one head: with rows that do not overlap, at all
     size_t before_bytes, bytes;
 };
 
-SharedPart shared_part(long long items, long long rows, long long T, int rep, int Hkv, int D, int sms) {
+SharedPart shared_part(long long items, long long rows, int rep, int sms) {
     SharedPart a;
     a.head_parts = (rep + 15) / 16;
     a.part_heads = (rep + a.head_parts - 1) / a.head_parts;
     const long long all = rows * a.part_heads;
     a.tile_rows = all <= 4 ? 4 : all <= 8 ? 8 : 16;
-    a.tile_toks = a.tile_rows / a.part_heads;
-    a.half_toks = 0;
-    a.ctas = sms * mxq::kv_attn_ctas_per_sm();
-    a.most_planes = items * ((rows + a.tile_toks - 1) / a.tile_toks);
+    a.tensor_cores = 0;
+    a.runners = 12LL * sms;  // warps
+    a.most_planes = items * ((all + a.tile_rows - 1) / a.tile_rows);
     a.planes = a.most_planes;
     return a;
 }
@@ -122,33 +122,34 @@ struct SharedPlan {
     size_t bytes;
 };
 
-// The groups' rows are taken by the kernel for few rows up to kFewPrefixRows, above by the
-// tensor cores'.
+// The groups' rows are taken by warps on their own up to kFewPrefixRows, above by the tensor cores.
 constexpr int kFewPrefixRows = 32;
 
 SharedPlan plan_shared(int T, int S, int N, int Hq, int Hkv, int D, int max_q, int max_group, int sms) {
     SharedPlan a;
     const int rep = Hq / Hkv;
-    a.own = shared_part(S, max_q, T, rep, Hkv, D, sms);
+    a.own = shared_part(S, max_q, rep, sms);
     const long long all = (long long)max_group * max_q, rows = all < T ? all : T;
     SharedPart& p = a.prefix;
-    p = shared_part(N, rows, T, rep, Hkv, D, sms);
+    p = shared_part(N, rows, rep, sms);
     if (rows * p.part_heads > kFewPrefixRows) {
+        p.tensor_cores = 1;
         p.head_parts = (rep + 127) / 128;
         p.part_heads = (rep + p.head_parts - 1) / p.head_parts;
         p.tile_rows = mxq::kv_prefill_rows(D);
-        p.half_toks = 128 / p.part_heads;
-        p.tile_toks = p.half_toks * (p.tile_rows / 128);
-        p.ctas = sms;
-        p.most_planes = N * ((rows + p.tile_toks - 1) / p.tile_toks);
+        p.runners = sms;
+        p.most_planes = N * ((rows * p.part_heads + p.tile_rows - 1) / p.tile_rows);
+    } else if (p.tile_rows != a.own.tile_rows) {
+        p.tile_rows = 16;  // (there is no kernel of 8 rows beside 4)
+        p.most_planes = N * ((rows * p.part_heads + 15) / 16);
     }
     // the groups have all rows between them
-    p.planes = T / p.tile_toks + (long long)N;
+    p.planes = (long long)T * p.part_heads / p.tile_rows + N;
     if (p.planes > p.most_planes) p.planes = p.most_planes;
     a.bytes = 0;
     for (SharedPart* x : {&a.prefix, &a.own}) {
-        x->before_bytes = align_up((size_t)(x == &a.own ? S : N) * sizeof(int2), 256) + 256;
-        const size_t places = (size_t)x->planes * Hkv * x->head_parts + x->ctas;
+        x->before_bytes = align_up((size_t)(x == &a.own ? S : N) * mxq::kv_shared_before_bytes(), 256) + 256;
+        const size_t places = (size_t)x->planes * Hkv * x->head_parts + x->runners;
         x->bytes = x->before_bytes + align_up(places * x->tile_rows * (D + 2) * sizeof(float), 256);
         a.bytes += x->bytes;
     }
@@ -158,9 +159,8 @@ SharedPlan plan_shared(int T, int S, int N, int Hq, int Hkv, int D, int max_q, i
 // As for AttnPlan: units of one head and of a run, and places, fit 32 bits.
 bool countable(const SharedPart& a, int Hkv, long long tokens) {
     constexpr long long kMost = (1LL << 30) - 64;
-    const long long units = tokens / (a.tile_rows > 16 ? 128 : 32) + 32, vheads = (long long)Hkv * a.head_parts;
-    if (a.most_planes > kMost / units || a.most_planes > kMost / vheads - a.ctas) return false;
-    return a.most_planes * units <= kMost / vheads * a.ctas;
+    const long long units = tokens / (a.tensor_cores ? 128 : 16) + 32, vheads = (long long)Hkv * a.head_parts;
+    return a.most_planes <= kMost / units && a.most_planes <= kMost / vheads - a.runners;
 }
 
 }  // namespace
@@ -491,9 +491,6 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
         x.wait_budget = mxq::wait_budget_cycles();
         x.head_parts = part.head_parts;
         x.part_heads = part.part_heads;
-        x.tile_toks = part.tile_toks;
-        x.half_toks = part.half_toks;
-        x.ctas = part.ctas;
         x.prefix = !i;
         x.groups_n = N;
         x.max_group = max_group;
@@ -501,13 +498,18 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
         x.prefix_lens = prefix_lens;
         x.max_planes = (int)part.planes;
         x.tile_rows = part.tile_rows;
+        x.on_tensor_cores = part.tensor_cores;
+        x.sms = sms < kMaxSms ? sms : kMaxSms;
+        mxq::kv_shared_shape(x, D);
         x.totals = reinterpret_cast<long long*>(ws);
-        x.before = reinterpret_cast<int2*>(ws + 256);
+        x.before = reinterpret_cast<mxq::Before*>(ws + 256);
         x.partial = reinterpret_cast<float*>(ws + part.before_bytes);
         ws += part.bytes;
-        if (mxq::launch_kv_shared_part(x, D, group_size, i == 1, s) != cudaSuccess) return MXQ_ERR_CUDA;
     }
-    const cudaError_t err = mxq::launch_kv_shared_join(p[0], p[1], D, s);
+    cudaError_t err = cudaSuccess;
+    if (p[0].on_tensor_cores) err = mxq::launch_kv_shared_many(p[0], p[1], D, group_size, s);
+    if (err == cudaSuccess) err = mxq::launch_kv_shared_lone(p[0], p[1], D, group_size, s);
+    if (err == cudaSuccess) err = mxq::launch_kv_shared_join(p[0], p[1], D, s);
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 

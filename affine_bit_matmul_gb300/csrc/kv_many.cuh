@@ -1,7 +1,7 @@
 // Attention of many query rows (prompts, chunks of them) over a paged 4-bit
 // key/value cache, on the 5th-generation tensor cores.
 //
-// The formulas are kv_few.cuh's; here keys and values become f16 numbers,
+// The formulas are kv_attention.cu's; here keys and values become f16 numbers,
 // s q + b rounded once (11 bits), scaled by a power of two for each 32 tokens that
 // keeps them within the type's range, and so do the queries (a
 // power of two for each row, exact) and the weights P (11 bits).  Products are
@@ -71,7 +71,9 @@ struct Shape {
 
 struct Piece {
     int row0, toks, p0, head0, heads, s, h, head_tiles, tail, k0, count, flags;
-    int p1, slot;  // shared prefixes: position of the last row, place of the result
+    // Shared prefixes: position of the last row, place of the result, and the first of its (token,
+    // query head) rows, of which `toks` is the number.
+    int p1, slot, flat0;
 };
 template <class P>
 __device__ __forceinline__ int last_position(const Piece& q) {
@@ -92,6 +94,13 @@ struct Meta {
 
 __device__ __forceinline__ int unit_token(const Piece& q, int k) {
     return (k < q.head_tiles ? k : q.tail + k - q.head_tiles) * kTile;
+}
+
+// Whether a row tile of a shared prefix has rows for one half only: both halves then take all of them,
+// for alternate units, and leave a result each.
+template <int D, int G, class P>
+__device__ __forceinline__ bool is_narrow(const Piece& q) {
+    return P::kShared && Shape<D, G>::MT == 2 && q.toks <= 128;
 }
 
 // Waits for this thread's tensor-memory loads; the registers named are not used
@@ -303,113 +312,29 @@ __device__ bool list_pieces(const KvAttnParams& p, Shared<D, G>& sh) {
     }
 }
 
-// The same for the groups of a call over shared prefixes, without a plan; the whole warp.
+// The same for the groups of a call over shared prefixes, by one lane.
 template <int D, int G>
-__device__ bool list_pieces(const KvSharedParams& p, Shared<D, G>& sh, int lane) {
-    const int per = (p.groups_n + 31) / 32, vheads = p.Hkv * p.head_parts, cta = blockIdx.x;
-    auto tiles_of = [](const Item& it) { return (it.len + kTile - 1) / kTile; };
-    long long mine = 0;
-    int mine_t = 0;
-    for (int i = lane * per; i < min(lane * per + per, p.groups_n); ++i) {
-        const Item it = item_of(p, i);
-        mine += it.planes * (tiles_of(it) + kEndUnits);
-        mine_t += it.planes;
-        if (it.bad && cta == 0) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
-    }
-    long long incl = mine;
-    int incl_t = mine_t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        const int y = __shfl_up_sync(0xFFFFFFFFu, incl_t, o);
-        if (lane >= o) {
-            incl += x;
-            incl_t += y;
-        }
-    }
-    const long long all = __shfl_sync(0xFFFFFFFFu, incl, 31) * vheads;
-    const bool fits = __shfl_sync(0xFFFFFFFFu, incl_t, 31) <= p.max_planes;
-    const long long each = fits ? run_length(all, p.ctas) : 0;
-    if (cta == 0) {
-        // for the joining kernel: what comes before each group
-        if (lane == 0) {
-            p.totals[0] = each;
-            if (!fits) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
-        }
-        long long u = incl - mine;
-        int t = incl_t - mine_t;
-        for (int i = lane * per; i < min(lane * per + per, p.groups_n); ++i) {
-            const Item it = item_of(p, i);
-            p.before[i] = make_int2((int)u, t);
-            u += it.planes * (tiles_of(it) + kEndUnits);
-            t += it.planes;
-        }
-    }
-    const long long u0 = cta * each;
-    long long left = each == 0 || u0 >= all ? 0 : (all - u0 < each ? all - u0 : each);
-    const uint32_t here =
-        __ballot_sync(0xFFFFFFFFu, u0 >= (incl - mine) * vheads && u0 < incl * vheads);
-    const int owner = here ? __ffs(here) - 1 : 0;
-    long long at = u0 - __shfl_sync(0xFFFFFFFFu, incl - mine, owner) * vheads;
-    int tile = __shfl_sync(0xFFFFFFFFu, incl_t - mine_t, owner) * vheads;
-    if (lane != 0) return true;
-    int i = owner * per, k = 0, vh = 0, plane = 0, tiles = 0;
-    Item it{};
-    if (left > 0) {
-        it = item_of(p, i);
-        tiles = tiles_of(it);
-        while (at >= (long long)it.planes * (tiles + kEndUnits) * vheads) {
-            at -= (long long)it.planes * (tiles + kEndUnits) * vheads;
-            tile += it.planes * vheads;
-            it = item_of(p, ++i);
-            tiles = tiles_of(it);
-        }
-        const int n = (int)(at / (tiles + kEndUnits));
-        k = (int)(at % (tiles + kEndUnits));
-        vh = n / it.planes;
-        plane = n % it.planes;
-        tile += n;
-    }
+__device__ bool list_pieces(const KvSharedParams& p, Shared<D, G>& sh, SharedWalk& walk) {
     const int rep = p.Hq / p.Hkv;
     for (int n = 0;; ++n) {
         const int slot = n % kPieceRing;
         if (!mbar_wait_sleep(&sh.piece_empty[slot], ((uint32_t)(n / kPieceRing) & 1u) ^ 1u, p.wait_budget))
             return false;
         Piece q{};
-        while (left > 0 && q.count == 0) {
-            while (it.planes == 0) {
-                it = item_of(p, ++i);
-                tiles = tiles_of(it);
-            }
-            const int units = tiles + kEndUnits, n_units = (int)(left < units - k ? left : units - k);
-            const int count = min(k + n_units, tiles) - k;  // the others are the row tile's end
-            if (count > 0) {
-                const int h = vh / p.head_parts, part = vh % p.head_parts;
-                q.row0 = it.row0 + plane * p.tile_toks;
-                q.toks = min(p.tile_toks, it.rows - plane * p.tile_toks);
-                q.p0 = q.p1 = it.len - 1;
-                q.head0 = h * rep + part * p.part_heads;
-                q.heads = min(p.part_heads, rep - part * p.part_heads);
-                q.s = i;
-                q.h = h;
-                q.k0 = k;
-                q.count = count;
-                q.slot = tile + cta;
-            }
-            left -= n_units;
-            k += n_units;
-            if (k == units && left > 0) {
-                k = 0;
-                ++tile;
-                if (++plane == it.planes) {
-                    plane = 0;
-                    if (++vh == vheads) {
-                        vh = 0;
-                        it = item_of(p, ++i);
-                        tiles = tiles_of(it);
-                    }
-                }
-            }
+        SharedPiece s;
+        if (walk.next(p, &s)) {
+            const int h = s.vh / p.head_parts, part = s.vh - h * p.head_parts;
+            q.heads = min(p.part_heads, rep - part * p.part_heads);
+            q.head0 = h * rep + part * p.part_heads;
+            q.flat0 = s.plane * p.tile_rows;
+            q.toks = min(p.tile_rows, s.it.rows * q.heads - q.flat0);
+            q.row0 = s.it.row0;
+            q.p0 = q.p1 = s.it.len - 1;
+            q.s = s.item;
+            q.h = h;
+            q.k0 = s.k0;
+            q.count = s.count;
+            q.slot = s.tile + blockIdx.x;
         }
         sh.pieces[slot] = q;
         mbar_arrive(&sh.piece_full[slot]);
@@ -630,16 +555,24 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
         if (!q) return false;
         const int count = q->count;
         if (count == 0) return true;
-        if (q->toks <= m * p.half_toks) {
-            // no rows in this half: only let the buffers go
-            for (int k = 0; k < count; ++k, ++jt) {
-                const int buf = jt % KB;
-                const uint32_t par = (uint32_t)(jt / KB) & 1u;
-                if (!warp_wait_sleep(&sh.k_full[buf], par, p.wait_budget)) return false;
-                if (lane == 0) mbar_arrive(&sh.k_empty[buf]);
-                if (!warp_wait_sleep(&sh.v_full[buf], par, p.wait_budget)) return false;
-                if (lane == 0) mbar_arrive(&sh.v_empty[buf]);
-            }
+        // the units of this half: all of them, or every other one
+        const bool narrow = is_narrow<D, G, P>(*q);
+        const int k_first = narrow ? m : 0, k_step = narrow ? 2 : 1;
+        // lets unit k's buffers go without using them
+        auto leave = [&](int k) {
+            const int j = jt + k, buf = j % KB;
+            const uint32_t par = (uint32_t)(j / KB) & 1u;
+            if (!warp_wait_sleep(&sh.k_full[buf], par, p.wait_budget)) return false;
+            if (lane == 0) mbar_arrive(&sh.k_empty[buf]);
+            if (!warp_wait_sleep(&sh.v_full[buf], par, p.wait_budget)) return false;
+            if (lane == 0) mbar_arrive(&sh.v_empty[buf]);
+            return true;
+        };
+        if (narrow ? k_first >= count : q->toks <= m * (P::kShared ? 128 : p.half_toks)) {
+            // no rows in this half
+            for (int k = 0; k < count; ++k)
+                if (!leave(k)) return false;
+            jt += count;
             list.done();
             continue;
         }
@@ -647,7 +580,8 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
         ++nq;
         // scores of tile i of the piece
         auto scores = [&](int i) {
-            const int j = jt + i / kSubs, sub = i % kSubs, buf = j % KB, a = at + i;
+            const int k = k_first + i / kSubs * k_step, j = jt + k, sub = i % kSubs, buf = j % KB, a = at + i;
+            if (narrow && sub == 0 && k > 0 && !leave(k - 1)) return false;
             if (!warp_wait_sleep(&sh.k_full[buf], (uint32_t)(j / KB) & 1u, p.wait_budget)) return false;
             // the buffer's earlier weights have been used
             if (i >= 2 && !warp_wait_sleep(&sh.pv_done[2 * m + (a & 1)], (uint32_t)((a >> 1) - 1) & 1u, p.wait_budget))
@@ -670,11 +604,11 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
             __syncwarp();
             return true;
         };
-        const int n_tiles = count * kSubs;
+        const int n_units = (count - k_first + k_step - 1) / k_step, n_tiles = n_units * kSubs;
         if (!scores(0)) return false;
         for (int i = 0; i < n_tiles; ++i) {
             if (i + 1 < n_tiles && !scores(i + 1)) return false;
-            const int j = jt + i / kSubs, sub = i % kSubs, buf = j % KB, a = at + i;
+            const int j = jt + k_first + i / kSubs * k_step, sub = i % kSubs, buf = j % KB, a = at + i;
             if (!warp_wait_sleep(&sh.v_full[buf], (uint32_t)(j / KB) & 1u, p.wait_budget) ||
                 !warp_wait_sleep(&sh.p_full[2 * m + (a & 1)], (uint32_t)(a >> 1) & 1u, p.wait_budget))
                 return false;
@@ -695,6 +629,7 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
             }
             __syncwarp();
         }
+        if (k_first + (n_units - 1) * k_step < count - 1 && !leave(count - 1)) return false;
         jt += count;
         at += n_tiles;
         list.done();
@@ -718,16 +653,31 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
         if (!q) return false;
         const int count = q->count;
         if (count == 0) return true;
-        const int heads = q->heads, tok0 = m * p.half_toks;
-        const int toks = min(p.half_toks, q->toks - tok0);
+        const int heads = q->heads, tok0 = P::kShared ? 0 : m * p.half_toks;
+        const bool narrow = is_narrow<D, G, P>(*q);
+        const int half0 = P::kShared && !narrow ? m * 128 : 0;  // first row of a shared prefix's half
+        const int k_first = narrow ? m : 0, k_step = narrow ? 2 : 1;
+        const int toks = P::kShared ? q->toks - half0 : min(p.half_toks, q->toks - tok0);
         if (toks <= 0) {
             jt += count;
             list.done();
             continue;
         }
-        const bool in = lr < toks * heads;
-        const int tok = in ? lr / heads : 0, hh = in ? lr % heads : 0;
+        // the half's rows, and where they begin among the sequence's or group's
+        const int rows = P::kShared ? min(128, toks) : toks * heads;
+        const int flat0 = P::kShared ? q->flat0 + half0 : 0;
+        const bool in = lr < rows;
+        const int tok = in ? (flat0 + lr) / heads : 0, hh = in ? (flat0 + lr) % heads : 0;
         const int row = q->row0 + tok0 + tok;
+        if (narrow && k_first >= count) {
+            // this half has no unit
+            if (in)
+                *reinterpret_cast<float2*>(p.partial + (long long)q->slot * SH::kPartialFloats + 2 * (m * 128 + lr)) =
+                    make_float2(-INFINITY, 0.f);
+            jt += count;
+            list.done();
+            continue;
+        }
         // positions of the half (all of a shared prefix's rows see all of it)
         const int first = P::kShared ? q->p0 : q->p0 + tok0, last = P::kShared ? first : first + toks - 1;
         const int pos = in ? (P::kShared ? first : first + tok) : -1;
@@ -740,7 +690,6 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
             const uint32_t base = qbuf + m * (D / 64) * (128 * 128) + (c / 8) * (128 * 128);
             int my_ex = 16;
             constexpr int kBatch = 8;
-            const int rows = toks * heads;
 #pragma unroll 1
             for (int i0 = 0; i0 < kLanes; i0 += kBatch) {
                 uint4 v[kBatch];
@@ -749,8 +698,8 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
                     // (rows past the last repeat it; their scores are not used)
                     const int at_row = min(quarter * 32 + (i0 + i) * kAtOnce + lane / kLanes, rows - 1);
                     v[i] = __ldg(reinterpret_cast<const uint4*>(
-                                     p.q + (long long)(q->row0 + tok0 + at_row / heads) * p.q_row_stride +
-                                     (long long)(q->head0 + at_row % heads) * p.q_head_stride) +
+                                     p.q + (long long)(q->row0 + tok0 + (flat0 + at_row) / heads) * p.q_row_stride +
+                                     (long long)(q->head0 + (flat0 + at_row) % heads) * p.q_head_stride) +
                                  c);
                 }
 #pragma unroll
@@ -793,7 +742,9 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
         // the next but one.
         if (!warp_wait_sleep(&sh.s_full[2 * m + (at & 1)], (uint32_t)(at >> 1) & 1u, p.wait_budget))
             return false;
-        for (int k = 0; k < count; ++k, ++jt) {
+        const int jt0 = jt, at0 = at;
+        for (int k = k_first; k < count; k += k_step) {
+            jt = jt0 + k;
             const volatile uint32_t* meta =
                 reinterpret_cast<const volatile uint32_t*>(&sh.meta[jt % kMetaRing]);
             // the values of this unit have been converted: their powers of two
@@ -853,7 +804,7 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
                         tmem_st8(s_at + i, y);
                     }
                     bool ok = true;
-                    if (k + sub > 0) {
+                    if (at != at0) {
                         // the sums so far, once the last tile's products are in
                         ok = warp_wait_sleep(&sh.pv_done[2 * m + ((at - 1) & 1)], (uint32_t)((at - 1) >> 1) & 1u, p.wait_budget);
                         tc_fence_after();
@@ -941,6 +892,7 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
                 mbar_arrive(&sh.p_full[2 * m + (at & 1)]);
             }
         }
+        jt = jt0 + count;
         // ---- the row's result, once the products of the last tile, and so of all, are in
         if (!warp_wait_sleep(&sh.pv_done[2 * m + ((at - 1) & 1)], (uint32_t)((at - 1) >> 1) & 1u, p.wait_budget))
             return false;
@@ -953,7 +905,7 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
         float* part = p.partial + (P::kShared ? q->slot
                                               : (long long)blockIdx.x * 2 + ((q->flags & kBegins) ? 1 : 0)) *
                                       SH::kPartialFloats;
-        const int dense = tok0 * heads + lr;
+        const int dense = P::kShared ? m * 128 + lr : tok0 * heads + lr;
         // A finished row goes through this half's query buffer, which is not needed any
         // more, so that the warp writes whole rows at a time.
         const uint32_t stage = qbuf + m * (D / 64) * (128 * 128);
@@ -988,7 +940,7 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
                 const int at_row = quarter * 32 + i * kAtOnce + lane / kLanes;
                 const uint4 v = ld_shared_v4(stage + (c / 8) * (128 * 128) + at_row * 128 +
                                              (((c % 8) ^ (at_row % 8)) * 16));
-                if (at_row < toks * heads)
+                if (at_row < rows)
                     *(reinterpret_cast<uint4*>(
                           p.out + ((long long)(q->row0 + tok0 + at_row / heads) * p.Hq + q->head0 +
                                    at_row % heads) * D) + c) = v;
@@ -1007,11 +959,15 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
     }
 }
 
-template <int D, int G, class P>
-__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const P p) {
+// Of a call over shared prefixes `other` is the sequences' own part.
+struct NoPart {};
+template <int D, int G, class P, class Other>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_prefill_kernel(const __grid_constant__ P p, const __grid_constant__ Other other) {
     using SH = Shape<D, G>;
     extern __shared__ uint8_t raw[];
     __shared__ Shared<D, G> sh;
+    __shared__ std::conditional_t<P::kShared, Sums<kThreads>, NoPart> part_sums[2];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t qbuf = base, kbuf = qbuf + SH::kQBytes, vbuf = kbuf + SH::KB * SH::kOpBytes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -1042,10 +998,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const P p) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
+    if constexpr (P::kShared) {
+        sum_items(p, part_sums[0]);
+        sum_items(other, part_sums[1]);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
+    SharedWalk walk;  // the listing warp's
+    if constexpr (P::kShared) {
+        if (warp == 18 || blockIdx.x == 0) {
+            const Scan mine = scan_sums(p, part_sums[0]), theirs = scan_sums(other, part_sums[1]);
+            const long long all = all_units(p, mine);
+            const int sms = share_of(all * p.unit_cost, all_units(other, theirs) * other.unit_cost, p.sms);
+            const long long run = run_length(p, all, sms);
+            if (blockIdx.x == 0) write_before(p, part_sums[0], mine, run);
+            if (warp == 18) walk.start(p, part_sums[0], mine, run, blockIdx.x);
+        }
+    }
 
     bool ok = true;
     if (warp < 4 * SH::MT) {
@@ -1060,8 +1031,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const P p) {
         __syncwarp();
         ok = warp_wait_sleep(&sh.drained[warp - 16], 0, kWaitBudgetCycles) && ok;
     } else if (warp == 18) {
-        if constexpr (P::kShared) ok = list_pieces<D, G>(p, sh, lane);
-        else if (lane == 0) ok = list_pieces<D, G>(p, sh);
+        if constexpr (P::kShared) {
+            if (lane == 0) ok = list_pieces<D, G>(p, sh, walk);
+        } else if (lane == 0) {
+            ok = list_pieces<D, G>(p, sh);
+        }
     }
     if (!ok) flag_status(p.status, MXQ_DEV_TIMEOUT);
     __syncwarp();

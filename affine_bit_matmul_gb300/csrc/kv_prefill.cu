@@ -156,7 +156,7 @@ template <int D, int G>
 cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     using SH = Shape<D, G>;
     static std::atomic<uint64_t> asked{0};  // devices on which the kernel may take its memory
-    cudaError_t err = allow_shared(kv_prefill_kernel<D, G, KvAttnParams>, SH::kSmem, asked);
+    cudaError_t err = allow_shared(kv_prefill_kernel<D, G, KvAttnParams, NoPart>, SH::kSmem, asked);
     if (err != cudaSuccess) return err;
     kv_plan_kernel<<<1, 1024, 0, stream>>>(p);
     err = cudaGetLastError();
@@ -172,7 +172,7 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D, G, KvAttnParams>, p);
+    err = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D, G, KvAttnParams, NoPart>, p, NoPart{});
     if (err != cudaSuccess) return err;
     cfg.gridDim = dim3((unsigned)p.ctas, 16);
     cfg.blockDim = dim3(256);

@@ -1,18 +1,29 @@
 // Attention over shared prefixes: what the two parts of a call, the groups' rows over
-// their prefixes and the sequences' rows over their own tokens, are made of.
+// their prefixes and the sequences' rows over their own tokens, are made of, and how they are cut.
 //
-// A part is a list of items (groups or sequences).  An item's rows are cut into `planes` row
-// tiles for each key/value head, all of which go over all of its tokens; the units of a
-// part (row tile, tile of tokens) are cut into runs of equal length, one for each CTA, as in
-// the calls without a prefix.  Row tiles are numbered in the order of the runs, so a CTA's
-// piece of row tile n has a place of its own at n + CTA: both numbers never decrease along
-// the units, and one of them grows from piece to piece.  The joining kernel finds a row's
-// pieces from the numbers of units and row tiles before its item alone.
+// A part is a list of items (groups or sequences).  For each key/value head an item's (token, query
+// head) rows, in order, are cut into `planes` row tiles of equal size, all of which go over all of its
+// tokens; the units of a part (row tile, tile of tokens) are cut into runs of equal length, one
+// for each runner (a CTA on the tensor cores, else a warp), as in the calls without a prefix.  Row tiles
+// are numbered in the order of the runs, so a runner's piece of row tile n has a place of its own at
+// n + runner: both numbers never decrease along the units, and one of them grows from piece to
+// piece.  The joining kernel finds a row's pieces from what comes before its item alone.
+//   The parts run beside each other, and what each may have of the GPU goes by their costs, from
+// the lengths, which only the device knows: every CTA works it out by itself.
 #pragma once
 
 #include "kv_attn_common.cuh"
 
 namespace mxq {
+
+// What the joining kernel has to know of an item (workspace).
+struct Before {
+    int units, planes;  // of one head, before it
+    int row0, rows, len, item_planes;
+    int group;          // a sequence's; -1: none
+    int pad;
+};
+
 namespace {
 
 struct Item {
@@ -22,14 +33,8 @@ struct Item {
     int bad;         // its arguments are out of range
 };
 
-__device__ __forceinline__ int items_of(const KvAttnParams&) { return 0; }
 __device__ __forceinline__ int items_of(const KvSharedParams& p) {
     return p.prefix ? p.groups_n : p.S;
-}
-
-// Units of a run: equal runs for all CTAs, the last of them shorter.
-__device__ __forceinline__ long long run_length(long long all, int ctas) {
-    return (all + ctas - 1) / ctas;
 }
 
 // Sequences of group g, [*a, *b).
@@ -75,9 +80,216 @@ __device__ __forceinline__ Item item_of(const KvSharedParams& p, int i) {
     r.row0 = a;
     r.rows = b - a;
     r.len = len;
-    r.planes = len > 0 ? (r.rows + p.tile_toks - 1) / p.tile_toks : 0;
+    r.planes = len > 0 ? (r.rows * p.part_heads + p.tile_rows - 1) / p.tile_rows : 0;
     return r;
 }
+
+__device__ __forceinline__ int tiles_of(const KvSharedParams& p, const Item& it) {
+    return (it.len + (1 << p.tile_shift) - 1) >> p.tile_shift;
+}
+// Units of an item's row tiles for one head: their tiles, and what the end of each costs.
+__device__ __forceinline__ int units_of(const KvSharedParams& p, const Item& it) {
+    return it.planes * (tiles_of(p, it) + p.end_units);
+}
+
+// The group that sequence s belongs to, or -1.
+__device__ __forceinline__ int group_with(const KvSharedParams& p, int s) {
+    if (!p.groups) return s / (p.S / p.groups_n);
+    int lo = 0, hi = p.groups_n - 1;  // the last group that starts at or before s
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (__ldg(p.groups + mid) <= s) lo = mid;
+        else hi = mid - 1;
+    }
+    return __ldg(p.groups + lo) <= s && s < __ldg(p.groups + lo + 1) ? lo : -1;
+}
+
+// The units of a part, summed up by a block of T threads: each thread's consecutive items.
+template <int T>
+struct Sums {
+    int units[T], planes[T];
+};
+
+template <int T>
+__device__ __forceinline__ void sum_items(const KvSharedParams& p, Sums<T>& s) {
+    const int n = items_of(p), per = (n + T - 1) / T;
+    int units = 0, planes = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x * per; i < min(((int)threadIdx.x + 1) * per, n); ++i) {
+        const Item it = item_of(p, i);
+        units += units_of(p, it);
+        planes += it.planes;
+        if (it.bad && blockIdx.x == 0) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
+    }
+    s.units[threadIdx.x] = units;
+    s.planes[threadIdx.x] = planes;
+}
+
+// The same for a warp, each lane with T / 32 threads' items: up to and with its own, and all.
+struct Scan {
+    long long units;    // of one head, all
+    int planes;
+    long long to_units; // up to this lane's
+    int to_planes;
+    int my_units, my_planes;
+};
+
+template <int T>
+__device__ __forceinline__ Scan scan_sums(const KvSharedParams& p, const Sums<T>& s) {
+    const int lane = threadIdx.x & 31;
+    Scan r;
+    r.my_units = r.my_planes = 0;
+#pragma unroll 4
+    for (int i = 0; i < T / 32; ++i) {
+        r.my_units += s.units[lane * (T / 32) + i];
+        r.my_planes += s.planes[lane * (T / 32) + i];
+    }
+    r.to_units = r.my_units;
+    r.to_planes = r.my_planes;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xFFFFFFFFu, r.to_units, o);
+        const int y = __shfl_up_sync(0xFFFFFFFFu, r.to_planes, o);
+        if (lane >= o) {
+            r.to_units += x;
+            r.to_planes += y;
+        }
+    }
+    r.units = __shfl_sync(0xFFFFFFFFu, r.to_units, 31);
+    r.planes = __shfl_sync(0xFFFFFFFFu, r.to_planes, 31);
+    // rows of groups that overlap can make more row tiles than there are places for: nothing is done
+    if (r.planes > p.max_planes) r.units = 0;
+    return r;
+}
+
+__device__ __forceinline__ long long all_units(const KvSharedParams& p, const Scan& s) {
+    return s.units * p.Hkv * p.head_parts;
+}
+
+// How many of `all` runners (or SMs) the first of two parts gets, by their costs.
+__device__ __forceinline__ int share_of(long long cost1, long long cost2, int all) {
+    if (cost1 == 0) return 0;
+    if (cost2 == 0) return all;
+    const int n = (int)(((double)cost1 * all) / ((double)cost1 + (double)cost2) + 0.5);
+    return min(max(n, 1), all - 1);
+}
+
+// Units of a run of `runners`, at least the part's least.
+__device__ __forceinline__ long long run_length(const KvSharedParams& p, long long all, int runners) {
+    if (all == 0 || runners <= 0) return 0;
+    const long long n = (all + runners - 1) / runners;
+    return n > p.least_run ? n : p.least_run;
+}
+
+// What the joining kernel needs, by the first block.
+template <int T>
+__device__ void write_before(const KvSharedParams& p, const Sums<T>& s, const Scan& scan, long long run) {
+    const int n = items_of(p), per = (n + T - 1) / T, from = threadIdx.x / (T / 32);
+    if (threadIdx.x == 0) {
+        p.totals[0] = run;
+        if (scan.planes > p.max_planes) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
+    }
+    // (every warp holds the whole scan)
+    int u = (int)(__shfl_sync(0xFFFFFFFFu, scan.to_units - scan.my_units, from));
+    int t = __shfl_sync(0xFFFFFFFFu, scan.to_planes - scan.my_planes, from);
+    for (int i = from * (T / 32); i < (int)threadIdx.x; ++i) {
+        u += s.units[i];
+        t += s.planes[i];
+    }
+    for (int i = threadIdx.x * per; i < min(((int)threadIdx.x + 1) * per, n); ++i) {
+        const Item it = item_of(p, i);
+        Before b;
+        b.units = u;
+        b.planes = t;
+        b.row0 = it.row0;
+        b.rows = it.rows;
+        b.len = it.len;
+        b.item_planes = it.planes;
+        b.group = p.prefix ? i : group_with(p, i);
+        b.pad = 0;
+        p.before[i] = b;
+        u += units_of(p, it);
+        t += it.planes;
+    }
+}
+
+// A run's pieces: units k0 .. k0 + count - 1 of row tile (item, vh, plane), number `tile`.
+struct SharedPiece {
+    int item, vh, plane, k0, count, tile;
+    Item it;
+};
+
+struct SharedWalk {
+    int i, vh, plane, k, tile, tiles;
+    long long left;
+    Item it;
+
+    __device__ void load(const KvSharedParams& p, int item) {
+        i = item;
+        it = item_of(p, i);
+        tiles = tiles_of(p, it);
+    }
+    // Run `runner` of length `run`, by a whole warp.
+    template <int T>
+    __device__ void start(const KvSharedParams& p, const Sums<T>& s, const Scan& scan, long long run, int runner) {
+        const int vheads = p.Hkv * p.head_parts;
+        const long long all = all_units(p, scan), u0 = runner * run;
+        left = run == 0 || u0 >= all ? 0 : (all - u0 < run ? all - u0 : run);
+        if (left == 0) return;
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, u0 >= (scan.to_units - scan.my_units) * vheads &&
+                                                             u0 < scan.to_units * vheads);
+        const int owner = __ffs(here) - 1;
+        long long at = u0 - __shfl_sync(0xFFFFFFFFu, scan.to_units - scan.my_units, owner) * vheads;
+        tile = __shfl_sync(0xFFFFFFFFu, scan.to_planes - scan.my_planes, owner) * vheads;
+        int t = owner * (T / 32);  // the thread whose items the run starts in
+        while (at >= (long long)s.units[t] * vheads) {
+            tile += s.planes[t] * vheads;
+            at -= (long long)s.units[t++] * vheads;
+        }
+        load(p, t * ((items_of(p) + T - 1) / T));
+        while (at >= (long long)units_of(p, it) * vheads) {
+            at -= (long long)units_of(p, it) * vheads;
+            tile += it.planes * vheads;
+            load(p, i + 1);
+        }
+        const int each = tiles + p.end_units, n = (int)(at / each);
+        k = (int)(at - (long long)n * each);
+        vh = n / it.planes;
+        plane = n - vh * it.planes;
+        tile += n;
+    }
+    __device__ bool next(const KvSharedParams& p, SharedPiece* out) {
+        while (left > 0) {
+            while (it.planes == 0) load(p, i + 1);
+            const int all = tiles + p.end_units, n = (int)(left < all - k ? left : all - k);
+            const int here = min(k + n, tiles) - k;  // the others are the row tile's end
+            if (here > 0) {
+                out->item = i;
+                out->vh = vh;
+                out->plane = plane;
+                out->k0 = k;
+                out->count = here;
+                out->tile = tile;
+                out->it = it;
+            }
+            left -= n;
+            k += n;
+            if (k == all && left > 0) {
+                k = 0;
+                ++tile;
+                if (++plane == it.planes) {
+                    plane = 0;
+                    if (++vh == p.Hkv * p.head_parts) {
+                        vh = 0;
+                        load(p, i + 1);
+                    }
+                }
+            }
+            if (here > 0) return true;
+        }
+        return false;
+    }
+};
 
 }  // namespace
 }  // namespace mxq

@@ -10,123 +10,119 @@ namespace mxq {
 namespace {
 
 template <int D, int G>
-cudaError_t launch(KvSharedParams& p, cudaStream_t stream) {
+cudaError_t launch(const KvSharedParams& prefix, const KvSharedParams& own, cudaStream_t stream) {
     using SH = Shape<D, G>;
     static std::atomic<uint64_t> asked{0};  // devices on which the kernel may take its memory
-    cudaError_t err = allow_shared(kv_prefill_kernel<D, G, KvSharedParams>, SH::kSmem, asked);
+    constexpr auto kernel = kv_prefill_kernel<D, G, KvSharedParams, KvSharedParams>;
+    const cudaError_t err = allow_shared(kernel, SH::kSmem, asked);
     if (err != cudaSuccess) return err;
-    p.tile_tokens = kTile;
-    p.end_units = kEndUnits;
-    kv_prefill_kernel<D, G, KvSharedParams><<<(unsigned)p.ctas, kThreads, SH::kSmem, stream>>>(p);
+    kernel<<<(unsigned)prefix.sms, kThreads, SH::kSmem, stream>>>(prefix, own);
     return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- joining
 
 // Pieces of a row of one part.
-struct Pieces1 {
-    long long at;  // floats before the first one's (largest score, sum) of this row
+struct RowPieces {
+    long long at;    // floats before the first one's (largest score, sum) of this row
     long long sums;  // ... and before its weighted sum
     int n;
+    int twice;       // 1: two for each place, the second of them 128 rows later
 };
 
-__device__ __forceinline__ Pieces1 pieces_of(const KvSharedParams& p, const Item& it, int item, int row,
-                                             int head, int D) {
-    Pieces1 r;
-    r.n = 0;
+__device__ __forceinline__ RowPieces pieces_of(const KvSharedParams& p, const Before& b, long long run, int row,
+                                               int head, int D) {
+    RowPieces r;
+    r.n = r.twice = 0;
     r.at = r.sums = 0;
-    const long long each = __ldcg(p.totals);
-    if (it.planes == 0 || each == 0) return r;
+    if (b.item_planes == 0 || run == 0) return r;
     const int rep = p.Hq / p.Hkv, h = head / rep, part = head % rep / p.part_heads;
     const int hh = head % rep % p.part_heads, heads = min(p.part_heads, rep - part * p.part_heads);
     const int vheads = p.Hkv * p.head_parts, vh = h * p.head_parts + part;
-    const int tiles = (it.len + p.tile_tokens - 1) / p.tile_tokens;
-    const int2 before = __ldcg(p.before + item);
-    const int n = vh * it.planes + row / p.tile_toks;
-    const long long u = (long long)before.x * vheads + (long long)n * (tiles + p.end_units);
-    const int c0 = (int)(u / each), c1 = (int)((u + tiles - 1) / each);
+    const int tiles = (b.len + (1 << p.tile_shift) - 1) >> p.tile_shift;
+    const int flat = row * heads + hh, plane = flat / p.tile_rows, in = flat - plane * p.tile_rows;
+    const int n = vh * b.item_planes + plane;
+    const long long u = (long long)b.units * vheads + (long long)n * (tiles + p.end_units);
+    const int c0 = (int)(u / run), c1 = (int)((u + tiles - 1) / run);
     const long long stride = (long long)p.tile_rows * (D + 2);
-    const int in = row % p.tile_toks * heads + hh;
-    r.n = c1 - c0 + 1;
-    r.at = ((long long)before.y * vheads + n + c0) * stride + 2 * in;
+    r.twice = p.on_tensor_cores && p.tile_rows == 256 && b.rows * heads - plane * 256 <= 128;
+    r.n = (c1 - c0 + 1) << r.twice;
+    r.at = ((long long)b.planes * vheads + n + c0) * stride + 2 * in;
     r.sums = r.at - 2 * in + 2 * p.tile_rows + (long long)in * D;
     return r;
 }
 
-// One warp joins a row of one query head, 32 pieces at a time: lane i takes the weight of piece
-// i, then all lanes add the pieces' sums in order.
+__device__ __forceinline__ Before before_of(const KvSharedParams& p, int i) {
+    const int4* at = reinterpret_cast<const int4*>(p.before + i);
+    const int4 x = __ldcg(at), y = __ldcg(at + 1);
+    return Before{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+}
+
+// One warp joins a row of one query head, 32 pieces at a time, those of the prefix before those of
+// the own tokens: lane i takes the weight of piece i, then all lanes add the pieces' sums in order.
 template <int D>
-__global__ void __launch_bounds__(256) kv_shared_join_kernel(const KvSharedParams a, const KvSharedParams b) {
-    pdl_wait();
+__global__ void __launch_bounds__(256) kv_shared_join_kernel(const __grid_constant__ KvSharedParams a,
+                                                             const __grid_constant__ KvSharedParams b) {
     constexpr int V = D / 32;
     const int lane = threadIdx.x & 31, s = blockIdx.x;
     const int head = blockIdx.y * 8 + threadIdx.x / 32;
+    pdl_wait();
     if (head >= b.Hq) return;
-    const Item own = item_of(b, s);
-    if (own.rows == 0) return;
-    // its group
-    int g = -1;
-    if (a.groups) {
-        int lo = 0, hi = a.groups_n - 1;  // the last group that starts at or before s
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (__ldg(a.groups + mid) <= s) lo = mid;
-            else hi = mid - 1;
-        }
-        if (__ldg(a.groups + lo) <= s && s < __ldg(a.groups + lo + 1)) g = lo;
-    } else {
-        g = s / (a.S / a.groups_n);
-    }
-    Item pre{};
+    const Before own = before_of(b, s);
+    if ((int)blockIdx.z >= own.rows) return;
+    const long long prefix_run = __ldcg(a.totals), own_run = __ldcg(b.totals);
+    Before pre{};
+    const int g = a.groups ? own.group : s / (a.S / a.groups_n);
     if (g >= 0) {
-        pre = item_of(a, g);
+        pre = before_of(a, g);
         if (own.row0 < pre.row0 || own.row0 + own.rows > pre.row0 + pre.rows) {
             if (lane == 0) flag_status(a.status, MXQ_DEV_BAD_SEQUENCE);
             return;
         }
     }
-    for (int j = 0; j < own.rows; ++j) {
+    for (int j = blockIdx.z; j < own.rows; j += gridDim.z) {
+        const RowPieces x = pieces_of(a, pre, prefix_run, own.row0 + j - pre.row0, head, D);
+        const RowPieces y = pieces_of(b, own, own_run, j, head, D);
+        const long long x_stride = (long long)a.tile_rows * (D + 2), y_stride = (long long)b.tile_rows * (D + 2);
+        const int n = x.n + y.n;
         float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] = 0.f;
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            const int mine = k0 + lane, many = min(32, n - k0);
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (mine < n)
+                ml = __ldcg(reinterpret_cast<const float2*>(mine < x.n ? a.partial + x.at + (mine >> x.twice) * x_stride + (mine & x.twice) * 256
+                                                                       : b.partial + y.at + (mine - x.n) * y_stride));
+            float top = ml.x;
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            const KvSharedParams& p = part ? b : a;
-            const Pieces1 x = part ? pieces_of(b, own, s, j, head, D)
-                                   : pieces_of(a, pre, g, own.row0 + j - pre.row0, head, D);
-            const long long stride = (long long)p.tile_rows * (D + 2);
-            for (int k0 = 0; k0 < x.n; k0 += 32) {
-                float2 ml = make_float2(-INFINITY, 0.f);
-                if (k0 + lane < x.n)
-                    ml = __ldcg(reinterpret_cast<const float2*>(p.partial + x.at + (k0 + lane) * stride));
-                float top = ml.x;
+            for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+            const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2_approx(m - ref), w = exp2_approx(ml.x - ref);
+            float sum = ml.y * w;
 #pragma unroll
-                for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-                const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-                const float f = exp2_approx(m - ref), w = exp2_approx(ml.x - ref);
-                float sum = ml.y * w;
+            for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
+            m = mn;
+            l = fmaf(l, f, sum);
 #pragma unroll
-                for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
-                m = mn;
-                l = fmaf(l, f, sum);
+            for (int i = 0; i < V; ++i) o[i] *= f;
+#pragma unroll 8
+            for (int k = 0; k < many; ++k) {
+                const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+                if (wk == 0.f) continue;  // (of a half without units there is no sum)
+                const int at = k0 + k;
+                const float* from = (at < x.n ? a.partial + x.sums + (at >> x.twice) * x_stride + (at & x.twice) * (128 * D)
+                                              : b.partial + y.sums + (at - x.n) * y_stride) + lane * V;
+                float v[V];
+                if constexpr (V == 2) {
+                    *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(from));
+                } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) o[i] *= f;
-                const int n = min(32, x.n - k0);
-#pragma unroll 4
-                for (int k = 0; k < n; ++k) {
-                    const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
-                    const float* y = p.partial + x.sums + (k0 + k) * stride + lane * V;
-                    float v[V];
-                    if constexpr (V == 2) {
-                        *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(y));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V; i += 4)
-                            *reinterpret_cast<float4*>(v + i) = __ldcg(reinterpret_cast<const float4*>(y + i));
-                    }
-#pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] = fmaf(v[i], wk, o[i]);
+                    for (int i = 0; i < V; i += 4)
+                        *reinterpret_cast<float4*>(v + i) = __ldcg(reinterpret_cast<const float4*>(from + i));
                 }
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = fmaf(v[i], wk, o[i]);
             }
         }
         const long long to = (long long)(own.row0 + j) * b.Hq + head;
@@ -144,9 +140,12 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(const KvSharedParam
 
 }  // namespace
 
-cudaError_t launch_kv_shared_many(KvSharedParams& p, int D, int G, cudaStream_t stream) {
+size_t kv_shared_before_bytes() { return sizeof(Before); }
+
+cudaError_t launch_kv_shared_many(const KvSharedParams& prefix, const KvSharedParams& own, int D, int G,
+                                  cudaStream_t stream) {
 #define MXQ_KV_SHARED(d, g) \
-    if (D == d && G == g) return launch<d, g>(p, stream);
+    if (D == d && G == g) return launch<d, g>(prefix, own, stream);
     MXQ_KV_SHARED(64, 32)
     MXQ_KV_SHARED(64, 64)
     MXQ_KV_SHARED(128, 32)
@@ -162,7 +161,7 @@ cudaError_t launch_kv_shared_many(KvSharedParams& p, int D, int G, cudaStream_t 
 cudaError_t launch_kv_shared_join(const KvSharedParams& prefix, const KvSharedParams& own, int D,
                                   cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)own.S, (unsigned)(own.Hq + 7) / 8);
+    cfg.gridDim = dim3((unsigned)own.S, (unsigned)(own.Hq + 7) / 8, (unsigned)(own.max_q < 64 ? own.max_q : 64));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};

@@ -229,18 +229,23 @@ struct KvSharedParams : KvAttnParams {
     const int32_t* groups;       // int32 [groups_n + 1], or null: S / groups_n sequences each
     const int32_t* prefix_lens;  // int32 [groups_n]
     int max_planes;              // row tiles of one head for which `partial` has places
-    // For each item (group or sequence): units and row tiles of one head before it; and units
-    // of a run.  Written by the part's kernel for the one that joins.
-    int2* before;
-    long long* totals;
-    int tile_rows, tile_tokens, end_units;  // of the part's kernel
+    struct Before* before;       // workspace: what the joining kernel needs of each item
+    long long* totals;           // workspace: units of a run
+    int tile_rows;               // rows of a row tile
+    int tile_shift, end_units;   // log2 of a tile's tokens; what the end of a row tile costs, in units
+    int unit_cost, least_run;    // of a unit, beside the other part's; units of a run, at least
+    int on_tensor_cores, sms;    // the prefixes' part: by that kernel; SMs of the device
 };
+size_t kv_shared_before_bytes();
 
-// Rows of one part by the kernel for few rows (tile_rows as for launch_kv_attn) or on the tensor
-// cores (tile_rows > 16), without the joining; `dependent`: beside the kernel before it.
-cudaError_t launch_kv_shared_part(KvSharedParams& p, int D, int G, bool dependent,
+// The kernels' choice of tile_shift ... least_run for a part.
+void kv_shared_shape(KvSharedParams& p, int D);
+// The groups' rows on the tensor cores (prefix.on_tensor_cores), beside which the second kernel runs.
+cudaError_t launch_kv_shared_many(const KvSharedParams& prefix, const KvSharedParams& own, int D, int G,
                                   cudaStream_t stream);
-cudaError_t launch_kv_shared_many(KvSharedParams& p, int D, int G, cudaStream_t stream);
+// Both parts, or the sequences' own tokens.
+cudaError_t launch_kv_shared_lone(const KvSharedParams& prefix, const KvSharedParams& own, int D, int G,
+                                  cudaStream_t stream);
 cudaError_t launch_kv_shared_join(const KvSharedParams& prefix, const KvSharedParams& own, int D,
                                   cudaStream_t stream);
 

@@ -226,12 +226,15 @@ def test_bad_entries_are_reported_and_harmless():
     import affine_bit_matmul_gb300 as mxq
 
     c = Case([100, 70], [3, 4], [20] * 7, [1] * 7, 4, 1, 128, 64, 16, seed=16)
-    good, good_lse, _ = c.run(q_starts=None)
+    good, good_lse, tol, _ = c.exact(128 ** -0.5)
+
+    def same(o, left):
+        # (where the tokens are cut, and so how they are added up, goes by all lengths)
+        assert (np.abs(o[left] - good[left]) <= tol[left]).all()
 
     def same_but(changed, **kw):
         o, lse, st = c.run(**{"q_starts": None, **kw})
-        left = [i for i in range(7) if i not in changed]
-        assert np.array_equal(o[left], good[left])
+        same(o, [i for i in range(7) if i not in changed])
         return o, lse, st
 
     # a page outside the cache: its tokens are invisible
@@ -253,8 +256,7 @@ def test_bad_entries_are_reported_and_harmless():
     for groups, lost in (([0, 3, 8], [3, 4, 5, 6]), ([-1, 3, 7], [0, 1, 2]), ([3, 0, 0], list(range(7)))):
         o, _, st = c.run(q_starts=None, group_starts=i32(groups))
         assert st == mxq.DEV_BAD_SEQUENCE
-        left = [i for i in range(7) if i not in lost]
-        assert np.array_equal(o[left], good[left])
+        same(o, [i for i in range(7) if i not in lost])
     o, _, st = same_but([3, 4, 5, 6], max_group=3)
     assert st == mxq.DEV_BAD_SEQUENCE and np.isnan(o[3:]).all()
     # rows out of range or too many: left out
