@@ -111,7 +111,7 @@ SharedPart shared_part(long long items, long long rows, int rep, int sms) {
     const long long all = rows * a.part_heads;
     a.tile_rows = all <= 4 ? 4 : all <= 8 ? 8 : 16;
     a.tensor_cores = 0;
-    a.runners = 12LL * sms;  // warps
+    a.runners = 16LL * sms;  // warps
     a.most_planes = items * ((all + a.tile_rows - 1) / a.tile_rows);
     a.planes = a.most_planes;
     return a;

@@ -1008,12 +1008,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sh.tmem;
     SharedWalk walk;  // the listing warp's
     if constexpr (P::kShared) {
-        if (warp == 18 || blockIdx.x == 0) {
-            const Scan mine = scan_sums(p, part_sums[0]), theirs = scan_sums(other, part_sums[1]);
+        if (warp == 18 || blockIdx.x == gridDim.x - 1) {
+            Scan mine, theirs;
+            scan_sums(part_sums[0], part_sums[1], mine, theirs);
             const long long all = all_units(p, mine);
             const int sms = share_of(all * p.unit_cost, all_units(other, theirs) * other.unit_cost, p.sms);
             const long long run = run_length(p, all, sms);
-            if (blockIdx.x == 0) write_before(p, part_sums[0], mine, run);
+            if (blockIdx.x == gridDim.x - 1) write_before(p, part_sums[0], mine, run);
             if (warp == 18) walk.start(p, part_sums[0], mine, run, blockIdx.x);
         }
     }

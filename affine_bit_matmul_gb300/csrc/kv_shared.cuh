@@ -125,73 +125,75 @@ __device__ __forceinline__ void sum_items(const KvSharedParams& p, Sums<T>& s) {
     s.planes[threadIdx.x] = planes;
 }
 
-// The same for a warp, each lane with T / 32 threads' items: up to and with its own, and all.
+// The same for a warp, each lane with T / 32 threads' items: up to and with its own, and all.  Units in the
+// high word, row tiles in the low one (both fit 31 bits).
 struct Scan {
-    long long units;    // of one head, all
-    int planes;
-    long long to_units; // up to this lane's
-    int to_planes;
-    int my_units, my_planes;
+    long long mine, upto, all;
+    __device__ int units() const { return (int)(all >> 32); }
+    __device__ int planes() const { return (int)all; }
+    __device__ int units_before() const { return (int)((upto - mine) >> 32); }
+    __device__ int units_upto() const { return (int)(upto >> 32); }
+    __device__ int planes_before() const { return (int)(upto - mine); }
 };
 
 template <int T>
-__device__ __forceinline__ Scan scan_sums(const KvSharedParams& p, const Sums<T>& s) {
+__device__ __forceinline__ void scan_sums(const Sums<T>& s, const Sums<T>& t, Scan& x, Scan& y) {
     const int lane = threadIdx.x & 31;
-    Scan r;
-    r.my_units = r.my_planes = 0;
+    x.mine = y.mine = 0;
 #pragma unroll 4
     for (int i = 0; i < T / 32; ++i) {
-        r.my_units += s.units[lane * (T / 32) + i];
-        r.my_planes += s.planes[lane * (T / 32) + i];
+        x.mine += (long long)s.units[lane * (T / 32) + i] << 32 | (unsigned)s.planes[lane * (T / 32) + i];
+        y.mine += (long long)t.units[lane * (T / 32) + i] << 32 | (unsigned)t.planes[lane * (T / 32) + i];
     }
-    r.to_units = r.my_units;
-    r.to_planes = r.my_planes;
+    x.upto = x.mine;
+    y.upto = y.mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xFFFFFFFFu, r.to_units, o);
-        const int y = __shfl_up_sync(0xFFFFFFFFu, r.to_planes, o);
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, x.upto, o), v = __shfl_up_sync(0xFFFFFFFFu, y.upto, o);
         if (lane >= o) {
-            r.to_units += x;
-            r.to_planes += y;
+            x.upto += u;
+            y.upto += v;
         }
     }
-    r.units = __shfl_sync(0xFFFFFFFFu, r.to_units, 31);
-    r.planes = __shfl_sync(0xFFFFFFFFu, r.to_planes, 31);
-    // rows of groups that overlap can make more row tiles than there are places for: nothing is done
-    if (r.planes > p.max_planes) r.units = 0;
-    return r;
+    x.all = __shfl_sync(0xFFFFFFFFu, x.upto, 31);
+    y.all = __shfl_sync(0xFFFFFFFFu, y.upto, 31);
 }
 
+// Rows of groups that overlap can make more row tiles than there are places for: nothing is done.
+__device__ __forceinline__ bool too_many(const KvSharedParams& p, const Scan& s) { return s.planes() > p.max_planes; }
+
 __device__ __forceinline__ long long all_units(const KvSharedParams& p, const Scan& s) {
-    return s.units * p.Hkv * p.head_parts;
+    return too_many(p, s) ? 0 : (long long)s.units() * (p.Hkv * p.head_parts);
 }
 
 // How many of `all` runners (or SMs) the first of two parts gets, by their costs.
 __device__ __forceinline__ int share_of(long long cost1, long long cost2, int all) {
     if (cost1 == 0) return 0;
     if (cost2 == 0) return all;
-    const int n = (int)(((double)cost1 * all) / ((double)cost1 + (double)cost2) + 0.5);
+    const int n = (int)(__fdividef((float)cost1, (float)cost1 + (float)cost2) * all + 0.5f);
     return min(max(n, 1), all - 1);
 }
 
 // Units of a run of `runners`, at least the part's least.
 __device__ __forceinline__ long long run_length(const KvSharedParams& p, long long all, int runners) {
     if (all == 0 || runners <= 0) return 0;
-    const long long n = (all + runners - 1) / runners;
+    // (most often it fits 32 bits, and the division is short)
+    const long long up = all + runners - 1;
+    const long long n = up >> 32 ? up / runners : (long long)((unsigned)up / (unsigned)runners);
     return n > p.least_run ? n : p.least_run;
 }
 
-// What the joining kernel needs, by the first block.
+// What the joining kernel needs, by one block.
 template <int T>
 __device__ void write_before(const KvSharedParams& p, const Sums<T>& s, const Scan& scan, long long run) {
     const int n = items_of(p), per = (n + T - 1) / T, from = threadIdx.x / (T / 32);
     if (threadIdx.x == 0) {
         p.totals[0] = run;
-        if (scan.planes > p.max_planes) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
+        if (too_many(p, scan)) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
     }
     // (every warp holds the whole scan)
-    int u = (int)(__shfl_sync(0xFFFFFFFFu, scan.to_units - scan.my_units, from));
-    int t = __shfl_sync(0xFFFFFFFFu, scan.to_planes - scan.my_planes, from);
+    int u = __shfl_sync(0xFFFFFFFFu, scan.units_before(), from);
+    int t = __shfl_sync(0xFFFFFFFFu, scan.planes_before(), from);
     for (int i = from * (T / 32); i < (int)threadIdx.x; ++i) {
         u += s.units[i];
         t += s.planes[i];
@@ -217,6 +219,9 @@ __device__ void write_before(const KvSharedParams& p, const Sums<T>& s, const Sc
 struct SharedPiece {
     int item, vh, plane, k0, count, tile;
     Item it;
+    // by those who need them: its key/value head, query heads, rows and the first of them in the
+    // item, position of the last row
+    int h, head0, heads, flat0, rows, p1;
 };
 
 struct SharedWalk {
@@ -236,11 +241,11 @@ struct SharedWalk {
         const long long all = all_units(p, scan), u0 = runner * run;
         left = run == 0 || u0 >= all ? 0 : (all - u0 < run ? all - u0 : run);
         if (left == 0) return;
-        const uint32_t here = __ballot_sync(0xFFFFFFFFu, u0 >= (scan.to_units - scan.my_units) * vheads &&
-                                                             u0 < scan.to_units * vheads);
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, u0 >= (long long)scan.units_before() * vheads &&
+                                                             u0 < (long long)scan.units_upto() * vheads);
         const int owner = __ffs(here) - 1;
-        long long at = u0 - __shfl_sync(0xFFFFFFFFu, scan.to_units - scan.my_units, owner) * vheads;
-        tile = __shfl_sync(0xFFFFFFFFu, scan.to_planes - scan.my_planes, owner) * vheads;
+        long long at = u0 - (long long)__shfl_sync(0xFFFFFFFFu, scan.units_before(), owner) * vheads;
+        tile = __shfl_sync(0xFFFFFFFFu, scan.planes_before(), owner) * vheads;
         int t = owner * (T / 32);  // the thread whose items the run starts in
         while (at >= (long long)s.units[t] * vheads) {
             tile += s.planes[t] * vheads;
@@ -252,8 +257,8 @@ struct SharedWalk {
             tile += it.planes * vheads;
             load(p, i + 1);
         }
-        const int each = tiles + p.end_units, n = (int)(at / each);
-        k = (int)(at - (long long)n * each);
+        const int each = tiles + p.end_units, n = (int)at / each;  // (an item's units fit 32 bits)
+        k = (int)at - n * each;
         vh = n / it.planes;
         plane = n - vh * it.planes;
         tile += n;

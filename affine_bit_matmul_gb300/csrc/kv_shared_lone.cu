@@ -16,8 +16,8 @@ cudaError_t launch_kv_shared_lone(const KvSharedParams& prefix, const KvSharedPa
 }
 
 // Costs are ns of one SM: the tensor cores' kernel takes some 3000 for a unit of 256 rows and 128
-// tokens of 128 values, 1700 where 128 rows are shared between its halves; warps on their own are bound by the memory with few rows, 110 for 32 tokens,
-// and by their instructions with 16, 130 for 16 tokens.
+// tokens of 128 values, 1700 where 128 rows are shared between its halves; warps on their own, for
+// 32 tokens, are bound by the memory with few rows, 110, and by their instructions with 16, 260.
 void kv_shared_shape(KvSharedParams& p, int D) {
     if (p.prefix && p.on_tensor_cores) {
         p.tile_shift = 7;
@@ -26,11 +26,11 @@ void kv_shared_shape(KvSharedParams& p, int D) {
         p.least_run = 1;
         return;
     }
-    const bool short_tiles = p.tile_rows == 16 || D == 256;
-    p.tile_shift = short_tiles ? 4 : 5;
-    p.end_units = short_tiles ? 4 : 2;
-    p.unit_cost = p.tile_rows == 16 ? (D == 256 ? 260 : 130) : D == 256 ? 110 : p.tile_rows == 8 ? 130 : 110;
-    p.least_run = short_tiles ? 4 : 2;
+    // (tiles of 16 tokens for heads of 256)
+    p.tile_shift = D == 256 ? 4 : 5;
+    p.end_units = D == 256 ? 4 : p.tile_rows == 16 ? 2 : 3;
+    p.unit_cost = p.tile_rows == 16 ? 260 : p.tile_rows == 8 ? 150 : 130;
+    p.least_run = D == 256 ? 4 : 2;
 }
 
 }  // namespace mxq

@@ -8,9 +8,14 @@ namespace {
 
 template <int D, int G, int KT1, int KT2>
 cudaError_t launch_lone_tiles(const KvSharedParams& prefix, const KvSharedParams& own, cudaStream_t stream) {
-    constexpr int c1 = Lone<D, G, KT1>::kCtas, c2 = Lone<D, G, KT2>::kCtas;
+    using LB = LoneBoth<D, G, KT1, KT2>;
+    static std::atomic<uint64_t> asked{0};  // devices on which the kernel may take its memory
+    constexpr auto kernel = kv_lone_kernel<D, G, KT1, KT2>;
+    const cudaError_t err = allow_shared(kernel, LB::kSmem, asked);
+    if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(own.sms * (c1 < c2 ? c1 : c2)));
+    cfg.gridDim = dim3((unsigned)(own.sms * LB::kCtas));
+    cfg.dynamicSmemBytes = LB::kSmem;
     cfg.blockDim = dim3(kLoneThreads);
     cfg.stream = stream;
     // beside the tensor cores' kernel, if there is one
@@ -19,7 +24,7 @@ cudaError_t launch_lone_tiles(const KvSharedParams& prefix, const KvSharedParams
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = prefix.on_tensor_cores ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kv_lone_kernel<D, G, KT1, KT2>, prefix, own);
+    return cudaLaunchKernelEx(&cfg, kernel, prefix, own);
 }
 
 template <int D, int G>

@@ -43,7 +43,10 @@ __device__ __forceinline__ RowPieces pieces_of(const KvSharedParams& p, const Be
     const int flat = row * heads + hh, plane = flat / p.tile_rows, in = flat - plane * p.tile_rows;
     const int n = vh * b.item_planes + plane;
     const long long u = (long long)b.units * vheads + (long long)n * (tiles + p.end_units);
-    const int c0 = (int)(u / run), c1 = (int)((u + tiles - 1) / run);
+    // (most often they fit 32 bits, and the divisions are short)
+    const bool large = (u + tiles) >> 32 != 0;
+    const int c0 = large ? (int)(u / run) : (int)((unsigned)u / (unsigned)run);
+    const int c1 = large ? (int)((u + tiles - 1) / run) : (int)((unsigned)(u + tiles - 1) / (unsigned)run);
     const long long stride = (long long)p.tile_rows * (D + 2);
     r.twice = p.on_tensor_cores && p.tile_rows == 256 && b.rows * heads - plane * 256 <= 128;
     r.n = (c1 - c0 + 1) << r.twice;
@@ -68,13 +71,14 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(const __grid_consta
     const int head = blockIdx.y * 8 + threadIdx.x / 32;
     pdl_wait();
     if (head >= b.Hq) return;
-    const Before own = before_of(b, s);
-    if ((int)blockIdx.z >= own.rows) return;
     const long long prefix_run = __ldcg(a.totals), own_run = __ldcg(b.totals);
-    Before pre{};
+    const Before own = before_of(b, s);
+    // (without a list of groups this does not wait for `own`)
     const int g = a.groups ? own.group : s / (a.S / a.groups_n);
+    Before pre{};
+    if (g >= 0) pre = before_of(a, g);
+    if ((int)blockIdx.z >= own.rows) return;
     if (g >= 0) {
-        pre = before_of(a, g);
         if (own.row0 < pre.row0 || own.row0 + own.rows > pre.row0 + pre.rows) {
             if (lane == 0) flag_status(a.status, MXQ_DEV_BAD_SEQUENCE);
             return;
@@ -106,7 +110,7 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(const __grid_consta
             l = fmaf(l, f, sum);
 #pragma unroll
             for (int i = 0; i < V; ++i) o[i] *= f;
-#pragma unroll 8
+#pragma unroll 16
             for (int k = 0; k < many; ++k) {
                 const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
                 if (wk == 0.f) continue;  // (of a half without units there is no sum)
