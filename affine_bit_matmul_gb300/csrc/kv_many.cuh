@@ -202,6 +202,7 @@ struct Shared {
     using SH = Shape<D, G>;
     uint64_t piece_full[kPieceRing], piece_empty[kPieceRing];
     uint64_t k_full[SH::KB], k_empty[SH::KB], v_full[SH::KB], v_empty[SH::KB];
+    uint64_t v_known[kMetaRing];  // the values' powers of two of a unit, before its buffer is free
     uint64_t q_full[SH::MT], s_full[2 * SH::MT], p_full[2 * SH::MT], pv_done[2 * SH::MT], drained[SH::MT];
     Piece pieces[kPieceRing];
     Meta meta[kMetaRing];
@@ -512,14 +513,19 @@ struct Convert {
             if (left == 0) left = sh.pieces[n % kPieceRing].count;
             const int buf = jt % KB;
             const int e = scale_bits(), here = state;
+            if (kv && lane == 0) {
+                // the softmax warps need no more of the values
+                sh.meta[jt % kMetaRing].v_exp[part] = (uint8_t)e;
+                mbar_arrive(&sh.v_known[jt % kMetaRing]);
+            }
             if (!warp_wait_sleep(kv ? &sh.v_empty[buf] : &sh.k_empty[buf], ((uint32_t)(jt / KB) & 1u) ^ 1u,
                            p.wait_budget))
                 return false;
             store((kv ? vbuf : kbuf) + buf * SH::kOpBytes, e);
-            if (lane == 0) {
+            if (!kv && lane == 0) {
                 Meta& meta = sh.meta[jt % kMetaRing];
-                (kv ? meta.v_exp : meta.k_exp)[part] = (uint8_t)e;
-                if (!kv) meta.there[part] = (uint8_t)here;
+                meta.k_exp[part] = (uint8_t)e;
+                meta.there[part] = (uint8_t)here;
             }
             fence_proxy_async_smem();  // the tensor cores read what was written
             __syncwarp();
@@ -558,20 +564,19 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
         // the units of this half: all of them, or every other one
         const bool narrow = is_narrow<D, G, P>(*q);
         const int k_first = narrow ? m : 0, k_step = narrow ? 2 : 1;
-        // lets unit k's buffers go without using them
-        auto leave = [&](int k) {
+        // lets unit k's keys or values go without using them
+        auto leave = [&](int k, uint64_t* full, uint64_t* empty) {
             const int j = jt + k, buf = j % KB;
-            const uint32_t par = (uint32_t)(j / KB) & 1u;
-            if (!warp_wait_sleep(&sh.k_full[buf], par, p.wait_budget)) return false;
-            if (lane == 0) mbar_arrive(&sh.k_empty[buf]);
-            if (!warp_wait_sleep(&sh.v_full[buf], par, p.wait_budget)) return false;
-            if (lane == 0) mbar_arrive(&sh.v_empty[buf]);
+            if (!warp_wait_sleep(&full[buf], (uint32_t)(j / KB) & 1u, p.wait_budget)) return false;
+            if (lane == 0) mbar_arrive(&empty[buf]);
             return true;
         };
+        auto leave_keys = [&](int k) { return leave(k, sh.k_full, sh.k_empty); };
+        auto leave_values = [&](int k) { return leave(k, sh.v_full, sh.v_empty); };
         if (narrow ? k_first >= count : q->toks <= m * (P::kShared ? 128 : p.half_toks)) {
             // no rows in this half
             for (int k = 0; k < count; ++k)
-                if (!leave(k)) return false;
+                if (!leave_keys(k) || !leave_values(k)) return false;
             jt += count;
             list.done();
             continue;
@@ -581,7 +586,7 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
         // scores of tile i of the piece
         auto scores = [&](int i) {
             const int k = k_first + i / kSubs * k_step, j = jt + k, sub = i % kSubs, buf = j % KB, a = at + i;
-            if (narrow && sub == 0 && k > 0 && !leave(k - 1)) return false;
+            if (narrow && sub == 0 && k > 0 && !leave_keys(k - 1)) return false;
             if (!warp_wait_sleep(&sh.k_full[buf], (uint32_t)(j / KB) & 1u, p.wait_budget)) return false;
             // the buffer's earlier weights have been used
             if (i >= 2 && !warp_wait_sleep(&sh.pv_done[2 * m + (a & 1)], (uint32_t)((a >> 1) - 1) & 1u, p.wait_budget))
@@ -608,7 +613,8 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
         if (!scores(0)) return false;
         for (int i = 0; i < n_tiles; ++i) {
             if (i + 1 < n_tiles && !scores(i + 1)) return false;
-            const int j = jt + k_first + i / kSubs * k_step, sub = i % kSubs, buf = j % KB, a = at + i;
+            const int k = k_first + i / kSubs * k_step, j = jt + k, sub = i % kSubs, buf = j % KB, a = at + i;
+            if (narrow && sub == 0 && k > 0 && !leave_values(k - 1)) return false;
             if (!warp_wait_sleep(&sh.v_full[buf], (uint32_t)(j / KB) & 1u, p.wait_budget) ||
                 !warp_wait_sleep(&sh.p_full[2 * m + (a & 1)], (uint32_t)(a >> 1) & 1u, p.wait_budget))
                 return false;
@@ -629,7 +635,8 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
             }
             __syncwarp();
         }
-        if (k_first + (n_units - 1) * k_step < count - 1 && !leave(count - 1)) return false;
+        if (k_first + (n_units - 1) * k_step < count - 1 && (!leave_keys(count - 1) || !leave_values(count - 1)))
+            return false;
         jt += count;
         at += n_tiles;
         list.done();
@@ -747,8 +754,8 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
             jt = jt0 + k;
             const volatile uint32_t* meta =
                 reinterpret_cast<const volatile uint32_t*>(&sh.meta[jt % kMetaRing]);
-            // the values of this unit have been converted: their powers of two
-            if (!warp_wait_sleep(&sh.v_full[jt % KB], (uint32_t)(jt / KB) & 1u, p.wait_budget))
+            // the values' powers of two: one ring ahead at most, since the units before are done with
+            if (!warp_wait_sleep(&sh.v_known[jt % kMetaRing], (uint32_t)(jt / kMetaRing) & 1u, p.wait_budget))
                 return false;
             const uint32_t v_exps = meta[1];
             const uint32_t two = __vmaxu4(v_exps, v_exps >> 16);
@@ -983,6 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.k_empty[i], SH::MT);
             mbar_init(&sh.v_empty[i], SH::MT);
         }
+        for (int i = 0; i < kMetaRing; ++i) mbar_init(&sh.v_known[i], 4);
         for (int i = 0; i < SH::MT; ++i) {
             mbar_init(&sh.q_full[i], 128);
             mbar_init(&sh.drained[i], 1);
