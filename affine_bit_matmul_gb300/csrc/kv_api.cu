@@ -407,6 +407,26 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
+// Calls over shared prefixes in which each sequence may go over its prefix for itself, in one kernel
+// and for short calls in one launch: where that takes no longer.  Times are of 152 SMs, in us: a row
+// tile and token of 128 values takes 30, 35 and 53 ps of the whole GPU for 4, 8 and 16 rows (32
+// sequences of 8192 tokens, 8 heads: 62, 73, 111 us), on the tensor cores 123 for a tile of up to 128
+// rows and 160 above.  What the calls take beside it: 8, and 22 in two parts with their joining.  The
+// lengths are not known here, only how many pages they may be in.  4 sequences after 573 tokens: 7.9 us, in
+// two parts 21.8.
+static bool each_for_itself(const AttnPlan& each, const SharedPlan& a, int S, int N, int Hkv, int D, int max_q,
+                     int max_group, const long long (&tokens)[2]) {
+    if (max_q > each.tile_toks) return false;
+    if (max_group == 1) return true;
+    const double size = D / 128.0 * 1e-6;
+    auto few = [](int rows) { return rows == 4 ? 30.0 : rows == 8 ? 35.0 : 53.0; };
+    const double own = few(each.tile_rows) * S * Hkv * each.head_parts * size;
+    const SharedPart& p = a.prefix;
+    const double shared = (p.tensor_cores ? (p.most_planes > N || max_group * (long long)max_q * p.part_heads > 128 ? 160.0 : 123.0)
+                                          : few(p.tile_rows)) * p.most_planes * Hkv * p.head_parts * size;
+    return 8 + own * (double)(tokens[0] + tokens[1]) <= 22 + shared * (double)tokens[0] + own * (double)tokens[1];
+}
+
 size_t mxq_kv_attention_shared_workspace_bytes(int T, int S, int N, int Hq, int Hkv, int D,
                                                int max_q_len, int max_group) {
     if (T < 0 || S < 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_q_len <= 0 ||
@@ -414,7 +434,9 @@ size_t mxq_kv_attention_shared_workspace_bytes(int T, int S, int N, int Hq, int 
         return 0;
     if (max_q_len > T) max_q_len = T > 0 ? T : 1;
     if (max_group > S) max_group = S > 0 ? S : 1;
-    return plan_shared(T, S, N, Hq, Hkv, D, max_q_len, max_group, kMaxSms).bytes;
+    const size_t parts = plan_shared(T, S, N, Hq, Hkv, D, max_q_len, max_group, kMaxSms).bytes;
+    const size_t each = plan_attn(T, S, Hq, Hkv, D, max_q_len, kMaxSms).few_bytes;
+    return parts > each ? parts : each;
 }
 
 mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long long q_head_stride,
@@ -450,7 +472,9 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
     const SharedPlan most = plan_shared(T, S, N, Hq, Hkv, D, max_q_len, max_group, kMaxSms);
     if (!countable(most.prefix, Hkv, tokens[0]) || !countable(most.own, Hkv, tokens[1]))
         return MXQ_ERR_UNSUPPORTED;
-    if (T > 0 && S > 0 && (!workspace || workspace_bytes < most.bytes)) return MXQ_ERR_WORKSPACE;
+    if (T > 0 && S > 0 &&
+        (!workspace || workspace_bytes < mxq_kv_attention_shared_workspace_bytes(T, S, N, Hq, Hkv, D, max_q_len, max_group)))
+        return MXQ_ERR_WORKSPACE;
     int sms = 0;
     const mxq_status st = mxq::check_current_device(&sms);
     if (st != MXQ_OK) return st;
@@ -462,18 +486,14 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
     if (dev_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess)
         return MXQ_ERR_CUDA;
     if (T == 0 || S == 0) return MXQ_OK;
-    mxq::KvSharedParams p[2];
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    for (int i = 0; i < 2; ++i) {
-        mxq::KvSharedParams& x = p[i];
-        const SharedPart& part = i ? a.own : a.prefix;
-        x = mxq::KvSharedParams();
+    auto set = [&](mxq::KvGroupParams& x) {
         x.q = static_cast<const __nv_bfloat16*>(q);
         x.q_row_stride = q_row_stride;
         x.q_head_stride = q_head_stride;
         x.pages = static_cast<const uint8_t*>(pages);
-        x.table = i ? page_table : prefix_table;
-        x.max_pages = i ? max_pages : max_prefix_pages;
+        x.table = page_table;
+        x.max_pages = max_pages;
         x.ctx_lens = ctx_lens;
         x.q_starts = q_starts;
         x.out = static_cast<__nv_bfloat16*>(out);
@@ -489,13 +509,40 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
         x.scale_log2 = (float)(scale * 1.4426950408889634);
         x.status = dev_status;
         x.wait_budget = mxq::wait_budget_cycles();
-        x.head_parts = part.head_parts;
-        x.part_heads = part.part_heads;
-        x.prefix = !i;
         x.groups_n = N;
         x.max_group = max_group;
         x.groups = group_starts;
         x.prefix_lens = prefix_lens;
+    };
+    const AttnPlan each = plan_attn(T, S, Hq, Hkv, D, max_q_len, sms < kMaxSms ? sms : kMaxSms);
+    if (each_for_itself(each, a, S, N, Hkv, D, max_q_len, max_group, tokens) &&
+        countable(each, S, Hkv, tokens[0] + tokens[1])) {
+        mxq::KvTwoParams x = mxq::KvTwoParams();
+        set(x);
+        x.prefix_table = prefix_table;
+        x.max_prefix_pages = max_prefix_pages;
+        x.head_parts = each.head_parts;
+        x.part_heads = each.part_heads;
+        x.tile_rows = each.tile_rows;
+        x.tile_toks = each.tile_toks;
+        x.max_rows = each.tile_toks;
+        x.ctas = each.ctas;
+        x.segs = reinterpret_cast<int*>(ws);
+        x.partial = reinterpret_cast<float*>(ws + each.seg_bytes);
+        return mxq::launch_kv_two(x, D, group_size, each.tile_rows, s) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
+    }
+    mxq::KvSharedParams p[2] = {};
+    for (int i = 0; i < 2; ++i) {
+        mxq::KvSharedParams& x = p[i];
+        const SharedPart& part = i ? a.own : a.prefix;
+        set(x);
+        if (!i) {
+            x.table = prefix_table;
+            x.max_pages = max_prefix_pages;
+        }
+        x.prefix = !i;
+        x.head_parts = part.head_parts;
+        x.part_heads = part.part_heads;
         x.max_planes = (int)part.planes;
         x.tile_rows = part.tile_rows;
         x.on_tensor_cores = part.tensor_cores;

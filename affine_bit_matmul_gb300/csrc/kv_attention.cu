@@ -58,9 +58,34 @@
 #include <cuda_runtime.h>
 
 #include "kv_attn_common.cuh"
+#include "kv_shared.cuh"
 
 namespace mxq {
 namespace {
+
+// What a sequence of a call over shared prefixes sees when its prefix is taken for it alone: the prefix's
+// tiles (head_tiles), then those of its own tokens.
+template <int TILE>
+__device__ __forceinline__ Span span_of(const KvTwoParams& p, int s, int plane) {
+    Span r = span_of<TILE>(static_cast<const KvAttnParams&>(p), s, plane);
+    const int own = r.p0 + r.toks > 0 ? (r.p0 + r.toks - 1) / TILE + 1 : 0;
+    r.head_tiles = r.tail = 0;
+    const int g = group_with(p, s);
+    if (g < 0) {
+        r.tiles = r.toks > 0 ? max(1, own) : 0;
+        return r;
+    }
+    const Item pre = item_of(p, g);
+    if (pre.bad) r.bad = 1;
+    if (r.toks > 0 && (r.row0 < pre.row0 || r.row0 + r.toks > pre.row0 + pre.rows)) {
+        // the group is left out, or the sequence's rows are not its
+        r.bad = 1;
+        r.toks = 0;
+    }
+    r.head_tiles = (pre.len + TILE - 1) / TILE;
+    r.tiles = r.toks > 0 ? max(1, r.head_tiles + own) : 0;
+    return r;
+}
 
 // Tokens whose value products a warp adds before it takes out what the values of a group
 // have in common.
@@ -117,6 +142,7 @@ struct Piece {
     int k0, seq0, end;        // first unit; numbers of its units in the run
     int flags;                // kBegins, kEnds
     int last;                 // no piece: the run is over
+    int group, prefix;        // shared prefixes: the sequence's group (-1: none), its tokens
 };
 // Pieces of the run that are known ahead: the copying warp looks up to two rounds of
 // its ring (24 tiles at most) ahead of the unit that is being worked on.
@@ -136,7 +162,8 @@ struct Walk {  // (no constructors: it lies in shared memory)
     Span sp;
 
     // the run's first unit is unit `at` of sequence s (of all its heads)
-    __device__ void start(const KvAttnParams& p, int s_, long long at, int units) {
+    template <class P>
+    __device__ void start(const P& p, int s_, long long at, int units) {
         s = s_;
         sp = span_of<TILE>(p, s, 0);
         const long long vheads = (long long)p.Hkv * p.head_parts;
@@ -153,7 +180,8 @@ struct Walk {  // (no constructors: it lies in shared memory)
         left = units;
     }
     // the run is one row tile
-    __device__ void whole(const KvAttnParams& p, int s_, int vh, const Span& span) {
+    template <class P>
+    __device__ void whole(const P& p, int s_, int vh, const Span& span) {
         s = s_;
         sp = span;
         h = vh / p.head_parts;
@@ -161,7 +189,8 @@ struct Walk {  // (no constructors: it lies in shared memory)
         k = seq = 0;
         left = sp.tiles;
     }
-    __device__ bool next(const KvAttnParams& p, Piece* out, Seg* seg) {
+    template <class P>
+    __device__ bool next(const P& p, Piece* out, Seg* seg) {
         bool found = false;
         while (left && !found) {
             while (sp.tiles == 0) sp = span_of<TILE>(p, ++s, 0);
@@ -184,6 +213,10 @@ struct Walk {  // (no constructors: it lies in shared memory)
                 q.end = seq + tiles;
                 q.flags = (k == 0 ? kBegins : 0) | (k + tiles == sp.tiles ? kEnds : 0);
                 q.last = 0;
+                if constexpr (P::kTwo) {
+                    q.group = group_with(p, s);
+                    q.prefix = q.group < 0 ? 0 : item_of(p, q.group).len;
+                }
                 *out = q;
                 if (q.flags != (kBegins | kEnds)) {
                     Seg g;
@@ -227,6 +260,7 @@ struct Tile {
     int unit, t0, state;
 };
 constexpr int kAll = 256;
+constexpr int kPrefix = 512;  // its tokens are a shared prefix's
 
 // Waits, within the budget, until a slot is given to unit n (whole warp).
 __device__ __forceinline__ bool unit_comes(const int* unit, int n, long long budget) {
@@ -245,8 +279,8 @@ __device__ __forceinline__ bool unit_comes(const int* unit, int n, long long bud
 // The copying warp, lane i filling slot i: units i, i + SLOTS, ...  Pages of at
 // most a tile are copied whole, of longer ones the four regions of the tile's
 // part.
-template <int D, int G, int TILE, int SLOTS>
-__device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int lane,
+template <int D, int G, int TILE, int SLOTS, class P>
+__device__ void copy_tiles(const P& p, const Piece* pieces, int lane,
                            uint32_t ring, Tile* tiles, uint64_t* full, uint64_t* empty) {
     constexpr int kMost = TILE / 16;
     constexpr uint32_t cb = kv_code_bytes(D, TILE), pb = kv_pair_bytes(D, G, TILE);
@@ -257,6 +291,7 @@ __device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int lane,
     uint32_t parity = 1;  // the first wait passes at once
     bool work = lane < SLOTS;
     int t0 = 0, id[kMost];
+    bool of_prefix = false;
     Piece q;
 
     auto look = [&]() {  // the pages of unit n, if there is one
@@ -273,11 +308,16 @@ __device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int lane,
         const int k = q.k0 + n - q.seq0;
         t0 = (k < q.head_tiles ? k : q.tail + k - q.head_tiles) * TILE;
         const int32_t* row = p.table + (long long)q.s * p.max_pages;
+        if constexpr (P::kTwo) {
+            of_prefix = k < q.head_tiles;
+            if (of_prefix) row = p.prefix_table + (long long)q.group * p.max_prefix_pages;
+        }
+        const int end_token = P::kTwo && of_prefix ? q.prefix : q.p0 + q.toks;
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
             const int t = t0 + i * size;
             id[i] = -2;  // not needed
-            if (i < count && t < q.p0 + q.toks) id[i] = __ldg(row + (t >> p.page_shift));
+            if (i < count && t < end_token) id[i] = __ldg(row + (t >> p.page_shift));
         }
     };
     if (work) look();
@@ -300,9 +340,10 @@ __device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int lane,
                         flag_status(p.status, MXQ_DEV_BAD_PAGE);
                 }
             }
-            if (state == (1 << kMost) - 1 && t0 + TILE - 1 <= q.p0 &&
+            if (state == (1 << kMost) - 1 && t0 + TILE - 1 <= (P::kTwo && of_prefix ? q.prefix - 1 : q.p0) &&
                 (!p.window || t0 > p1 - p.window || t0 + TILE <= p.sinks))
                 state |= kAll;
+            if (P::kTwo && of_prefix) state |= kPrefix;
             tiles[lane].t0 = t0;
             tiles[lane].state = state;
             *const_cast<volatile int*>(&tiles[lane].unit) = n;
@@ -344,9 +385,9 @@ __device__ void copy_tiles(const KvAttnParams& p, const Piece* pieces, int lane,
     if (lane < SLOTS && n > lane) mbar_wait(&full[lane], (uint32_t)((n - lane) / SLOTS - 1) & 1u);
 }
 
-template <int D, int G, int KT>
+template <int D, int G, int KT, class P>
 __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kCtas)
-    kv_attn_kernel(const KvAttnParams p) {
+    kv_attn_kernel(const P p) {
     using SH = Shape<D, G, KT>;
     constexpr int TILE = SH::kTile, SUB = TILE / 16;  // a warp takes 16 tokens at a time
     constexpr int kWarps = SH::kWarps, kThreads = SH::kThreads, kSlots = SH::kSlots;
@@ -371,6 +412,12 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
     const int cta = blockIdx.x;
     Seg* seg = reinterpret_cast<Seg*>(p.segs) + (long long)cta * 2;
 
+    if constexpr (P::kTwo) {
+        // groups that no sequence is found in are reported too
+        if (cta == 0 && p.status)
+            for (int g = threadIdx.x; g < p.groups_n; g += kThreads)
+                if (item_of(p, g).bad) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
+    }
     // every CTA finds its own run: the tiles of all sequences, then its share (or its
     // row tile)
     const int per = (p.S + kThreads - 1) / kThreads;
@@ -484,9 +531,11 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
         // rows with a window of 1024: 22.7 us, 23.4 without), and else worked out under a mask
         // (8 rows of 128 values in groups of 32: 93 us, 97 held).
         constexpr bool kHeld = KT == 4 && D <= 128;
+        // (a row of a shared prefix may have any position)
+        constexpr int kNoRow = P::kTwo ? INT_MIN : -1;
         auto position = [&](int kt) {
             const int row = kt * 4 + i4;
-            return row < rows ? p0 + row / heads : -1;
+            return row < rows ? p0 + row / heads : kNoRow;  // (no row sees as little)
         };
         int held[KT];
 #pragma unroll
@@ -648,7 +697,9 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int t = tile.t0 + 16 * b + r + 8 * i;
-                        const bool live = ((tile.state >> b) & 1) && t <= p1 &&
+                        // (all rows see the same of a shared prefix)
+                        const bool flat = P::kTwo && (tile.state & kPrefix);
+                        const bool live = ((tile.state >> b) & 1) && t <= (flat ? sp.prefix - 1 : p1) &&
                                           (!p.window || t > p0 - p.window || t < p.sinks);
                         if (!live) {
                             for (int g = i4; g < NG; g += 4)
@@ -657,7 +708,7 @@ __global__ void __launch_bounds__(Shape<D, G, KT>::kThreads, Shape<D, G, KT>::kC
                         }
 #pragma unroll
                         for (int kt = 0; kt < KT; ++kt)
-                            if (!(live && t <= pos[kt] &&
+                            if (!(live && (flat ? pos[kt] != kNoRow : t <= pos[kt]) &&
                                   (!p.window || t > pos[kt] - p.window || t < p.sinks)))
                                 sc[b][kt][i] = -INFINITY;
                     }
@@ -978,11 +1029,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParam
     }
 }
 
-template <int D, int G, int KT>
-cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
+template <int D, int G, int KT, class P>
+cudaError_t launch(const P& p, cudaStream_t stream) {
     using SH = Shape<D, G, KT>;
     static std::atomic<uint64_t> asked{0};  // devices on which the kernel may take its memory
-    cudaError_t err = allow_shared(kv_attn_kernel<D, G, KT>, SH::kSmem, asked);
+    cudaError_t err = allow_shared(kv_attn_kernel<D, G, KT, P>, SH::kSmem, asked);
     if (err != cudaSuccess) return err;
     // Where each CTA can have a row tile of its own and the longest possible one is short, and
     // longer than an equal share of row tiles like it by at most 2 tiles a warp, nothing is
@@ -996,15 +1047,16 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
         most = most < seen ? most : seen;
     }
     const long long row_tiles = (long long)p.S * p.Hkv * p.head_parts;
+    if constexpr (P::kTwo) most += ((long long)p.max_prefix_pages * p.page_size + SH::kTile - 1) / SH::kTile;
     if (row_tiles <= p.ctas && most <= kUncutTiles &&
         most * (p.ctas - row_tiles) <= 2LL * SH::kWarps * p.ctas) {
-        KvAttnParams one = p;
+        P one = p;
         one.whole = 1;
-        kv_attn_kernel<D, G, KT><<<(unsigned)row_tiles, SH::kThreads, SH::kSmem, stream>>>(one);
+        kv_attn_kernel<D, G, KT, P><<<(unsigned)row_tiles, SH::kThreads, SH::kSmem, stream>>>(one);
         return cudaGetLastError();
     }
     const unsigned grid = (unsigned)p.ctas;
-    kv_attn_kernel<D, G, KT><<<grid, SH::kThreads, SH::kSmem, stream>>>(p);
+    kv_attn_kernel<D, G, KT, P><<<grid, SH::kThreads, SH::kSmem, stream>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     // the second kernel's blocks are placed as the first one's finish
@@ -1018,11 +1070,12 @@ cudaError_t launch(const KvAttnParams& p, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D>, p, (int)SH::kRows);
+    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D>, static_cast<const KvAttnParams&>(p), (int)SH::kRows);
 }
 
 }  // namespace
 
+#ifndef MXQ_KV_TWO
 size_t kv_attn_seg_bytes(int ctas) { return (size_t)ctas * 2 * sizeof(Seg); }
 
 size_t kv_attn_partial_bytes(int ctas, int tile_rows, int D) {
@@ -1030,24 +1083,36 @@ size_t kv_attn_partial_bytes(int ctas, int tile_rows, int D) {
 }
 
 int kv_attn_ctas_per_sm() { return Shape<128, 64, 1>::kCtas; }
+#endif
 
-cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int G, int tile_rows,
-                           cudaStream_t stream) {
 #define MXQ_KV_ATTN(d, g)                                        \
     if (D == d && G == g)                                        \
         return tile_rows <= 4   ? launch<d, g, 1>(p, stream)     \
                : tile_rows <= 8 ? launch<d, g, 2>(p, stream)     \
                                 : launch<d, g, 4>(p, stream);
-    MXQ_KV_ATTN(64, 32)
-    MXQ_KV_ATTN(64, 64)
-    MXQ_KV_ATTN(128, 32)
-    MXQ_KV_ATTN(128, 64)
-    MXQ_KV_ATTN(128, 128)
-    MXQ_KV_ATTN(256, 32)
-    MXQ_KV_ATTN(256, 64)
+#define MXQ_KV_ATTN_ALL   \
+    MXQ_KV_ATTN(64, 32)   \
+    MXQ_KV_ATTN(64, 64)   \
+    MXQ_KV_ATTN(128, 32)  \
+    MXQ_KV_ATTN(128, 64)  \
+    MXQ_KV_ATTN(128, 128) \
+    MXQ_KV_ATTN(256, 32)  \
+    MXQ_KV_ATTN(256, 64)  \
     MXQ_KV_ATTN(256, 128)
-#undef MXQ_KV_ATTN
+
+#ifdef MXQ_KV_TWO
+cudaError_t launch_kv_two(const KvTwoParams& p, int D, int G, int tile_rows, cudaStream_t stream) {
+    MXQ_KV_ATTN_ALL
     return cudaErrorInvalidValue;
 }
+#else
+cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int G, int tile_rows,
+                           cudaStream_t stream) {
+    MXQ_KV_ATTN_ALL
+    return cudaErrorInvalidValue;
+}
+#endif
+#undef MXQ_KV_ATTN_ALL
+#undef MXQ_KV_ATTN
 
 }  // namespace mxq

@@ -38,7 +38,7 @@ __device__ __forceinline__ int items_of(const KvSharedParams& p) {
 }
 
 // Sequences of group g, [*a, *b).
-__device__ __forceinline__ void group_of(const KvSharedParams& p, int g, int* a, int* b) {
+__device__ __forceinline__ void group_of(const KvGroupParams& p, int g, int* a, int* b) {
     if (p.groups) {
         *a = __ldg(p.groups + g);
         *b = __ldg(p.groups + g + 1);
@@ -49,11 +49,12 @@ __device__ __forceinline__ void group_of(const KvSharedParams& p, int g, int* a,
     }
 }
 
-__device__ __forceinline__ Item item_of(const KvSharedParams& p, int i) {
+// (`prefix`: a group, with its prefix in pages of a table of `width`, or a sequence)
+__device__ __forceinline__ Item item_of(const KvGroupParams& p, int i, bool prefix, int width) {
     Item r;
     int a = i, b = i + 1, most = p.max_q, len;
     r.bad = 0;
-    if (p.prefix) {
+    if (prefix) {
         group_of(p, i, &a, &b);
         if (a < 0 || b > p.S || a > b || b - a > p.max_group) {
             r.bad = 1;
@@ -72,7 +73,7 @@ __device__ __forceinline__ Item item_of(const KvSharedParams& p, int i) {
         r.bad = 1;
         a = b = 0;  // none of its rows
     }
-    const int room = p.max_pages * p.page_size;
+    const int room = width * p.page_size;
     if (len < 0 || len > room) {
         r.bad = 1;
         len = min(max(len, 0), room);
@@ -84,6 +85,13 @@ __device__ __forceinline__ Item item_of(const KvSharedParams& p, int i) {
     return r;
 }
 
+__device__ __forceinline__ Item item_of(const KvSharedParams& p, int i) {
+    return item_of(p, i, p.prefix, p.max_pages);
+}
+__device__ __forceinline__ Item item_of(const KvTwoParams& p, int g) {
+    return item_of(p, g, true, p.max_prefix_pages);
+}
+
 __device__ __forceinline__ int tiles_of(const KvSharedParams& p, const Item& it) {
     return (it.len + (1 << p.tile_shift) - 1) >> p.tile_shift;
 }
@@ -93,7 +101,7 @@ __device__ __forceinline__ int units_of(const KvSharedParams& p, const Item& it)
 }
 
 // The group that sequence s belongs to, or -1.
-__device__ __forceinline__ int group_with(const KvSharedParams& p, int s) {
+__device__ __forceinline__ int group_with(const KvGroupParams& p, int s) {
     if (!p.groups) return s / (p.S / p.groups_n);
     int lo = 0, hi = p.groups_n - 1;  // the last group that starts at or before s
     while (lo < hi) {

@@ -180,7 +180,7 @@ cudaError_t launch_kv_read(const KvRowsParams& p, int D, int G, int sms, cudaStr
 // Attention over the cache.  A row tile is up to `tile_rows` rows, each one
 // (token, query head) of one sequence and key/value head.
 struct KvAttnParams {
-    static constexpr bool kShared = false;
+    static constexpr bool kShared = false, kTwo = false;
     const __nv_bfloat16* q;  // bf16 [T, Hq, D], strides in values
     long long q_row_stride, q_head_stride;
     const uint8_t* pages;
@@ -219,19 +219,32 @@ size_t kv_attn_seg_bytes(int ctas);
 size_t kv_attn_partial_bytes(int ctas, int tile_rows, int D);
 int kv_attn_ctas_per_sm();
 
-// One of the two parts of an attention call over shared prefixes: each group's rows over its
-// prefix, or each sequence's rows over its own tokens.  `table` and `max_pages` are that part's,
-// `ctx_lens` the sequences' own lengths.
-struct KvSharedParams : KvAttnParams {
-    static constexpr bool kShared = true;
-    int prefix;                  // which part
+// Groups of sequences with shared prefixes.
+struct KvGroupParams : KvAttnParams {
+    int prefix;                  // whether what is listed are the groups, or else the sequences
     int groups_n, max_group;     // groups, the most sequences of one
     const int32_t* groups;       // int32 [groups_n + 1], or null: S / groups_n sequences each
     const int32_t* prefix_lens;  // int32 [groups_n]
+    int tile_rows;               // rows of a row tile
+};
+
+// A call over shared prefixes in which each sequence goes over its prefix for itself; `table` and
+// `max_pages` are the sequences' own.
+struct KvTwoParams : KvGroupParams {
+    static constexpr bool kTwo = true;
+    const int32_t* prefix_table;
+    int max_prefix_pages;
+};
+cudaError_t launch_kv_two(const KvTwoParams& p, int D, int G, int tile_rows, cudaStream_t stream);
+
+// One of the two parts of an attention call over shared prefixes: each group's rows over its
+// prefix, or each sequence's rows over its own tokens.  `table` and `max_pages` are that part's,
+// `ctx_lens` the sequences' own lengths.
+struct KvSharedParams : KvGroupParams {
+    static constexpr bool kShared = true;
     int max_planes;              // row tiles of one head for which `partial` has places
     struct Before* before;       // workspace: what the joining kernel needs of each item
     long long* totals;           // workspace: units of a run
-    int tile_rows;               // rows of a row tile
     int tile_shift, end_units;   // log2 of a tile's tokens; what the end of a row tile costs, in units
     int unit_cost, least_run;    // of a unit, beside the other part's; units of a run, at least
     int on_tensor_cores, sms;    // the prefixes' part: by that kernel; SMs of the device
