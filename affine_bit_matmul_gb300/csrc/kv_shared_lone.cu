@@ -15,14 +15,14 @@ cudaError_t launch_kv_shared_lone(const KvSharedParams& prefix, const KvSharedPa
                       : launch_kv_shared_lone_256(prefix, own, G, stream);
 }
 
-// Costs are ns of one SM: the tensor cores' kernel takes some 3000 for a unit of 256 rows and 128
+// Costs are ns of one SM: the tensor cores' kernel takes some 2600 for a unit of 256 rows and 128
 // tokens of 128 values, 1700 where 128 rows are shared between its halves; warps on their own, for
 // 32 tokens, are bound by the memory with few rows, 110, and by their instructions with 16, 260.
 void kv_shared_shape(KvSharedParams& p, int D) {
     if (p.prefix && p.on_tensor_cores) {
         p.tile_shift = 7;
         p.end_units = kEndUnits;
-        p.unit_cost = (long long)p.max_group * p.max_q * p.part_heads <= 128 ? 1700 : 3000;
+        p.unit_cost = (long long)p.max_group * p.max_q * p.part_heads <= 128 ? 1700 : 2600;
         p.least_run = 1;
         return;
     }

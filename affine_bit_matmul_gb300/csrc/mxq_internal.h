@@ -276,7 +276,7 @@ struct KvReorderParams {
     int S, W, layers, n_pages, H, max_pages, page_size;
     int32_t* status;
 };
-cudaError_t launch_kv_reorder(const KvReorderParams& p, int D, int G, cudaStream_t stream);
+cudaError_t launch_kv_reorder(KvReorderParams p, int D, int G, cudaStream_t stream);
 size_t kv_reorder_move_bytes();
 
 }  // namespace mxq

@@ -9,6 +9,18 @@ from tests.test_gpu_kv_cache import SHAPES, dev_bf16, host, i32
 
 pytestmark = pytest.mark.gpu
 
+# The calls choose by the width of the page tables whether a group's prefix is taken for all of its rows at once
+# or each sequence goes over it for itself: both have to be right for any lengths.
+WIDE = 0
+
+
+@pytest.fixture(autouse=True, params=["as wide as needed", "wide"])
+def table_width(request):
+    global WIDE
+    WIDE = 200000 if request.param == "wide" else 0
+    yield
+    WIDE = 0
+
 
 class Case:
     """Groups of sequences over one cache in shuffled pages; slots that nothing wrote hold NaN scales."""
@@ -24,7 +36,8 @@ class Case:
         self.cache = ku.Cache(len(order), kv_heads, D, page, G, fill=0xFF)
         tables, at = [], 0
         for part in (used[:len(prefix)], used[len(prefix):]):
-            t = np.full((len(part), max(max(part), 1)), -1, dtype=np.int32)
+            wide = 0 if tables else WIDE // page  # of the prefixes' table
+            t = np.full((len(part), max(max(part), 1, wide)), -1, dtype=np.int32)
             for i, n in enumerate(part):
                 t[i, :n] = order[at:at + n]
                 at += n
@@ -190,6 +203,12 @@ def test_as_the_same_tokens_without_sharing():
         lens.append(c.prefix[g] + 40)
     o = host(mxq.kv_attention(c.q_d, c.pages_d, i32(whole), i32(lens))).astype(np.float64)
     assert ku.relative(c.run(q_starts=None)[0], o) <= 2 * ku.MOST_RELATIVE
+
+
+def test_a_long_batch_with_little_to_share():
+    # each sequence for itself over contexts that are cut
+    Case([900, 30], [1, 1], [2500, 3000], [1, 1], 8, 8, 128, 64, 64, seed=21).check(q_starts=None)
+    Case([900] * 40, [1] * 40, [300] * 40, [2] * 40, 8, 2, 128, 64, 64, seed=22).check()
 
 
 def test_many_groups_and_long_prefixes_are_cut_anywhere():
