@@ -433,7 +433,9 @@ size_t mxq_kv_attention_workspace_bytes(int T, int S, int Hq, int Hkv, int D, in
  *   group_starts: int32 [N + 1] or NULL; q_starts: int32 [S + 1], or NULL: one row
  *   per sequence (T == S)
  *   max_q_len, max_group: the most rows of a sequence and the most sequences of
- *   a group, host-side bounds; max_group decides which kernel takes the prefixes
+ *   a group, host-side bounds
+ * These bounds and the widths of the page tables decide how: a group's prefix for all of its
+ * rows, or, where that takes no longer, for each sequence by itself.
  * Invalid entries as for mxq_kv_attention: pages outside [0, n_pages) are
  * invisible (MXQ_DEV_BAD_PAGE), lengths are clamped, a sequence or group whose
  * rows or sequences are out of range, decrease or exceed the bounds is left out
@@ -442,7 +444,7 @@ size_t mxq_kv_attention_workspace_bytes(int T, int S, int Hq, int Hkv, int D, in
  * arguments.
  * Accuracy: that of mxq_kv_attention for few rows in the own tokens and in
  * prefixes of up to 32 rows (times query heads to a key/value head) in a group,
- * that for more rows in the other prefixes.  There are no windows: a layer with
+ * at least that for more rows in the other prefixes.  There are no windows: a layer with
  * one reads few tokens of each sequence anyway.                              */
 mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long long q_head_stride,
                                    const void* pages, const int32_t* prefix_table,
