@@ -502,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const long long row0 = (long long)prompt * p.W;
     const int all_steps = (p.V - 1) / (kPieces * V4::kSize) + 1;
+    pdl_wait();
     if constexpr (CLUSTER) {
         if (warp == 0) {
             const int n = find_rows(p, rows, row0);
@@ -786,25 +787,25 @@ cudaError_t launch_of(const BeamParams& p, cudaStream_t s) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr = {};
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    // a kernel's blocks are placed while the one before it finishes
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)p.ctas;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = p.ctas ? 2 : 1;
     if (p.ctas) {
         cfg.gridDim = dim3((unsigned)(p.N * p.ctas));
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = (unsigned)p.ctas;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         return cudaLaunchKernelEx(&cfg, beam_kernel<F32, true>, p);
     }
     const long long ctas = ((long long)p.N * p.W * p.parts - 1) / kWarps + 1;
-    beam_kernel<F32, false><<<(unsigned)(ctas < 2 * kSms ? ctas : 2 * kSms), kThreads, kSmem, s>>>(p);
-    err = cudaGetLastError();
+    cfg.gridDim = dim3((unsigned)(ctas < 2 * kSms ? ctas : 2 * kSms));
+    err = cudaLaunchKernelEx(&cfg, beam_kernel<F32, false>, p);
     if (err != cudaSuccess) return err;
-    // the second kernel's blocks are placed while the first one finishes
     cfg.gridDim = dim3((unsigned)p.N);
     cfg.dynamicSmemBytes = 0;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
     return cudaLaunchKernelEx(&cfg, beam_best_kernel, p);
 }
 

@@ -565,14 +565,16 @@ __global__ void __launch_bounds__(kLoneThreads, (LoneBoth<D, G, KT1, KT2>::kCtas
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Sums<kLoneThreads> prefix_sums, own_sums;
     __shared__ LoneRing<LB::kSlots> rings[kLoneWarps];
-    pdl_launch_dependents();
-    sum_items(a, prefix_sums);
-    sum_items(b, own_sums);
     if (threadIdx.x < kLoneWarps) {
         for (int i = 0; i < LB::kSlots; ++i) mbar_init(&rings[threadIdx.x].full[i], 1);
         mbar_init(&rings[threadIdx.x].query, 1);
         mbar_init_fence();
     }
+    // (the tensor cores' kernel has waited for what comes before the call, and is not waited for here)
+    if (!a.on_tensor_cores) pdl_wait();
+    pdl_launch_dependents();
+    sum_items(a, prefix_sums);
+    sum_items(b, own_sums);
     __syncthreads();
     const int warp = threadIdx.x / 32;
     Scan prefix, own;

@@ -978,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t qbuf = base, kbuf = qbuf + SH::kQBytes, vbuf = kbuf + SH::KB * SH::kOpBytes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    pdl_launch_dependents();
+    if constexpr (!P::kShared) pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPieceRing; ++i) {
             mbar_init(&sh.piece_full[i], 1);
@@ -1007,6 +1007,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     if constexpr (P::kShared) {
+        // what comes before the call is over; the sequences' own part may begin
+        pdl_wait();
+        pdl_launch_dependents();
         sum_items(p, part_sums[0]);
         sum_items(other, part_sums[1]);
     }

@@ -18,12 +18,13 @@ cudaError_t launch_lone_tiles(const KvSharedParams& prefix, const KvSharedParams
     cfg.dynamicSmemBytes = LB::kSmem;
     cfg.blockDim = dim3(kLoneThreads);
     cfg.stream = stream;
-    // beside the tensor cores' kernel, if there is one
+    // beside the tensor cores' kernel, if there is one; else its blocks are placed while what comes
+    // before finishes
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = prefix.on_tensor_cores ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, prefix, own);
 }
 

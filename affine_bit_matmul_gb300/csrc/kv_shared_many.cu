@@ -16,8 +16,18 @@ cudaError_t launch(const KvSharedParams& prefix, const KvSharedParams& own, cuda
     constexpr auto kernel = kv_prefill_kernel<D, G, KvSharedParams, KvSharedParams>;
     const cudaError_t err = allow_shared(kernel, SH::kSmem, asked);
     if (err != cudaSuccess) return err;
-    kernel<<<(unsigned)prefix.sms, kThreads, SH::kSmem, stream>>>(prefix, own);
-    return cudaGetLastError();
+    // its blocks are placed while what comes before finishes
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)prefix.sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = SH::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, prefix, own);
 }
 
 // ---------------------------------------------------------------- joining
