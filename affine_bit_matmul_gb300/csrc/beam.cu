@@ -71,16 +71,25 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float from_ordered(uint32_t u) {
     return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
-// A candidate, logit and a row's offset (two fp32 numbers, the second within half a step of the
-// first), as a key: the sum in 48 bits, an fp32 number and what its rounding left.
-__device__ __forceinline__ unsigned long long sum_key(float x, float2 off) {
-    float s = x + off.x, e = 0.f;
+// a + b and, if it is finite, what its rounding left.
+__device__ __forceinline__ float sum_of(float a, float b, float* left) {
+    const float s = a + b, y = s - a;
+    *left = (a - (s - y)) + (b - y);
+    return s;
+}
+// A candidate, a logit, its row's largest one and the row's offset (two fp32 numbers, the second within
+// half a step of the first), as a key: the sum in 48 bits, an fp32 number and what its rounding left.
+__device__ __forceinline__ unsigned long long sum_key(float x, float top, float2 off) {
+    float e0, e;
+    const float d = sum_of(x, -top, &e0);
+    float s = sum_of(d, off.x, &e);
     if (fabsf(s) < INFINITY) {
-        const float y = s - x;
-        e = (x - (s - y)) + (off.x - y) + off.y;
+        e = e0 + e + off.y;
         const float t = s + e;
         e = e - (t - s);
         s = t;
+    } else {
+        e = 0.f;
     }
     return (unsigned long long)ordered(s + 0.f) << 32 | ordered(e + 0.f);
 }
@@ -108,9 +117,9 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
     uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 
@@ -269,6 +278,8 @@ __device__ __forceinline__ Key block_first(Key k, Key* room) {
 }
 
 struct Rows {
+    float score[kMostW];
+    bool ended[kMostW];
     float2 offset[kMostW];
     float top[kMostW];
     unsigned long long sum[kMostW];
@@ -286,14 +297,19 @@ __device__ __forceinline__ bool in_use(const BeamParams& p, long long row) {
 }
 
 // A prompt's rows in use, by one warp: beams that have ended, or have no score, have no candidates
-// in their logits.
+// in their logits.  Scores and ends are kept, as the results may take their place, and are read in L2:
+// the second kernel starts when the first one has waited for what comes before the call.
 __device__ __forceinline__ int find_rows(const BeamParams& p, Rows& r, long long row0) {
     const int lane = threadIdx.x & 31;
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kMostW; i += 32) {
         const int w = i + lane;
-        const bool in = w < p.W && in_use(p, row0 + w);
+        const float score = w < p.W ? __ldcg(p.scores + row0 + w) : 0.f;
+        const bool ended = w < p.W && p.done && __ldcg(p.done + row0 + w);
+        const bool in = w < p.W && fabsf(score) < INFINITY && !ended;
+        r.score[w] = score;
+        r.ended[w] = ended;
         const uint32_t live = __ballot_sync(0xFFFFFFFFu, in);
         const int at = n + __popc(live & ((1u << lane) - 1u));
         if (w < p.W) r.place[w] = in ? at : -1;
@@ -315,7 +331,7 @@ struct Best {
 
 // The best K candidates of a prompt out of its rows' lists; one CTA.
 __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Best& s, int prompt) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, row0 = prompt * p.W, parts = r.parts;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, parts = r.parts;
     // entries: the lists of the rows in use, and K + 1 of each row, for those that have no other ones
     const int each_row = parts * p.K, in_lists = r.live * each_row, all = in_lists + p.W * (p.K + 1);
     auto entry = [&](int i) {
@@ -333,14 +349,14 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
         if (r.place[w] < 0) continue;
         const float2* st = p.stats + r.place0 + r.place[w] * parts;
         const float2 x = lane < parts ? __ldcg(st + lane) : make_float2(-INFINITY, 0.f);
-        float m = x.x;  // in powers of two
+        float m = x.x;
         for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, __ldcg(st + i).x);
         m = from_ordered(__reduce_max_sync(0xFFFFFFFFu, ordered(m)));
         // the parts' sums in units of 2^-31, which are added without rounding (there are less than
         // 2^31 terms of at most 1; a part of -inf has the sum 0)
         bool ok = true;
         auto scaled = [&](float2 y) {
-            const float l = y.x == -INFINITY ? y.y : y.y * exp2_approx(y.x - m);
+            const float l = y.x == -INFINITY ? y.y : y.y * exp2_approx((y.x - m) * kLog2e);
             ok = ok && l < INFINITY;  // (a number)
             return ok ? (unsigned long long)((double)l * 0x1p31) : 0ull;
         };
@@ -356,13 +372,11 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
     }
     __syncthreads();
     for (int w = tid; w < p.W; w += kThreads) {
-        // in 64 bits, as two fp32 numbers; not a number where no logit is finite, or one is +inf
-        // or not a number
+        // in 64 bits, as two fp32 numbers, of a candidate with the row's largest logit; not a number where
+        // no logit is finite, or one is +inf or not a number
         float2 off = make_float2(NAN, 0.f);
         if (r.place[w] >= 0 && r.sum[w]) {
-            // (the powers of two are of products with log2 e as an fp32 number)
-            const double x = (double)__ldg(p.scores + row0 + w) -
-                             ((double)r.top[w] * (1.0 / (double)kLog2e) + (log((double)r.sum[w]) - 21.487562597358306));  // 31 ln 2
+            const double x = (double)r.score[w] - (log((double)r.sum[w]) - 21.487562597358306);  // 31 ln 2
             off.x = (float)x;
             off.y = (float)(x - (double)off.x);
         }
@@ -376,7 +390,7 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
             const int w = r.row[i / each_row];
             const float2 off = r.offset[w];
             if (x == 0 || off.x - off.x != 0.f) return k;
-            k.value = sum_key(from_ordered((uint32_t)(x >> 32)), off);
+            k.value = sum_key(from_ordered((uint32_t)(x >> 32)), r.top[w], off);
             k.back = ~((uint32_t)w * (uint32_t)p.V + ~(uint32_t)x);
             return k;
         }
@@ -385,8 +399,8 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
         const int w = (i - in_lists) / (p.K + 1), e = (i - in_lists) - w * (p.K + 1);
         const float off = r.offset[w].x;
         if (off - off == 0.f) return k;
-        const float score = __ldg(p.scores + row0 + w);
-        const bool ended = p.done && __ldg(p.done + row0 + w) && fabsf(score) < INFINITY;
+        const float score = r.score[w];
+        const bool ended = r.ended[w] && fabsf(score) < INFINITY;
         int t = e - 1;
         float y = -INFINITY;
         if (e == 0) {
@@ -396,7 +410,7 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
         } else if (t >= p.V || (ended && t == p.end)) {
             return k;
         }
-        k.value = sum_key(y, make_float2(0.f, 0.f));
+        k.value = sum_key(y, 0.f, make_float2(0.f, 0.f));
         k.back = ~((uint32_t)w * (uint32_t)p.V + (uint32_t)t);
         return k;
     };
@@ -444,7 +458,7 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
         p.out_scores[to] = from_ordered((uint32_t)(k.value >> 32));
         p.parents[to] = w;
         p.tokens[to] = t;
-        if (p.out_done) p.out_done[to] = (p.done && __ldg(p.done + row0 + w)) || t == p.end;
+        if (p.out_done) p.out_done[to] = r.ended[w] || t == p.end;
     };
     const int n = s.count;
     if (n <= Best::kKeys) {
@@ -624,11 +638,11 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
             most = fmaxf(most, top[i]);
         }
         // ---- sum of exponentials
-        // exp x as 2^(x log2 e - m), where m is the largest x log2 e, rounded
+        // of x - m: a row of one large number of either sign is level, too
         const float was = m;
-        m = fmaxf(m, most * kLog2e);
+        m = fmaxf(m, most);
         const float ref = m == -INFINITY ? 0.f : m;
-        l *= exp2_approx(was - ref);
+        l *= exp2_approx((was - ref) * kLog2e);
         const uint64_t ref2 = pair_of(-ref, -ref), log2 = pair_of(kLog2e, kLog2e);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
@@ -636,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
 #pragma unroll
             for (int j = 0; j < V4::kSize; j += 2) {
                 float a, b;
-                parts_of(fma_pair(pair_of(v[i].at(j), v[i].at(j + 1)), log2, ref2), &a, &b);
+                parts_of(mul_pair(add_pair(pair_of(v[i].at(j), v[i].at(j + 1)), ref2), log2), &a, &b);
                 const uint64_t e = pair_of(exp2_approx(a), exp2_approx(b));
                 sum = j ? add_pair(sum, e) : e;
             }
@@ -717,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
         rank_keys(keys, have, p.K, list);
         for (int i = have + lane; i < p.K; i += 32) list[i] = 0ull;
         const float mw = from_ordered(__reduce_max_sync(0xFFFFFFFFu, ordered(m)));
-        l *= exp2_approx(m - (mw == -INFINITY ? 0.f : mw));
+        l *= exp2_approx((m - (mw == -INFINITY ? 0.f : mw)) * kLog2e);
 #pragma unroll
         for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
         if (lane == 0) p.stats[place] = make_float2(mw, l);
@@ -842,6 +856,8 @@ mxq_status mxq_beam_select(const void* logits, long long row_stride, int fp32, c
     // tokens are counted in 32 bits, over a prompt's beams too, and CTAs
     if ((long long)W * V > 0x7FFFFFFF - 65536 || N > 0x7FFFFFFF / 8 ||
         (long long)W * (c.parts + 1) * (K + 1) > 0x7FFFFFFF) return MXQ_ERR_UNSUPPORTED;
+    // a prompt's results take the place of its own scores only
+    if (N > 1 && K != W && (out_scores == scores || (done && out_done == done))) return MXQ_ERR_INVALID_ARG;
     if (N > 0 && (!workspace || workspace_bytes < mxq_beam_select_workspace_bytes(N, W, V, K, fp32)))
         return MXQ_ERR_WORKSPACE;
     const mxq_status st = mxq::check_current_device(nullptr);

@@ -468,6 +468,7 @@ size_t mxq_kv_attention_shared_workspace_bytes(int T, int S, int N, int Hq, int 
  *   candidate end_token with its score as it is, and its logits are not read
  *   out_scores: fp32, parents (w): int32, tokens (v): int32, all [N, K]
  *   out_done: uint8 [N, K] or NULL: the parent had ended or the token is end_token
+ *   (with K == W out_scores and out_done may be scores and done themselves)
  *   workspace: mxq_beam_select_workspace_bytes(N, W, V, K, fp32) bytes, 256-byte
  *   aligned, overwritten
  * A beam whose score is not finite is not in use: all its candidates, and any that
