@@ -156,11 +156,32 @@ SharedPlan plan_shared(int T, int S, int N, int Hq, int Hkv, int D, int max_q, i
     return a;
 }
 
-// As for AttnPlan: units of one head and of a run, and places, fit 32 bits.
-bool countable(const SharedPart& a, int Hkv, long long tokens) {
+// As for AttnPlan: units of one head and of a run, places, and the rows times query heads fit 32 bits.
+bool countable(const SharedPart& a, int T, int Hkv, long long tokens) {
     constexpr long long kMost = (1LL << 30) - 64;
     const long long units = tokens / (a.tensor_cores ? 128 : 16) + 32, vheads = (long long)Hkv * a.head_parts;
-    return a.most_planes <= kMost / units && a.most_planes <= kMost / vheads - a.runners;
+    return a.most_planes <= kMost / units && a.most_planes <= kMost / vheads - a.runners &&
+           (long long)T * a.part_heads <= kMost;
+}
+
+// Calls over shared prefixes in which each sequence may go over its prefix for itself, in one kernel
+// and for short calls in one launch: where that takes no longer.  Times are of 152 SMs, in us: a row
+// tile and token of 128 values takes 30, 35 and 53 ps of the whole GPU for 4, 8 and 16 rows (32
+// sequences of 8192 tokens, 8 heads: 62, 73, 111 us), on the tensor cores 123 for a tile of up to 128
+// rows and 160 above.  What the calls take beside it: 8, and 22 in two parts with their joining.  The
+// lengths are not known here, only how many pages they may be in.  4 sequences after 573 tokens: 7.9 us, in
+// two parts 21.8.
+bool each_for_itself(const AttnPlan& each, const SharedPlan& a, int S, int N, int Hkv, int D, int max_q,
+                     int max_group, const long long (&tokens)[2]) {
+    if (max_q > each.tile_toks) return false;
+    if (max_group == 1) return true;
+    const double size = D / 128.0 * 1e-6;
+    auto few = [](int rows) { return rows == 4 ? 30.0 : rows == 8 ? 35.0 : 53.0; };
+    const double own = few(each.tile_rows) * S * Hkv * each.head_parts * size;
+    const SharedPart& p = a.prefix;
+    const double shared = (p.tensor_cores ? (p.most_planes > N || max_group * (long long)max_q * p.part_heads > 128 ? 160.0 : 123.0)
+                                          : few(p.tile_rows)) * p.most_planes * Hkv * p.head_parts * size;
+    return 8 + own * (double)(tokens[0] + tokens[1]) <= 22 + shared * (double)tokens[0] + own * (double)tokens[1];
 }
 
 }  // namespace
@@ -407,26 +428,6 @@ mxq_status mxq_kv_attention(const void* q, long long q_row_stride, long long q_h
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
-// Calls over shared prefixes in which each sequence may go over its prefix for itself, in one kernel
-// and for short calls in one launch: where that takes no longer.  Times are of 152 SMs, in us: a row
-// tile and token of 128 values takes 30, 35 and 53 ps of the whole GPU for 4, 8 and 16 rows (32
-// sequences of 8192 tokens, 8 heads: 62, 73, 111 us), on the tensor cores 123 for a tile of up to 128
-// rows and 160 above.  What the calls take beside it: 8, and 22 in two parts with their joining.  The
-// lengths are not known here, only how many pages they may be in.  4 sequences after 573 tokens: 7.9 us, in
-// two parts 21.8.
-static bool each_for_itself(const AttnPlan& each, const SharedPlan& a, int S, int N, int Hkv, int D, int max_q,
-                     int max_group, const long long (&tokens)[2]) {
-    if (max_q > each.tile_toks) return false;
-    if (max_group == 1) return true;
-    const double size = D / 128.0 * 1e-6;
-    auto few = [](int rows) { return rows == 4 ? 30.0 : rows == 8 ? 35.0 : 53.0; };
-    const double own = few(each.tile_rows) * S * Hkv * each.head_parts * size;
-    const SharedPart& p = a.prefix;
-    const double shared = (p.tensor_cores ? (p.most_planes > N || max_group * (long long)max_q * p.part_heads > 128 ? 160.0 : 123.0)
-                                          : few(p.tile_rows)) * p.most_planes * Hkv * p.head_parts * size;
-    return 8 + own * (double)(tokens[0] + tokens[1]) <= 22 + shared * (double)tokens[0] + own * (double)tokens[1];
-}
-
 size_t mxq_kv_attention_shared_workspace_bytes(int T, int S, int N, int Hq, int Hkv, int D,
                                                int max_q_len, int max_group) {
     if (T < 0 || S < 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_q_len <= 0 ||
@@ -460,7 +461,8 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
         return MXQ_ERR_INVALID_ARG;
     if (!stride_ok(q_row_stride) || !stride_ok(q_head_stride)) return MXQ_ERR_INVALID_ARG;
     const long long tokens[2] = {(long long)max_prefix_pages * page_size, (long long)max_pages * page_size};
-    if (tokens[0] > kMaxInt || tokens[1] > kMaxInt || T > kMaxInt || S > kMaxInt || N > kMaxInt)
+    if (tokens[0] > kMaxInt || tokens[1] > kMaxInt || T > kMaxInt || S > kMaxInt || N > kMaxInt ||
+        Hq > 65535 * 8)
         return MXQ_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(pages, 16) || !aligned(out, 16) || !aligned(prefix_table, 4) ||
         !aligned(prefix_lens, 4) || !aligned(group_starts, 4) || !aligned(page_table, 4) ||
@@ -470,7 +472,7 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
     if (max_q_len > T && T > 0) max_q_len = T;
     if (max_group > S && S > 0) max_group = S;
     const SharedPlan most = plan_shared(T, S, N, Hq, Hkv, D, max_q_len, max_group, kMaxSms);
-    if (!countable(most.prefix, Hkv, tokens[0]) || !countable(most.own, Hkv, tokens[1]))
+    if (!countable(most.prefix, T, Hkv, tokens[0]) || !countable(most.own, T, Hkv, tokens[1]))
         return MXQ_ERR_UNSUPPORTED;
     if (T > 0 && S > 0 &&
         (!workspace || workspace_bytes < mxq_kv_attention_shared_workspace_bytes(T, S, N, Hq, Hkv, D, max_q_len, max_group)))
@@ -480,7 +482,7 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
     if (st != MXQ_OK) return st;
     const SharedPlan a =
         plan_shared(T, S, N, Hq, Hkv, D, max_q_len, max_group, sms < kMaxSms ? sms : kMaxSms);
-    if (!countable(a.prefix, Hkv, tokens[0]) || !countable(a.own, Hkv, tokens[1]))
+    if (!countable(a.prefix, T, Hkv, tokens[0]) || !countable(a.own, T, Hkv, tokens[1]))
         return MXQ_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dev_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess)

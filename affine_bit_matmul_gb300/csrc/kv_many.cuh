@@ -1002,13 +1002,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init_fence();
     }
+    // what comes before the call is over, and holds no tensor memory any more
+    if constexpr (P::kShared) pdl_wait();
     if (warp == 18) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
     if constexpr (P::kShared) {
-        // what comes before the call is over; the sequences' own part may begin
-        pdl_wait();
+        // the sequences' own part may begin
         pdl_launch_dependents();
         sum_items(p, part_sums[0]);
         sum_items(other, part_sums[1]);

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(const __grid_consta
             }
         }
         const long long to = (long long)(own.row0 + j) * b.Hq + head;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l > 0.f ? 1.f / l : l;  // (0, or not a number)
         uint32_t w[V / 2];
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) w[i] = cvt_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
