@@ -101,7 +101,7 @@ __device__ __forceinline__ LonePages lone_pages(const KvSharedParams& p, const S
     LonePages r;
     r.first = t0 >> p.page_shift;
     const int page = r.first + (threadIdx.x & 31);
-    r.id = q.count && page <= q.p1 >> p.page_shift ? __ldcg(p.table + (long long)q.item * p.max_pages + page) : -2;
+    r.id = q.count && page <= q.p1 >> p.page_shift ? __ldg(p.table + (long long)q.item * p.max_pages + page) : -2;
     return r;
 }
 
@@ -278,7 +278,7 @@ __device__ __forceinline__ bool lone_run(const KvSharedParams& p, int runner, Lo
                 if (in)
                     raw[u] = LN::kQueryAhead
                                  ? *reinterpret_cast<const uint4*>(raw_rows + rr * (D * 2) + (8 * i4 + 32 * u) * 2)
-                                 : __ldcg(reinterpret_cast<const uint4*>(src + 32 * u));
+                                 : __ldg(reinterpret_cast<const uint4*>(src + 32 * u));
                 big = max_u16x2(big, max_u16x2(raw[u].x & 0x7FFF7FFFu, raw[u].y & 0x7FFF7FFFu));
                 big = max_u16x2(big, max_u16x2(raw[u].z & 0x7FFF7FFFu, raw[u].w & 0x7FFF7FFFu));
             }
@@ -570,8 +570,10 @@ __global__ void __launch_bounds__(kLoneThreads, (LoneBoth<D, G, KT1, KT2>::kCtas
         mbar_init(&rings[threadIdx.x].query, 1);
         mbar_init_fence();
     }
-    // (the tensor cores' kernel has waited for what comes before the call, and is not waited for here)
-    if (!a.on_tensor_cores) pdl_wait();
+    // The tensor cores' kernel has waited for what comes before the call, and is not waited for here;
+    // nothing that L1 may hold from then is read.
+    if (a.on_tensor_cores) __threadfence();
+    else pdl_wait();
     pdl_launch_dependents();
     sum_items(a, prefix_sums);
     sum_items(b, own_sums);

@@ -26,8 +26,6 @@ struct Before {
 
 namespace {
 
-// (Read in L2: the warps' kernel beside the tensor cores' starts when that one has waited for what comes
-// before the call, and does not wait for it itself.)
 struct Item {
     int row0, rows;  // of q
     int len;         // tokens
@@ -42,8 +40,8 @@ __device__ __forceinline__ int items_of(const KvSharedParams& p) {
 // Sequences of group g, [*a, *b).
 __device__ __forceinline__ void group_of(const KvGroupParams& p, int g, int* a, int* b) {
     if (p.groups) {
-        *a = __ldcg(p.groups + g);
-        *b = __ldcg(p.groups + g + 1);
+        *a = __ldg(p.groups + g);
+        *b = __ldg(p.groups + g + 1);
     } else {
         const int each = p.S / p.groups_n;
         *a = g * each;
@@ -63,13 +61,13 @@ __device__ __forceinline__ Item item_of(const KvGroupParams& p, int i, bool pref
             a = b = 0;
         }
         most = (int)min((long long)p.max_group * p.max_q, (long long)p.T);
-        len = __ldcg(p.prefix_lens + i);
+        len = __ldg(p.prefix_lens + i);
     } else {
-        len = __ldcg(p.ctx_lens + i);
+        len = __ldg(p.ctx_lens + i);
     }
     if (p.q_starts) {
-        a = __ldcg(p.q_starts + a);
-        b = __ldcg(p.q_starts + b);
+        a = __ldg(p.q_starts + a);
+        b = __ldg(p.q_starts + b);
     }
     if (a < 0 || b > p.T || a > b || b - a > most) {
         r.bad = 1;
@@ -108,10 +106,10 @@ __device__ __forceinline__ int group_with(const KvGroupParams& p, int s) {
     int lo = 0, hi = p.groups_n - 1;  // the last group that starts at or before s
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (__ldcg(p.groups + mid) <= s) lo = mid;
+        if (__ldg(p.groups + mid) <= s) lo = mid;
         else hi = mid - 1;
     }
-    return __ldcg(p.groups + lo) <= s && s < __ldcg(p.groups + lo + 1) ? lo : -1;
+    return __ldg(p.groups + lo) <= s && s < __ldg(p.groups + lo + 1) ? lo : -1;
 }
 
 // The units of a part, summed up by a block of T threads: each thread's consecutive items.
