@@ -5,12 +5,10 @@
 // A row's candidates are in the order of its logits x, so each warp takes parts of rows, on
 // its own: it reads a part once, keeps the K largest logits with their tokens, the largest one
 // m and sum exp(x - m).  Then one CTA a prompt adds the sums to the rows' logarithms in 64 bits,
-// turns the lists' logits into candidates and takes the best K of all: the first of the prompt's
-// cluster where all prompts' clusters run at once, else a second kernel's.
+// turns the lists' logits into candidates and takes the best K of all.
 //   Selecting without sorting: a lane's vectors at one place of all steps are a slot, 128 of
 // them a warp, whose largest logits are known in the end.  At least K logits are at or above the K-th
-// largest of those, and a number a little below that is found bit by bit.  Only the slots that
-// reach it, few more than K, are looked at again, and what is not below it goes to shared memory, where
+// largest of those.  Only the slots that reach it, few more than K, are looked at again, and what is not below it goes to shared memory, where
 // each of those logits counts how many are ahead of it.  Keys are (value, ~token), so no two are
 // equal.  When there are too many (level logits) the K best stay, and equal logits with later
 // tokens than all that were there cannot come in.
@@ -20,6 +18,10 @@
 //   A lane copies what it will look at (and its neighbour, where a row does not begin at 16
 // bytes) with asynchronous 16-byte copies two steps ahead; nothing in the loop waits for another
 // warp.
+//   64 prompts of 8 beams of 131072 bf16 logits, 134 MB: 42 us, of which the first kernel takes some 34, 3.9 TB/s. It
+// issues 10 instructions a logit of its lanes, 2.4 a cycle and SM while it runs, and the looks at slots of all warps
+// fall together at the end, when the memory is idle.  Small calls are a chain: scores, logits, slots, lists, a second
+// launch: 10 us for 1 prompt of 4 beams of 32768.
 #include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -36,12 +38,9 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostK = 64;
 constexpr int kMostW = 64;
-constexpr int kMostCtas = 8;   // of a cluster
-constexpr int kMostClusters = 32;  // that run at once
 constexpr int kVecs = 4;       // 16-byte vectors of a lane in a step
 constexpr int kRoom = 96;      // keys of a warp: K and those of one look at 32 lanes
 constexpr int kStages = 3;
-constexpr int kFewK = 16;      // found one by one
 constexpr int kLook = 2;       // vectors of a lane that are looked at again at once
 constexpr int kPieces = kVecs * 32;              // of 16 bytes in a step
 constexpr int kStageBytes = (kPieces + 1) * 16;  // and one more, where rows are not aligned
@@ -58,9 +57,9 @@ struct BeamParams {
     float* out_scores;
     int32_t *parents, *tokens;
     uint8_t* out_done;
-    int N, W, V, K, ctas, steps, parts, end;
-    float2* stats;              // workspace: [prompt][row in use][part] largest logit, sum
-    unsigned long long* lists;  // workspace: [prompt][row in use][part][K] keys, 0 where there is none
+    int N, W, V, K, steps, parts, end;
+    float2* stats;              // workspace: [prompt][row][part] largest logit, sum
+    unsigned long long* lists;  // workspace: [prompt][K][row][part] keys, 0 where there is none
 };
 
 // Whether x orders before y as fp32 numbers is whether these order so as unsigned ones.
@@ -206,7 +205,8 @@ __device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
     a = x;
 }
 
-// The K-th largest of four values of each lane, taken away from the top; for small K.
+// The K-th largest of four values of each lane, taken away from the top (bit by bit instead: 1 to 6 us more
+// for K up to 32, 5 us less of 112 for 64 of 64 x 8 x 50001).
 __device__ __forceinline__ uint32_t kth_of(uint32_t (&x)[4], int K) {
     order(x[0], x[1]);
     order(x[2], x[3]);
@@ -225,29 +225,6 @@ __device__ __forceinline__ uint32_t kth_of(uint32_t (&x)[4], int K) {
             x[3] = 0;
         }
     }
-}
-
-// From N values of each lane a lower bound of the K-th largest of all that K of them are not below.
-template <int N>
-__device__ __forceinline__ uint32_t bound_in(const uint32_t (&x)[N], int K) {
-    uint32_t both = ~0u, any = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        both &= x[i];
-        any |= x[i];
-    }
-    any = __reduce_or_sync(0xFFFFFFFFu, any);
-    const int high = 31 - __clz(any & ~__reduce_and_sync(0xFFFFFFFFu, both));  // -1: all are equal
-    uint32_t t = high < 0 ? any : high == 31 ? 0u : any >> (high + 1) << (high + 1);
-    for (int bit = high; bit >= 0; --bit) {
-        const uint32_t c = t | 1u << bit;
-        int count = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) count += __popc(__ballot_sync(0xFFFFFFFFu, x[i] >= c));
-        if (count >= K) t = c;
-        if (count == K) break;
-    }
-    return t;
 }
 
 struct Key {
@@ -283,13 +260,10 @@ struct Rows {
     float2 offset[kMostW];
     float top[kMostW];
     unsigned long long sum[kMostW];
-    int8_t place[kMostW];   // of a row: its number among those in use; -1: ended or without a score
-    uint8_t row[kMostW];    // and back
-    int live, parts, steps; // rows in use; parts of a row, steps of a part
-    long long place0;       // of the prompt's parts
+    bool used[kMostW];      // neither ended nor without a score
+    uint8_t row[kMostW];    // those that are
+    int live;               // and their number
 };
-constexpr int kClusterWarps = kMostCtas * kWarps;
-constexpr int kClusterPlaces = kClusterWarps + kMostW;
 
 // Whether beam `row` of all has logits that count.
 __device__ __forceinline__ bool in_use(const BeamParams& p, long long row) {
@@ -298,8 +272,8 @@ __device__ __forceinline__ bool in_use(const BeamParams& p, long long row) {
 
 // A prompt's rows in use, by one warp: beams that have ended, or have no score, have no candidates
 // in their logits.  Scores and ends are kept, as the results may take their place, and are read in L2:
-// the second kernel starts when the first one has waited for what comes before the call.
-__device__ __forceinline__ int find_rows(const BeamParams& p, Rows& r, long long row0) {
+// this kernel starts when the first one has waited for what comes before the call.
+__device__ __forceinline__ void find_rows(const BeamParams& p, Rows& r, long long row0) {
     const int lane = threadIdx.x & 31;
     int n = 0;
 #pragma unroll
@@ -312,42 +286,46 @@ __device__ __forceinline__ int find_rows(const BeamParams& p, Rows& r, long long
         r.ended[w] = ended;
         const uint32_t live = __ballot_sync(0xFFFFFFFFu, in);
         const int at = n + __popc(live & ((1u << lane) - 1u));
-        if (w < p.W) r.place[w] = in ? at : -1;
+        r.used[w] = in;
         if (in) r.row[at] = w;
         n += __popc(live);
     }
     if (lane == 0) r.live = n;
-    return n;
 }
 
-// What the first CTA selects with, where the ring was.
+// What a CTA selects with.
 struct Best {
     static constexpr int kKeys = 1024;
     Key keys[kKeys];
-    uint32_t groups[kThreads / 2];
+    uint32_t groups[kThreads / 4];
     Key first[kWarps];
     int count;
 };
 
 // The best K candidates of a prompt out of its rows' lists; one CTA.
 __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Best& s, int prompt) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, parts = r.parts;
-    // entries: the lists of the rows in use, and K + 1 of each row, for those that have no other ones
-    const int each_row = parts * p.K, in_lists = r.live * each_row, all = in_lists + p.W * (p.K + 1);
-    auto entry = [&](int i) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, parts = p.parts, span = p.W * parts;
+    const long long row0 = (long long)prompt * p.W;
+    // entries: the first of the lists of the rows in use, the second ones, ...; and K + 1 of each row, for
+    // those that have no other ones
+    const int lists = r.live * parts, in_lists = lists * p.K, all = in_lists + p.W * (p.K + 1);
+    auto entry = [&](int i, int* w) {
+        *w = 0;
         if (i >= in_lists) return 0ull;
-        const int n = i / each_row;
-        return __ldcg(p.lists + (r.place0 + r.place[r.row[n]] * parts) * p.K + (i - n * each_row));
+        const unsigned rank = (unsigned)i / lists, list = i - rank * lists, n = list / (unsigned)parts;
+        *w = r.row[n];
+        return __ldcg(p.lists + ((long long)prompt * p.K + rank) * span + *w * parts + (list - n * parts));
     };
     constexpr int kHeld = 2;  // entries that a thread keeps
     unsigned long long held[kHeld];
+    int held_row[kHeld];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) held[i] = tid + i * kThreads < all ? entry(tid + i * kThreads) : 0;
+    for (int i = 0; i < kHeld; ++i) held[i] = entry(tid + i * kThreads, &held_row[i]);
     // ---- the rows' logarithms
     if (tid == 0) s.count = 0;
     for (int w = warp; w < p.W; w += kWarps) {
-        if (r.place[w] < 0) continue;
-        const float2* st = p.stats + r.place0 + r.place[w] * parts;
+        if (!r.used[w]) continue;
+        const float2* st = p.stats + (row0 + w) * parts;
         const float2 x = lane < parts ? __ldcg(st + lane) : make_float2(-INFINITY, 0.f);
         float m = x.x;
         for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, __ldcg(st + i).x);
@@ -375,7 +353,7 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
         // in 64 bits, as two fp32 numbers, of a candidate with the row's largest logit; not a number where
         // no logit is finite, or one is +inf or not a number
         float2 off = make_float2(NAN, 0.f);
-        if (r.place[w] >= 0 && r.sum[w]) {
+        if (r.used[w] && r.sum[w]) {
             const double x = (double)r.score[w] - (log((double)r.sum[w]) - 21.487562597358306);  // 31 ln 2
             off.x = (float)x;
             off.y = (float)(x - (double)off.x);
@@ -383,11 +361,11 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
         r.offset[w] = off;
     }
     __syncthreads();
-    // what entry i, x in a list, is as a candidate
-    auto candidate = [&](int i, unsigned long long x) {
+    // what entry i, x in a list of a row, is as a candidate
+    auto candidate = [&](int i, unsigned long long x, int list_row) {
         Key k{0, 0};
         if (i < in_lists) {
-            const int w = r.row[i / each_row];
+            const int w = list_row;
             const float2 off = r.offset[w];
             if (x == 0 || off.x - off.x != 0.f) return k;
             k.value = sum_key(from_ordered((uint32_t)(x >> 32)), r.top[w], off);
@@ -414,34 +392,29 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
         k.back = ~((uint32_t)w * (uint32_t)p.V + (uint32_t)t);
         return k;
     };
-    auto nth = [&](int i) { return candidate(i, entry(i)); };
+    auto nth = [&](int i) {
+        int w;
+        const unsigned long long x = entry(i, &w);
+        return candidate(i, x, w);
+    };
     Key mine[kHeld];
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         mine[i] = Key{0, 0};
-        if (tid + i * kThreads < all) mine[i] = candidate(tid + i * kThreads, held[i]);
+        if (tid + i * kThreads < all) mine[i] = candidate(tid + i * kThreads, held[i], held_row[i]);
         most = max(most, (uint32_t)(mine[i].value >> 32));
     }
     for (int i = tid + kHeld * kThreads; i < all; i += kThreads) most = max(most, (uint32_t)(nth(i).value >> 32));
-    // groups of 4 or 2 threads
+    // the K-th largest of groups of 4 threads
     most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-    if (p.K <= 40) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-    const int each = p.K <= 40 ? 4 : 2;
-    if (tid % each == 0) s.groups[tid / each] = most;
+    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+    if (tid % 4 == 0) s.groups[tid / 4] = most;
     __syncthreads();
-    uint32_t bound;
-    if (p.K <= 40) {
-        uint32_t x[4];
+    uint32_t x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = s.groups[i * 32 + lane];
-        bound = p.K <= kFewK ? kth_of(x, p.K) : bound_in(x, p.K);
-    } else {
-        uint32_t x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = s.groups[i * 32 + lane];
-        bound = bound_in(x, p.K);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = s.groups[i * 32 + lane];
+    const uint32_t bound = kth_of(x, p.K);
     auto take = [&](const Key& k) {
         if (k.value == 0 || (uint32_t)(k.value >> 32) < bound) return;
         const int at = atomicAdd(&s.count, 1);
@@ -484,7 +457,8 @@ __device__ __forceinline__ void best_of_prompt(const BeamParams& p, Rows& r, Bes
 }
 
 // The best K of a warp's n keys (at most kRoom), in order where `to` is.
-__device__ __forceinline__ void rank_keys(const unsigned long long* keys, int n, int K, unsigned long long* to) {
+__device__ __forceinline__ void rank_keys(const unsigned long long* keys, int n, int K, unsigned long long* to,
+                                          long long step = 1) {
     const int lane = threadIdx.x & 31;
     unsigned long long k[kRoom / 32];
     int rank[kRoom / 32];
@@ -501,42 +475,21 @@ __device__ __forceinline__ void rank_keys(const unsigned long long* keys, int n,
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kRoom / 32; ++i)
-        if (k[i] && rank[i] < K) to[rank[i]] = k[i];
+        if (k[i] && rank[i] < K) to[rank[i] * step] = k[i];
     __syncwarp();
 }
 
-// CLUSTER: a prompt's CTAs take its parts, and its first one the best of them.
-//   Bound by the memory.
-template <bool F32, bool CLUSTER>
+template <bool F32>
 __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
     using V4 = Vec<F32>;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Rows rows;
-    const int prompt = CLUSTER ? (int)blockIdx.x / p.ctas : 0, cta = CLUSTER ? (int)blockIdx.x % p.ctas : (int)blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-    const long long row0 = (long long)prompt * p.W;
-    const int all_steps = (p.V - 1) / (kPieces * V4::kSize) + 1;
+    const int all_steps = (p.V - 1) / (kPieces * V4::kSize) + 1, parts = p.parts;
     pdl_wait();
-    if constexpr (CLUSTER) {
-        if (warp == 0) {
-            const int n = find_rows(p, rows, row0);
-            if (lane == 0) {
-                // a part for each warp of the cluster, if it is a step at least
-                const int most = p.ctas * kWarps / max(n, 1);
-                const int steps = (all_steps - 1) / max(1, min(most, all_steps)) + 1;
-                rows.steps = steps;
-                rows.parts = (all_steps - 1) / steps + 1;
-                rows.place0 = (long long)prompt * kClusterPlaces;
-            }
-        }
-        __syncthreads();
-    } else {
-        pdl_launch_dependents();
-    }
-    const int parts = CLUSTER ? rows.parts : p.parts, part_steps = CLUSTER ? rows.steps : p.steps;
+    pdl_launch_dependents();
     // this warp's parts: every so many of all rows
-    const long long items = CLUSTER ? (long long)rows.live * parts : (long long)p.N * p.W * parts;
-    const int stride = (CLUSTER ? p.ctas : (int)gridDim.x) * kWarps;
+    const long long items = (long long)p.N * p.W * parts;
+    const int stride = (int)gridDim.x * kWarps;
     const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
     unsigned long long* keys = reinterpret_cast<unsigned long long*>(smem + kRingBytes) + warp * kRoom;
     uint8_t* slots = smem + kRingBytes + kWarps * kRoom * 8 + warp * kPieces;
@@ -549,10 +502,10 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
     auto begin = [&](At& a, long long item) {
         for (a.item = item; a.item < items; a.item += stride) {
             const long long i = a.item / parts;
-            if (!CLUSTER && !in_use(p, i)) continue;
-            a.x = p.logits + (CLUSTER ? row0 + rows.row[i] : i) * p.row_stride;
-            a.step = a.step0 = (int)(a.item - i * parts) * part_steps;
-            a.end = min(a.step + part_steps, all_steps);
+            if (!in_use(p, i)) continue;
+            a.x = p.logits + i * p.row_stride;
+            a.step = a.step0 = (int)(a.item - i * parts) * p.steps;
+            a.end = min(a.step + p.steps, all_steps);
             return;
         }
     };
@@ -602,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
         }
         cp_async_commit();
     };
-    begin(ahead_at, cta * kWarps + warp);
+    begin(ahead_at, (int)blockIdx.x * kWarps + warp);
     At at = ahead_at;
     issue();
     issue();
@@ -668,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
         uint32_t slot_key[kVecs];
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) slot_key[i] = value_key(so_far[i]);
-        const uint32_t t = p.K <= kFewK ? kth_of(slot_key, p.K) : bound_in(slot_key, p.K);
+        const uint32_t t = kth_of(slot_key, p.K);
         // (what is left of the bits of -inf may be no number)
         float bound = from_ordered(max(t, ordered(-INFINITY)));
         // the slots that reach it, in order
@@ -726,50 +679,37 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
                 if (full) bound = from_ordered(min(ordered(bound) + 1u, ordered(INFINITY)));
             }
         }
-        const long long place = (CLUSTER ? rows.place0 : 0) + was_at.item;
-        unsigned long long* list = p.lists + place * p.K;
-        rank_keys(keys, have, p.K, list);
-        for (int i = have + lane; i < p.K; i += 32) list[i] = 0ull;
+        const long long span = (long long)p.W * parts, place0 = was_at.item / span * span;
+        unsigned long long* list = p.lists + place0 * p.K + (was_at.item - place0);
+        rank_keys(keys, have, p.K, list, span);
+        for (int i = have + lane; i < p.K; i += 32) list[i * span] = 0ull;
         const float mw = from_ordered(__reduce_max_sync(0xFFFFFFFFu, ordered(m)));
         l *= exp2_approx((m - (mw == -INFINITY ? 0.f : mw)) * kLog2e);
 #pragma unroll
         for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-        if (lane == 0) p.stats[place] = make_float2(mw, l);
+        if (lane == 0) p.stats[was_at.item] = make_float2(mw, l);
         m = -INFINITY;
         l = 0.f;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) so_far[i] = -INFINITY;
     }
     cp_async_wait<0>();
-    if constexpr (CLUSTER) {
-        if (p.ctas > 1) cluster_sync();
-        else __syncthreads();
-        if (cta == 0) best_of_prompt(p, rows, *reinterpret_cast<Best*>(smem), prompt);
-    }
 }
 
 __global__ void __launch_bounds__(kThreads) beam_best_kernel(const BeamParams p) {
     __shared__ Rows rows;
     __shared__ Best best;
-    if (threadIdx.x < 32) {
-        find_rows(p, rows, (long long)blockIdx.x * p.W);
-        if (threadIdx.x == 0) {
-            rows.parts = p.parts;
-            rows.place0 = (long long)blockIdx.x * p.W * p.parts;
-        }
-        // every row has places, in use or not
-        __syncwarp();
-        for (int w = threadIdx.x; w < p.W; w += 32)
-            if (rows.place[w] >= 0) rows.place[w] = w;
-    }
+    if (threadIdx.x < 32) find_rows(p, rows, (long long)blockIdx.x * p.W);
     __syncthreads();
     pdl_wait();
     best_of_prompt(p, rows, best, blockIdx.x);
 }
 
-// How a call is cut: CTAs of a prompt's cluster (0: no clusters), steps of a part of a row, its
-// parts (of clusters: told on the device, where the rows in use are known).  Each warp that runs at
-// once has one part, if it is a step at least.
+// How a call is cut: steps of a part of a row, its parts.  Each warp has one part of two steps at least: a
+// step each makes twice the lists (8 beams of 50001 tokens for 8 prompts: 15.6 us, of single steps 21.6).  One CTA
+// an SM up to 16384 steps, two above, where the memory counts more than the lists: 24 and 64 prompts of these
+// 19.4 and 35.0 us with one, 22.6 and 31.8 with two; 32 and 64 of 4 beams of 131072 tokens 14.6 and 21.2, 16.9 and
+// 20.8.  (A cluster for each prompt, whose first CTA takes the best: 18.3 us for the 8 prompts, 25.3 for the 24.)
 struct Cut {
     int ctas, steps, parts;
     long long places;
@@ -777,46 +717,35 @@ struct Cut {
 constexpr int kSms = 152;
 Cut cut_of(int N, int W, int V, int fp32) {
     const int steps = (V - 1) / (kPieces * (fp32 ? 4 : 8)) + 1;
+    const long long rows = (long long)N * W, most = (rows * steps <= 16384 ? 1 : 2) * kSms;  // CTAs
+    const long long each = rows ? most * kWarps / rows : steps;
     Cut c{};
-    if (N <= kMostClusters) {
-        for (c.ctas = 1; c.ctas < kMostCtas && c.ctas * kWarps < (long long)W * steps;) c.ctas *= 2;
-        c.places = (long long)N * kClusterPlaces;
-    } else {
-        const long long rows = (long long)N * W, warps = 2 * kSms * kWarps;
-        c.parts = warps / rows < 1 ? 1 : warps / rows < steps ? (int)(warps / rows) : steps;
-        c.steps = (steps - 1) / c.parts + 1;
-        c.parts = (steps - 1) / c.steps + 1;
-        c.places = rows * c.parts;
-    }
+    c.parts = each < 1 ? 1 : each < steps ? (int)each : steps;
+    c.steps = (steps - 1) / c.parts + 1;
+    if (c.steps == 1 && steps > 1) c.steps = 2;
+    c.parts = (steps - 1) / c.steps + 1;
+    c.places = rows * c.parts;
+    c.ctas = (int)(c.places <= (most - 1) * kWarps ? (c.places + kWarps - 1) / kWarps : most);
     return c;
 }
 
 template <bool F32>
-cudaError_t launch_of(const BeamParams& p, cudaStream_t s) {
-    static std::atomic<uint64_t> asked[2] = {};  // devices on which the kernels may take their memory
-    cudaError_t err = p.ctas ? allow_shared(beam_kernel<F32, true>, kSmem, asked[1])
-                             : allow_shared(beam_kernel<F32, false>, kSmem, asked[0]);
+cudaError_t launch_of(const BeamParams& p, int ctas, cudaStream_t s) {
+    static std::atomic<uint64_t> asked{0};  // devices on which the kernel may take its memory
+    cudaError_t err = allow_shared(beam_kernel<F32>, kSmem, asked);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     // a kernel's blocks are placed while the one before it finishes
-    cudaLaunchAttribute attrs[2] = {};
-    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[0].val.programmaticStreamSerializationAllowed = 1;
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim.x = (unsigned)p.ctas;
-    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
-    cfg.attrs = attrs;
-    cfg.numAttrs = p.ctas ? 2 : 1;
-    if (p.ctas) {
-        cfg.gridDim = dim3((unsigned)(p.N * p.ctas));
-        return cudaLaunchKernelEx(&cfg, beam_kernel<F32, true>, p);
-    }
-    const long long ctas = ((long long)p.N * p.W * p.parts - 1) / kWarps + 1;
-    cfg.gridDim = dim3((unsigned)(ctas < 2 * kSms ? ctas : 2 * kSms));
-    err = cudaLaunchKernelEx(&cfg, beam_kernel<F32, false>, p);
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, beam_kernel<F32>, p);
     if (err != cudaSuccess) return err;
     cfg.gridDim = dim3((unsigned)p.N);
     cfg.dynamicSmemBytes = 0;
@@ -876,7 +805,6 @@ mxq_status mxq_beam_select(const void* logits, long long row_stride, int fp32, c
     p.W = W;
     p.V = V;
     p.K = K;
-    p.ctas = c.ctas;
     p.steps = c.steps;
     p.parts = c.parts;
     p.end = end_token;
@@ -884,7 +812,7 @@ mxq_status mxq_beam_select(const void* logits, long long row_stride, int fp32, c
     p.lists = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) +
                                                     mxq::stat_bytes(c));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t err = fp32 ? mxq::launch_of<true>(p, s) : mxq::launch_of<false>(p, s);
+    const cudaError_t err = fp32 ? mxq::launch_of<true>(p, c.ctas, s) : mxq::launch_of<false>(p, c.ctas, s);
     return err == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
 }
 
