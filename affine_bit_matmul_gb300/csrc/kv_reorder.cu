@@ -13,6 +13,8 @@
 // beginnings.  They work out the one column that they need by themselves, unless the table is
 // written in place: then they run after it, from a list.
 //   Copies are bound by the memory, small calls by a chain of loads (parents, lengths, table, pages).
+//   16 groups of 8 over 16 layers, 26 MB read and as many written: 19.8 us with 4 pieces of 16 bytes of a thread in
+// flight (20.7 with 2, 22.5 with 8; 22.9 in blocks of 512 threads, 20.8 of 128), 3 of them the chain; 1 group of 4: 4.1 us.
 #include <cstdint>
 #include <cuda_runtime.h>
 

@@ -73,6 +73,9 @@ __device__ __forceinline__ Before before_of(const KvSharedParams& p, int i) {
 
 // One warp joins a row of one query head, 32 pieces at a time, those of the prefix before those of
 // the own tokens: lane i takes the weight of piece i, then all lanes add the pieces' sums in order.
+//   A chain of loads: what comes before the item, the pieces' maxima, the sums.  7 us of a call with 64 rows of 32
+// heads, 4 of them until the kernel before has ended for it too; 25 us for 256 rows with 34 MB of pieces, which are
+// in L2.
 template <int D>
 __global__ void __launch_bounds__(256) kv_shared_join_kernel(const __grid_constant__ KvSharedParams a,
                                                              const __grid_constant__ KvSharedParams b) {

@@ -40,7 +40,7 @@ def attend(L, q=FAKE, pages=FAKE, ptable=FAKE, plens=FAKE, groups=FAKE, table=FA
     (dict(lse=ODD2), 2), (dict(lens=ODD2), 2), (dict(plens=ODD2), 2), (dict(groups=ODD2), 2), (dict(ptable=ODD2), 2), (dict(st=ODD2), 2),
     (dict(ws=ODD), 2), (dict(ws=None), 6), (dict(wsb=64), 6),
     # more units than 32 bits count
-    (dict(T=1 << 20, S=1 << 20, width=1 << 20, group=8, wsb=1 << 62), 3), (dict(T=1 << 22, S=1 << 22, N=1 << 20, pwidth=1 << 20, wsb=1 << 62), 3)])
+    (dict(T=1 << 20, S=1 << 20, width=1 << 20, group=8, wsb=1 << 62), 3), (dict(Hq=8 << 16, wsb=1 << 62), 3), (dict(T=1 << 22, S=1 << 22, N=1 << 20, pwidth=1 << 20, wsb=1 << 62), 3)])
 def test_shared_attention_argument_checks(L, kw, code):
     assert attend(L, **kw) == code
 
@@ -55,7 +55,9 @@ def select(L, x=FAKE, scores=FAKE, done=None, so=FAKE, po=FAKE, to=FAKE, do=None
     (dict(W=2, V=3, K=7, stride=3), 1), (dict(stride=-1), 1), (dict(done=FAKE, end=-1), 1), (dict(done=FAKE, end=1000), 1),
     (dict(do=FAKE, end=1000), 1), (dict(x=None), 1), (dict(scores=None), 1), (dict(so=None), 1), (dict(po=None), 1), (dict(to=None), 1),
     (dict(x=ODD1), 2), (dict(x=ODD2, fp32=1), 2), (dict(scores=ODD2), 2), (dict(so=ODD2), 2), (dict(po=ODD2), 2), (dict(to=ODD2), 2),
-    (dict(ws=ODD), 2), (dict(W=64, V=1 << 25), 3), (dict(ws=None), 6), (dict(wsb=64), 6)])
+    (dict(ws=ODD), 2), (dict(W=64, V=1 << 25), 3), (dict(ws=None), 6), (dict(wsb=64), 6),
+    # results in the place of scores, or ends, of another number of beams
+    (dict(K=2), 1), (dict(K=2, so=OTHER, done=FAKE, do=FAKE), 1)])
 def test_select_argument_checks(L, kw, code):
     assert select(L, **kw) == code
 
