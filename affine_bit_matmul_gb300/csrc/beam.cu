@@ -160,7 +160,7 @@ struct Vec {
         const uint8_t* at = row + (long long)v * kBytes;
         const int off = (int)(reinterpret_cast<uintptr_t>(at) & 15);
         if (off == 0 && v + kSize <= V) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+            const uint4 x = *(reinterpret_cast<const uint4*>(at));
             w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
             return;
         }
@@ -168,8 +168,8 @@ struct Vec {
 #pragma unroll
         for (int i = 0; i < kSize; ++i) {
             if (v + i >= V) continue;
-            if constexpr (F32) w[i] = __ldg(reinterpret_cast<const uint32_t*>(at) + i);
-            else w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(at) + i) << (i & 1 ? 16 : 0);
+            if constexpr (F32) w[i] = *(reinterpret_cast<const uint32_t*>(at) + i);
+            else w[i / 2] |= (uint32_t)*(reinterpret_cast<const uint16_t*>(at) + i) << (i & 1 ? 16 : 0);
         }
         cut(V - v);
     }
@@ -267,7 +267,7 @@ struct Rows {
 
 // Whether beam `row` of all has logits that count.
 __device__ __forceinline__ bool in_use(const BeamParams& p, long long row) {
-    return fabsf(__ldg(p.scores + row)) < INFINITY && !(p.done && __ldg(p.done + row));
+    return fabsf(p.scores[row]) < INFINITY && !(p.done && p.done[row]);
 }
 
 // A prompt's rows in use, by one warp: beams that have ended, or have no score, have no candidates
@@ -533,11 +533,11 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p) {
                     for (int b = off; b < 16 && at + b < end; b += V4::kBytes) {
                         if constexpr (F32)
                             asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + i * 16 + b),
-                                         "r"(__ldg(reinterpret_cast<const uint32_t*>(at + b)))
+                                         "r"(*(reinterpret_cast<const uint32_t*>(at + b)))
                                          : "memory");
                         else
                             asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + i * 16 + b),
-                                         "h"(__ldg(reinterpret_cast<const uint16_t*>(at + b)))
+                                         "h"(*(reinterpret_cast<const uint16_t*>(at + b)))
                                          : "memory");
                     }
                 }

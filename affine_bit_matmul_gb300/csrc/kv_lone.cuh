@@ -105,7 +105,7 @@ __device__ __forceinline__ LonePages lone_pages(const KvSharedParams& p, const S
     LonePages r;
     r.first = t0 >> p.page_shift;
     const int page = r.first + (threadIdx.x & 31);
-    r.id = q.count && page <= q.p1 >> p.page_shift ? __ldg(p.table + (long long)q.item * p.max_pages + page) : -2;
+    r.id = q.count && page <= q.p1 >> p.page_shift ? *(p.table + (long long)q.item * p.max_pages + page) : -2;
     return r;
 }
 
@@ -282,7 +282,7 @@ __device__ __forceinline__ bool lone_run(const KvSharedParams& p, int runner, Lo
                 if (in)
                     raw[u] = LN::kQueryAhead
                                  ? *reinterpret_cast<const uint4*>(raw_rows + rr * (D * 2) + (8 * i4 + 32 * u) * 2)
-                                 : __ldg(reinterpret_cast<const uint4*>(src + 32 * u));
+                                 : *(reinterpret_cast<const uint4*>(src + 32 * u));
                 big = max_u16x2(big, max_u16x2(raw[u].x & 0x7FFF7FFFu, raw[u].y & 0x7FFF7FFFu));
                 big = max_u16x2(big, max_u16x2(raw[u].z & 0x7FFF7FFFu, raw[u].w & 0x7FFF7FFFu));
             }

@@ -396,7 +396,7 @@ struct Convert {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = look_t + 16 * i;
-            id[i] = t <= look_p1 ? __ldg(row + (t >> p.page_shift)) : -2;
+            id[i] = t <= look_p1 ? row[t >> p.page_shift] : -2;
         }
         return true;
     }
@@ -709,7 +709,7 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
                 for (int i = 0; i < kBatch; ++i) {
                     // (rows past the last repeat it; their scores are not used)
                     const int at_row = min(quarter * 32 + (i0 + i) * kAtOnce + lane / kLanes, rows - 1);
-                    v[i] = __ldg(reinterpret_cast<const uint4*>(
+                    v[i] = *(reinterpret_cast<const uint4*>(
                                      p.q + (long long)(q->row0 + tok0 + (flat0 + at_row) / heads) * p.q_row_stride +
                                      (long long)(q->head0 + (flat0 + at_row) % heads) * p.q_head_stride) +
                                  c);

@@ -26,6 +26,8 @@ struct Before {
 
 namespace {
 
+// (What a call reads may be written while its first kernel's blocks are placed: plain loads, not those for what
+// stays as it is.)
 struct Item {
     int row0, rows;  // of q
     int len;         // tokens
@@ -40,8 +42,8 @@ __device__ __forceinline__ int items_of(const KvSharedParams& p) {
 // Sequences of group g, [*a, *b).
 __device__ __forceinline__ void group_of(const KvGroupParams& p, int g, int* a, int* b) {
     if (p.groups) {
-        *a = __ldg(p.groups + g);
-        *b = __ldg(p.groups + g + 1);
+        *a = *(p.groups + g);
+        *b = *(p.groups + g + 1);
     } else {
         const int each = p.S / p.groups_n;
         *a = g * each;
@@ -61,13 +63,13 @@ __device__ __forceinline__ Item item_of(const KvGroupParams& p, int i, bool pref
             a = b = 0;
         }
         most = (int)min((long long)p.max_group * p.max_q, (long long)p.T);
-        len = __ldg(p.prefix_lens + i);
+        len = *(p.prefix_lens + i);
     } else {
-        len = __ldg(p.ctx_lens + i);
+        len = *(p.ctx_lens + i);
     }
     if (p.q_starts) {
-        a = __ldg(p.q_starts + a);
-        b = __ldg(p.q_starts + b);
+        a = *(p.q_starts + a);
+        b = *(p.q_starts + b);
     }
     if (a < 0 || b > p.T || a > b || b - a > most) {
         r.bad = 1;
@@ -106,10 +108,10 @@ __device__ __forceinline__ int group_with(const KvGroupParams& p, int s) {
     int lo = 0, hi = p.groups_n - 1;  // the last group that starts at or before s
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (__ldg(p.groups + mid) <= s) lo = mid;
+        if (*(p.groups + mid) <= s) lo = mid;
         else hi = mid - 1;
     }
-    return __ldg(p.groups + lo) <= s && s < __ldg(p.groups + lo + 1) ? lo : -1;
+    return *(p.groups + lo) <= s && s < *(p.groups + lo + 1) ? lo : -1;
 }
 
 // The units of a part, summed up by a block of T threads: each thread's consecutive items.

@@ -84,7 +84,7 @@ def test_beams(N, W, k):
 
 def test_all_chunk_sizes():
     rng = np.random.default_rng(5)
-    for N in (1, 20, 40, 80, 160):  # 1, 2, 4 and 8 vectors a thread
+    for N in (1, 20, 40, 80, 160):  # parts of two steps to whole rows, one and two blocks an SM
         for fp32 in (False, True):
             check(logits(rng, N, 4, 33001, fp32), -10 * rng.random((N, 4)), 6, fp32=fp32)
 
