@@ -579,29 +579,36 @@ __global__ void __launch_bounds__(kLoneThreads, (LoneBoth<D, G, KT1, KT2>::kCtas
     if (a.on_tensor_cores) __threadfence();
     else pdl_wait();
     pdl_launch_dependents();
-    sum_items(a, prefix_sums);
+    // Runners of the two parts.  Beside the other kernel they are the first CTAs, which are on the SMs
+    // that it leaves; else consecutive ones are on different SMs.
+    const int all = gridDim.x * kLoneWarps;
+    int first = 0, second = all;
+    if (a.on_tensor_cores) {
+        // the SMs that the other kernel leaves; it needs them all for itself if there is nothing else
+        const int sms = (int)__ldcg(a.totals + 1);
+        if (sms < a.sms) second = (int)((long long)all * (a.sms - sms) / a.sms);
+        if ((int)blockIdx.x * kLoneWarps >= second) {
+            // (a CTA that begins when the other kernel ends, with 3 us of lists before it would find nothing to do)
+            pdl_wait();
+            return;
+        }
+    }
+    if (!a.on_tensor_cores) sum_items(a, prefix_sums);
+    else prefix_sums.units[threadIdx.x] = prefix_sums.planes[threadIdx.x] = 0;
     sum_items(b, own_sums);
     __syncthreads();
     const int warp = threadIdx.x / 32;
     Scan prefix, own;
     scan_sums(prefix_sums, own_sums, prefix, own);
     const long long prefix_cost = all_units(a, prefix) * a.unit_cost, own_cost = all_units(b, own) * b.unit_cost;
-    // Runners of the two parts.  Beside the other kernel they are the first CTAs, which are on the SMs
-    // that it leaves; else consecutive ones are on different SMs.
-    const int all = gridDim.x * kLoneWarps;
     const int runner = a.on_tensor_cores ? blockIdx.x * kLoneWarps + warp : warp * gridDim.x + blockIdx.x;
-    int first = 0, second = all;
-    if (a.on_tensor_cores) {
-        // the SMs that the other kernel leaves; it needs them all for itself if there is nothing else
-        const int sms = share_of(prefix_cost, own_cost, a.sms);
-        if (sms < a.sms) second = (int)((long long)all * (a.sms - sms) / a.sms);
-    } else {
+    if (!a.on_tensor_cores) {
         first = share_of(prefix_cost, own_cost, all);
         second = all - first;
     }
     const long long own_run = run_length(b, all_units(b, own), second);
     const long long prefix_run = a.on_tensor_cores ? 0 : run_length(a, all_units(a, prefix), first);
-    if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.x == (a.on_tensor_cores ? (second - 1) / kLoneWarps : gridDim.x - 1)) {
         write_before(b, own_sums, own, own_run);
         if (!a.on_tensor_cores) write_before(a, prefix_sums, prefix, prefix_run);
     }

@@ -1014,8 +1014,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     if constexpr (P::kShared) {
-        // the sequences' own part may begin
-        pdl_launch_dependents();
+        // the sequences' own part may begin, once the last CTA has said on how many SMs this one is
+        if (blockIdx.x != gridDim.x - 1) pdl_launch_dependents();
         sum_items(p, part_sums[0]);
         sum_items(other, part_sums[1]);
     }
@@ -1031,7 +1031,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long all = all_units(p, mine);
             const int sms = share_of(all * p.unit_cost, all_units(other, theirs) * other.unit_cost, p.sms);
             const long long run = run_length(p, all, sms);
-            if (blockIdx.x == gridDim.x - 1) write_before(p, part_sums[0], mine, run);
+            if (blockIdx.x == gridDim.x - 1) {
+                if (warp == 18) {
+                    if (lane == 0) p.totals[1] = sms;
+                    __threadfence();
+                    __syncwarp();
+                    pdl_launch_dependents();
+                }
+                write_before(p, part_sums[0], mine, run);
+            }
             if (warp == 18) walk.start(p, part_sums[0], mine, run, blockIdx.x);
         }
     }
