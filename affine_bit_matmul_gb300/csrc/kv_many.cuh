@@ -28,7 +28,7 @@
 // tile, all of which see the whole prefix; the first SMs take them, by the costs of both parts, and all pieces go to
 // the workspace.  Tiles of up to 128 rows are for both halves, which take alternate units: 2.4 us a unit of
 // 128 tokens then, 2.6 to 3.1 of 256 rows.  256 rows of 32 heads, 8 of 128 values, over 32768 tokens and 512 of
-// their own: 220 us, and 25 for the join.
+// their own: 217 us, and 25 for the join.
 //   4 D flops per visible pair and head: a chunk of 2048 tokens that ends at 8192, 32 query
 // heads of 128 values, takes 285 us, 840 TFLOP/s (score tiles of 128 tokens, one a half:
 // 333 us); a whole prompt of 8192, 642 us.  Bound by the softmax warps' instructions:

@@ -9,7 +9,8 @@
 // n + runner: both numbers never decrease along the units, and one of them grows from piece to
 // piece.  The joining kernel finds a row's pieces from what comes before its item alone.
 //   The parts run beside each other, and what each may have of the GPU goes by their costs, from
-// the lengths, which only the device knows: every CTA works it out by itself.
+// the lengths, which only the device knows: every CTA works it out by itself, but for those beside the tensor
+// cores' kernel, whose last CTA says so before they start.
 #pragma once
 
 #include "kv_attn_common.cuh"
