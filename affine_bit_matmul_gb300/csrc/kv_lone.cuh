@@ -84,17 +84,7 @@ __device__ __forceinline__ void lone_walk(const KvSharedParams& p, LoneRing<SLOT
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
         SharedPiece q;
-        q.count = 0;
-        if (ring.walk.next(p, &q)) {
-            const int rep = p.Hq / p.Hkv, part = q.vh % p.head_parts;
-            q.h = q.vh / p.head_parts;
-            q.heads = min(p.part_heads, rep - part * p.part_heads);
-            q.head0 = q.h * rep + part * p.part_heads;
-            q.flat0 = q.plane * p.tile_rows;
-            q.rows = min(p.tile_rows, q.it.rows * q.heads - q.flat0);
-            // position of the last row, which sees most
-            q.p1 = p.prefix ? q.it.len - 1 : q.it.len - q.it.rows + (q.flat0 + max(q.rows, 1) - 1) / q.heads;
-        }
+        if (!ring.walk.next(p, &q)) q.count = 0;
         ring.pieces[number % kLonePieces] = q;
     }
     __syncwarp();
@@ -183,7 +173,7 @@ template <int D, int SLOTS>
 __device__ __forceinline__ void lone_queries(const KvSharedParams& p, LoneRing<SLOTS>& ring, const SharedPiece& q,
                                              uint32_t to) {
     const int lane = threadIdx.x & 31;
-    if (q.count == 0 || q.rows <= 0) return;
+    if (q.count == 0) return;
     if (lane == 0) mbar_expect_tx(&ring.query, q.rows * D * 2);
     __syncwarp();
     if (lane < q.rows) {
@@ -263,7 +253,7 @@ __device__ __forceinline__ bool lone_run(const KvSharedParams& p, int runner, Lo
         uint32_t v_bound = 0;  // ... whose bf16 bits these are
         float v_up = 0.f;      // 2^7 over that
         if (LN::kQueryShared) __syncwarp();  // (the last piece's have been used)
-        if (LN::kQueryAhead && rows > 0) {
+        if (LN::kQueryAhead) {
             if (!warp_wait_sleep(&ring.query, (uint32_t)queried & 1u, p.wait_budget)) return lone_stop(ring, u, true, queried);
             ++queried;
         }
@@ -337,7 +327,7 @@ __device__ __forceinline__ bool lone_run(const KvSharedParams& p, int runner, Lo
         bool asked = false;  // the next piece's
         if (LN::kQueryAhead) {
             const SharedPiece& q = ring.pieces[(n_piece + 1) % kLonePieces];
-            asked = q.count && q.rows > 0;
+            asked = q.count;
             lone_queries<D>(p, ring, q, smem_u32(raw_rows));
         }
 

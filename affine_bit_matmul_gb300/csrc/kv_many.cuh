@@ -321,7 +321,6 @@ __device__ bool list_pieces(const KvAttnParams& p, Shared<D, G>& sh) {
 // The same for the groups of a call over shared prefixes, by one lane.
 template <int D, int G>
 __device__ bool list_pieces(const KvSharedParams& p, Shared<D, G>& sh, SharedWalk& walk) {
-    const int rep = p.Hq / p.Hkv;
     for (int n = 0;; ++n) {
         const int slot = n % kPieceRing;
         if (!mbar_wait_sleep(&sh.piece_empty[slot], ((uint32_t)(n / kPieceRing) & 1u) ^ 1u, p.wait_budget))
@@ -329,15 +328,14 @@ __device__ bool list_pieces(const KvSharedParams& p, Shared<D, G>& sh, SharedWal
         Piece q{};
         SharedPiece s;
         if (walk.next(p, &s)) {
-            const int h = s.vh / p.head_parts, part = s.vh - h * p.head_parts;
-            q.heads = min(p.part_heads, rep - part * p.part_heads);
-            q.head0 = h * rep + part * p.part_heads;
-            q.flat0 = s.plane * p.tile_rows;
-            q.toks = min(p.tile_rows, s.it.rows * q.heads - q.flat0);
+            q.heads = s.heads;
+            q.head0 = s.head0;
+            q.flat0 = s.flat0;
+            q.toks = s.rows;
             q.row0 = s.it.row0;
-            q.p0 = q.p1 = s.it.len - 1;
+            q.p0 = q.p1 = s.p1;
             q.s = s.item;
-            q.h = h;
+            q.h = s.h;
             q.k0 = s.k0;
             q.count = s.count;
             q.slot = s.tile + blockIdx.x;

@@ -36,12 +36,12 @@ struct Item {
     int bad;         // its arguments are out of range
 };
 
-__device__ __forceinline__ int items_of(const KvSharedParams& p) {
+__host__ __device__ __forceinline__ int items_of(const KvSharedParams& p) {
     return p.prefix ? p.groups_n : p.S;
 }
 
 // Sequences of group g, [*a, *b).
-__device__ __forceinline__ void group_of(const KvGroupParams& p, int g, int* a, int* b) {
+__host__ __device__ __forceinline__ void group_of(const KvGroupParams& p, int g, int* a, int* b) {
     if (p.groups) {
         *a = *(p.groups + g);
         *b = *(p.groups + g + 1);
@@ -53,7 +53,7 @@ __device__ __forceinline__ void group_of(const KvGroupParams& p, int g, int* a, 
 }
 
 // (`prefix`: a group, with its prefix in pages of a table of `width`, or a sequence)
-__device__ __forceinline__ Item item_of(const KvGroupParams& p, int i, bool prefix, int width) {
+__host__ __device__ __forceinline__ Item item_of(const KvGroupParams& p, int i, bool prefix, int width) {
     Item r;
     int a = i, b = i + 1, most = p.max_q, len;
     r.bad = 0;
@@ -88,18 +88,18 @@ __device__ __forceinline__ Item item_of(const KvGroupParams& p, int i, bool pref
     return r;
 }
 
-__device__ __forceinline__ Item item_of(const KvSharedParams& p, int i) {
+__host__ __device__ __forceinline__ Item item_of(const KvSharedParams& p, int i) {
     return item_of(p, i, p.prefix, p.max_pages);
 }
-__device__ __forceinline__ Item item_of(const KvTwoParams& p, int g) {
+__host__ __device__ __forceinline__ Item item_of(const KvTwoParams& p, int g) {
     return item_of(p, g, true, p.max_prefix_pages);
 }
 
-__device__ __forceinline__ int tiles_of(const KvSharedParams& p, const Item& it) {
+__host__ __device__ __forceinline__ int tiles_of(const KvSharedParams& p, const Item& it) {
     return (it.len + (1 << p.tile_shift) - 1) >> p.tile_shift;
 }
 // Units of an item's row tiles for one head: their tiles, and what the end of each costs.
-__device__ __forceinline__ int units_of(const KvSharedParams& p, const Item& it) {
+__host__ __device__ __forceinline__ int units_of(const KvSharedParams& p, const Item& it) {
     return it.planes * (tiles_of(p, it) + p.end_units);
 }
 
@@ -230,8 +230,8 @@ __device__ void write_before(const KvSharedParams& p, const Sums<T>& s, const Sc
 struct SharedPiece {
     int item, vh, plane, k0, count, tile;
     Item it;
-    // by those who need them: its key/value head, query heads, rows and the first of them in the
-    // item, position of the last row
+    // its key/value head, query heads, rows (one at least) and the first of them in the item, position of the last
+    // row, which sees most
     int h, head0, heads, flat0, rows, p1;
 };
 
@@ -240,7 +240,7 @@ struct SharedWalk {
     long long left;
     Item it;
 
-    __device__ void load(const KvSharedParams& p, int item) {
+    __host__ __device__ void load(const KvSharedParams& p, int item) {
         i = item;
         it = item_of(p, i);
         tiles = tiles_of(p, it);
@@ -276,11 +276,17 @@ struct SharedWalk {
         plane = n - vh * it.planes;
         tile += n;
     }
-    __device__ bool next(const KvSharedParams& p, SharedPiece* out) {
+    // An item has the planes that its largest head part fills: where the heads do not divide evenly, the last ones
+    // of a smaller part may have no rows.  They count (units, numbers), but are no pieces.
+    __host__ __device__ bool next(const KvSharedParams& p, SharedPiece* out) {
+        const int rep = p.Hq / p.Hkv;
         while (left > 0) {
             while (it.planes == 0) load(p, i + 1);
             const int all = tiles + p.end_units, n = (int)(left < all - k ? left : all - k);
-            const int here = min(k + n, tiles) - k;  // the others are the row tile's end
+            const int h = vh / p.head_parts, part = vh - h * p.head_parts;
+            const int heads = min(p.part_heads, rep - part * p.part_heads);
+            const int flat0 = plane * p.tile_rows, rows = min(p.tile_rows, it.rows * heads - flat0);
+            const int here = rows > 0 ? min(k + n, tiles) - k : 0;  // the others are the row tile's end
             if (here > 0) {
                 out->item = i;
                 out->vh = vh;
@@ -289,6 +295,12 @@ struct SharedWalk {
                 out->count = here;
                 out->tile = tile;
                 out->it = it;
+                out->h = h;
+                out->head0 = h * rep + part * p.part_heads;
+                out->heads = heads;
+                out->flat0 = flat0;
+                out->rows = rows;
+                out->p1 = it.len - 1 - (p.prefix ? 0 : it.rows - 1 - (flat0 + rows - 1) / heads);
             }
             left -= n;
             k += n;
