@@ -170,7 +170,9 @@ __device__ __forceinline__ void scan_sums(const Sums<T>& s, const Sums<T>& t, Sc
     y.all = __shfl_sync(0xFFFFFFFFu, y.upto, 31);
 }
 
-// Rows of groups that overlap can make more row tiles than there are places for: nothing is done.
+// Rows of groups that overlap can make more row tiles than there are places for: nothing is done, and the joining
+// kernel, which is told by kLeftOut in place of a run's units, writes nothing.
+constexpr long long kLeftOut = -1;
 __device__ __forceinline__ bool too_many(const KvSharedParams& p, const Scan& s) { return s.planes() > p.max_planes; }
 
 __device__ __forceinline__ long long all_units(const KvSharedParams& p, const Scan& s) {
@@ -198,10 +200,12 @@ __device__ __forceinline__ long long run_length(const KvSharedParams& p, long lo
 template <int T>
 __device__ void write_before(const KvSharedParams& p, const Sums<T>& s, const Scan& scan, long long run) {
     const int n = items_of(p), per = (n + T - 1) / T, from = threadIdx.x / (T / 32);
+    const bool left_out = too_many(p, scan);
     if (threadIdx.x == 0) {
-        p.totals[0] = run;
-        if (too_many(p, scan)) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
+        p.totals[0] = left_out ? kLeftOut : run;
+        if (left_out) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
     }
+    if (left_out) return;
     // (every warp holds the whole scan)
     int u = __shfl_sync(0xFFFFFFFFu, scan.units_before(), from);
     int t = __shfl_sync(0xFFFFFFFFu, scan.planes_before(), from);

@@ -439,9 +439,11 @@ size_t mxq_kv_attention_workspace_bytes(int T, int S, int Hq, int Hkv, int D, in
  * Invalid entries as for mxq_kv_attention: pages outside [0, n_pages) are
  * invisible (MXQ_DEV_BAD_PAGE), lengths are clamped, a sequence or group whose
  * rows or sequences are out of range, decrease or exceed the bounds is left out
- * with its rows of out, and the whole call where groups overlap so that their rows
- * are more than T (MXQ_DEV_BAD_SEQUENCE).  The result is deterministic for given
- * arguments.
+ * with its rows of out (MXQ_DEV_BAD_SEQUENCE).  Where group_starts or q_starts
+ * decrease, so that groups or sequences overlap, that may be more of them, up to the
+ * whole call: a row that is written then is that of one of the sequences that have
+ * it, after the prefix of one of the groups that have the sequence.  Otherwise the
+ * result is deterministic for given arguments.
  * Accuracy: that of mxq_kv_attention for few rows in the own tokens and in
  * prefixes of up to 32 rows (times query heads to a key/value head) in a group,
  * at least that for more rows in the other prefixes.  There are no windows: a layer with

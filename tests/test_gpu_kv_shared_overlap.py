@@ -1,0 +1,52 @@
+"""Attention over shared prefixes with starts that decrease: what is written is right, the rest as it was."""
+
+import numpy as np
+import pytest
+
+from tests import test_gpu_kv_shared as shared
+from tests.test_gpu_kv_cache import i32
+from tests.test_gpu_kv_shared import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(params=["as wide as needed", "wide"])
+def width(request):
+    shared.WIDE = 200000 if request.param == "wide" else 0
+    yield request.param
+    shared.WIDE = 0
+
+
+def left_or_right(case, starts, max_group):
+    """The status is set, and every row is untouched or right for a group that has its sequence."""
+    import affine_bit_matmul_gb300 as mxq
+
+    o, lse, st = case.run(q_starts=None, group_starts=i32(starts), max_group=max_group)
+    assert st == mxq.DEV_BAD_SEQUENCE
+    written = ~np.isnan(o).any((1, 2))
+    assert np.isnan(o[~written]).all() and np.isnan(lse[~written]).all() and not np.isnan(lse[written]).any()
+    fits = np.zeros(len(o), dtype=bool)
+    seqs = len(case.own)
+    for g, (a, b) in enumerate(zip(starts[:-1], starts[1:])):
+        if not 0 <= a <= b <= seqs or b - a > max_group:
+            continue
+        # all sequences after this group's prefix
+        case.groups = np.asarray([0] * (g + 1) + [seqs] * (len(starts) - 1 - g), dtype=np.int32)
+        ref, ref_lse, tol, lse_tol = case.exact(128 ** -0.5)
+        with np.errstate(invalid="ignore"):
+            same = (np.abs(o - ref) <= tol).all((1, 2)) & (np.abs(lse - ref_lse) <= lse_tol).all(1)
+        fits[a:b] |= same[a:b]
+    assert (written <= fits).all(), "rows %s" % np.flatnonzero(written & ~fits)
+    return written
+
+
+@pytest.mark.parametrize("seqs", [3, 7, 300])
+def test_groups_that_overlap(width, seqs):
+    # the second and fourth group decrease; the others are all sequences, or those but one
+    case = Case([70, 40, 90, 20, 130], [seqs, 0, 0, 0, 0], [20] * seqs, [1] * seqs, 8, 2, 128, 64, 32, seed=seqs)
+    left_or_right(case, [0, seqs, 0, seqs, 1, seqs], seqs)
+
+
+def test_a_group_that_decreases_leaves_the_others(width):
+    case = Case([70, 40, 90], [4, 3, 3], [20] * 10, [1] * 10, 8, 2, 128, 64, 32, seed=5)
+    assert left_or_right(case, [0, 7, 4, 10], 7)[:4].all()
