@@ -100,7 +100,9 @@ bool countable(const AttnPlan& a, int S, int Hkv, long long tokens) {
 struct SharedPart {
     int head_parts, part_heads, tile_rows, tensor_cores;
     long long runners;
-    long long planes, most_planes;  // row tiles of one head: with rows that do not overlap, at all
+    // row tiles of one head: those that there are places for, as many as items can have between them whose rows do
+    // not overlap; and with starts that decrease, so that they do
+    long long planes, most_planes;
     size_t before_bytes, bytes;
 };
 
@@ -113,7 +115,6 @@ SharedPart shared_part(long long items, long long rows, int rep, int sms) {
     a.tensor_cores = 0;
     a.runners = 16LL * sms;  // warps
     a.most_planes = items * ((all + a.tile_rows - 1) / a.tile_rows);
-    a.planes = a.most_planes;
     return a;
 }
 
@@ -145,12 +146,12 @@ SharedPlan plan_shared(int T, int S, int N, int Hq, int Hkv, int D, int max_q, i
         p.tile_rows = 16;  // (there is no kernel of 8 rows beside 4)
         p.most_planes = N * ((rows * p.part_heads + 15) / 16);
     }
-    // the groups have all rows between them
-    p.planes = (long long)T * p.part_heads / p.tile_rows + N;
-    if (p.planes > p.most_planes) p.planes = p.most_planes;
     a.bytes = 0;
     for (SharedPart* x : {&a.prefix, &a.own}) {
-        x->before_bytes = align_up((size_t)(x == &a.own ? S : N) * mxq::kv_shared_before_bytes(), 256) + 256;
+        const int items = x == &a.own ? S : N;
+        x->planes = (long long)T * x->part_heads / x->tile_rows + items;
+        if (x->planes > x->most_planes) x->planes = x->most_planes;
+        x->before_bytes = align_up((size_t)items * mxq::kv_shared_before_bytes(), 256) + 256;
         const size_t places = (size_t)x->planes * Hkv * x->head_parts + x->runners;
         x->bytes = x->before_bytes + align_up(places * x->tile_rows * (D + 2) * sizeof(float), 256);
         a.bytes += x->bytes;
@@ -158,12 +159,13 @@ SharedPlan plan_shared(int T, int S, int N, int Hq, int Hkv, int D, int max_q, i
     return a;
 }
 
-// As for AttnPlan: units of one head and of a run, places, and the rows times query heads fit 32 bits.
+// As for AttnPlan: units of one head and of a run, places, and the rows times query heads fit 32 bits, for rows that do
+// not overlap; and the row tiles that a block's threads count where they do, each one more than there are places at most.
 bool countable(const SharedPart& a, int T, int Hkv, long long tokens) {
     constexpr long long kMost = (1LL << 30) - 64;
     const long long units = tokens / (a.tensor_cores ? 128 : 16) + 32, vheads = (long long)Hkv * a.head_parts;
-    return a.most_planes <= kMost / units && a.most_planes <= kMost / vheads - a.runners &&
-           (long long)T * a.part_heads <= kMost;
+    return a.planes <= kMost / units && a.planes <= kMost / vheads - a.runners && (long long)T * a.part_heads <= kMost &&
+           (a.most_planes <= 2 * kMost || a.planes < 2 * kMost / mxq::kKvListThreads);
 }
 
 // Calls over shared prefixes in which each sequence may go over its prefix for itself, in one kernel

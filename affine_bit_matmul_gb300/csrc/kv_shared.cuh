@@ -121,19 +121,24 @@ struct Sums {
     int units[T], planes[T];
 };
 
+// Starts that decrease let items overlap: their row tiles may then be any number.  A thread's count stops at one more
+// than there are places for, so that the sum of all, at most kKvListThreads times that (countable), tells; the units,
+// which may have lost their highest bits, are not used then.
 template <int T>
 __device__ __forceinline__ void sum_items(const KvSharedParams& p, Sums<T>& s) {
+    static_assert(T <= kKvListThreads);
     const int n = items_of(p), per = (n + T - 1) / T;
-    int units = 0, planes = 0;
+    unsigned units = 0;
+    long long planes = 0;
 #pragma unroll 4
     for (int i = threadIdx.x * per; i < min(((int)threadIdx.x + 1) * per, n); ++i) {
         const Item it = item_of(p, i);
-        units += units_of(p, it);
+        units += (unsigned)units_of(p, it);
         planes += it.planes;
         if (it.bad && blockIdx.x == 0) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
     }
-    s.units[threadIdx.x] = units;
-    s.planes[threadIdx.x] = planes;
+    s.units[threadIdx.x] = (int)units;
+    s.planes[threadIdx.x] = (int)min(planes, p.max_planes + 1LL);
 }
 
 // The same for a warp, each lane with T / 32 threads' items: up to and with its own, and all.  Units in the
@@ -170,8 +175,8 @@ __device__ __forceinline__ void scan_sums(const Sums<T>& s, const Sums<T>& t, Sc
     y.all = __shfl_sync(0xFFFFFFFFu, y.upto, 31);
 }
 
-// Rows of groups that overlap can make more row tiles than there are places for: nothing is done, and the joining
-// kernel, which is told by kLeftOut in place of a run's units, writes nothing.
+// Items that overlap can make more row tiles than there are places for: nothing is done, and the joining kernel, which
+// is told by kLeftOut in place of a run's units, writes nothing.
 constexpr long long kLeftOut = -1;
 __device__ __forceinline__ bool too_many(const KvSharedParams& p, const Scan& s) { return s.planes() > p.max_planes; }
 

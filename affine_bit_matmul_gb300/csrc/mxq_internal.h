@@ -250,6 +250,7 @@ struct KvSharedParams : KvGroupParams {
     int on_tensor_cores, sms;    // the prefixes' part: by that kernel; SMs of the device
 };
 size_t kv_shared_before_bytes();
+constexpr int kKvListThreads = 608;  // the most threads of a block that adds up a part's items
 
 // The kernels' choice of tile_shift ... least_run for a part.
 void kv_shared_shape(KvSharedParams& p, int D);

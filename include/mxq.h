@@ -441,8 +441,8 @@ size_t mxq_kv_attention_workspace_bytes(int T, int S, int Hq, int Hkv, int D, in
  * rows or sequences are out of range, decrease or exceed the bounds is left out
  * with its rows of out (MXQ_DEV_BAD_SEQUENCE).  Where group_starts or q_starts
  * decrease, so that groups or sequences overlap, that may be more of them, up to the
- * whole call: a row that is written then is that of one of the sequences that have
- * it, after the prefix of one of the groups that have the sequence.  Otherwise the
+ * whole call: a value that is written then is that of one of the sequences that have
+ * its row, after the prefix of one of the groups that have the sequence.  Otherwise the
  * result is deterministic for given arguments.
  * Accuracy: that of mxq_kv_attention for few rows in the own tokens and in
  * prefixes of up to 32 rows (times query heads to a key/value head) in a group,

@@ -50,3 +50,22 @@ def test_groups_that_overlap(width, seqs):
 def test_a_group_that_decreases_leaves_the_others(width):
     case = Case([70, 40, 90], [4, 3, 3], [20] * 10, [1] * 10, 8, 2, 128, 64, 32, seed=5)
     assert left_or_right(case, [0, 7, 4, 10], 7)[:4].all()
+
+
+def test_sequences_that_overlap(width):
+    import affine_bit_matmul_gb300 as mxq
+
+    case = Case([70], [9], [60] * 9, [40] + [0] * 8, 8, 2, 128, 64, 32, seed=6)
+    # five sequences of 40 rows: more row tiles than 40 rows can have
+    o, lse, st = case.run(q_starts=i32([0, 40, 0, 40, 0, 40, 0, 40, 0, 40]), max_q_len=40)
+    assert st == mxq.DEV_BAD_SEQUENCE and np.isnan(o).all() and np.isnan(lse).all()
+    # one that decreases, with its rows in the next one only
+    o, lse, st = case.run(q_starts=i32([0, 30, 20, 40, 40, 40, 40, 40, 40, 40]), max_q_len=40)
+    assert st == mxq.DEV_BAD_SEQUENCE
+
+
+def test_one_long_sequence_among_short_ones(width):
+    rows = [1] * 40
+    rows[17] = 300
+    case = Case([100, 40], [25, 15], [max(r, 5 + i) for i, r in enumerate(rows)], rows, 8, 2, 128, 64, 32, seed=7)
+    case.check()

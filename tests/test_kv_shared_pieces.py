@@ -48,6 +48,7 @@ static int walk(bool prefix, int rep, int most, int tile_rows, const std::vector
         units += units_of(p, item_of(p, i));
         planes += item_of(p, i).planes;
     }
+    if (planes > (long long)p.T * p.part_heads / tile_rows + items) return wrong("more row tiles than places", p, rep, items, 0, 0);
     SharedWalk w{};
     w.load(p, 0);
     w.left = units * vheads;
