@@ -84,7 +84,7 @@ __device__ __forceinline__ void lone_walk(const KvSharedParams& p, LoneRing<SLOT
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
         SharedPiece q;
-        if (!ring.walk.next(p, &q)) q.count = 0;
+        if (ring.walk.next(p, &q)) find_rows(p, q);
         ring.pieces[number % kLonePieces] = q;
     }
     __syncwarp();

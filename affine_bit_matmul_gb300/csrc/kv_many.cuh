@@ -345,6 +345,7 @@ __device__ bool list_pieces(const KvSharedParams& p, Shared<D, G>& sh, SharedWal
         Piece q{};
         SharedPiece s;
         if (walk.next(p, &s)) {
+            find_rows(p, s);
             q.heads = s.heads;
             q.head0 = s.head0;
             q.flat0 = s.flat0;

@@ -175,9 +175,8 @@ __device__ __forceinline__ void scan_sums(const Sums<T>& s, const Sums<T>& t, Sc
     y.all = __shfl_sync(0xFFFFFFFFu, y.upto, 31);
 }
 
-// Items that overlap can make more row tiles than there are places for: nothing is done, and the joining kernel, which
-// is told by kLeftOut in place of a run's units, writes nothing.
-constexpr long long kLeftOut = -1;
+// Items that overlap can make more row tiles than there are places for: nothing is done, and the joining kernel finds
+// all items without rows.
 __device__ __forceinline__ bool too_many(const KvSharedParams& p, const Scan& s) { return s.planes() > p.max_planes; }
 
 __device__ __forceinline__ long long all_units(const KvSharedParams& p, const Scan& s) {
@@ -207,10 +206,9 @@ __device__ void write_before(const KvSharedParams& p, const Sums<T>& s, const Sc
     const int n = items_of(p), per = (n + T - 1) / T, from = threadIdx.x / (T / 32);
     const bool left_out = too_many(p, scan);
     if (threadIdx.x == 0) {
-        p.totals[0] = left_out ? kLeftOut : run;
+        p.totals[0] = run;
         if (left_out) flag_status(p.status, MXQ_DEV_BAD_SEQUENCE);
     }
-    if (left_out) return;
     // (every warp holds the whole scan)
     int u = __shfl_sync(0xFFFFFFFFu, scan.units_before(), from);
     int t = __shfl_sync(0xFFFFFFFFu, scan.planes_before(), from);
@@ -224,9 +222,9 @@ __device__ void write_before(const KvSharedParams& p, const Sums<T>& s, const Sc
         b.units = u;
         b.planes = t;
         b.row0 = it.row0;
-        b.rows = it.rows;
+        b.rows = left_out ? 0 : it.rows;
         b.len = it.len;
-        b.item_planes = it.planes;
+        b.item_planes = left_out ? 0 : it.planes;
         b.group = p.prefix ? i : group_with(p, i);
         b.pad = 0;
         p.before[i] = b;
@@ -239,10 +237,26 @@ __device__ void write_before(const KvSharedParams& p, const Sums<T>& s, const Sc
 struct SharedPiece {
     int item, vh, plane, k0, count, tile;
     Item it;
-    // its key/value head, query heads, rows (one at least) and the first of them in the item, position of the last
-    // row, which sees most
+    // find_rows: its key/value head, query heads, rows (one at least) and the first of them in the item, position of
+    // the last row, which sees most
     int h, head0, heads, flat0, rows, p1;
 };
+
+// The query heads of head part vh.
+__host__ __device__ __forceinline__ int heads_of(const KvSharedParams& p, int vh) {
+    return min(p.part_heads, p.Hq / p.Hkv - vh % p.head_parts * p.part_heads);
+}
+
+// What follows from a piece's numbers.
+__host__ __device__ __forceinline__ void find_rows(const KvSharedParams& p, SharedPiece& q) {
+    const int rep = p.Hq / p.Hkv, part = q.vh % p.head_parts;
+    q.h = q.vh / p.head_parts;
+    q.heads = heads_of(p, q.vh);
+    q.head0 = q.h * rep + part * p.part_heads;
+    q.flat0 = q.plane * p.tile_rows;
+    q.rows = min(p.tile_rows, q.it.rows * q.heads - q.flat0);
+    q.p1 = p.prefix ? q.it.len - 1 : q.it.len - q.it.rows + (q.flat0 + q.rows - 1) / q.heads;
+}
 
 struct SharedWalk {
     int i, vh, plane, k, tile, tiles;
@@ -286,16 +300,13 @@ struct SharedWalk {
         tile += n;
     }
     // An item has the planes that its largest head part fills: where the heads do not divide evenly, the last ones
-    // of a smaller part may have no rows.  They count (units, numbers), but are no pieces.
+    // of a smaller part may have no rows.  They count (units, numbers), but are no pieces.  False, and a count of 0, when
+    // the run is over.
     __host__ __device__ bool next(const KvSharedParams& p, SharedPiece* out) {
-        const int rep = p.Hq / p.Hkv;
         while (left > 0) {
             while (it.planes == 0) load(p, i + 1);
             const int all = tiles + p.end_units, n = (int)(left < all - k ? left : all - k);
-            const int h = vh / p.head_parts, part = vh - h * p.head_parts;
-            const int heads = min(p.part_heads, rep - part * p.part_heads);
-            const int flat0 = plane * p.tile_rows, rows = min(p.tile_rows, it.rows * heads - flat0);
-            const int here = rows > 0 ? min(k + n, tiles) - k : 0;  // the others are the row tile's end
+            const int here = min(k + n, tiles) - k;  // the others are the row tile's end
             if (here > 0) {
                 out->item = i;
                 out->vh = vh;
@@ -304,12 +315,6 @@ struct SharedWalk {
                 out->count = here;
                 out->tile = tile;
                 out->it = it;
-                out->h = h;
-                out->head0 = h * rep + part * p.part_heads;
-                out->heads = heads;
-                out->flat0 = flat0;
-                out->rows = rows;
-                out->p1 = it.len - 1 - (p.prefix ? 0 : it.rows - 1 - (flat0 + rows - 1) / heads);
             }
             left -= n;
             k += n;
@@ -324,8 +329,9 @@ struct SharedWalk {
                     }
                 }
             }
-            if (here > 0) return true;
+            if (here > 0 && out->plane * p.tile_rows < out->it.rows * heads_of(p, out->vh)) return true;
         }
+        out->count = 0;
         return false;
     }
 };

@@ -85,7 +85,6 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(const __grid_consta
     pdl_wait();
     if (head >= b.Hq) return;
     const long long prefix_run = __ldcg(a.totals), own_run = __ldcg(b.totals);
-    if (prefix_run == kLeftOut || own_run == kLeftOut) return;
     const Before own = before_of(b, s);
     // (without a list of groups this does not wait for `own`)
     const int g = a.groups ? own.group : s / (a.S / a.groups_n);

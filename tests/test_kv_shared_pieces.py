@@ -57,6 +57,7 @@ static int walk(bool prefix, int rep, int most, int tile_rows, const std::vector
     std::vector<char> taken((size_t)(planes * vheads), 0);
     SharedPiece q;
     while (w.next(p, &q)) {
+        find_rows(p, q);
         if (q.rows <= 0 || q.count <= 0) return wrong("no rows", p, rep, q.item, q.plane, q.vh);
         if (q.p1 >= q.it.len) return wrong("a position past the tokens", p, rep, q.item, q.plane, q.vh);
         if (q.tile < 0 || q.tile >= planes * vheads || taken[q.tile]) return wrong("a place twice", p, rep, q.item, q.plane, q.vh);
@@ -70,6 +71,7 @@ static int walk(bool prefix, int rep, int most, int tile_rows, const std::vector
             if (last > q.p1) return wrong("a row that sees more", p, rep, q.item, q.plane, q.vh);
         }
     }
+    if (q.count) return wrong("a piece after the last", p, rep, items, 0, 0);
     for (int i = 0; i < items; ++i) {
         const Item it = item_of(p, i);
         for (int r = it.row0; r < it.row0 + it.rows; ++r)
