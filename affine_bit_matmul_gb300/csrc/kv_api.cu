@@ -1,4 +1,5 @@
 // C ABI of the key/value cache operators: argument checks, planning, launches.
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <cuda_runtime.h>
@@ -537,6 +538,9 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
         x.partial = reinterpret_cast<float*>(ws + each.seg_bytes);
         return mxq::launch_kv_two(x, D, group_size, each.tile_rows, s) == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA;
     }
+    // spread over all bits, so that what lies in a workspace is no call's
+    static std::atomic<uint64_t> calls{0};
+    const uint64_t call = (++calls * 0x9E3779B97F4A7C15u) & ~255ull;
     mxq::KvSharedParams p[2] = {};
     for (int i = 0; i < 2; ++i) {
         mxq::KvSharedParams& x = p[i];
@@ -555,6 +559,7 @@ mxq_status mxq_kv_attention_shared(const void* q, long long q_row_stride, long l
         x.sms = sms < kMaxSms ? sms : kMaxSms;
         mxq::kv_shared_shape(x, D);
         x.totals = reinterpret_cast<long long*>(ws);
+        x.call = call;
         x.before = reinterpret_cast<mxq::Before*>(ws + 256);
         x.partial = reinterpret_cast<float*>(ws + part.before_bytes);
         ws += part.bytes;

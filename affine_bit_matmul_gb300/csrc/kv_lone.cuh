@@ -564,24 +564,27 @@ __global__ void __launch_bounds__(kLoneThreads, (LoneBoth<D, G, KT1, KT2>::kCtas
         mbar_init(&rings[threadIdx.x].query, 1);
         mbar_init_fence();
     }
-    // The tensor cores' kernel has waited for what comes before the call, and is not waited for here;
-    // nothing that L1 may hold from then is read.
-    if (a.on_tensor_cores) __threadfence();
-    else pdl_wait();
-    pdl_launch_dependents();
+    // The tensor cores' kernel has waited for what comes before the call, and is not waited for here: what is read
+    // comes behind its word.
+    if (!a.on_tensor_cores) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     // Runners of the two parts.  Beside the other kernel they are the first CTAs, which are on the SMs
     // that it leaves; else consecutive ones are on different SMs.
     const int all = gridDim.x * kLoneWarps;
     int first = 0, second = all;
     if (a.on_tensor_cores) {
         // the SMs that the other kernel leaves; it needs them all for itself if there is nothing else
-        const int sms = (int)__ldcg(a.totals + 1);
+        const int sms = said_sms(a);
+        pdl_launch_dependents();
         if (sms < a.sms) second = (int)((long long)all * (a.sms - sms) / a.sms);
         if ((int)blockIdx.x * kLoneWarps >= second) {
             // (a CTA that begins when the other kernel ends, with 3 us of lists before it would find nothing to do)
             pdl_wait();
             return;
         }
+        heard();
     }
     if (!a.on_tensor_cores) sum_items(a, prefix_sums);
     else prefix_sums.units[threadIdx.x] = prefix_sums.planes[threadIdx.x] = 0;

@@ -1044,8 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long run = run_length(p, all, sms);
             if (blockIdx.x == gridDim.x - 1) {
                 if (warp == 18) {
-                    if (lane == 0) p.totals[1] = sms;
-                    __threadfence();
+                    if (lane == 0) say_sms(p, sms);
                     __syncwarp();
                     pdl_launch_dependents();
                 }

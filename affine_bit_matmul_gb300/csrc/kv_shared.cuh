@@ -183,6 +183,25 @@ __device__ __forceinline__ long long all_units(const KvSharedParams& p, const Sc
     return too_many(p, s) ? 0 : (long long)s.units() * (p.Hkv * p.head_parts);
 }
 
+// On how many SMs the tensor cores' part is: said by one thread of that kernel with the call's number (SMs are
+// fewer than 256), in one word, so that who finds the number has the SMs, and with a fence (heard) all that was there when
+// they were said, the call's arguments among it.  The joining kernel takes the word back: a graph's next replay has
+// the same number.
+__device__ __forceinline__ void say_sms(const KvSharedParams& p, int sms) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.totals + 1), "l"(p.call | (unsigned)sms) : "memory");
+}
+// The same, read in the kernel beside it; where the number is another's, once that kernel is over.
+__device__ __forceinline__ int said_sms(const KvSharedParams& p) {
+    unsigned long long x;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(p.totals + 1) : "memory");
+    if ((x ^ p.call) >> 8) {
+        pdl_wait();
+        x = (unsigned long long)__ldcg(p.totals + 1);
+    }
+    return (int)(x & 255u);
+}
+__device__ __forceinline__ void heard() { __threadfence(); }
+
 // How many of `all` runners (or SMs) the first of two parts gets, by their costs.
 __device__ __forceinline__ int share_of(long long cost1, long long cost2, int all) {
     if (cost1 == 0) return 0;

@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(256) kv_shared_join_kernel(const __grid_consta
     const int lane = threadIdx.x & 31, s = blockIdx.x;
     const int head = blockIdx.y * 8 + threadIdx.x / 32;
     pdl_wait();
+    if (s == 0 && head == 0 && blockIdx.z == 0) a.totals[1] = 0;  // (see say_sms)
     if (head >= b.Hq) return;
     const long long prefix_run = __ldcg(a.totals), own_run = __ldcg(b.totals);
     const Before own = before_of(b, s);

@@ -244,7 +244,8 @@ struct KvSharedParams : KvGroupParams {
     static constexpr bool kShared = true;
     int max_planes;              // row tiles of one head for which `partial` has places
     struct Before* before;       // workspace: what the joining kernel needs of each item
-    long long* totals;           // workspace: units of a run; SMs of the tensor cores' part
+    long long* totals;           // workspace: units of a run; SMs of the tensor cores' part, with `call`
+    unsigned long long call;     // a number that no other call has, a multiple of 256
     int tile_shift, end_units;   // log2 of a tile's tokens; what the end of a row tile costs, in units
     int unit_cost, least_run;    // of a unit, beside the other part's; units of a run, at least
     int on_tensor_cores, sms;    // the prefixes' part: by that kernel; SMs of the device
