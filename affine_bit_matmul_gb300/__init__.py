@@ -1012,9 +1012,8 @@ def kv_attention_shared_workspace_bytes(rows: int, seqs: int, groups: int, heads
                                         head_dim: int, max_q_len: int = 1, max_group=None) -> int:
     """Workspace bytes for kv_attention_shared of ``rows`` query rows in ``seqs`` sequences and
     ``groups`` groups of at most ``max_group`` sequences (default: all of them)."""
-    return int(lib().mxq_kv_attention_shared_workspace_bytes(
-        rows, seqs, groups, heads, kv_heads, head_dim, _int32(max_q_len),
-        max(seqs, 1) if max_group is None else _int32(max_group)))
+    return int(lib().mxq_kv_attention_shared_workspace_bytes(*map(_int32, (
+        rows, seqs, groups, heads, kv_heads, head_dim, max_q_len, max(seqs, 1) if max_group is None else max_group))))
 
 
 def kv_attention_shared(q, pages, prefix_table, prefix_lens, page_table, ctx_lens, group_starts=None,
@@ -1093,6 +1092,7 @@ def kv_attention_shared(q, pages, prefix_table, prefix_lens, page_table, ctx_len
     if max_q_len <= 0 or max_group <= 0:
         raise ValueError("max_q_len and max_group must be positive")
     max_q_len, max_group = _int32(max_q_len), _int32(max_group)
+    S, N, max_prefix_pages, max_pages = map(_int32, (S, N, max_prefix_pages, max_pages))
     L = lib()
     if workspace is None:
         need = L.mxq_kv_attention_shared_workspace_bytes(T, S, N, Hq, Hkv, D, max_q_len, max_group)
@@ -1173,6 +1173,8 @@ def beam_select(logits, scores, k=None, done=None, end_token: int = 0, scores_ou
     if done is not None:
         done_out_at = outs[3].data_ptr()
     fp32 = 1 if logits.dtype is torch.float32 else 0
+    N, V = _int32(N), _int32(V)
+    end = _int32(end_token) if done is not None else 0
     L = lib()
     if workspace is None:
         workspace = _empty((L.mxq_beam_select_workspace_bytes(N, W, V, k, fp32),), torch.uint8, dev, stream)
@@ -1181,7 +1183,7 @@ def beam_select(logits, scores, k=None, done=None, end_token: int = 0, scores_ou
     with ctx:
         _check(L.mxq_beam_select(logits.data_ptr(), row, fp32, scores_at, done_at, outs[0].data_ptr(),
                                  outs[1].data_ptr(), outs[2].data_ptr(), done_out_at, N, W, V, k,
-                                 end_token if done is not None else 0, ws_at, workspace.numel(), st),
+                                 end, ws_at, workspace.numel(), st),
                "mxq_beam_select")
     return tuple(outs)
 
@@ -1233,6 +1235,7 @@ def kv_reorder(pages, page_table, home_table, ctx_lens, parents, head_dim: int, 
     if tuple(table_out.shape) != (S, max_pages) or lens_out.numel() != S:
         raise ValueError("table_out must be [S, max_pages] and lens_out have S entries")
     status = None if dev_status is None else _flat(dev_status, "dev_status", torch.int32, on)
+    S, max_pages, layers = map(_int32, (S, max_pages, layers))
     L = lib()
     if workspace is None:
         workspace = _empty((L.mxq_kv_reorder_workspace_bytes(S),), torch.uint8, dev, stream)

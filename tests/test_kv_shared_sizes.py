@@ -40,3 +40,14 @@ def test_calls_that_cannot_be_counted_are_refused(L):
     # 2^22 row tiles of 2^10 tiles of tokens; row tiles of sequences that may overlap
     assert attend(L, 1 << 22, 1 << 22, 1, 4, 1, 64, 1 << 10, 4, 1 << 22) == 3
     assert attend(L, 1 << 24, 1 << 22, 1, 4, 1, 64, 1, 1 << 20, 1) == 3
+
+
+def test_sizes_past_32_bits_are_not_taken_for_their_lowest_bits(L):
+    import affine_bit_matmul_gb300 as mxq
+
+    small = mxq.kv_attention_shared_workspace_bytes(4, 4, 2, 8, 2, 128, 1, 2)
+    assert mxq.kv_attention_shared_workspace_bytes(4, 2 ** 32 + 4, 2, 8, 2, 128, 1, 2) > small
+    assert mxq.kv_attention_shared_workspace_bytes(2 ** 32 + 4, 4, 2, 8, 2, 128, 2 ** 33, 2) > small
+    for bad in ((4, 4, 2 ** 32, 8, 2, 128), (4, 4, 2, 8, 2 ** 32 + 2, 128), (4, 4, 2, 8 - 2 ** 32, 2, 128)):
+        assert mxq.kv_attention_shared_workspace_bytes(*bad, 1, 2) == (0 if bad[2] == 2 else mxq.kv_attention_shared_workspace_bytes(
+            4, 4, 2 ** 31 - 1, 8, 2, 128, 1, 2))
