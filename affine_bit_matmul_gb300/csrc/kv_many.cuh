@@ -108,23 +108,6 @@ __device__ __forceinline__ bool is_narrow(const Piece& q) {
     return P::kShared && Shape<D, G>::MT == 2 && q.toks <= 128;
 }
 
-// What half m of a piece's row tile has, for all of the half's warps: tokens (rows of a shared prefix), and the
-// first of its units and their distance.  It has no part in the piece where it has no rows or units.
-struct Half {
-    int toks, k_first, k_step;
-    bool idle;
-};
-template <int D, int G, class P>
-__device__ __forceinline__ Half half_of(const P& p, const Piece& q, int m) {
-    const bool narrow = is_narrow<D, G, P>(q);
-    Half h;
-    h.toks = P::kShared ? min(128, narrow ? q.toks : q.toks - m * 128) : min(p.half_toks, q.toks - m * p.half_toks);
-    h.k_first = narrow ? m : 0;
-    h.k_step = narrow ? 2 : 1;
-    h.idle = h.toks <= 0 || h.k_first >= q.count;
-    return h;
-}
-
 // Waits for this thread's tensor-memory loads; the registers named are not used
 // before.
 __device__ __forceinline__ void tmem_ld_wait_of(uint32_t (&r)[16]) {
@@ -584,8 +567,7 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
         if (count == 0) return true;
         // the units of this half: all of them, or every other one
         const bool narrow = is_narrow<D, G, P>(*q);
-        const Half half = half_of<D, G, P>(p, *q, m);
-        const int k_first = half.k_first, k_step = half.k_step;
+        const int k_first = narrow ? m : 0, k_step = narrow ? 2 : 1;
         // lets unit k's keys or values go without using them
         auto leave = [&](int k, uint64_t* full, uint64_t* empty) {
             const int j = jt + k, buf = j % KB;
@@ -595,7 +577,8 @@ __device__ bool issue_products(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint
         };
         auto leave_keys = [&](int k) { return leave(k, sh.k_full, sh.k_empty); };
         auto leave_values = [&](int k) { return leave(k, sh.v_full, sh.v_empty); };
-        if (half.idle) {
+        if (narrow ? k_first >= count : q->toks <= m * (P::kShared ? 128 : p.half_toks)) {
+            // no rows in this half
             for (int k = 0; k < count; ++k)
                 if (!leave_keys(k) || !leave_values(k)) return false;
             jt += count;
@@ -684,17 +667,22 @@ __device__ bool softmax(const P& p, Shared<D, G>& sh, uint32_t qbuf, uint32_t tm
         const int heads = q->heads, tok0 = P::kShared ? 0 : m * p.half_toks;
         const bool narrow = is_narrow<D, G, P>(*q);
         const int half0 = P::kShared && !narrow ? m * 128 : 0;  // first row of a shared prefix's half
-        const Half half = half_of<D, G, P>(p, *q, m);
-        const int toks = half.toks, k_first = half.k_first, k_step = half.k_step;
+        const int k_first = narrow ? m : 0, k_step = narrow ? 2 : 1;
+        const int toks = P::kShared ? q->toks - half0 : min(p.half_toks, q->toks - tok0);
+        if (toks <= 0) {
+            jt += count;
+            list.done();
+            continue;
+        }
         // the half's rows, and where they begin among the sequence's or group's
-        const int rows = P::kShared ? toks : toks * heads;
+        const int rows = P::kShared ? min(128, toks) : toks * heads;
         const int flat0 = P::kShared ? q->flat0 + half0 : 0;
         const bool in = lr < rows;
         const int tok = in ? (flat0 + lr) / heads : 0, hh = in ? (flat0 + lr) % heads : 0;
         const int row = q->row0 + tok0 + tok;
-        if (half.idle) {
-            // without a unit for its rows it still has a place among the results
-            if (narrow && in)
+        if (narrow && k_first >= count) {
+            // this half has no unit
+            if (in)
                 *reinterpret_cast<float2*>(p.partial + (long long)q->slot * SH::kPartialFloats + 2 * (m * 128 + lr)) =
                     make_float2(-INFINITY, 0.f);
             jt += count;
