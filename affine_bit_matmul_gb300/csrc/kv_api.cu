@@ -174,7 +174,7 @@ bool countable(const SharedPart& a, int T, int Hkv, long long tokens) {
 // tile and token of 128 values takes 30, 35 and 53 ps of the whole GPU for 4, 8 and 16 rows (32
 // sequences of 8192 tokens, 8 heads: 62, 73, 111 us), on the tensor cores 123 for a tile of up to 128
 // rows and 160 above.  What the calls take beside it: 8, and 22 in two parts with their joining.  The
-// lengths are not known here, only how many pages they may be in.  4 sequences after 573 tokens: 7.9 us, in
+// lengths are not known here, only how many pages they may be in.  4 sequences after 573 tokens: 8.2 us, in
 // two parts 21.8.
 bool each_for_itself(const AttnPlan& each, const SharedPlan& a, int S, int N, int Hkv, int D, int max_q,
                      int max_group, const long long (&tokens)[2]) {

@@ -8,8 +8,8 @@
 // piece of a row tile leaves its (largest score, sum, weighted sum) in the workspace as it is.  No warp
 // waits for another, and nothing is shared but the list of items.  Where contexts are short, the ends of
 // row tiles are most of the work, and they cost a few stores here.
-//   16 groups of 8 sequences, 32 query heads over 8 of 128 values, 2048 + 256 tokens (51 MB of cache): 53.7 us of
-// 58 for the call.  Bound by instructions, 18.7 million of its warps at 1.35 a cycle and SM: 38% of a warp's time
+//   16 groups of 8 sequences, 32 query heads over 8 of 128 values, 2048 + 256 tokens (51 MB of cache): some 53 us of
+// 57 for the call.  Bound by instructions, 18.7 million of its warps at 1.35 a cycle and SM: 38% of a warp's time
 // goes by without the next one having been fetched, since the warps of an SM are at different places of loops that
 // are longer than the nearest caches.  12 us are the start (lists, pieces, page numbers, queries, first tiles).
 #pragma once
