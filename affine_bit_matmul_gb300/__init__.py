@@ -1029,7 +1029,11 @@ def kv_attention_shared(q, pages, prefix_table, prefix_lens, page_table, ctx_len
     query rows ``q_starts[i]:q_starts[i+1]`` (int32 [S+1], at most ``max_q_len`` each; None: one
     row per sequence) are the last of them: row j of n sees the whole prefix and the own tokens up
     to ``ctx_lens[i] - n + j``.  ``scale`` defaults to D^-1/2.  ``lse`` (fp32 [T, heads]) receives
-    the log sum exp.  Returns out bf16 [T, heads, D]; a row that sees nothing is 0."""
+    the log sum exp.  Returns out bf16 [T, heads, D]; a row that sees nothing is 0.
+
+    Where groups have more than 32 rows (times query heads to a key/value head), by ``max_group`` and
+    ``max_q_len``, the prefix's keys, values and weights may be rounded to 11 bits, as kv_attention does for
+    prompts; else keys are as the cache holds them, and weights times value scales have 11 bits."""
     if stream is None:
         done = _direct().kv_attention_shared(q, pages, prefix_table, prefix_lens, page_table, ctx_lens, group_starts,
                                              q_starts, max_q_len, max_group, group_size, scale, out, lse, workspace,
