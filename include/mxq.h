@@ -435,7 +435,8 @@ size_t mxq_kv_attention_workspace_bytes(int T, int S, int Hq, int Hkv, int D, in
  *   max_q_len, max_group: the most rows of a sequence and the most sequences of
  *   a group, host-side bounds
  * These bounds and the widths of the page tables decide how: a group's prefix for all of its
- * rows, or, where that takes no longer, for each sequence by itself.
+ * rows, or, where that takes no longer, for each sequence by itself.  Sequences with some tens of
+ * rows of their own, or more, are faster by mxq_kv_attention over tables that name the prefix's pages.
  * Invalid entries as for mxq_kv_attention: pages outside [0, n_pages) are
  * invisible (MXQ_DEV_BAD_PAGE), lengths are clamped, a sequence or group whose
  * rows or sequences are out of range, decrease or exceed the bounds is left out
