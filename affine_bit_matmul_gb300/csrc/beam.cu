@@ -12,7 +12,7 @@
 // each of those logits counts how many are ahead of it.  Keys are (value, ~token), so no two are
 // equal.  When there are too many (level logits) the K best stay, and equal logits with later
 // tokens than all that were there cannot come in.
-//   Candidates are compared in 48 bits: two beams' are sums of different scores.  All rows are
+//   Candidates are compared in 48 bits, none past the 53rd: two beams' are sums of different scores.  All rows are
 // cut at the same tokens, whatever their alignment, so that equal rows have equal sums, and equal
 // candidates of equal beams go to the lowest beam.
 //   A lane copies what it will look at (and its neighbour, where a row does not begin at 16
@@ -77,7 +77,10 @@ __device__ __forceinline__ float sum_of(float a, float b, float* left) {
     return s;
 }
 // A candidate, a logit, its row's largest one and the row's offset (two fp32 numbers, the second within
-// half a step of the first), as a key: the sum in 48 bits, an fp32 number and what its rounding left.
+// half a step of the first), as a key: the sum, an fp32 number and what its rounding left.  The two of them
+// can say more than 53 bits, where the second is far smaller: beside a logit of -1e30 or of the type's lowest
+// number, which stands for a token that is not allowed, a beam's score would still count, and such tokens of
+// all beams are level as 64-bit numbers.  So the rest is rounded to them.
 __device__ __forceinline__ unsigned long long sum_key(float x, float top, float2 off) {
     float e0, e;
     const float d = sum_of(x, -top, &e0);
@@ -87,6 +90,12 @@ __device__ __forceinline__ unsigned long long sum_key(float x, float top, float2
         const float t = s + e;
         e = e - (t - s);
         s = t;
+        // steps of 2^-52 of s's power of two (rests above 2^-30 of it have no finer bits but for one)
+        const uint32_t pow = __float_as_uint(s) & 0x7F800000u;
+        if (pow > (30u << 23) && fabsf(e) < __uint_as_float(pow - (30u << 23))) {
+            const float c = __uint_as_float((pow - (29u << 23)) | 0x00400000u);
+            e = (e + c) - c;
+        }
     } else {
         e = 0.f;
     }

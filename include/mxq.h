@@ -479,10 +479,11 @@ size_t mxq_kv_attention_shared_workspace_bytes(int T, int S, int N, int Hq, int 
  * others), count as -inf, which is a score like another: where there are fewer than K
  * above it the lowest w V + v of those follow.  -inf logits are tokens that are not
  * allowed.
- * Candidates are compared in 48 bits; sums over a row are fp32 in parts, which are
- * added in 64 bits (scores are within 2^-18 and their rounding, of rows of up to 2^20
- * tokens).  The result is
- * deterministic, and equal rows with equal scores have equal candidates.
+ * Candidates are compared in 48 bits and none past the 53rd: tokens whose logits are
+ * very low (-1e30, the type's lowest number) are level for all beams of a prompt.  Sums
+ * over a row are fp32 in parts, which are added in 64 bits (scores are within 2^-18 and
+ * their rounding, of rows of up to 2^20 tokens).  The result is deterministic, and equal
+ * rows with equal scores have equal candidates.
  * Requirements: 1 <= W <= 64, 1 <= K <= 64, K <= W V; V > 0, W V < 2^31 - 65536;
  * 0 <= end_token < V where done or out_done is given.                        */
 mxq_status mxq_beam_select(const void* logits, long long row_stride, int fp32, const float* scores,
