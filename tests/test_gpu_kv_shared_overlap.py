@@ -69,3 +69,33 @@ def test_one_long_sequence_among_short_ones(width):
     rows[17] = 300
     case = Case([100, 40], [25, 15], [max(r, 5 + i) for i, r in enumerate(rows)], rows, 8, 2, 128, 64, 32, seed=7)
     case.check()
+
+
+@pytest.mark.parametrize("starts", [[0, 1, 2, 3, 4, 5, 6, 9], [0, 1, 2, 3, 4, 2, 6, 7], [-3, 1, 2, 3, 4, 5, 6, 7], [5, 1, 5, 1, 5, 1, 5, 1],
+                                    [0, 2, 4, 7, 7, 7, 7, 7], [0, 1, 1, 3, 3, 5, 6, 7]])
+@pytest.mark.parametrize("groups", [[3, 4], [7, 0]])
+def test_sequences_beside_malformed_ones(width, groups, starts):
+    import affine_bit_matmul_gb300 as mxq
+
+    case = Case([100, 70], groups, [20] * 7, [1] * 7, 4, 1, 128, 64, 16, seed=16)
+    o, lse, st = case.run(q_starts=i32(starts), max_q_len=2)
+    fine = [0 <= a <= b <= 7 and b - a <= 2 for a, b in zip(starts[:-1], starts[1:])]
+    assert st == (0 if all(fine) else mxq.DEV_BAD_SEQUENCE)
+    of = {}  # row -> the sequences that have it
+    for i in np.flatnonzero(fine):
+        for row in range(starts[i], starts[i + 1]):
+            of.setdefault(row, []).append(i)
+    written = ~np.isnan(o).any((1, 2))
+    assert not written[[row for row in range(7) if row not in of]].any()
+    # where the starts of a group's first or last sequence are malformed its rows are not known
+    edges = np.concatenate([[0], np.cumsum(groups)])
+    known = [0 <= starts[a] <= starts[b] <= 7 for a, b in zip(edges[:-1], edges[1:])]
+    for row, seqs in of.items():
+        if len(seqs) > 1:
+            continue
+        i = seqs[0]
+        case.starts = np.asarray([starts[i]] * (i + 1) + [starts[i + 1]] * (7 - i), dtype=np.int32)
+        ref, ref_lse, tol, lse_tol = case.exact(128 ** -0.5)
+        right = written[row] and (np.abs(o - ref) <= tol)[row].all() and (np.abs(lse - ref_lse) <= lse_tol)[row].all()
+        inside = any(k and a <= i < b and starts[a] <= starts[i] and starts[i + 1] <= starts[b] for k, a, b in zip(known, edges[:-1], edges[1:]))
+        assert right if inside else right or not written[row]
